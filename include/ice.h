@@ -496,6 +496,206 @@ ice_status ice_decode_step(const ice_params *p, const ice_index *idx, const void
 ice_status ice_decode_plan(const ice_params *p, int32_t budget_tokens, int32_t max_sel, int32_t *step_plan,
                            int32_t *attention_plan);
 
+/* ------------------------------------------------- queries, keys, values -- */
+/*
+ * From a layer's projection to what the index and the caches take: the norm
+ * of queries and keys per head and the position rotation in one pass, in the
+ * layouts of the entry points below.
+ *
+ * A view of rows [B, T, heads, d] in device memory: row (b, t, h) starts
+ * b * batch + t * token + h * head elements behind data, its d elements
+ * contiguous.  data is 16-byte aligned and the strides are multiples of 16
+ * bytes, so one projection's output holds q, k and v side by side, and an
+ * output view may put heads before tokens (K, V [B, Hkv, N, d] of
+ * ice_build_index: batch = Hkv N d, token = d, head = N d).
+ */
+typedef struct ice_rows {
+    void *data;
+    int64_t batch, token, head; /* strides in elements, >= 0 */
+} ice_rows;
+
+/*
+ * Norm and rotation of q and k.
+ *   norm      (q_norm / k_norm not NULL: d weights of dtype, device memory)
+ *             r = 1 / sqrt(mean(x^2) + eps) over the head's d elements,
+ *             x <- (x r) w, in fp32;
+ *   rotation  (table not NULL) the first rotary_dim elements of a head in
+ *             pairs, (a, b) <- (a cos - b sin, b cos + a sin) in fp32: pair i
+ *             is (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved.
+ * Results are rounded once, to dtype.
+ */
+typedef struct ice_rope {
+    const float *table;   /* device [n_positions, rotary_dim / 2, 2]: cos, sin (ice_rope_table), 16-byte aligned */
+    int32_t n_positions;
+    int32_t rotary_dim;   /* a multiple of 16, 16 .. d */
+    int32_t interleaved;  /* 0 or 1 */
+    float eps;            /* >= 0 */
+    const void *q_norm, *k_norm; /* 16-byte aligned */
+} ice_rope;
+
+/*
+ * Fills table [n_positions, rotary_dim / 2, 2] with cos and sin of position *
+ * inv_freq[i] (inv_freq: device, rotary_dim / 2 doubles).  The angle and its
+ * cosine and sine are taken in fp64 and rounded once, so far positions keep
+ * their angle.  Once per model: the table depends on nothing else.
+ */
+ice_status ice_rope_table(const double *inv_freq, int32_t rotary_dim, int32_t n_positions, float *table,
+                          void *stream);
+
+/*
+ * Norm and rotation of the n_new tokens of every sequence, from q [B, n_new,
+ * Hq, d] and k, v [B, n_new, Hkv, d] to q_out, k_out, v_out (v is copied).
+ * The outputs are what ice_build_index (k_out, v_out as [B, Hkv, N, d]),
+ * ice_select_pages and ice_decode_step (q_out as [B, Hq, d], n_new = 1) and
+ * ice_insert_tokens (k_out, v_out as [B, Hkv, d], n_new = 1) take.  A NULL
+ * input (with its output NULL) is left out; rope may be NULL (a copy into
+ * another layout).  An output may be its input (same data and strides); other
+ * overlaps are not allowed.
+ *  - positions: device [B, n_new] int32, or NULL: token i of sequence b is at
+ *    position start[b] + i (start: device [B] int32; NULL means 0).
+ *  - counts: device [B] int32, or NULL: only the first counts[b] tokens of a
+ *    sequence are taken (clamped to 0 .. n_new); the rows behind them are
+ *    neither read nor written, in a padded batch.
+ *  - A position outside [0, n_positions) sets ICE_ERR_CAPACITY in err_dev and
+ *    leaves that token's rows of q_out, k_out and v_out as they were.
+ *  - n_new = 0 does nothing.
+ */
+ice_status ice_qkv_rope(const ice_params *p, int32_t n_new, const ice_rows *q, const ice_rows *k, const ice_rows *v,
+                        const int32_t *positions, const int32_t *start, const int32_t *counts, const ice_rope *rope,
+                        const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out, int32_t *err_dev,
+                        void *stream);
+
+/* ------------------------------------------------------ pages in 4 bits -- */
+/*
+ * A page of 16 tokens of one KV head as a 4-bit record of ICE_RECORD4_BYTES
+ * bytes (4.5 bits an element; 16 bf16 tokens take 8192 bytes).  The d
+ * elements of a row are two groups of 64; a group holds
+ *   step = bf16((max - min) / 15), mid = bf16((max + min) / 2),
+ *   code = clamp(rint((x - mid) / step + 7.5), 0, 15)   (0 when step = 0),
+ * and stands for mid + step (code - 7.5).  A group with an infinite or NaN
+ * element (or whose max - min overflows fp32) holds mid = NaN and stands for
+ * NaN throughout.  Bytes of a record:
+ *   [0, 1024)     K codes: 64 bytes a token; a 4-byte word holds 8 codes, the
+ *                 first in the lowest bits; the codes of elements 8 w .. 8 w +
+ *                 7 are word 4 (w % 4) + w / 4 of the token;
+ *   [1024, 1152)  K: (step, mid) of the token's two groups, bf16, 8 bytes a
+ *                 token;
+ *   [1152, 2176)  V codes: elements 4 p .. 4 p + 3 of token t are the half
+ *                 t % 2 (low first) of word ((t / 2) * 8 + p % 8) * 4 + p / 8;
+ *   [2176, 2304)  V: (step, mid), as K's.
+ */
+#define ICE_RECORD4_BYTES 2304
+
+/* Bytes of the 4-bit records of a unit's pool, [U, page_cap, ICE_RECORD4_BYTES]. */
+ice_status ice_pool4_bytes(const ice_params *p, size_t *bytes);
+
+/*
+ * The index's pool in 4 bits: page pg of unit u becomes record [u, pg] of
+ * records [U, page_cap, ICE_RECORD4_BYTES] (16-byte aligned, see
+ * ice_pool4_bytes), for the first n_pages[u] pages; pad slots become zero
+ * codes, step and mid.  With first_token > 0 only the tokens first_token ..
+ * n_indexed[u] - 1 of every unit are written, at their page and slot, and
+ * nothing else: after ice_insert_tokens, first_token = the token count before
+ * it.  (A new page's pad slots are then left as they were; no entry point
+ * reads them.)
+ * Reads idx->n_pages, page_len, pool_k and pool_v (device memory or a host
+ * pool's device pointers), with first_token > 0 n_indexed, token_page,
+ * token_slot, pool_k and pool_v; the other arrays of idx may be NULL.  The
+ * selection needs none of the pool: with the records written, the pool's own
+ * memory can be given back.
+ * A token whose page or slot lies outside the capacities sets
+ * ICE_ERR_CAPACITY in err_dev and is skipped.
+ */
+ice_status ice_pool4_pack(const ice_params *p, const ice_index *idx, int32_t first_token, void *records,
+                          int32_t *err_dev, void *stream);
+
+/* The other way: the values that the records of the first n_pages[u] pages
+ * stand for, rounded to dtype, into idx->pool_k and pool_v (pad slots zero).
+ * Reads idx->n_pages and page_len; the other arrays of idx may be NULL. */
+ice_status ice_pool4_unpack(const ice_params *p, const ice_index *idx, const void *records, int32_t *err_dev,
+                            void *stream);
+
+/*
+ * A token-ordered paged cache of 4-bit records: token i of sequence b is in
+ * slot i % 16 of block i / 16, whose page is table[b, i / 16]; record
+ * records[page, h] holds it for KV head h.  Sequences may share pages.  It
+ * holds the tokens that the semantic index does not: the window of newest
+ * tokens while the index covers the prompt, or all tokens of a layer that
+ * attends to everything.
+ */
+typedef struct ice_cache4 {
+    void *records;        /* device [n_pages, Hkv, ICE_RECORD4_BYTES], 16-byte aligned */
+    const int32_t *table; /* device [B, max_pages] int32 */
+    int32_t n_pages;      /* pages that records holds */
+    int32_t max_pages;    /* blocks a sequence can have */
+} ice_cache4;
+
+/*
+ * Appends the n_new tokens of every sequence: ice_qkv_rope's norm, rotation
+ * and rounding to dtype, then K and V in 4 bits into the cache at tokens
+ * start[b] .. start[b] + counts[b] - 1 (start: device [B] int32, required;
+ * counts as in ice_qkv_rope).  q (NULL: left out) goes to q_out as there.
+ * positions (NULL: the cache positions start[b] + i) gives the rotation's
+ * positions.  Only the appended tokens' bytes of a record are written: tokens
+ * before them and slots behind them stay as they were.  Tokens of one call
+ * must fall into different slots (two sequences that share a page they both
+ * append to do not).
+ * ICE_ERR_CAPACITY in err_dev, and that token left out, when its cache
+ * position is outside [0, 16 max_pages), its page outside [0, n_pages) or its
+ * rotation position outside [0, n_positions).
+ */
+ice_status ice_cache4_append(const ice_params *p, int32_t n_new, const ice_rows *q, const ice_rows *k,
+                             const ice_rows *v, const int32_t *positions, const int32_t *start, const int32_t *counts,
+                             const ice_rope *rope, const ice_rows *q_out, const ice_cache4 *cache, int32_t *err_dev,
+                             void *stream);
+
+/* The values that tokens start[b] .. start[b] + counts[b] - 1 (counts NULL:
+ * n_new) of the cache stand for, rounded to dtype, as rows (b, i, h) of k_out
+ * and v_out: the input of ice_build_index when a window moves into the index.
+ * Rows behind counts[b] and rows of tokens outside the cache (which set
+ * ICE_ERR_CAPACITY in err_dev) are left as they were. */
+ice_status ice_cache4_read(const ice_params *p, int32_t n_new, const ice_cache4 *cache, const int32_t *start,
+                           const int32_t *counts, const ice_rows *k_out, const ice_rows *v_out, int32_t *err_dev,
+                           void *stream);
+
+/* Workspace bytes of the two attention calls below (zero-filled once before
+ * its first use and left so by every call, like a decode workspace; calls
+ * that share one must not overlap on the GPU). */
+ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes);
+
+/*
+ * Attention of one query token a sequence over a token-ordered cache:
+ *   O[b, h] = sum_j exp(scale q . k_j) v_j / sum_j exp(scale q . k_j)
+ * over tokens j < lens[b] (device [B] int32; clamped to 0 .. 16 max_pages,
+ * ICE_ERR_CAPACITY in err_dev when it was outside).  Q [B, Hq, d] (dtype), O
+ * [B, Hq, d] float; lse [B, Hq] float or NULL: log sum_j exp(scale q . k_j),
+ * which joins this result with attention over other tokens.  A sequence of no
+ * token gives O = 0 and lse = -inf.  The pages are split evenly over the GPU,
+ * whatever the lengths; every run of a call gives the same bits.
+ * A page outside [0, n_pages) sets ICE_ERR_CAPACITY in err_dev and its tokens
+ * are left out.  A bounded wait that gives up sets ICE_ERR_TIMEOUT and leaves
+ * NaN in the rows it concerns.
+ */
+ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_cache4 *cache, const int32_t *lens,
+                                  float scale, float *O, float *lse, void *ws, size_t ws_bytes, int32_t *err_dev,
+                                  void *stream);
+
+/*
+ * Masked sparse attention (step a10, [A] 关键设计 1) over the selected pages
+ * of a 4-bit pool, read in place, and over a cache's tokens in the same
+ * softmax: unit u attends to the first page_len[u, pg] slots of each page pg
+ * = sel_pages[u, 0 .. sel_count[u]) ([U, max_sel], as ice_select_pages writes
+ * them) of records [U, page_cap, ICE_RECORD4_BYTES], and, with cache not
+ * NULL, to tokens j < lens[b] of the cache (the window of newest tokens, [B]
+ * section 六).  page_len [U, page_cap] int32 is the index's.  O, lse, scale
+ * and the device-side conditions as in ice_cache4_attn_decode; sel_count is
+ * clamped to 0 .. max_sel and page_len to 0 .. 16.
+ */
+ice_status ice_sparse_attn_decode4(const ice_params *p, const void *Q, const void *records, const int32_t *page_len,
+                                   const int32_t *sel_pages, const int32_t *sel_count, int32_t max_sel,
+                                   const ice_cache4 *cache, const int32_t *lens, float scale, float *O, float *lse,
+                                   void *ws, size_t ws_bytes, int32_t *err_dev, void *stream);
+
 /* ----------------------------------------------------- host page pool --- */
 /*
  * Step a12: the page pool in pinned host memory, with the selected pages of

@@ -52,6 +52,22 @@ class IceIndex(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in INDEX_FIELDS]
 
 
+class IceRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
+class IceRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_positions", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p)]
+
+
+class IceCache4(ctypes.Structure):
+    _fields_ = [("records", ctypes.c_void_p), ("table", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -66,6 +82,7 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     pp, pi = ctypes.POINTER(IceParams), ctypes.POINTER(IceIndex)
+    pr, po, pc = ctypes.POINTER(IceRows), ctypes.POINTER(IceRope), ctypes.POINTER(IceCache4)
     sigs = {
         "ice_status_string": ([i32], ctypes.c_char_p),
         "ice_last_error": ([], ctypes.c_char_p),
@@ -92,6 +109,16 @@ def load() -> ctypes.CDLL:
         "ice_sparse_attn_decode_noalloc": ([pp, P, P, P, P, P, i32, f32, P, P], i32),
         "ice_insert_workspace_bytes": ([pp, ctypes.POINTER(sz)], i32),
         "ice_insert_tokens": ([pp, pi, P, P, P, sz, P, P], i32),
+        "ice_rope_table": ([P, i32, i32, P, P], i32),
+        "ice_qkv_rope": ([pp, i32, pr, pr, pr, P, P, P, po, pr, pr, pr, P, P], i32),
+        "ice_cache4_append": ([pp, i32, pr, pr, pr, P, P, P, po, pr, pc, P, P], i32),
+        "ice_cache4_read": ([pp, i32, pc, P, P, pr, pr, P, P], i32),
+        "ice_pool4_bytes": ([pp, ctypes.POINTER(sz)], i32),
+        "ice_pool4_pack": ([pp, pi, i32, P, P, P], i32),
+        "ice_pool4_unpack": ([pp, pi, P, P, P], i32),
+        "ice_attn4_workspace_bytes": ([pp, ctypes.POINTER(sz)], i32),
+        "ice_cache4_attn_decode": ([pp, P, pc, P, f32, P, P, P, sz, P, P], i32),
+        "ice_sparse_attn_decode4": ([pp, P, P, P, P, P, i32, pc, P, f32, P, P, P, sz, P, P], i32),
         "ice_host_pool_create": ([sz, sz, i32, ctypes.POINTER(P)], i32),
         "ice_host_pool_destroy": ([P], i32),
         "ice_host_pool_pointers": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P)], i32),
@@ -114,7 +141,9 @@ def exported_symbols() -> list[str]:
             "ice_select_pages",
             "ice_gather_pages", "ice_sparse_attn_decode", "ice_sparse_attn_decode_noalloc", "ice_decode_step",
             "ice_decode_plan",
-            "ice_insert_workspace_bytes", "ice_insert_tokens", "ice_host_pool_create", "ice_host_pool_destroy",
+            "ice_insert_workspace_bytes", "ice_insert_tokens", "ice_rope_table", "ice_qkv_rope",
+            "ice_cache4_append", "ice_cache4_read", "ice_pool4_bytes", "ice_pool4_pack", "ice_pool4_unpack",
+            "ice_attn4_workspace_bytes", "ice_cache4_attn_decode", "ice_sparse_attn_decode4", "ice_host_pool_create", "ice_host_pool_destroy",
             "ice_host_pool_pointers", "ice_host_pool_staging_bytes", "ice_host_pool_gather_h2d"]
 
 
@@ -434,6 +463,121 @@ def ice_decode_plan(params, budget_tokens: int, max_sel: int) -> tuple[int, int]
     a, b = ctypes.c_int32(0), ctypes.c_int32(0)
     _check(load().ice_decode_plan(ctypes.byref(params), budget_tokens, max_sel, ctypes.byref(a), ctypes.byref(b)))
     return a.value, b.value
+
+
+# ------------------------------------------- rows, rotation, 4-bit pages --
+ICE_RECORD4_BYTES = 2304
+
+
+def rows(t: torch.Tensor) -> IceRows:
+    """A tensor [B, T, heads, d] (elements of a head contiguous, any other strides) as ice_rows; [B, heads, T, d]
+    tensors pass ``t.transpose(1, 2)``.  The tensor must outlive the view."""
+    if t.dim() != 4 or t.shape[-1] != HEAD_DIM or t.stride(-1) != 1:
+        raise IceError(ICE_ERR_INVALID_ARG, f"rows are [B, T, heads, {HEAD_DIM}] with contiguous elements: got "
+                                            f"{tuple(t.shape)}, strides {t.stride()}")
+    st = t.stride()
+    # the stride of a dimension of size 1 is never used
+    r = IceRows(t.data_ptr(), *(st[i] if t.shape[i] > 1 else 0 for i in range(3)))
+    r.keep = t
+    return r
+
+
+class Rope:
+    """ice_rope: cos/sin table [n_positions, rotary_dim / 2, 2] (fp32, see ice_rope_table) or None, and norm weights
+    [d] of q and k or None."""
+
+    def __init__(self, table=None, interleaved: bool = False, q_norm=None, k_norm=None, eps: float = 1e-6):
+        if table is not None and (table.dtype != torch.float32 or not table.is_contiguous() or table.dim() != 3 or
+                                  table.shape[2] != 2):
+            raise IceError(ICE_ERR_INVALID_ARG, "a rope table is a contiguous fp32 [n_positions, rotary_dim / 2, 2]")
+        for w in (q_norm, k_norm):
+            if w is not None and (tuple(w.shape) != (HEAD_DIM,) or not w.is_contiguous()):
+                raise IceError(ICE_ERR_INVALID_ARG, f"norm weights are contiguous [{HEAD_DIM}]")
+        n, half = (table.shape[0], table.shape[1]) if table is not None else (0, 0)
+        self.keep = (table, q_norm, k_norm)
+        self.struct = IceRope(_ptr(table), n, 2 * half, int(interleaved), eps, _ptr(q_norm), _ptr(k_norm))
+
+
+class Cache4:
+    """ice_cache4: records [n_pages, Hkv, ICE_RECORD4_BYTES] (uint8) and the block table [B, max_pages] (int32)."""
+
+    def __init__(self, records: torch.Tensor, table: torch.Tensor):
+        if records.dtype != torch.uint8 or records.dim() != 3 or records.shape[2] != ICE_RECORD4_BYTES or \
+                not records.is_contiguous():
+            raise IceError(ICE_ERR_INVALID_ARG, f"records are contiguous uint8 [n_pages, Hkv, {ICE_RECORD4_BYTES}]")
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
+            raise IceError(ICE_ERR_INVALID_ARG, "a block table is contiguous int32 [B, max_pages]")
+        self.keep = (records, table)
+        self.struct = IceCache4(records.data_ptr(), table.data_ptr(), records.shape[0], table.shape[1])
+
+
+def _ref(x):
+    """A struct (or its holder) by reference; None stays NULL."""
+    if x is None:
+        return None
+    return ctypes.byref(getattr(x, "struct", x))
+
+
+def ice_rope_table(inv_freq, n_positions: int, table, stream=None):
+    """table [n_positions, len(inv_freq), 2] fp32 from inv_freq (fp64, device)."""
+    if inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
+        raise IceError(ICE_ERR_INVALID_ARG, "inv_freq is contiguous fp64")
+    if table.dtype != torch.float32 or tuple(table.shape) != (n_positions, inv_freq.numel(), 2) or \
+            not table.is_contiguous():
+        raise IceError(ICE_ERR_INVALID_ARG, "table is contiguous fp32 [n_positions, len(inv_freq), 2]")
+    _check(load().ice_rope_table(_ptr(inv_freq), 2 * inv_freq.numel(), n_positions, _ptr(table), _stream(stream)))
+
+
+def ice_qkv_rope(params, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out, err, stream=None):
+    """q, k, v and the outputs are ``rows(...)`` views (or None), rope a Rope (or None)."""
+    _check(load().ice_qkv_rope(ctypes.byref(params), n_new, _ref(q), _ref(k), _ref(v), _ptr(positions), _ptr(start),
+                               _ptr(counts), _ref(rope), _ref(q_out), _ref(k_out), _ref(v_out), _ptr(err),
+                               _stream(stream)))
+
+
+def ice_cache4_append(params, n_new, q, k, v, positions, start, counts, rope, q_out, cache, err, stream=None):
+    _check(load().ice_cache4_append(ctypes.byref(params), n_new, _ref(q), _ref(k), _ref(v), _ptr(positions),
+                                    _ptr(start), _ptr(counts), _ref(rope), _ref(q_out), _ref(cache), _ptr(err),
+                                    _stream(stream)))
+
+
+def ice_cache4_read(params, n_new, cache, start, counts, k_out, v_out, err, stream=None):
+    _check(load().ice_cache4_read(ctypes.byref(params), n_new, _ref(cache), _ptr(start), _ptr(counts), _ref(k_out),
+                                  _ref(v_out), _ptr(err), _stream(stream)))
+
+
+def ice_pool4_bytes(params: IceParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ice_pool4_bytes(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def ice_pool4_pack(params, index, first_token: int, records, err, stream=None):
+    _check(load().ice_pool4_pack(ctypes.byref(params), _ref(index), first_token, _ptr(records), _ptr(err),
+                                 _stream(stream)))
+
+
+def ice_pool4_unpack(params, index, records, err, stream=None):
+    _check(load().ice_pool4_unpack(ctypes.byref(params), _ref(index), _ptr(records), _ptr(err), _stream(stream)))
+
+
+def ice_attn4_workspace_bytes(params: IceParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ice_attn4_workspace_bytes(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def ice_cache4_attn_decode(params, Q, cache, lens, scale, O, lse, ws, err, stream=None):
+    _check(load().ice_cache4_attn_decode(ctypes.byref(params), _ptr(Q), _ref(cache), _ptr(lens), float(scale), _ptr(O),
+                                         _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)))
+
+
+def ice_sparse_attn_decode4(params, Q, records, page_len, sel_pages, sel_count, cache, lens, scale, O, lse, ws, err,
+                            stream=None):
+    _check(load().ice_sparse_attn_decode4(ctypes.byref(params), _ptr(Q), _ptr(records), _ptr(page_len),
+                                          _ptr(sel_pages), _ptr(sel_count), sel_pages.shape[-1], _ref(cache),
+                                          _ptr(lens), float(scale), _ptr(O), _ptr(lse), _ptr(ws), _nbytes(ws),
+                                          _ptr(err), _stream(stream)))
 
 
 # ----------------------------------------------------- buffer helpers -----

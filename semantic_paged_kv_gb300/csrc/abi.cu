@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "common.cuh"
@@ -93,14 +94,17 @@ ice_status check_params(const ice_params *p) {
 
 bool aligned16(const void *x) { return ((uintptr_t)x & 15u) == 0; }
 
-ice_status check_index(const ice_index *x) {
+// with_pool = false: the pool may be NULL (the call does not read it).
+ice_status check_index(const ice_index *x, bool with_pool = true) {
     if (!x) return fail(ICE_ERR_INVALID_ARG, "index is NULL");
     const void *ptrs[] = {x->n_parents, x->n_pages, x->n_indexed, x->m2, x->parent_tok, x->parent_keys,
                           x->parent_e, x->parent_corr, x->parent_first_page, x->parent_last_page,
                           x->parent_n_pages, x->page_parent, x->page_len, x->page_next, x->page_tokens,
-                          x->token_parent, x->token_page, x->token_slot, x->pool_k, x->pool_v};
+                          x->token_parent, x->token_page, x->token_slot};
     for (const void *q : ptrs)
         if (!q) return fail(ICE_ERR_INVALID_ARG, "an ice_index array pointer is NULL");
+    for (const void *q : {x->pool_k, x->pool_v})
+        if (!q && with_pool) return fail(ICE_ERR_INVALID_ARG, "an ice_index array pointer is NULL");
     if (!aligned16(x->parent_keys) || !aligned16(x->pool_k) || !aligned16(x->pool_v))
         return fail(ICE_ERR_INVALID_ARG, "parent_keys, pool_k and pool_v must be 16-byte aligned");
     return ICE_OK;
@@ -510,8 +514,9 @@ ice_status ice_decode_workspace_bytes(const ice_params *p, int32_t budget_tokens
 }
 
 static ice_status select_checks(const ice_params *p, const ice_index *idx, const void *Q, int32_t budget_tokens,
-                                int32_t *sel_pages, int32_t *sel_count, int32_t max_sel, const DecodeWs &w) {
-    ice_status st = check_index(idx);
+                                int32_t *sel_pages, int32_t *sel_count, int32_t max_sel, const DecodeWs &w,
+                                bool with_pool) {
+    ice_status st = check_index(idx, with_pool);
     if (st) return st;
     if ((st = check_level2(p, idx))) return st;
     if (!Q || !sel_pages || !sel_count) return fail(ICE_ERR_INVALID_ARG, "Q, sel_pages and sel_count must be non-NULL");
@@ -539,7 +544,7 @@ ice_status ice_select_pages(const ice_params *p, const ice_index *idx, const voi
     DecodeWs w;
     ice_status st = decode_common(p, budget_tokens, max_sel, ws, ws_bytes, &w);
     if (st) return st;
-    if ((st = select_checks(p, idx, Q, budget_tokens, sel_pages, sel_count, max_sel, w))) return st;
+    if ((st = select_checks(p, idx, Q, budget_tokens, sel_pages, sel_count, max_sel, w, false))) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p->n_levels == 3)
         return cuda_status(launch_select3(*p, *idx, Q, w, sel_pages, sel_count, max_sel, err_dev, s),
@@ -603,7 +608,7 @@ ice_status ice_decode_step(const ice_params *p, const ice_index *idx, const void
     DecodeWs w;
     ice_status st = decode_common(p, budget_tokens, max_sel, ws, ws_bytes, &w);
     if (st) return st;
-    if ((st = select_checks(p, idx, Q, budget_tokens, sel_pages, sel_count, max_sel, w))) return st;
+    if ((st = select_checks(p, idx, Q, budget_tokens, sel_pages, sel_count, max_sel, w, true))) return st;
     if (!O) return fail(ICE_ERR_INVALID_ARG, "decode needs a non-NULL O");
     const bool no_buffer = !kbuf && !vbuf && !buf_len;  // pages gathered on chip only
     if (!no_buffer && (!kbuf || !vbuf || !buf_len))
@@ -663,6 +668,218 @@ ice_status ice_decode_plan(const ice_params *p, int32_t budget_tokens, int32_t m
     if (step_plan) *step_plan = decode_plan(*p, k_pages_of(budget_tokens), max_sel);
     if (attention_plan) *attention_plan = attention_mma_fits(*p, max_sel) ? ICE_PLAN_ATTN_MMA : ICE_PLAN_ATTN_SIMT;
     return ICE_OK;
+}
+
+// ------------------------------------------------- rows and 4-bit pages ----
+// A view of rows: 16-byte aligned base and strides, no negative stride.
+static ice_status check_rows(const ice_params *p, const ice_rows *r, const char *what) {
+    if (!r) return fail(ICE_ERR_INVALID_ARG, "%s is NULL", what);
+    if (!r->data || !aligned16(r->data))
+        return fail(ICE_ERR_INVALID_ARG, "%s must be a 16-byte aligned device pointer", what);
+    const int64_t vec = p->dtype == ICE_BF16 ? 8 : 4;
+    for (int64_t x : {r->batch, r->token, r->head})
+        if (x < 0 || x % vec)
+            return fail(ICE_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes and not negative", what);
+    return ICE_OK;
+}
+
+// Input and output views go together (both or neither).
+static ice_status check_rows_pair(const ice_params *p, const ice_rows *in, const ice_rows *out, const char *what,
+                                  const char *what_out) {
+    if (!in && !out) return ICE_OK;
+    ice_status st = check_rows(p, in, what);
+    return st ? st : check_rows(p, out, what_out);
+}
+
+static ice_status check_rope(const ice_rope *r) {
+    if (!r) return ICE_OK;
+    if (r->table) {
+        if (!aligned16(r->table)) return fail(ICE_ERR_INVALID_ARG, "rope table must be 16-byte aligned");
+        if (r->rotary_dim < 16 || r->rotary_dim > kHeadDim || r->rotary_dim % 16)
+            return fail(ICE_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 in 16 .. %d", kHeadDim);
+        if (r->n_positions < 1) return fail(ICE_ERR_INVALID_ARG, "n_positions must be >= 1");
+        if (r->interleaved != 0 && r->interleaved != 1)
+            return fail(ICE_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+    }
+    if ((r->q_norm && !aligned16(r->q_norm)) || (r->k_norm && !aligned16(r->k_norm)))
+        return fail(ICE_ERR_INVALID_ARG, "q_norm and k_norm must be 16-byte aligned");
+    if ((r->q_norm || r->k_norm) && !(r->eps >= 0.f)) return fail(ICE_ERR_INVALID_ARG, "eps must be >= 0");
+    return ICE_OK;
+}
+
+// n_new tokens a sequence; the launches' CTA counts stay within 2^31.
+static ice_status check_new(const ice_params *p, int32_t n_new) {
+    if (n_new < 0) return fail(ICE_ERR_INVALID_ARG, "n_new must be >= 0");
+    if ((long long)p->batch * n_new * (p->n_q_heads + 2ll * p->n_kv_heads) > (1ll << 32))
+        return fail(ICE_ERR_UNSUPPORTED, "too many rows in one call (batch * n_new * heads > 2^32)");
+    return ICE_OK;
+}
+
+static ice_status check_cache4(const ice_cache4 *c) {
+    if (!c) return fail(ICE_ERR_INVALID_ARG, "cache is NULL");
+    if (!c->records || !aligned16(c->records))
+        return fail(ICE_ERR_INVALID_ARG, "cache records must be a 16-byte aligned device pointer");
+    if (!c->table) return fail(ICE_ERR_INVALID_ARG, "cache table is NULL");
+    if (c->n_pages < 1 || c->max_pages < 1) return fail(ICE_ERR_INVALID_ARG, "n_pages and max_pages must be >= 1");
+    if (c->max_pages > (1 << 27) - 1)
+        return fail(ICE_ERR_UNSUPPORTED, "max_pages must be below 2^27 (token positions are int32)");
+    return ICE_OK;
+}
+
+ice_status ice_rope_table(const double *inv_freq, int32_t rotary_dim, int32_t n_positions, float *table,
+                          void *stream) {
+    if (!inv_freq || !table || !aligned16(table))
+        return fail(ICE_ERR_INVALID_ARG, "inv_freq and a 16-byte aligned table must be non-NULL");
+    if (rotary_dim < 16 || rotary_dim > kHeadDim || rotary_dim % 16)
+        return fail(ICE_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 in 16 .. %d", kHeadDim);
+    if (n_positions < 1) return fail(ICE_ERR_INVALID_ARG, "n_positions must be >= 1");
+    return cuda_status(launch_rope_table(inv_freq, rotary_dim, n_positions, table, static_cast<cudaStream_t>(stream)),
+                       "ice_rope_table");
+}
+
+ice_status ice_qkv_rope(const ice_params *p, int32_t n_new, const ice_rows *q, const ice_rows *k, const ice_rows *v,
+                        const int32_t *positions, const int32_t *start, const int32_t *counts, const ice_rope *rope,
+                        const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out, int32_t *err_dev,
+                        void *stream) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if ((st = check_new(p, n_new))) return st;
+    if ((st = check_rows_pair(p, q, q_out, "q", "q_out")) || (st = check_rows_pair(p, k, k_out, "k", "k_out")) ||
+        (st = check_rows_pair(p, v, v_out, "v", "v_out")) || (st = check_rope(rope)))
+        return st;
+    if (n_new == 0) return ICE_OK;
+    return cuda_status(launch_qkv_rope(*p, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out,
+                                       err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_qkv_rope");
+}
+
+ice_status ice_cache4_append(const ice_params *p, int32_t n_new, const ice_rows *q, const ice_rows *k,
+                             const ice_rows *v, const int32_t *positions, const int32_t *start, const int32_t *counts,
+                             const ice_rope *rope, const ice_rows *q_out, const ice_cache4 *cache, int32_t *err_dev,
+                             void *stream) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if ((st = check_new(p, n_new))) return st;
+    if ((st = check_rows_pair(p, q, q_out, "q", "q_out")) || (st = check_rows(p, k, "k")) ||
+        (st = check_rows(p, v, "v")) || (st = check_rope(rope)) || (st = check_cache4(cache)))
+        return st;
+    if (!start) return fail(ICE_ERR_INVALID_ARG, "start is NULL");
+    if (n_new == 0) return ICE_OK;
+    return cuda_status(launch_cache4_append(*p, n_new, q, k, v, positions, start, counts, rope, q_out, *cache, err_dev,
+                                            static_cast<cudaStream_t>(stream)),
+                       "ice_cache4_append");
+}
+
+ice_status ice_cache4_read(const ice_params *p, int32_t n_new, const ice_cache4 *cache, const int32_t *start,
+                           const int32_t *counts, const ice_rows *k_out, const ice_rows *v_out, int32_t *err_dev,
+                           void *stream) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if ((st = check_new(p, n_new))) return st;
+    if ((st = check_cache4(cache)) || (st = check_rows(p, k_out, "k_out")) || (st = check_rows(p, v_out, "v_out")))
+        return st;
+    if (!start) return fail(ICE_ERR_INVALID_ARG, "start is NULL");
+    if (n_new == 0) return ICE_OK;
+    return cuda_status(launch_cache4_read(*p, n_new, *cache, start, counts, *k_out, *v_out, err_dev,
+                                          static_cast<cudaStream_t>(stream)),
+                       "ice_cache4_read");
+}
+
+ice_status ice_pool4_bytes(const ice_params *p, size_t *bytes) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (!bytes) return fail(ICE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = (size_t)units_of(*p) * (size_t)p->page_cap * ICE_RECORD4_BYTES;
+    return ICE_OK;
+}
+
+// The index arrays, records and CTA count of the two conversions.
+static ice_status pool4_common(const ice_params *p, const ice_index *idx, const void *records) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (!idx) return fail(ICE_ERR_INVALID_ARG, "index is NULL");
+    if (!idx->pool_k || !idx->pool_v || !aligned16(idx->pool_k) || !aligned16(idx->pool_v))
+        return fail(ICE_ERR_INVALID_ARG, "pool_k and pool_v must be 16-byte aligned");
+    if (!records || !aligned16(records))
+        return fail(ICE_ERR_INVALID_ARG, "records must be a 16-byte aligned device pointer");
+    if ((long long)units_of(*p) * p->page_cap > (1ll << 31))
+        return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * page_cap > 2^31)");
+    return ICE_OK;
+}
+
+ice_status ice_pool4_pack(const ice_params *p, const ice_index *idx, int32_t first_token, void *records,
+                          int32_t *err_dev, void *stream) {
+    ice_status st = pool4_common(p, idx, records);
+    if (st) return st;
+    if (first_token < 0) return fail(ICE_ERR_INVALID_ARG, "first_token must be >= 0");
+    if (first_token == 0 && (!idx->n_pages || !idx->page_len))
+        return fail(ICE_ERR_INVALID_ARG, "n_pages and page_len must be non-NULL");
+    if (first_token > 0 && (!idx->n_indexed || !idx->token_page || !idx->token_slot))
+        return fail(ICE_ERR_INVALID_ARG, "n_indexed, token_page and token_slot must be non-NULL");
+    return cuda_status(launch_pool4_pack(*p, *idx, first_token, records, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_pool4_pack");
+}
+
+ice_status ice_pool4_unpack(const ice_params *p, const ice_index *idx, const void *records, int32_t *err_dev,
+                            void *stream) {
+    (void)err_dev;  // nothing the device can find here
+    ice_status st = pool4_common(p, idx, records);
+    if (st) return st;
+    if (!idx->n_pages || !idx->page_len) return fail(ICE_ERR_INVALID_ARG, "n_pages and page_len must be non-NULL");
+    return cuda_status(launch_pool4_unpack(*p, *idx, records, static_cast<cudaStream_t>(stream)), "ice_pool4_unpack");
+}
+
+ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (!bytes) return fail(ICE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = attn4_workspace(*p);
+    return ICE_OK;
+}
+
+static ice_status attn4_common(const ice_params *p, const void *Q, const float *O, const float *lse, void *ws,
+                               size_t ws_bytes) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (!Q || !O) return fail(ICE_ERR_INVALID_ARG, "attention needs non-NULL Q and O");
+    if (!aligned16(Q) || !aligned16(O)) return fail(ICE_ERR_INVALID_ARG, "Q and O must be 16-byte aligned");
+    if ((uintptr_t)lse & 3u) return fail(ICE_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+    return check_ws(ws, ws_bytes, attn4_workspace(*p));
+}
+
+ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_cache4 *cache, const int32_t *lens,
+                                  float scale, float *O, float *lse, void *ws, size_t ws_bytes, int32_t *err_dev,
+                                  void *stream) {
+    ice_status st = attn4_common(p, Q, O, lse, ws, ws_bytes);
+    if (st) return st;
+    if ((st = check_cache4(cache))) return st;
+    if (!lens) return fail(ICE_ERR_INVALID_ARG, "lens is NULL");
+    return cuda_status(launch_attn4(*p, Q, nullptr, nullptr, nullptr, nullptr, 0, cache, lens, scale, O, lse, ws,
+                                    err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_cache4_attn_decode");
+}
+
+ice_status ice_sparse_attn_decode4(const ice_params *p, const void *Q, const void *records, const int32_t *page_len,
+                                   const int32_t *sel_pages, const int32_t *sel_count, int32_t max_sel,
+                                   const ice_cache4 *cache, const int32_t *lens, float scale, float *O, float *lse,
+                                   void *ws, size_t ws_bytes, int32_t *err_dev, void *stream) {
+    ice_status st = attn4_common(p, Q, O, lse, ws, ws_bytes);
+    if (st) return st;
+    if (!records || !aligned16(records))
+        return fail(ICE_ERR_INVALID_ARG, "records must be a 16-byte aligned device pointer");
+    if (!page_len || !sel_pages || !sel_count)
+        return fail(ICE_ERR_INVALID_ARG, "page_len, sel_pages and sel_count must be non-NULL");
+    if (max_sel < 1) return fail(ICE_ERR_INVALID_ARG, "max_sel must be >= 1");
+    if (max_sel > (1 << 27) - 1) return fail(ICE_ERR_UNSUPPORTED, "max_sel must be below 2^27");
+    if (cache) {
+        if ((st = check_cache4(cache))) return st;
+        if (!lens) return fail(ICE_ERR_INVALID_ARG, "a cache needs lens");
+    } else if (lens) {
+        return fail(ICE_ERR_INVALID_ARG, "lens without a cache");
+    }
+    return cuda_status(launch_attn4(*p, Q, records, page_len, sel_pages, sel_count, max_sel, cache, lens, scale, O,
+                                    lse, ws, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_sparse_attn_decode4");
 }
 
 }  // extern "C"

@@ -188,6 +188,31 @@ cudaError_t launch_decode_cluster2(const ice_params &p, const ice_index &idx, co
                                    int32_t *sel_pages, int32_t *sel_count, int max_sel, void *kbuf, void *vbuf,
                                    int32_t *buf_len, float scale, float *O, int32_t *err, cudaStream_t s);
 
+// ------------------------------------------------- rows and 4-bit pages ----
+// Blocks of 16 cache slots that a run of n >= 1 tokens can touch.
+inline int cache4_blocks(int n) { return (int)(((long long)n + 2 * 15) / 16); }
+cudaError_t launch_rope_table(const double *inv_freq, int rotary_dim, int n_positions, float *table, cudaStream_t s);
+cudaError_t launch_qkv_rope(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k, const ice_rows *v,
+                            const int32_t *positions, const int32_t *start, const int32_t *counts,
+                            const ice_rope *rope, const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out,
+                            int32_t *err, cudaStream_t s);
+cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k,
+                                 const ice_rows *v, const int32_t *positions, const int32_t *start,
+                                 const int32_t *counts, const ice_rope *rope, const ice_rows *q_out,
+                                 const ice_cache4 &cache, int32_t *err, cudaStream_t s);
+cudaError_t launch_cache4_read(const ice_params &p, int n_new, const ice_cache4 &cache, const int32_t *start,
+                               const int32_t *counts, const ice_rows &k_out, const ice_rows &v_out, int32_t *err,
+                               cudaStream_t s);
+cudaError_t launch_pool4_pack(const ice_params &p, const ice_index &idx, int first_token, void *records, int32_t *err,
+                              cudaStream_t s);
+cudaError_t launch_pool4_unpack(const ice_params &p, const ice_index &idx, const void *records, cudaStream_t s);
+size_t attn4_workspace(const ice_params &p);
+// records NULL: no selected pages; cache NULL: no token-ordered pages.
+cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records, const int32_t *page_len,
+                         const int32_t *sel_pages, const int32_t *sel_count, int max_sel, const ice_cache4 *cache,
+                         const int32_t *lens, float scale, float *O, float *lse, void *ws, int32_t *err,
+                         cudaStream_t s);
+
 // Allocation-free attention: scratch in the library's static device array.
 size_t attention_noalloc_bytes(const ice_params &p, int max_sel);
 cudaError_t launch_attention_noalloc(const ice_params &p, const void *Q, const void *kbuf, const void *vbuf,

@@ -1,0 +1,253 @@
+// Semantic pages to 4-bit records and back, and rows out of a 4-bit cache.
+//
+// ice_pool4_pack: page pg of a unit -> its record; group extremes, step, mid
+// and codes as in ice.h.  ice_pool4_unpack and ice_cache4_read: mid + step
+// (code - 7.5), rounded to the storage type.
+//
+// All three move each page once, and are bound by HBM: a bf16 page is 8192
+// bytes, its record 2304.  One warp per page: 8 lanes a row (two 16-byte
+// vectors of a bf16 row each), four rows at a time; the record is put
+// together (or taken apart) in shared memory, because its V part interleaves
+// two tokens, and moved in 16-byte vectors.
+#include "common.cuh"
+#include "internal.h"
+#include "quant4.cuh"
+
+namespace ice {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kVecs = q4::kRecord / 16;
+
+// Rows [n, 128] of one page (n <= 16) into a record in shared memory.
+template <typename T>
+__device__ __forceinline__ void page_to_record(const T *kp, const T *vp, int len, unsigned char *rec) {
+    const int lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const T *src = which ? vp : kp;
+#pragma unroll
+        for (int it = 0; it < kPage / 4; ++it) {
+            const int t = it * 4 + row;
+            float a[8] = {}, b[8] = {};
+            if (t < len) {
+                load8<T>(src + t * kHeadDim + l * 8, a);
+                load8<T>(src + t * kHeadDim + (l + 8) * 8, b);
+            }
+            uint32_t ca, cb;
+            float2 sm[2];
+            q4::quantise_row<T>(a, b, l, l + 8, ca, cb, sm);
+            if (which)
+                q4::put_v(rec, t, l, l + 8, ca, cb);
+            else
+                q4::put_k(rec, t, l, l + 8, ca, cb);
+            if (l == 0)
+                *reinterpret_cast<uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + t * 8) = q4::pack_meta(sm);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_pool4_pack(const T *__restrict__ pool_k, const T *__restrict__ pool_v,
+                                                            const int32_t *__restrict__ n_pages,
+                                                            const int32_t *__restrict__ page_len, int page_cap,
+                                                            int per_unit, unsigned char *__restrict__ records) {
+    __shared__ __align__(16) unsigned char s_rec[kWarps][q4::kRecord];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int u = blockIdx.x / per_unit, pg = (blockIdx.x % per_unit) * kWarps + warp;
+    dep_wait();
+    if (pg >= min(n_pages[u], page_cap)) return;
+    const size_t at = (size_t)u * page_cap + pg;
+    const int len = min(max(page_len[at], 0), kPage);
+    page_to_record<T>(pool_k + at * kPage * kHeadDim, pool_v + at * kPage * kHeadDim, len, s_rec[warp]);
+    __syncwarp();
+    uint4 *dst = reinterpret_cast<uint4 *>(records + at * q4::kRecord);
+    const uint4 *src = reinterpret_cast<const uint4 *>(s_rec[warp]);
+    for (int i = lane; i < kVecs; i += 32) dst[i] = src[i];
+}
+
+// Tokens first .. n_indexed - 1 of every unit, one row of 8 lanes each.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_pool4_tokens(
+    const T *__restrict__ pool_k, const T *__restrict__ pool_v, const int32_t *__restrict__ n_indexed,
+    const int32_t *__restrict__ token_page, const int32_t *__restrict__ token_slot, int page_cap, int n_cap, int first,
+    unsigned char *__restrict__ records, int32_t *__restrict__ err) {
+    const int lane = threadIdx.x & 31, l = lane & 7;
+    const int u = blockIdx.x;
+    dep_wait();
+    const int n = min(n_indexed[u], n_cap);
+    // whole warps stay in the loop: the quantiser shuffles
+    for (int base = first + (threadIdx.x >> 5) * 4; base < n; base += kWarps * 4) {
+        const int tok = base + (lane >> 3);
+        int pg = -1, slot = 0;
+        if (tok < n) {
+            pg = token_page[(size_t)u * n_cap + tok];
+            slot = token_slot[(size_t)u * n_cap + tok];
+            if (pg < 0 || pg >= page_cap || slot < 0 || slot >= kPage) {
+                set_err(err, ICE_ERR_CAPACITY);
+                pg = -1;
+            }
+        }
+        const size_t at = (size_t)u * page_cap + (pg < 0 ? 0 : pg);
+        unsigned char *rec = records + at * q4::kRecord;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const T *src = (which ? pool_v : pool_k) + (at * kPage + slot) * kHeadDim;
+            float a[8] = {}, b[8] = {};
+            if (pg >= 0) {
+                load8<T>(src + l * 8, a);
+                load8<T>(src + (l + 8) * 8, b);
+            }
+            uint32_t ca, cb;
+            float2 sm[2];
+            q4::quantise_row<T>(a, b, l, l + 8, ca, cb, sm);
+            if (pg < 0) continue;
+            if (which)
+                q4::put_v(rec, slot, l, l + 8, ca, cb);
+            else
+                q4::put_k(rec, slot, l, l + 8, ca, cb);
+            if (l == 0)
+                *reinterpret_cast<uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + slot * 8) = q4::pack_meta(sm);
+        }
+    }
+}
+
+// The K (which = 0) or V vectors l and l + 8 of a token of a record in shared memory.
+__device__ __forceinline__ void row_values(const unsigned char *rec, int which, int t, int l, float (&a)[8],
+                                           float (&b)[8]) {
+    const uint2 m = *reinterpret_cast<const uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + t * 8);
+    q4::values_of(which ? q4::get_v(rec, t, l) : q4::get_k(rec, t, l), q4::unpack_meta(m.x), a);
+    q4::values_of(which ? q4::get_v(rec, t, l + 8) : q4::get_k(rec, t, l + 8), q4::unpack_meta(m.y), b);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_pool4_unpack(const unsigned char *__restrict__ records,
+                                                              const int32_t *__restrict__ n_pages,
+                                                              const int32_t *__restrict__ page_len, int page_cap,
+                                                              int per_unit, T *__restrict__ pool_k,
+                                                              T *__restrict__ pool_v) {
+    __shared__ __align__(16) unsigned char s_rec[kWarps][q4::kRecord];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
+    const int u = blockIdx.x / per_unit, pg = (blockIdx.x % per_unit) * kWarps + warp;
+    dep_wait();
+    if (pg >= min(n_pages[u], page_cap)) return;
+    const size_t at = (size_t)u * page_cap + pg;
+    const int len = min(max(page_len[at], 0), kPage);
+    const uint4 *src = reinterpret_cast<const uint4 *>(records + at * q4::kRecord);
+    uint4 *buf = reinterpret_cast<uint4 *>(s_rec[warp]);
+    for (int i = lane; i < kVecs; i += 32) buf[i] = src[i];
+    __syncwarp();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        T *dst = (which ? pool_v : pool_k) + at * kPage * kHeadDim;
+#pragma unroll
+        for (int it = 0; it < kPage / 4; ++it) {
+            const int t = it * 4 + row;
+            float a[8] = {}, b[8] = {};
+            if (t < len) row_values(s_rec[warp], which, t, l, a, b);
+            store8<T>(dst + t * kHeadDim + l * 8, a);
+            store8<T>(dst + t * kHeadDim + (l + 8) * 8, b);
+        }
+    }
+}
+
+// Tokens start .. start + count - 1 of a sequence, one warp per block of 16
+// cache slots and KV head.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32) k_cache4_read(const unsigned char *__restrict__ records,
+                                                             const int32_t *__restrict__ table, int n_pages,
+                                                             int max_pages, int n_kv_heads, int blocks, int n_new,
+                                                             const int32_t *__restrict__ start,
+                                                             const int32_t *__restrict__ counts, ice_rows k_out,
+                                                             ice_rows v_out, int32_t *__restrict__ err,
+                                                             long long n_items) {
+    __shared__ __align__(16) unsigned char s_rec[kWarps][q4::kRecord];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
+    const long long item = (long long)blockIdx.x * kWarps + warp;
+    dep_wait();
+    if (item >= n_items) return;
+    const int h = (int)(item % n_kv_heads);
+    const int x = (int)(item / n_kv_heads % blocks);
+    const int b = (int)(item / n_kv_heads / blocks);
+    const long long s0 = start[b];
+    const int cnt = counts ? min(max(counts[b], 0), n_new) : n_new;
+    const long long blk = (s0 >> 4) + x;  // block of 16 cache slots (floor also for a negative start)
+    const long long t0 = blk * kPage;
+    const long long ta = t0 > s0 ? t0 : s0, tb = t0 + kPage < s0 + cnt ? t0 + kPage : s0 + cnt;
+    if (ta >= tb) return;
+    int pg = -1;
+    if (blk >= 0 && blk < max_pages) pg = table[(size_t)b * max_pages + blk];
+    if (pg < 0 || pg >= n_pages) {
+        if (lane == 0) set_err(err, ICE_ERR_CAPACITY);
+        return;
+    }
+    const uint4 *src = reinterpret_cast<const uint4 *>(records + ((size_t)pg * n_kv_heads + h) * q4::kRecord);
+    uint4 *buf = reinterpret_cast<uint4 *>(s_rec[warp]);
+    for (int i = lane; i < kVecs; i += 32) buf[i] = src[i];
+    __syncwarp();
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const ice_rows &o = which ? v_out : k_out;
+#pragma unroll
+        for (int it = 0; it < kPage / 4; ++it) {
+            const int t = it * 4 + row;
+            if (t0 + t < ta || t0 + t >= tb) continue;
+            float a[8], c[8];
+            row_values(s_rec[warp], which, t, l, a, c);
+            T *dst = static_cast<T *>(o.data) + b * o.batch + (t0 + t - s0) * o.token + h * o.head;
+            store8<T>(dst + l * 8, a);
+            store8<T>(dst + (l + 8) * 8, c);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t pack_t(const ice_params &p, const ice_index &idx, int first, void *records, int32_t *err, cudaStream_t s) {
+    const T *k = static_cast<const T *>(idx.pool_k), *v = static_cast<const T *>(idx.pool_v);
+    unsigned char *r = static_cast<unsigned char *>(records);
+    if (first > 0)
+        return launch_dependent(k_pool4_tokens<T>, dim3(units_of(p)), dim3(kWarps * 32), 0, s, k, v, idx.n_indexed,
+                                idx.token_page, idx.token_slot, p.page_cap, p.n_cap, first, r, err);
+    const int per_unit = ceil_div(p.page_cap, kWarps);
+    return launch_dependent(k_pool4_pack<T>, dim3((unsigned)per_unit * units_of(p)), dim3(kWarps * 32), 0, s, k, v,
+                            idx.n_pages, idx.page_len, p.page_cap, per_unit, r);
+}
+
+template <typename T>
+cudaError_t unpack_t(const ice_params &p, const ice_index &idx, const void *records, cudaStream_t s) {
+    const int per_unit = ceil_div(p.page_cap, kWarps);
+    return launch_dependent(k_pool4_unpack<T>, dim3((unsigned)per_unit * units_of(p)), dim3(kWarps * 32), 0, s,
+                            static_cast<const unsigned char *>(records), idx.n_pages, idx.page_len, p.page_cap,
+                            per_unit, static_cast<T *>(idx.pool_k), static_cast<T *>(idx.pool_v));
+}
+
+template <typename T>
+cudaError_t read_t(const ice_params &p, int n_new, const ice_cache4 &c, const int32_t *start, const int32_t *counts,
+                   const ice_rows &k_out, const ice_rows &v_out, int32_t *err, cudaStream_t s) {
+    const int blocks = cache4_blocks(n_new);
+    const long long items = (long long)p.batch * blocks * p.n_kv_heads;
+    return launch_dependent(k_cache4_read<T>, dim3((unsigned)ceil_div(items, kWarps)), dim3(kWarps * 32), 0, s,
+                            static_cast<const unsigned char *>(c.records), c.table, c.n_pages, c.max_pages,
+                            p.n_kv_heads, blocks, n_new, start, counts, k_out, v_out, err, items);
+}
+
+}  // namespace
+
+cudaError_t launch_pool4_pack(const ice_params &p, const ice_index &idx, int first_token, void *records, int32_t *err,
+                              cudaStream_t s) {
+    return p.dtype == ICE_BF16 ? pack_t<__nv_bfloat16>(p, idx, first_token, records, err, s)
+                               : pack_t<float>(p, idx, first_token, records, err, s);
+}
+
+cudaError_t launch_pool4_unpack(const ice_params &p, const ice_index &idx, const void *records, cudaStream_t s) {
+    return p.dtype == ICE_BF16 ? unpack_t<__nv_bfloat16>(p, idx, records, s) : unpack_t<float>(p, idx, records, s);
+}
+
+cudaError_t launch_cache4_read(const ice_params &p, int n_new, const ice_cache4 &cache, const int32_t *start,
+                               const int32_t *counts, const ice_rows &k_out, const ice_rows &v_out, int32_t *err,
+                               cudaStream_t s) {
+    return p.dtype == ICE_BF16 ? read_t<__nv_bfloat16>(p, n_new, cache, start, counts, k_out, v_out, err, s)
+                               : read_t<float>(p, n_new, cache, start, counts, k_out, v_out, err, s);
+}
+
+}  // namespace ice

@@ -1,0 +1,411 @@
+// Queries, keys and values from a layer's projection: the norm per head and
+// the position rotation in one pass (ice_qkv_rope), and the same with K and V
+// appended to a paged cache in 4 bits (ice_cache4_append).
+//
+//   norm      y = (x r) w, r = 1 / sqrt(mean(x^2) + eps); the sum of squares
+//             is an error-free double-float sum, so r is the correctly
+//             rounded value;
+//   rotation  (a, b) <- (a cos - b sin, b cos + a sin), each product rounded
+//             once (no contraction).  Keys of an fp32 cache take fp64
+//             products: their codes are decided as if exactly.
+//
+// Both are bound by HBM for prompts (each row read and written once) and by
+// latency for single tokens.  8 lanes hold a row as two 8-element vectors: for
+// pairs (i, i + rotary_dim / 2) vectors l and l + rotary_dim / 16, so that
+// both elements of a pair are in one lane and nothing is exchanged but the
+// norm's sum.  k_qkv_rope: 8 lanes take four heads of one token, whose cos and
+// sin stay in registers; all loads are issued before the arithmetic.
+// k_cache4_append: its first CTAs take the queries that way; then one warp per
+// block of 16 cache slots and KV head quantises up to 16 rows, four at a time,
+// into a record in shared memory, and writes the record (all 16 slots new) or
+// only the new tokens' bytes of it.
+#include "common.cuh"
+#include "internal.h"
+#include "quant4.cuh"
+
+namespace ice {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kGroups = kThreads / 8;  // rows in flight per CTA
+constexpr int kHeads = 4;              // heads per lane group
+
+struct RopeArgs {
+    ice_rows q, k, v, qo, ko, vo;
+    int nq, nk;  // chunks of kHeads heads of q and of k (v's come after them)
+    int hq, hkv, n_new;
+    const int32_t *positions, *start, *counts;
+    const float *table;
+    int n_positions, rotary, interleaved;
+    float eps;
+    const void *wq, *wk;
+    int32_t *err;
+};
+
+// Which vectors of a row a lane holds, and which of them are rotated.
+struct LaneVecs {
+    int wa, wb;
+    bool ra, rb;
+};
+__device__ __forceinline__ LaneVecs lane_vecs(const RopeArgs &A, int l) {
+    LaneVecs v;
+    const int rd = A.table ? A.rotary : 0;
+    if (A.interleaved || rd == 0) {
+        v.wa = l, v.wb = l + 8;
+        v.ra = v.wa * 8 < rd, v.rb = v.wb * 8 < rd;
+    } else {
+        const int nv = rd / 16;  // vectors of half the rotated elements
+        const bool r = l < nv;
+        v.wa = r ? l : rd / 8 + 2 * (l - nv);
+        v.wb = r ? l + nv : v.wa + 1;
+        v.ra = v.rb = r;
+    }
+    return v;
+}
+
+// cos and sin of a lane's 8 pairs.
+__device__ __forceinline__ void load_angles(const RopeArgs &A, const LaneVecs &v, int pos, float (&c)[8],
+                                            float (&s)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    const float *row = A.table + (size_t)pos * A.rotary;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // pairs 8 wa ..; interleaved: pairs 4 wa .. of vector A, then 4 wb .. of B
+        const bool on = A.interleaved ? (i < 2 ? v.ra : v.rb) : v.ra;
+        const int pair = A.interleaved ? (i < 2 ? 4 * v.wa + 2 * i : 4 * v.wb + 2 * (i - 2)) : 8 * v.wa + 2 * i;
+        if (on) {
+            const float4 f = *reinterpret_cast<const float4 *>(row + 2 * pair);
+            c[2 * i] = f.x, s[2 * i] = f.y, c[2 * i + 1] = f.z, s[2 * i + 1] = f.w;
+        }
+    }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void rotate_pair(float &a, float &b, float c, float s) {
+    if (kWide) {
+        const double x = (double)a * c - (double)b * s, y = (double)b * c + (double)a * s;
+        a = (float)x, b = (float)y;
+    } else {
+        const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+        a = x, b = y;
+    }
+}
+
+template <bool kWide>
+__device__ __forceinline__ void rotate(const RopeArgs &A, const LaneVecs &v, float (&a)[8], float (&b)[8],
+                                       const float (&c)[8], const float (&s)[8]) {
+    if (A.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (v.ra) rotate_pair<kWide>(a[2 * i], a[2 * i + 1], c[i], s[i]);
+            if (v.rb) rotate_pair<kWide>(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
+        }
+    } else if (v.ra) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rotate_pair<kWide>(a[e], b[e], c[e], s[e]);
+    }
+}
+
+// x <- (x r) w over the 8 lanes of a row (every lane of the warp calls it).
+template <typename T>
+__device__ __forceinline__ void norm_row(float (&a)[8], float (&b)[8], const float (&wa)[8], const float (&wb)[8],
+                                         float eps, bool on) {
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float f = e < 8 ? a[e & 7] : b[e & 7];
+        const float t = __fmul_rn(f, f);
+        float sum, er;
+        two_sum(hi, t, sum, er);
+        hi = sum;
+        lo += sizeof(T) == 2 ? er : er + fmaf(f, f, -t);  // bf16 squares are exact
+    }
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) {
+        const float ohi = __shfl_xor_sync(0xffffffffu, hi, off), olo = __shfl_xor_sync(0xffffffffu, lo, off);
+        float sum, er;
+        two_sum(hi, ohi, sum, er);
+        hi = sum;
+        lo += olo + er;
+    }
+    // an overflowed sum is infinite (its error terms are not numbers): r = 0, as in plain fp32
+    const float total = isfinite(hi) ? hi + lo : hi;
+    const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(total, 1.f / kHeadDim), eps));
+    if (on) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = __fmul_rn(__fmul_rn(a[e], r), wa[e]);
+            b[e] = __fmul_rn(__fmul_rn(b[e], r), wb[e]);
+        }
+    }
+}
+
+// Position of token i of sequence b; -1 when the table does not hold it.
+__device__ __forceinline__ int position_of(const RopeArgs &A, int b, int i) {
+    if (!A.table) return 0;
+    const long long pos = A.positions ? (long long)A.positions[(size_t)b * A.n_new + i]
+                                      : (long long)(A.start ? A.start[b] : 0) + i;
+    return pos >= 0 && pos < A.n_positions ? (int)pos : -1;
+}
+
+__device__ __forceinline__ int count_of(const RopeArgs &A, int b) {
+    return A.counts ? min(max(A.counts[b], 0), A.n_new) : A.n_new;
+}
+
+// Heads chunk * kHeads .. of token (b, i): q, then k, then v.  Every lane of
+// the warp calls it (the norm shuffles); `live` lanes have a token.
+template <typename T>
+__device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int chunk, bool live) {
+    const int l = threadIdx.x & 7;
+    const int kind = chunk < A.nq ? 0 : (chunk < A.nq + A.nk ? 1 : 2);
+    const int h0 = (kind == 0 ? chunk : (kind == 1 ? chunk - A.nq : chunk - A.nq - A.nk)) * kHeads;
+    const int heads = kind == 0 ? A.hq : A.hkv;
+    const ice_rows &in = kind == 0 ? A.q : (kind == 1 ? A.k : A.v);
+    const ice_rows &out = kind == 0 ? A.qo : (kind == 1 ? A.ko : A.vo);
+    int pos = 0;
+    if (live) {
+        live = i < count_of(A, b);
+        pos = live ? position_of(A, b, i) : 0;
+        if (pos < 0) {
+            set_err(A.err, ICE_ERR_CAPACITY);
+            live = false;
+        }
+    }
+    const LaneVecs v = lane_vecs(A, l);
+    const T *src = static_cast<const T *>(in.data) + (long long)b * in.batch + (long long)i * in.token;
+    T *dst = static_cast<T *>(out.data) + (long long)b * out.batch + (long long)i * out.token;
+    float a[kHeads][8], c[kHeads][8];
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[j][e] = c[j][e] = 0.f;
+        if (live && h0 + j < heads) {
+            load8<T>(src + (h0 + j) * in.head + v.wa * 8, a[j]);
+            load8<T>(src + (h0 + j) * in.head + v.wb * 8, c[j]);
+        }
+    }
+    const bool turn = live && kind != 2 && A.table;
+    float co[8], si[8];
+    if (turn) load_angles(A, v, pos, co, si);
+    const T *w = static_cast<const T *>(kind == 0 ? A.wq : A.wk);
+    const bool norm = kind != 2 && w;
+    float wa[8] = {}, wb[8] = {};
+    if (norm) {
+        load8<T>(w + v.wa * 8, wa);
+        load8<T>(w + v.wb * 8, wb);
+    }
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j) {
+        if (A.wq || A.wk) norm_row<T>(a[j], c[j], wa, wb, A.eps, norm);
+        if (turn) rotate<false>(A, v, a[j], c[j], co, si);
+        if (live && h0 + j < heads) {
+            store8<T>(dst + (h0 + j) * out.head + v.wa * 8, a[j]);
+            store8<T>(dst + (h0 + j) * out.head + v.wb * 8, c[j]);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_qkv_rope(const __grid_constant__ RopeArgs A, long long n_items,
+                                                       int n_chunks) {
+    dep_wait();
+    const long long item = (long long)blockIdx.x * kGroups + threadIdx.x / 8;
+    const bool live = item < n_items;
+    const long long at = live ? item : 0;
+    const long long tok = at / n_chunks;
+    dense_chunk<T>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % n_chunks), live);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constant__ RopeArgs A, long long q_items,
+                                                            int q_blocks, long long n_items, int blocks,
+                                                            unsigned char *__restrict__ records,
+                                                            const int32_t *__restrict__ table, int n_pages,
+                                                            int max_pages) {
+    __shared__ __align__(16) unsigned char s_rec[kThreads / 32][q4::kRecord];
+    dep_wait();
+    if ((int)blockIdx.x < q_blocks) {  // the queries
+        const long long item = (long long)blockIdx.x * kGroups + threadIdx.x / 8;
+        const bool live = item < q_items;
+        const long long at = live ? item : 0;
+        const long long tok = at / A.nq;
+        dense_chunk<T>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % A.nq), live);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
+    const long long item = (long long)(blockIdx.x - q_blocks) * (kThreads / 32) + warp;
+    if (item >= n_items) return;
+    const int h = (int)(item % A.hkv);
+    const int x = (int)(item / A.hkv % blocks);
+    const int b = (int)(item / A.hkv / blocks);
+    const long long s0 = A.start[b];
+    const int cnt = count_of(A, b);
+    const long long blk = (s0 >> 4) + x;  // block of 16 cache slots (floor also for a negative start)
+    const long long t0 = blk * kPage;
+    const long long ta = t0 > s0 ? t0 : s0, tb = t0 + kPage < s0 + cnt ? t0 + kPage : s0 + cnt;
+    if (ta >= tb) return;
+    int pg = -1;
+    if (blk >= 0 && blk < max_pages) pg = table[(size_t)b * max_pages + blk];
+    if (pg < 0 || pg >= n_pages) {
+        if (lane == 0) set_err(A.err, ICE_ERR_CAPACITY);
+        return;
+    }
+    unsigned char *rec = s_rec[warp];
+    const LaneVecs v = lane_vecs(A, l);
+    const T *w = static_cast<const T *>(A.wk);
+    float wa[8] = {}, wb[8] = {};
+    if (w) {
+        load8<T>(w + v.wa * 8, wa);
+        load8<T>(w + v.wb * 8, wb);
+    }
+    unsigned done = 0;  // tokens of the block that are written
+#pragma unroll
+    for (int it = 0; it < kPage / 4; ++it) {
+        const int t = it * 4 + row;
+        bool live = t0 + t >= ta && t0 + t < tb;
+        const int i = live ? (int)(t0 + t - s0) : 0;
+        int pos = 0;
+        if (live) {
+            pos = position_of(A, b, i);
+            if (pos < 0) {
+                set_err(A.err, ICE_ERR_CAPACITY);
+                live = false;
+            }
+        }
+        const unsigned rows = __ballot_sync(0xffffffffu, live);
+        if (!rows) continue;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (rows >> (8 * r) & 1u) done |= 1u << (it * 4 + r);
+        float a[8] = {}, c[8] = {}, va[8] = {}, vc[8] = {};
+        if (live) {
+            const T *ks = static_cast<const T *>(A.k.data) + b * A.k.batch + i * A.k.token + h * A.k.head;
+            const T *vs = static_cast<const T *>(A.v.data) + b * A.v.batch + i * A.v.token + h * A.v.head;
+            load8<T>(ks + v.wa * 8, a);
+            load8<T>(ks + v.wb * 8, c);
+            load8<T>(vs + l * 8, va);
+            load8<T>(vs + (l + 8) * 8, vc);
+        }
+        if (w) norm_row<T>(a, c, wa, wb, A.eps, true);
+        if (live && A.table) {
+            float co[8], si[8];
+            load_angles(A, v, pos, co, si);
+            rotate<sizeof(T) == 4>(A, v, a, c, co, si);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = round_to<T>(a[e]), c[e] = round_to<T>(c[e]);
+        uint32_t ca, cb;
+        float2 sm[2];
+        q4::quantise_row<T>(a, c, v.wa, v.wb, ca, cb, sm);
+        q4::put_k(rec, t, v.wa, v.wb, ca, cb);
+        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kKMeta + t * 8) = q4::pack_meta(sm);
+        q4::quantise_row<T>(va, vc, l, l + 8, ca, cb, sm);
+        q4::put_v(rec, t, l, l + 8, ca, cb);
+        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kVMeta + t * 8) = q4::pack_meta(sm);
+    }
+    __syncwarp();
+    unsigned char *out = records + ((size_t)pg * A.hkv + h) * q4::kRecord;
+    if (done == 0xFFFFu) {
+        for (int i = lane; i < q4::kRecord / 16; i += 32)
+            reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(rec)[i];
+        return;
+    }
+    // only the new tokens: K rows of four 16-byte vectors, the (step, mid) pairs, V in 2-byte pieces
+#pragma unroll
+    for (int i = lane; i < kPage * 4; i += 32)
+        if (done >> (i >> 2) & 1u) reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(rec)[i];
+    {
+        const int t = lane & 15, off = (lane < 16 ? q4::kKMeta : q4::kVMeta) + t * 8;
+        if (done >> t & 1u) *reinterpret_cast<uint2 *>(out + off) = *reinterpret_cast<const uint2 *>(rec + off);
+    }
+    for (unsigned m = done; m; m &= m - 1) {
+        const int off = q4::v_piece(__ffs(m) - 1, lane);
+        *reinterpret_cast<uint16_t *>(out + off) = *reinterpret_cast<const uint16_t *>(rec + off);
+    }
+}
+
+__global__ void k_rope_table(const double *__restrict__ inv_freq, int half, long long n, float2 *__restrict__ table) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    double s, c;
+    sincos((double)(i / half) * inv_freq[i % half], &s, &c);
+    table[i] = make_float2((float)c, (float)s);
+}
+
+RopeArgs rope_args(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k, const ice_rows *v,
+                   const int32_t *positions, const int32_t *start, const int32_t *counts, const ice_rope *rope,
+                   const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out, int32_t *err) {
+    RopeArgs A{};
+    if (q) A.q = *q;
+    if (k) A.k = *k;
+    if (v) A.v = *v;
+    if (q_out) A.qo = *q_out;
+    if (k_out) A.ko = *k_out;
+    if (v_out) A.vo = *v_out;
+    A.hq = p.n_q_heads;
+    A.hkv = p.n_kv_heads;
+    A.n_new = n_new;
+    A.positions = positions;
+    A.start = start;
+    A.counts = counts;
+    if (rope) {
+        A.table = rope->table;
+        A.n_positions = rope->n_positions;
+        A.rotary = rope->rotary_dim;
+        A.interleaved = rope->interleaved;
+        A.eps = rope->eps;
+        A.wq = rope->q_norm;
+        A.wk = rope->k_norm;
+    }
+    A.err = err;
+    return A;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const double *inv_freq, int rotary_dim, int n_positions, float *table, cudaStream_t s) {
+    const long long n = (long long)n_positions * (rotary_dim / 2);
+    k_rope_table<<<(unsigned)ceil_div(n, 256), 256, 0, s>>>(inv_freq, rotary_dim / 2, n,
+                                                           reinterpret_cast<float2 *>(table));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_qkv_rope(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k, const ice_rows *v,
+                            const int32_t *positions, const int32_t *start, const int32_t *counts,
+                            const ice_rope *rope, const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out,
+                            int32_t *err, cudaStream_t s) {
+    RopeArgs A = rope_args(p, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out, err);
+    const int per = ceil_div(p.n_kv_heads, kHeads);
+    A.nq = q ? ceil_div(p.n_q_heads, kHeads) : 0;
+    A.nk = k ? per : 0;
+    const int n_chunks = A.nq + A.nk + (v ? per : 0);
+    if (!n_chunks) return cudaSuccess;
+    const long long items = (long long)p.batch * n_new * n_chunks;
+    const dim3 grid((unsigned)ceil_div(items, kGroups));
+    if (p.dtype == ICE_BF16)
+        return launch_dependent(k_qkv_rope<__nv_bfloat16>, grid, dim3(kThreads), 0, s, A, items, n_chunks);
+    return launch_dependent(k_qkv_rope<float>, grid, dim3(kThreads), 0, s, A, items, n_chunks);
+}
+
+cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k,
+                                 const ice_rows *v, const int32_t *positions, const int32_t *start,
+                                 const int32_t *counts, const ice_rope *rope, const ice_rows *q_out,
+                                 const ice_cache4 &cache, int32_t *err, cudaStream_t s) {
+    RopeArgs A = rope_args(p, n_new, q, k, v, positions, start, counts, rope, q_out, nullptr, nullptr, err);
+    A.nq = q ? ceil_div(p.n_q_heads, kHeads) : 0;
+    const long long q_items = (long long)p.batch * n_new * A.nq;
+    const int q_blocks = ceil_div(q_items, kGroups);
+    const int blocks = cache4_blocks(n_new);
+    const long long items = (long long)p.batch * blocks * p.n_kv_heads;
+    const dim3 grid((unsigned)(q_blocks + ceil_div(items, kThreads / 32)));
+    unsigned char *r = static_cast<unsigned char *>(cache.records);
+    if (p.dtype == ICE_BF16)
+        return launch_dependent(k_cache4_append<__nv_bfloat16>, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items,
+                                blocks, r, cache.table, cache.n_pages, cache.max_pages);
+    return launch_dependent(k_cache4_append<float>, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items, blocks, r,
+                            cache.table, cache.n_pages, cache.max_pages);
+}
+
+}  // namespace ice
