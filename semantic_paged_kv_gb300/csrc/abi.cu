@@ -854,6 +854,8 @@ ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_
     if (st) return st;
     if ((st = check_cache4(cache))) return st;
     if (!lens) return fail(ICE_ERR_INVALID_ARG, "lens is NULL");
+    if ((long long)units_of(*p) * cache->max_pages > (1ll << 38))
+        return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * max_pages > 2^38)");
     return cuda_status(launch_attn4(*p, Q, nullptr, nullptr, nullptr, nullptr, 0, cache, lens, scale, O, lse, ws,
                                     err_dev, static_cast<cudaStream_t>(stream)),
                        "ice_cache4_attn_decode");
@@ -877,6 +879,8 @@ ice_status ice_sparse_attn_decode4(const ice_params *p, const void *Q, const voi
     } else if (lens) {
         return fail(ICE_ERR_INVALID_ARG, "lens without a cache");
     }
+    if ((long long)units_of(*p) * (max_sel + (cache ? (long long)cache->max_pages : 0)) > (1ll << 38))
+        return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * pages > 2^38)");
     return cuda_status(launch_attn4(*p, Q, records, page_len, sel_pages, sel_count, max_sel, cache, lens, scale, O,
                                     lse, ws, err_dev, static_cast<cudaStream_t>(stream)),
                        "ice_sparse_attn_decode4");

@@ -5,17 +5,50 @@
 // papernotes.org "IceCache: Memory-Efficient KV-cache Management for
 // Long-Sequence LLMs", 关键设计 1, over the unit's pages only.
 //
-// One CTA per unit, one warp per page at a time: two lanes a token for the
-// scores (one group of 64 each), four elements a lane for the values.
+// Bound by HBM (a page of 16 tokens of one KV head is one 2304-byte record,
+// read once), and next to that by instruction issue: at the measured copy rate
+// an SM gets a page every ~100 clocks.
+//
+// Work: the pages of all units, one after another, are cut into equal runs,
+// one per CTA, whatever the units' lengths; a unit that a run cuts leaves
+// partial results in the workspace, joined by its last CTA in run order (so
+// the bits do not depend on timing).  Inside a CTA page f goes to warp f % 8,
+// which streams its records through its own ring of slots, one bulk copy each.
+//
+// Per page and warp, with tokens as the rows (M = 16) and the g <= 8 query
+// heads as the columns (N = 8) of m16n8k16 products, so that a group of 8
+// heads fills the tile:
+//   S^T = K Q^T: the record keeps a token's codes in the order of the A
+//     fragments, so a lane's 16-byte loads are its fragments.  A code c at bit
+//     0 (or 4) of a half is the fp16 number c 2^-24 (c 2^-20): one AND per
+//     pair turns codes into operands, nothing is converted; the queries carry
+//     the factor 16 between the two.  Each group of 64 has its accumulator:
+//     S = sum_groups step (q . c) + (mid - 7.5 step) sum q.
+//   softmax: the running maximum only moves when a score passes it by 2^8 (one
+//     vote per page instead of reductions); sums stay in their lanes until the
+//     end of the unit.
+//   O^T += V^T (step P)^T: V codes as operands the same way (the record pairs
+//     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
+//     by a power of two that follows the largest step; the 8 x 8 transposes of
+//     P by movmatrix.  sum (mid - 7.5 step) P joins at the end of the unit.
+#include <cuda_fp16.h>
+#include <float.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
+#include "tc_common.cuh"
 
 namespace ice {
 namespace {
 
+using namespace tc;
+
 constexpr int kWarps = 8;
-constexpr int kMaxG = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
+constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
+constexpr int kMinRun = kWarps;    // pages of a run, at least: one per warp
 
 struct Attn4Args {
     const void *Q;
@@ -25,142 +58,674 @@ struct Attn4Args {
     const unsigned char *cache;  // token-ordered pages (NULL: none)
     const int32_t *table, *lens;
     int n_pages, max_pages;
-    int g, hq, hkv;
+    int g, hq, hkv, units;
     float scale;
     float *O, *lse;
-    int32_t *err;
+    float *part_o, *part_ml;
+    int32_t *ticket, *err;
+    unsigned long long wait_ns;
+    int fault_skip;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_attn4(const __grid_constant__ Attn4Args A) {
-    __shared__ float s_q[kMaxG][kHeadDim];
-    __shared__ float s_p[kWarps][kPage];
-    __shared__ float s_ml[kWarps][kMaxG][2];
-    extern __shared__ float s_o[];  // [kWarps][g][128]
-    const int u = blockIdx.x, b = u / A.hkv, h = u % A.hkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    dep_wait();
-    const T *q = static_cast<const T *>(A.Q) + ((size_t)b * A.hq + (size_t)h * A.g) * kHeadDim;
-    for (int i = threadIdx.x; i < A.g * kHeadDim; i += blockDim.x) s_q[i / kHeadDim][i % kHeadDim] = Elem<T>::load(q + i);
-    __syncthreads();
-    int n_sel = 0, n_tok = 0;
-    if (A.pool) n_sel = min(max(A.sel_count[u], 0), A.max_sel);
+template <int HN> struct Shape {
+    static constexpr int kSlots = HN == 1 ? 4 : 6;
+    static constexpr int kHeads = 8 * HN;
+    static constexpr int kCtas = HN == 1 ? 2 : 1;  // per SM
+};
+
+template <int HN> struct Smem {
+    unsigned char ring[kWarps][Shape<HN>::kSlots][q4::kRecord];
+    float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
+    float ml[kWarps][Shape<HN>::kHeads][2];
+    int2 units[kUnits];  // (selected pages, cache tokens) of the units from u0 on
+    unsigned long long full[kWarps][Shape<HN>::kSlots];
+    long long sum[kWarps], total;
+    long long start0;  // pages before unit u0
+    int u0, last;
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+// D = A B + C, m16n8k16, fp16 in (subnormals kept), fp32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+// 2^e as a float, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Exponent of a positive finite float (-127 for subnormals).
+__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
+
+constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
+// Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+
+// A warp's running state over the pages of one unit.  Lane (r, c) = (lane / 4,
+// lane % 4); o[hn][t][0..3]: elements of head 8 hn + 2 c + (i & 1), row r of
+// tile t (i < 2) or row r + 8; tile t = 2 j + k, row half i / 2: element
+// 32 j + 4 r + 2 k + i / 2.
+template <int HN> struct State {
+    float o[HN][8][4];
+    float m[HN][2], l[HN][2];
+    float off[HN][2][2];         // sum of P (mid - 7.5 step), by group and head (this lane's tokens)
+    float vscale[2], vlimit[2];  // of each group: power of two on step P, and the step that it holds up to
+    __device__ __forceinline__ void init() {
+#pragma unroll
+        for (int hn = 0; hn < HN; ++hn) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t) o[hn][t][0] = o[hn][t][1] = o[hn][t][2] = o[hn][t][3] = 0.f;
+            m[hn][0] = m[hn][1] = -FLT_MAX;
+            l[hn][0] = l[hn][1] = 0.f;
+            off[hn][0][0] = off[hn][0][1] = off[hn][1][0] = off[hn][1][1] = 0.f;
+        }
+        vscale[0] = vscale[1] = pow2(120);
+        vlimit[0] = vlimit[1] = 0.f;
+    }
+};
+
+// The group's queries as B fragments (columns = heads), in fp16 after a common
+// power of two, and what the scores need of them.
+template <int NQ, int HN> struct Queries {
+    uint32_t f[NQ][HN][8][2];
+    float sum[HN][2][2];  // scale log2(e) sum q over a group, for this lane's columns (heads 2 c, 2 c + 1)
+    float factor;         // scale log2(e) over the powers of two of q and of the codes
+};
+
+template <typename T, int NQ, int HN>
+__device__ __forceinline__ void load_queries(const T *Qg, int g, float scale, Queries<NQ, HN> &q) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const float sl = scale * 1.4426950408889634f;
+    float x[HN][4][8];
+    float big = 0.f;
+#pragma unroll
+    for (int hn = 0; hn < HN; ++hn) {
+        const int head = 8 * hn + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[hn][i][e] = 0.f;
+            if (head < g) load8<T>(Qg + (size_t)head * kHeadDim + 32 * i + 8 * c, x[hn][i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[hn][i][e]));
+        }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
+    const float up = pow2(e2);
+    q.factor = sl * pow2(24) * pow2(-e2);
+#pragma unroll
+    for (int hn = 0; hn < HN; ++hn) {
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[i >> 1] += x[hn][i][e];
+            // code e of a word is in half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float w = (p & 1) ? 0.0625f * up : up;
+                const float a = x[hn][i][p] * w, b = x[hn][i][p + 4] * w;
+                const __half2 hi = __floats2half2_rn(a, b);
+                q.f[0][hn][2 * i + (p >> 1)][p & 1] = h2_bits(hi);
+                if (NQ > 1) {  // fp32 queries: the remainder
+                    const float2 back = __half22float2(hi);
+                    q.f[NQ - 1][hn][2 * i + (p >> 1)][p & 1] = h2_bits(__floats2half2_rn(a - back.x, b - back.y));
+                }
+            }
+        }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+            s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 1);
+            s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) q.sum[hn][gr][e] = sl * __shfl_sync(0xffffffffu, s[gr], 4 * (2 * c + e));
+        }
+    }
+}
+
+// Folds one page (record at shared address `rec`, its first `len` >= 1 slots).
+template <int NQ, int HN>
+__device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t rec, int len, State<HN> &st) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    // ---- S^T = K Q^T, an accumulator per group
+    float s[HN][4];
+    {
+        const uint4 k0 = lds128(rec + r * 64 + c * 16), k1 = lds128(rec + 512 + r * 64 + c * 16);
+        const uint2 m0 = lds64(rec + q4::kKMeta + r * 8), m1 = lds64(rec + q4::kKMeta + 64 + r * 8);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        float acc[HN][2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x0 = w0[i] >> (8 * k), x1 = w1[i] >> (8 * k);
+                const uint32_t a[4] = {x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh};
+#pragma unroll
+                for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        float(&d)[4] = acc[hn][i >> 1];
+                        if ((i & 1) | k | n)
+                            mma_f16(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1], d);
+                        else
+                            mma_f16(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1], zero);
+                    }
+            }
+        const float2 g00 = q4::unpack_meta(m0.x), g01 = q4::unpack_meta(m0.y);  // token r
+        const float2 g10 = q4::unpack_meta(m1.x), g11 = q4::unpack_meta(m1.y);  // token r + 8
+        const float b00 = fmaf(-7.5f, g00.x, g00.y), b01 = fmaf(-7.5f, g01.x, g01.y);
+        const float b10 = fmaf(-7.5f, g10.x, g10.y), b11 = fmaf(-7.5f, g11.x, g11.y);
+#pragma unroll
+        for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float s0 = fmaf(g01.x, acc[hn][1][e], g00.x * acc[hn][0][e]);
+                const float s1 = fmaf(g11.x, acc[hn][1][2 + e], g10.x * acc[hn][0][2 + e]);
+                s[hn][e] = fmaf(s0, q.factor, fmaf(b01, q.sum[hn][1][e], b00 * q.sum[hn][0][e]));
+                s[hn][2 + e] = fmaf(s1, q.factor, fmaf(b11, q.sum[hn][1][e], b10 * q.sum[hn][0][e]));
+            }
+    }
+    const uint2 n0 = lds64(rec + q4::kVMeta + r * 8), n1 = lds64(rec + q4::kVMeta + 64 + r * 8);
+    float2 v0[2] = {q4::unpack_meta(n0.x), q4::unpack_meta(n0.y)};  // token r: (step, mid) of both groups
+    float2 v1[2] = {q4::unpack_meta(n1.x), q4::unpack_meta(n1.y)};  // token r + 8
+    if (len < kPage) {  // slots behind the last token may hold anything
+        if (r >= len) {
+            v0[0] = v0[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hn = 0; hn < HN; ++hn) s[hn][0] = s[hn][1] = -INFINITY;
+        }
+        if (r + 8 >= len) {
+            v1[0] = v1[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int hn = 0; hn < HN; ++hn) s[hn][2] = s[hn][3] = -INFINITY;
+        }
+    }
+    // ---- the running maxima and the scale of step P, only when one has to move
+    bool move = v0[0].x > st.vlimit[0] || v1[0].x > st.vlimit[0] || v0[1].x > st.vlimit[1] || v1[1].x > st.vlimit[1];
+#pragma unroll
+    for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            move = move || s[hn][e] > st.m[hn][e] + kLazy || s[hn][2 + e] > st.m[hn][e] + kLazy;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(s[hn][e], s[hn][2 + e]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                mx = fmaxf(mx, st.m[hn][e]);
+                const float al = exp2_fast(st.m[hn][e] - mx);
+                st.m[hn][e] = mx;
+                st.l[hn][e] *= al;
+                st.off[hn][0][e] *= al;
+                st.off[hn][1][e] *= al;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    st.o[hn][t][e] *= al;
+                    st.o[hn][t][2 + e] *= al;
+                }
+            }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+            float mx = fmaxf(v0[gr].x, v1[gr].x);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            if (mx > st.vlimit[gr]) {
+                // steps up to [2^5, 2^6) now, up to 2^7 before the scale moves again: with P <= 2^8 below fp16's 2^16
+                const int e = min(5 - exponent_of(mx), 119);  // >= -122
+                const float to = pow2(e), down = to / st.vscale[gr];
+                st.vscale[gr] = to;
+                st.vlimit[gr] = pow2(min(7 - e, 127));
+#pragma unroll
+                for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+                    for (int t = 4 * gr; t < 4 * gr + 4; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st.o[hn][t][i] *= down;
+            }
+        }
+    }
+    // ---- P, and step P in hi + lo parts, transposed to B fragments
+    uint32_t bh[HN][2][2], bl[HN][2][2];  // [group][token half]
+#pragma unroll
+    for (int hn = 0; hn < HN; ++hn) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = exp2_fast(s[hn][i] - st.m[hn][i & 1]);
+        st.l[hn][0] += p[0] + p[2];
+        st.l[hn][1] += p[1] + p[3];
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+            const float f0 = v0[gr].x * st.vscale[gr], f1 = v1[gr].x * st.vscale[gr];
+            const float c0 = fmaf(-7.5f, v0[gr].x, v0[gr].y), c1 = fmaf(-7.5f, v1[gr].x, v1[gr].y);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                st.off[hn][gr][e] = fmaf(p[2 + e], c1, fmaf(p[e], c0, st.off[hn][gr][e]));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float f = half ? f1 : f0;
+                const float x = p[2 * half] * f, y = p[2 * half + 1] * f;
+                const __half2 hi = __floats2half2_rn(x, y);
+                const float2 back = __half22float2(hi);
+                bh[hn][gr][half] = transpose8(h2_bits(hi));
+                bl[hn][gr][half] = transpose8(h2_bits(__floats2half2_rn(x - back.x, y - back.y)));
+            }
+        }
+    }
+    // ---- O^T += V^T (step P)^T
+    {
+        const uint4 x0 = lds128(rec + q4::kV + c * 128 + r * 16), x1 = lds128(rec + q4::kV + 512 + c * 128 + r * 16);
+        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t y0 = w0[j] >> (8 * k), y1 = w1[j] >> (8 * k);
+                const uint32_t a[4] = {y0 & kLow, y0 & kHigh, y1 & kLow, y1 & kHigh};
+#pragma unroll
+                for (int hn = 0; hn < HN; ++hn) {
+                    float(&o)[4] = st.o[hn][2 * j + k];
+                    mma_f16(o, a, bh[hn][j >> 1][0], bh[hn][j >> 1][1], o);
+                    mma_f16(o, a, bl[hn][j >> 1][0], bl[hn][j >> 1][1], o);
+                }
+            }
+    }
+}
+
+// (selected pages, cache tokens) of a unit, within the arrays' bounds.
+__device__ __forceinline__ int2 unit_counts(const Attn4Args &A, int u) {
+    int2 n = make_int2(0, 0);
+    if (A.pool) n.x = min(max(A.sel_count[u], 0), A.max_sel);
     if (A.cache) {
-        n_tok = A.lens[b];
-        const long long most = (long long)A.max_pages * kPage;
-        if ((n_tok < 0 || n_tok > most) && threadIdx.x == 0) set_err(A.err, ICE_ERR_CAPACITY);
-        n_tok = (int)min((long long)max(n_tok, 0), most);
+        const int t = A.lens[u / A.hkv], most = A.max_pages * kPage;  // < 2^31
+        if (t < 0 || t > most) set_err(A.err, ICE_ERR_CAPACITY);
+        n.y = min(max(t, 0), most);
     }
-    const int n = n_sel + (n_tok + kPage - 1) / kPage;
-    float m[kMaxG], l[kMaxG], o[kMaxG][4];
-#pragma unroll
-    for (int i = 0; i < kMaxG; ++i) {
-        m[i] = -INFINITY;
-        l[i] = o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    }
-    for (int x = warp; x < n; x += kWarps) {
-        const unsigned char *rec;
-        int len;
-        if (x < n_sel) {
-            const int pg = A.sel_pages[(size_t)u * A.max_sel + x];
-            if (pg < 0 || pg >= A.page_cap) {
-                if (lane == 0) set_err(A.err, ICE_ERR_CAPACITY);
-                continue;
-            }
-            len = min(A.page_len[(size_t)u * A.page_cap + pg], kPage);
-            rec = A.pool + ((size_t)u * A.page_cap + pg) * q4::kRecord;
-        } else {
-            const int blk = x - n_sel;
-            const int pg = A.table[(size_t)b * A.max_pages + blk];
-            if (pg < 0 || pg >= A.n_pages) {
-                if (lane == 0) set_err(A.err, ICE_ERR_CAPACITY);
-                continue;
-            }
-            len = min(n_tok - blk * kPage, kPage);
-            rec = A.cache + ((size_t)pg * A.hkv + h) * q4::kRecord;
-        }
-        if (len <= 0) continue;
-        const int t = lane >> 1, gr = lane & 1;
-        const float2 km = q4::unpack_meta(*reinterpret_cast<const uint32_t *>(rec + q4::kKMeta + t * 8 + gr * 4));
-        float kv[64];
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            float y[8];
-            q4::values_of(q4::get_k(rec, t, gr * 8 + w), km, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kv[w * 8 + e] = y[e];
-        }
-#pragma unroll
-        for (int hh = 0; hh < kMaxG; ++hh) {
-            if (hh >= A.g) break;
-            float d = 0.f;
-#pragma unroll
-            for (int e = 0; e < 64; ++e) d = fmaf(kv[e], s_q[hh][gr * 64 + e], d);
-            d += __shfl_xor_sync(0xffffffffu, d, 1);
-            const float s = t < len ? d * A.scale : -INFINITY;
-            float mx = s;
-#pragma unroll
-            for (int off = 2; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(m[hh], mx);
-            const float al = m[hh] == -INFINITY ? 0.f : expf(m[hh] - mn);
-            const float p = t < len ? expf(s - mn) : 0.f;
-            float sum = p;
-#pragma unroll
-            for (int off = 2; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            m[hh] = mn;
-            l[hh] = l[hh] * al + sum;
-            __syncwarp();
-            if (gr == 0) s_p[warp][t] = p;
-            __syncwarp();
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int tt = 0; tt < len; ++tt) {
-                const float2 vm =
-                    q4::unpack_meta(*reinterpret_cast<const uint32_t *>(rec + q4::kVMeta + tt * 8 + (lane >> 4) * 4));
-                const uint32_t c = *reinterpret_cast<const uint16_t *>(rec + q4::v_piece(tt, lane));
-                const float pp = s_p[warp][tt];
-                acc.x = fmaf(pp, fmaf(vm.x, (float)(c & 15u) - 7.5f, vm.y), acc.x);
-                acc.y = fmaf(pp, fmaf(vm.x, (float)(c >> 4 & 15u) - 7.5f, vm.y), acc.y);
-                acc.z = fmaf(pp, fmaf(vm.x, (float)(c >> 8 & 15u) - 7.5f, vm.y), acc.z);
-                acc.w = fmaf(pp, fmaf(vm.x, (float)(c >> 12 & 15u) - 7.5f, vm.y), acc.w);
-            }
-            o[hh][0] = fmaf(o[hh][0], al, acc.x);
-            o[hh][1] = fmaf(o[hh][1], al, acc.y);
-            o[hh][2] = fmaf(o[hh][2], al, acc.z);
-            o[hh][3] = fmaf(o[hh][3], al, acc.w);
+    return n;
+}
+__device__ __forceinline__ int pages_of(int2 n) { return n.x + (n.y + kPage - 1) / kPage; }
+
+template <typename T, int NQ, int HN>
+__global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __grid_constant__ Attn4Args A) {
+    constexpr int NS = Shape<HN>::kSlots;
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    Smem<HN> &S = *reinterpret_cast<Smem<HN> *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    const int g = A.g;
+    if (lane == 0)
+        for (int i = 0; i < NS; ++i) mbar_init(&S.full[warp][i], 1);
+    mbar_init_fence();
+    dep_wait();
+
+    // ---- the CTA's run of pages: a prefix sum over the units' page counts
+    const int per = (A.units + kThreads - 1) / kThreads;
+    const int ua = min(tid * per, A.units), ub = min(ua + per, A.units);
+    long long mine = 0;
+    for (int u = ua; u < ub; ++u) {
+        const int n = pages_of(unit_counts(A, u));
+        mine += n;
+        if (n == 0 && u % (int)gridDim.x == (int)blockIdx.x) {  // no page: nobody else writes these rows
+            const size_t row = (size_t)(u / A.hkv) * A.hq + (size_t)(u % A.hkv) * g;
+            float4 *o = reinterpret_cast<float4 *>(A.O + row * kHeadDim);
+            for (int i = 0; i < g * kHeadDim / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (A.lse)
+                for (int i = 0; i < g; ++i) A.lse[row + i] = -INFINITY;
         }
     }
+    long long before = mine;
 #pragma unroll
-    for (int hh = 0; hh < kMaxG; ++hh) {
-        if (hh >= A.g) break;
-        if (lane == 0) s_ml[warp][hh][0] = m[hh], s_ml[warp][hh][1] = l[hh];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s_o[((size_t)warp * A.g + hh) * kHeadDim + lane * 4 + e] = o[hh][e];
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += y;
+    }
+    if (lane == 31) S.sum[warp] = before;
+    __syncthreads();
+    long long total = 0;
+    before -= mine;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += S.sum[w];
+        total += S.sum[w];
+    }
+    long long share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < kMinRun) share = kMinRun;
+    const long long f0 = (long long)blockIdx.x * share;
+    const int run = (int)min(share, total - f0);
+    if (run <= 0) return;  // the whole CTA
+    if (f0 >= before && f0 < before + mine) {
+        long long at = before;
+        for (int u = ua; u < ub; ++u) {
+            const int n = pages_of(unit_counts(A, u));
+            if (f0 < at + n) {
+                S.u0 = u;
+                S.start0 = at;
+                break;
+            }
+            at += n;
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < A.g * kHeadDim; i += blockDim.x) {
-        const int hh = i / kHeadDim;
-        float M = -INFINITY, L = 0.f, acc = 0.f;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_ml[w][hh][0]);
-        for (int w = 0; w < kWarps; ++w) {
-            const float wt = s_ml[w][hh][0] == -INFINITY ? (s_ml[w][hh][1] == 0.f ? 0.f : 1.f) : expf(s_ml[w][hh][0] - M);
-            L = fmaf(s_ml[w][hh][1], wt, L);
-            acc = fmaf(s_o[((size_t)w * A.g + hh) * kHeadDim + i % kHeadDim], wt, acc);
+    const int u0 = S.u0;
+    for (int i = tid; i < kUnits && u0 + i < A.units; i += kThreads) S.units[i] = unit_counts(A, u0 + i);
+    __syncthreads();
+
+    // A position in the run: page f (from the run's start) of unit u0 + i, whose pages start at `us`.
+    struct Cursor {
+        int f, i, us, n;
+        int2 cnt;
+    };
+    auto counts_at = [&](int i) { return i < kUnits ? S.units[i] : unit_counts(A, u0 + i); };
+    auto settle = [&](Cursor &k) {  // the unit that holds page k.f < run
+        while (k.f >= k.us + k.n) {
+            k.us += k.n;
+            k.cnt = counts_at(++k.i);
+            k.n = pages_of(k.cnt);
         }
-        const size_t row = (size_t)b * A.hq + (size_t)h * A.g + hh;
-        A.O[row * kHeadDim + i % kHeadDim] = L == 0.f ? 0.f : acc / L;
-        if (A.lse && i % kHeadDim == 0) A.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
+    };
+    Cursor prod;  // the next page to be looked up
+    prod.f = (int)((warp - f0) & (kWarps - 1));
+    prod.i = 0;
+    prod.us = (int)(S.start0 - f0);
+    prod.cnt = S.units[0];
+    prod.n = pages_of(prod.cnt);
+    Cursor cons = prod;
+    struct Next {  // a page to be copied: its id and unit
+        int id, u;
+        bool sel, ok;  // a selected page; false past the run
+    };
+    auto look_up = [&]() {
+        Next p{-1, 0, false, prod.f < run};
+        if (!p.ok) return p;
+        settle(prod);
+        const int x = prod.f - prod.us;
+        p.u = u0 + prod.i;
+        p.sel = x < prod.cnt.x;
+        p.id = p.sel ? A.sel_pages[(size_t)p.u * A.max_sel + x]
+                     : A.table[(size_t)(p.u / A.hkv) * A.max_pages + (x - prod.cnt.x)];
+        prod.f += kWarps;
+        return p;
+    };
+    // Starts a page's copy; its length if it is a selected page (0 when it does not exist), -1 when the length follows
+    // from its place.
+    const uint64_t pol = l2_evict_first();
+    int issued = 0;
+    auto issue = [&](const Next &p) -> int {
+        if (!p.ok) return 0;
+        const bool good = p.id >= 0 && p.id < (p.sel ? A.page_cap : A.n_pages);
+        int len = p.sel ? 0 : -1;
+        const unsigned char *src = nullptr;
+        if (!good) {
+            if (lane == 0) set_err(A.err, ICE_ERR_CAPACITY);
+            len = 0;
+        } else if (p.sel) {
+            const size_t at = (size_t)p.u * A.page_cap + p.id;
+            len = min(max(A.page_len[at], 0), kPage);
+            src = A.pool + at * q4::kRecord;
+        } else {
+            src = A.cache + ((size_t)p.id * A.hkv + p.u % A.hkv) * q4::kRecord;
+        }
+        if (lane == 0 && !A.fault_skip) {  // fault injection: the wait below gives up
+            unsigned long long *bar = &S.full[warp][issued % NS];
+            mbar_expect_tx(bar, good ? (uint32_t)q4::kRecord : 0u);
+            if (good)
+                asm volatile(
+                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
+                    "[%3], %4;" ::"r"(su32(S.ring[warp][issued % NS])),
+                    "l"(reinterpret_cast<uint64_t>(src)), "r"((uint32_t)q4::kRecord), "r"(su32(bar)), "l"(pol)
+                    : "memory");
+        }
+        ++issued;
+        return len;
+    };
+    int len_of[NS];
+    Next next;  // looked up one page ahead of its copy, so that the id is there by then
+    {
+        Next first[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) first[i] = look_up();
+        next = look_up();
+#pragma unroll
+        for (int i = 0; i < NS; ++i) len_of[i] = issue(first[i]);
     }
+
+    State<HN> st;
+    Queries<NQ, HN> q;
+    bool dead = false;
+    int taken = 0;
+    int seg_i = 0, seg_us = cons.us, seg_n = cons.n;  // the unit being attended, by all warps alike
+    for (int fa = 0; fa < run;) {
+        const int fb = min(run, seg_us + seg_n);
+        const int u = u0 + seg_i, b = u / A.hkv, h = u % A.hkv;
+        const size_t row0 = (size_t)b * A.hq + (size_t)h * g;
+        st.init();
+        bool bad = false, any = false;
+        if (cons.f < fb) {
+            load_queries<T, NQ, HN>(static_cast<const T *>(A.Q) + row0 * kHeadDim, g, A.scale, q);
+            settle(cons);
+        }
+        while (cons.f < fb) {
+            any = true;
+            int len = len_of[0];
+            if (len < 0) len = min(kPage, cons.cnt.y - (cons.f - cons.us - cons.cnt.x) * kPage);
+            const int slot = taken % NS;
+            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&S.full[warp][slot], (taken / NS) & 1, A.wait_ns));
+            if (dead) {
+                bad = true;
+                cons.f += kWarps;
+                continue;  // nothing more is issued; the end waits for what is in flight
+            }
+            if (len > 0) attend_page4<NQ, HN>(q, su32(S.ring[warp][slot]), len, st);
+            __syncwarp();
+            ++taken;
+            cons.f += kWarps;
+#pragma unroll
+            for (int i = 0; i + 1 < NS; ++i) len_of[i] = len_of[i + 1];
+            len_of[NS - 1] = issue(next);
+            next = look_up();
+        }
+        if (dead) set_err(A.err, ICE_ERR_TIMEOUT);
+
+        // ---- the warps' results to shared memory
+        __syncthreads();  // the last unit's have been read
+#pragma unroll
+        for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = st.l[hn][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                const int head = 8 * hn + 2 * c + e;
+                if (r == 0) {
+                    S.ml[warp][head][0] = st.m[hn][e];
+                    S.ml[warp][head][1] = bad ? __int_as_float(0x7fc00000) : l;
+                }
+                if (any) {
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr) {
+                        float off = st.off[hn][gr][e];
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) off += __shfl_xor_sync(0xffffffffu, off, x);
+                        const float back = 1.f / st.vscale[gr], lo = pow2(24), hi = pow2(20);
+#pragma unroll
+                        for (int j = 2 * gr; j < 2 * gr + 2; ++j)
+                            *reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]) =
+                                make_float4(fmaf(st.o[hn][2 * j][e] * lo, back, off), fmaf(st.o[hn][2 * j][2 + e] * hi, back, off),
+                                            fmaf(st.o[hn][2 * j + 1][e] * lo, back, off),
+                                            fmaf(st.o[hn][2 * j + 1][2 + e] * hi, back, off));
+                    }
+                }
+            }
+        __syncthreads();
+        // ---- joined: 32 threads a head, 4 elements each
+        const bool whole = seg_us >= 0 && seg_us + seg_n <= run;
+        const size_t part = ((size_t)blockIdx.x * 2 + (seg_us > 0 ? 1 : 0)) * g;
+        for (int hh = tid >> 5; hh < g; hh += kWarps) {
+            float M = -FLT_MAX, L = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, S.ml[w][hh][0]);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < kWarps; ++w) {
+                const float l = S.ml[w][hh][1];
+                if (l == 0.f) continue;
+                const float wt = exp2_fast(S.ml[w][hh][0] - M);
+                const float4 x = *reinterpret_cast<const float4 *>(&S.o[w][hh][4 * lane]);
+                L = fmaf(l, wt, L);
+                acc.x = fmaf(x.x, wt, acc.x), acc.y = fmaf(x.y, wt, acc.y);
+                acc.z = fmaf(x.z, wt, acc.z), acc.w = fmaf(x.w, wt, acc.w);
+            }
+            if (whole) {
+                if (L == L) {
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+                } else {
+                    acc.x = acc.y = acc.z = acc.w = L;
+                }
+                *reinterpret_cast<float4 *>(A.O + (row0 + hh) * kHeadDim + 4 * lane) = acc;
+                if (A.lse && lane == 0) A.lse[row0 + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+                *reinterpret_cast<float4 *>(A.part_o + (part + hh) * kHeadDim + 4 * lane) = acc;
+                if (lane == 0) *reinterpret_cast<float2 *>(A.part_ml + (part + hh) * 2) = make_float2(M, L);
+            }
+        }
+        if (!whole) {
+            // the unit's runs: CTAs ca .. cb; a run's part is its second one when the unit starts inside the run
+            const long long us = f0 + seg_us;
+            const int ca = (int)(us / share), cb = (int)((us + seg_n - 1) / share);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) S.last = atomicAdd(A.ticket + u, 1) == cb - ca;
+            __syncthreads();
+            if (S.last) {
+                __threadfence();
+                float *wt = &S.o[0][0][0];  // [runs][g] weights: at most kHeads * kWarps * kRow
+                auto part_at = [&](int k) {
+                    return ((size_t)(ca + k) * 2 + (us > (long long)(ca + k) * share ? 1 : 0)) * g;
+                };
+                const int runs = cb - ca + 1;
+                for (int hh = warp; hh < g; hh += kWarps) {
+                    float M = -FLT_MAX, L = 0.f;
+                    for (int k = lane; k < runs; k += 32) M = fmaxf(M, __ldcg(A.part_ml + (part_at(k) + hh) * 2));
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+                    for (int k = lane; k < runs; k += 32) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(A.part_ml + (part_at(k) + hh) * 2));
+                        const float x = ml.y == 0.f ? 0.f : exp2_fast(ml.x - M);
+                        wt[k * g + hh] = x;
+                        L = fmaf(ml.y, x, L);
+                    }
+#pragma unroll
+                    for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+                    __syncwarp();
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < runs; ++k) {
+                        const float x = wt[k * g + hh];
+                        const float4 y =
+                            __ldcg(reinterpret_cast<const float4 *>(A.part_o + (part_at(k) + hh) * kHeadDim + 4 * lane));
+                        acc.x = fmaf(y.x, x, acc.x), acc.y = fmaf(y.y, x, acc.y);
+                        acc.z = fmaf(y.z, x, acc.z), acc.w = fmaf(y.w, x, acc.w);
+                    }
+                    if (L == L) {
+                        const float inv = L > 0.f ? 1.f / L : 0.f;
+                        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+                    } else {
+                        acc.x = acc.y = acc.z = acc.w = L;
+                    }
+                    *reinterpret_cast<float4 *>(A.O + (row0 + hh) * kHeadDim + 4 * lane) = acc;
+                    if (A.lse && lane == 0)
+                        A.lse[row0 + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+                }
+                if (tid == 0) A.ticket[u] = 0;
+            }
+        }
+        // ---- the next unit with pages
+        fa = fb;
+        if (fa < run) {
+            while (fa >= seg_us + seg_n) {
+                seg_us += seg_n;
+                seg_n = pages_of(counts_at(++seg_i));
+            }
+        }
+    }
+    // copies still in flight (after a wait that gave up)
+    if (dead && !A.fault_skip)
+        for (int k = taken; k < issued; ++k) mbar_wait(&S.full[warp][k % NS], (k / NS) & 1, A.wait_ns);
+}
+
+int device_sms() {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 1;
+}
+
+struct Attn4Ws {
+    int32_t *ticket;  // [units] zero between calls
+    float *part_ml;   // [2 runs, g, 2]
+    float *part_o;    // [2 runs, g, 128]
+    size_t bytes;
+};
+Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
+    Attn4Ws w{};
+    char *b = static_cast<char *>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *r = b ? b + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return r;
+    };
+    const size_t g = p.n_q_heads / p.n_kv_heads, parts = 2 * 2 * (size_t)sms * g;
+    w.ticket = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * units_of(p)));
+    w.part_ml = reinterpret_cast<float *>(take(sizeof(float) * parts * 2));
+    w.part_o = reinterpret_cast<float *>(take(sizeof(float) * parts * kHeadDim));
+    w.bytes = off;
+    return w;
+}
+
+template <typename T, int NQ, int HN>
+cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
+    auto kern = k_attn4<T, NQ, HN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<HN>));
+    if (e != cudaSuccess) return e;
+    // every CTA resident at once (no CTA waits for another, but equal runs should start together)
+    const long long most = (long long)A.units * ((A.pool ? A.max_sel : 0) + (long long)(A.cache ? A.max_pages : 0));
+    const long long runs = (most + kMinRun - 1) / kMinRun;
+    const int grid = (int)(runs < (long long)sms * Shape<HN>::kCtas ? (runs > 0 ? runs : 1) : sms * Shape<HN>::kCtas);
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<HN>), s, A);
 }
 
 }  // namespace
 
-size_t attn4_workspace(const ice_params &) { return 256; }
+size_t attn4_workspace(const ice_params &p) { return ws_layout(p, device_sms(), nullptr).bytes; }
 
 cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records, const int32_t *page_len,
                          const int32_t *sel_pages, const int32_t *sel_count, int max_sel, const ice_cache4 *cache,
                          const int32_t *lens, float scale, float *O, float *lse, void *ws, int32_t *err,
                          cudaStream_t s) {
-    (void)ws;
     Attn4Args A{};
     A.Q = Q;
     A.pool = static_cast<const unsigned char *>(records);
@@ -171,14 +736,18 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
         A.table = cache->table, A.n_pages = cache->n_pages, A.max_pages = cache->max_pages;
         A.lens = lens;
     }
-    A.g = p.n_q_heads / p.n_kv_heads, A.hq = p.n_q_heads, A.hkv = p.n_kv_heads;
+    A.g = p.n_q_heads / p.n_kv_heads, A.hq = p.n_q_heads, A.hkv = p.n_kv_heads, A.units = units_of(p);
     A.scale = scale;
     A.O = O, A.lse = lse, A.err = err;
-    const size_t smem = sizeof(float) * kWarps * A.g * kHeadDim;
-    auto kern = p.dtype == ICE_BF16 ? k_attn4<__nv_bfloat16> : k_attn4<float>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(units_of(p)), dim3(kWarps * 32), smem, s, A);
+    const int sms = device_sms();
+    const Attn4Ws w = ws_layout(p, sms, ws);
+    A.ticket = w.ticket, A.part_ml = w.part_ml, A.part_o = w.part_o;
+    const bool fault = fault_armed("timeout");
+    A.wait_ns = fault ? kFaultWaitNs : kWaitNs;
+    A.fault_skip = fault ? 1 : 0;
+    if (p.dtype == ICE_BF16)
+        return A.g <= 8 ? launch_t<__nv_bfloat16, 1, 1>(A, sms, s) : launch_t<__nv_bfloat16, 1, 2>(A, sms, s);
+    return A.g <= 8 ? launch_t<float, 2, 1>(A, sms, s) : launch_t<float, 2, 2>(A, sms, s);
 }
 
 }  // namespace ice
