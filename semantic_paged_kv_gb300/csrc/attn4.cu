@@ -10,10 +10,14 @@
 // an SM gets a page every ~100 clocks.
 //
 // Work: the pages of all units, one after another, are cut into equal runs,
-// one per CTA, whatever the units' lengths; a unit that a run cuts leaves
-// partial results in the workspace, joined by its last CTA in run order (so
-// the bits do not depend on timing).  Inside a CTA page f goes to warp f % 8,
-// which streams its records through its own ring of slots, one bulk copy each.
+// one per CTA, whatever the units' lengths; a unit counts kOver pages more
+// than it has (what starting and ending one costs), so that many short units
+// do not gather in few CTAs.  A unit that a run cuts leaves partial results in
+// the workspace, joined by its last CTA in run order (so the bits do not
+// depend on timing).  Inside a CTA place f of the run goes to warp f % 8, slot f
+// / 8 % 4 of its ring; a warp looks up its pages 16 at a time, one a lane, well
+// before their copies start, so that its loop over pages does little else than
+// attend.
 //
 // Per page and warp, with tokens as the rows (M = 16) and the g <= 8 query
 // heads as the columns (N = 8) of m16n8k16 products, so that a group of 8
@@ -46,9 +50,13 @@ using namespace tc;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kSlots = 4;          // pages of a warp's ring
+constexpr int kBatch = 16;         // places looked up at a time
+constexpr int kLenShift = 58;      // device addresses are below 2^57
+constexpr int kOver = 16;          // places that a unit takes beside its pages
 constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
-constexpr int kMinRun = kWarps;    // pages of a run, at least: one per warp
+constexpr int kMinRun = kWarps;    // places of a run, at least: one page per warp
 
 struct Attn4Args {
     const void *Q;
@@ -68,19 +76,19 @@ struct Attn4Args {
 };
 
 template <int HN> struct Shape {
-    static constexpr int kSlots = HN == 1 ? 4 : 6;
     static constexpr int kHeads = 8 * HN;
     static constexpr int kCtas = HN == 1 ? 2 : 1;  // per SM
 };
 
 template <int HN> struct Smem {
-    unsigned char ring[kWarps][Shape<HN>::kSlots][q4::kRecord];
+    unsigned char ring[kWarps][kSlots][q4::kRecord];
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
     float ml[kWarps][Shape<HN>::kHeads][2];
-    int2 units[kUnits];  // (selected pages, cache tokens) of the units from u0 on
-    unsigned long long full[kWarps][Shape<HN>::kSlots];
-    long long sum[kWarps], total;
-    long long start0;  // pages before unit u0
+    int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
+    unsigned long long full[kWarps][kSlots];
+    unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
+    long long sum[kWarps];
+    long long start0;  // places before unit u0
     int u0, last;
 };
 
@@ -94,14 +102,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
-// D = A B + C, m16n8k16, fp16 in (subnormals kept), fp32 accumulate.
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                        const float (&c)[4]) {
+// D += A B, and D = A B; m16n8k16, fp16 in (subnormals kept), fp32 accumulate.
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -207,11 +221,10 @@ __device__ __forceinline__ void load_queries(const T *Qg, int g, float scale, Qu
     }
 }
 
-// Folds one page (record at shared address `rec`, its first `len` >= 1 slots).
+// Folds one page (record at shared address `rec`, its first `len` slots; whatever the others hold).
 template <int NQ, int HN>
 __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t rec, int len, State<HN> &st) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
     // ---- S^T = K Q^T, an accumulator per group
     float s[HN][4];
     {
@@ -231,9 +244,9 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
                     for (int n = 0; n < NQ; ++n) {
                         float(&d)[4] = acc[hn][i >> 1];
                         if ((i & 1) | k | n)
-                            mma_f16(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1], d);
+                            mma_add(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1]);
                         else
-                            mma_f16(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1], zero);
+                            mma_first(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1]);
                     }
             }
         const float2 g00 = q4::unpack_meta(m0.x), g01 = q4::unpack_meta(m0.y);  // token r
@@ -266,12 +279,12 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
         }
     }
     // ---- the running maxima and the scale of step P, only when one has to move
-    bool move = v0[0].x > st.vlimit[0] || v1[0].x > st.vlimit[0] || v0[1].x > st.vlimit[1] || v1[1].x > st.vlimit[1];
+    bool move = (v0[0].x > st.vlimit[0]) | (v1[0].x > st.vlimit[0]) | (v0[1].x > st.vlimit[1]) | (v1[1].x > st.vlimit[1]);
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            move = move || s[hn][e] > st.m[hn][e] + kLazy || s[hn][2 + e] > st.m[hn][e] + kLazy;
+            move |= (s[hn][e] > st.m[hn][e] + kLazy) | (s[hn][2 + e] > st.m[hn][e] + kLazy);
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn)
@@ -352,8 +365,8 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
 #pragma unroll
                 for (int hn = 0; hn < HN; ++hn) {
                     float(&o)[4] = st.o[hn][2 * j + k];
-                    mma_f16(o, a, bh[hn][j >> 1][0], bh[hn][j >> 1][1], o);
-                    mma_f16(o, a, bl[hn][j >> 1][0], bl[hn][j >> 1][1], o);
+                    mma_add(o, a, bh[hn][j >> 1][0], bh[hn][j >> 1][1]);
+                    mma_add(o, a, bl[hn][j >> 1][0], bl[hn][j >> 1][1]);
                 }
             }
     }
@@ -371,26 +384,51 @@ __device__ __forceinline__ int2 unit_counts(const Attn4Args &A, int u) {
     return n;
 }
 __device__ __forceinline__ int pages_of(int2 n) { return n.x + (n.y + kPage - 1) / kPage; }
+// Places of a unit of n pages: kOver, then the pages; none without pages.
+__device__ __forceinline__ int places_of(int n) { return n > 0 ? n + kOver : 0; }
+
+// A unit of a run: index i from u0, first page at place `first` (from the run's start), n pages.
+struct UnitAt {
+    int i, first, n;
+    int2 cnt;
+    __device__ __forceinline__ int end() const { return first + n; }
+};
+
+// The rest of a wait: true when the phase of the given parity is complete, false after limit_ns.
+__device__ __noinline__ bool wait_more(unsigned long long *bar, uint32_t parity, unsigned long long limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+}
+
+// Row of O and lse from the sums over all pages (this lane's 4 elements).
+__device__ __forceinline__ void put_row(const Attn4Args &A, size_t row, float4 acc, float M, float L) {
+    const int lane = threadIdx.x & 31;
+    const float inv = L > 0.f ? 1.f / L : L;  // no token: 0; NaN stays
+    if (L == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4 *>(A.O + row * kHeadDim + 4 * lane) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
 
 template <typename T, int NQ, int HN>
 __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __grid_constant__ Attn4Args A) {
-    constexpr int NS = Shape<HN>::kSlots;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem<HN> &S = *reinterpret_cast<Smem<HN> *>(smem_raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = A.g;
-    if (lane == 0)
-        for (int i = 0; i < NS; ++i) mbar_init(&S.full[warp][i], 1);
+    if (tid < kWarps * kSlots) mbar_init(&S.full[0][0] + tid, 1);
     mbar_init_fence();
     dep_wait();
 
-    // ---- the CTA's run of pages: a prefix sum over the units' page counts
+    // ---- the CTA's run of places: a prefix sum over the units
+    const bool all = A.units <= kUnits;  // every unit's counts stay at hand
     const int per = (A.units + kThreads - 1) / kThreads;
     const int ua = min(tid * per, A.units), ub = min(ua + per, A.units);
     long long mine = 0;
     for (int u = ua; u < ub; ++u) {
-        const int n = pages_of(unit_counts(A, u));
-        mine += n;
+        const int2 cnt = unit_counts(A, u);
+        if (all) S.units[u] = cnt;
+        const int n = pages_of(cnt);
+        mine += places_of(n);
         if (n == 0 && u % (int)gridDim.x == (int)blockIdx.x) {  // no page: nobody else writes these rows
             const size_t row = (size_t)(u / A.hkv) * A.hq + (size_t)(u % A.hkv) * g;
             float4 *o = reinterpret_cast<float4 *>(A.O + row * kHeadDim);
@@ -421,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     if (f0 >= before && f0 < before + mine) {
         long long at = before;
         for (int u = ua; u < ub; ++u) {
-            const int n = pages_of(unit_counts(A, u));
+            const int n = places_of(pages_of(all ? S.units[u] : unit_counts(A, u)));
             if (f0 < at + n) {
                 S.u0 = u;
                 S.start0 = at;
@@ -431,128 +469,136 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         }
     }
     __syncthreads();
-    const int u0 = S.u0;
-    for (int i = tid; i < kUnits && u0 + i < A.units; i += kThreads) S.units[i] = unit_counts(A, u0 + i);
-    __syncthreads();
-
-    // A position in the run: page f (from the run's start) of unit u0 + i, whose pages start at `us`.
-    struct Cursor {
-        int f, i, us, n;
-        int2 cnt;
-    };
-    auto counts_at = [&](int i) { return i < kUnits ? S.units[i] : unit_counts(A, u0 + i); };
-    auto settle = [&](Cursor &k) {  // the unit that holds page k.f < run
-        while (k.f >= k.us + k.n) {
-            k.us += k.n;
-            k.cnt = counts_at(++k.i);
-            k.n = pages_of(k.cnt);
-        }
-    };
-    Cursor prod;  // the next page to be looked up
-    prod.f = (int)((warp - f0) & (kWarps - 1));
-    prod.i = 0;
-    prod.us = (int)(S.start0 - f0);
-    prod.cnt = S.units[0];
-    prod.n = pages_of(prod.cnt);
-    Cursor cons = prod;
-    struct Next {  // a page to be copied: its id and unit
-        int id, u;
-        bool sel, ok;  // a selected page; false past the run
-    };
-    auto look_up = [&]() {
-        Next p{-1, 0, false, prod.f < run};
-        if (!p.ok) return p;
-        settle(prod);
-        const int x = prod.f - prod.us;
-        p.u = u0 + prod.i;
-        p.sel = x < prod.cnt.x;
-        p.id = p.sel ? A.sel_pages[(size_t)p.u * A.max_sel + x]
-                     : A.table[(size_t)(p.u / A.hkv) * A.max_pages + (x - prod.cnt.x)];
-        prod.f += kWarps;
-        return p;
-    };
-    // Starts a page's copy; its length if it is a selected page (0 when it does not exist), -1 when the length follows
-    // from its place.
-    const uint64_t pol = l2_evict_first();
-    int issued = 0;
-    auto issue = [&](const Next &p) -> int {
-        if (!p.ok) return 0;
-        const bool good = p.id >= 0 && p.id < (p.sel ? A.page_cap : A.n_pages);
-        int len = p.sel ? 0 : -1;
-        const unsigned char *src = nullptr;
-        if (!good) {
-            if (lane == 0) set_err(A.err, ICE_ERR_CAPACITY);
-            len = 0;
-        } else if (p.sel) {
-            const size_t at = (size_t)p.u * A.page_cap + p.id;
-            len = min(max(A.page_len[at], 0), kPage);
-            src = A.pool + at * q4::kRecord;
-        } else {
-            src = A.cache + ((size_t)p.id * A.hkv + p.u % A.hkv) * q4::kRecord;
-        }
-        if (lane == 0 && !A.fault_skip) {  // fault injection: the wait below gives up
-            unsigned long long *bar = &S.full[warp][issued % NS];
-            mbar_expect_tx(bar, good ? (uint32_t)q4::kRecord : 0u);
-            if (good)
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, "
-                    "[%3], %4;" ::"r"(su32(S.ring[warp][issued % NS])),
-                    "l"(reinterpret_cast<uint64_t>(src)), "r"((uint32_t)q4::kRecord), "r"(su32(bar)), "l"(pol)
-                    : "memory");
-        }
-        ++issued;
-        return len;
-    };
-    int len_of[NS];
-    Next next;  // looked up one page ahead of its copy, so that the id is there by then
-    {
-        Next first[NS];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) first[i] = look_up();
-        next = look_up();
-#pragma unroll
-        for (int i = 0; i < NS; ++i) len_of[i] = issue(first[i]);
+    const int u0 = S.u0, base = all ? 0 : u0;
+    if (!all) {
+        for (int i = tid; i < kUnits && u0 + i < A.units; i += kThreads) S.units[i] = unit_counts(A, u0 + i);
+        __syncthreads();
     }
+    auto unit_at = [&](int i, int place) {  // unit u0 + i, whose places start at `place`
+        UnitAt x;
+        x.i = i;
+        x.cnt = u0 - base + i < kUnits ? S.units[u0 - base + i] : unit_counts(A, u0 + i);
+        x.n = pages_of(x.cnt);
+        x.first = place + (x.n > 0 ? kOver : 0);
+        return x;
+    };
+    UnitAt unit = unit_at(0, (int)(S.start0 - f0));
 
+    // ---- the warp's pages: places n = 0 .. of the warp are places warp + 8 n of the run
+    const int places = run > warp ? (run - warp + kWarps - 1) / kWarps : 0;
+    unsigned long long *pages = S.page[warp];
+    UnitAt look = unit;
+    auto look_up = [&](int n) {  // place n of this lane
+        const int f = warp + kWarps * n;
+        unsigned long long e = 0;
+        if (n < places) {
+            while (f >= look.end()) look = unit_at(look.i + 1, look.end());
+            if (f >= look.first) {
+                const int x = f - look.first, u = u0 + look.i;
+                // a page that does not exist is copied from the first one and attended with length 0
+                const unsigned char *src;
+                int len = 0;
+                if (x < look.cnt.x) {
+                    src = A.pool;
+                    const int id = A.sel_pages[(size_t)u * A.max_sel + x];
+                    if (id >= 0 && id < A.page_cap) {
+                        const size_t at = (size_t)u * A.page_cap + id;
+                        src += at * q4::kRecord;
+                        len = min(max(A.page_len[at], 0), kPage);
+                    } else {
+                        set_err(A.err, ICE_ERR_CAPACITY);
+                    }
+                } else {
+                    src = A.cache;
+                    const int b = u / A.hkv, blk = x - look.cnt.x;
+                    const int id = A.table[(size_t)b * A.max_pages + blk];
+                    if (id >= 0 && id < A.n_pages) {
+                        src += ((size_t)id * A.hkv + (u - b * A.hkv)) * q4::kRecord;
+                        len = min(kPage, look.cnt.y - blk * kPage);
+                    } else {
+                        set_err(A.err, ICE_ERR_CAPACITY);
+                    }
+                }
+                e = reinterpret_cast<unsigned long long>(src) | (unsigned long long)len << kLenShift;
+            }
+        }
+        pages[n & (2 * kBatch - 1)] = e;
+    };
+    int looked = 2 * kBatch;
+    look_up(lane);
+    __syncwarp();
+    auto look_further = [&]() {
+        if (lane < kBatch) look_up(looked + lane);
+        looked += kBatch;
+        __syncwarp();
+    };
+    const uint64_t pol = l2_evict_first();
+    const uint32_t ring = su32(S.ring[warp][0]), full = su32(&S.full[warp][0]);
+    const bool copies = lane == 0 && !A.fault_skip;  // fault injection: the waits for pages give up
+    auto issue = [&](int n) {                        // the copy of place n, if it is a page
+        const unsigned long long e = pages[n & (2 * kBatch - 1)];
+        const uint32_t slot = n & (kSlots - 1);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %0, 0;\n\t"
+            "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t"
+            "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%3], [%4], %2, [%1], "
+            "%5;\n\t}" ::"r"((int)(copies && e != 0)),
+            "r"(full + slot * 8), "r"((uint32_t)q4::kRecord), "r"(ring + slot * q4::kRecord),
+            "l"(e & ((1ull << kLenShift) - 1)), "l"(pol)
+            : "memory");
+    };
+    int issued = 0;  // places whose copy was started
+    for (; issued < kSlots - 1; ++issued) issue(issued);
+
+    const int r = lane >> 2, c = lane & 3;
     State<HN> st;
     Queries<NQ, HN> q;
-    bool dead = false;
-    int taken = 0;
-    int seg_i = 0, seg_us = cons.us, seg_n = cons.n;  // the unit being attended, by all warps alike
-    for (int fa = 0; fa < run;) {
-        const int fb = min(run, seg_us + seg_n);
-        const int u = u0 + seg_i, b = u / A.hkv, h = u % A.hkv;
-        const size_t row0 = (size_t)b * A.hq + (size_t)h * g;
+    bool dead = false;  // a wait gave up, for place `stopped`
+    int stopped = 0;
+    uint32_t phase = 0;  // of the warp's slots
+    for (;;) {
+        // the next unit with pages in the run
+        while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end());
+        if (unit.first >= run) break;
+        const int pa = max(unit.first, 0), pb = min(unit.end(), run);
+        const int u = u0 + unit.i, b = u / A.hkv;
+        const size_t row0 = (size_t)b * A.hq + (size_t)(u - b * A.hkv) * g;
         st.init();
-        bool bad = false, any = false;
-        if (cons.f < fb) {
-            load_queries<T, NQ, HN>(static_cast<const T *>(A.Q) + row0 * kHeadDim, g, A.scale, q);
-            settle(cons);
-        }
-        while (cons.f < fb) {
-            any = true;
-            int len = len_of[0];
-            if (len < 0) len = min(kPage, cons.cnt.y - (cons.f - cons.us - cons.cnt.x) * kPage);
-            const int slot = taken % NS;
-            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait(&S.full[warp][slot], (taken / NS) & 1, A.wait_ns));
-            if (dead) {
-                bad = true;
-                cons.f += kWarps;
-                continue;  // nothing more is issued; the end waits for what is in flight
+        int n = (pa + ((warp - pa) & (kWarps - 1))) / kWarps;
+        const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
+        const bool any = n < n_end;
+        if (any) load_queries<T, NQ, HN>(static_cast<const T *>(A.Q) + row0 * kHeadDim, g, A.scale, q);
+        if (any && !dead) {
+            for (; issued < n + kSlots - 1; ++issued) {  // (after places without a page)
+                if (issued >= looked) look_further();
+                issue(issued);
             }
-            if (len > 0) attend_page4<NQ, HN>(q, su32(S.ring[warp][slot]), len, st);
-            __syncwarp();
-            ++taken;
-            cons.f += kWarps;
-#pragma unroll
-            for (int i = 0; i + 1 < NS; ++i) len_of[i] = len_of[i + 1];
-            len_of[NS - 1] = issue(next);
-            next = look_up();
+            while (n < n_end) {
+                while (looked - n <= kBatch) look_further();
+                const int stop = min(n_end, looked - (kSlots - 1));
+                for (; n < stop; ++n) {
+                    const uint32_t slot = n & (kSlots - 1);
+                    issue(n + kSlots - 1);
+                    if (!__all_sync(0xffffffffu, mbar_test(&S.full[warp][slot], (phase >> slot) & 1u)))
+                        if (!wait_more(&S.full[warp][slot], (phase >> slot) & 1u, A.wait_ns)) {
+                            dead = true;
+                            break;
+                        }
+                    phase ^= 1u << slot;
+                    attend_page4<NQ, HN>(q, ring + slot * q4::kRecord,
+                                         (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
+                    __syncwarp();
+                }
+                issued = n + kSlots - 1 + (dead ? 1 : 0);
+                if (dead) break;
+            }
+            stopped = n;
         }
-        if (dead) set_err(A.err, ICE_ERR_TIMEOUT);
+        const bool bad = any && dead;
+        if (bad) set_err(A.err, ICE_ERR_TIMEOUT);
 
         // ---- the warps' results to shared memory
-        __syncthreads();  // the last unit's have been read
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
@@ -575,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
 #pragma unroll
                         for (int j = 2 * gr; j < 2 * gr + 2; ++j)
                             *reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]) =
-                                make_float4(fmaf(st.o[hn][2 * j][e] * lo, back, off), fmaf(st.o[hn][2 * j][2 + e] * hi, back, off),
+                                make_float4(fmaf(st.o[hn][2 * j][e] * lo, back, off),
+                                            fmaf(st.o[hn][2 * j][2 + e] * hi, back, off),
                                             fmaf(st.o[hn][2 * j + 1][e] * lo, back, off),
                                             fmaf(st.o[hn][2 * j + 1][2 + e] * hi, back, off));
                     }
@@ -583,12 +630,14 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             }
         __syncthreads();
         // ---- joined: 32 threads a head, 4 elements each
-        const bool whole = seg_us >= 0 && seg_us + seg_n <= run;
-        const size_t part = ((size_t)blockIdx.x * 2 + (seg_us > 0 ? 1 : 0)) * g;
-        for (int hh = tid >> 5; hh < g; hh += kWarps) {
+        const bool whole = unit.first >= 0 && unit.end() <= run;
+        const size_t part = ((size_t)blockIdx.x * 2 + (unit.first > 0 ? 1 : 0)) * g;
+        for (int hh = warp; hh < g; hh += kWarps) {
             float M = -FLT_MAX, L = 0.f;
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) M = fmaxf(M, S.ml[w][hh][0]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float l = S.ml[w][hh][1];
                 if (l == 0.f) continue;
@@ -599,14 +648,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 acc.z = fmaf(x.z, wt, acc.z), acc.w = fmaf(x.w, wt, acc.w);
             }
             if (whole) {
-                if (L == L) {
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
-                    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-                } else {
-                    acc.x = acc.y = acc.z = acc.w = L;
-                }
-                *reinterpret_cast<float4 *>(A.O + (row0 + hh) * kHeadDim + 4 * lane) = acc;
-                if (A.lse && lane == 0) A.lse[row0 + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+                put_row(A, row0 + hh, acc, M, L);
             } else {
                 *reinterpret_cast<float4 *>(A.part_o + (part + hh) * kHeadDim + 4 * lane) = acc;
                 if (lane == 0) *reinterpret_cast<float2 *>(A.part_ml + (part + hh) * 2) = make_float2(M, L);
@@ -614,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         }
         if (!whole) {
             // the unit's runs: CTAs ca .. cb; a run's part is its second one when the unit starts inside the run
-            const long long us = f0 + seg_us;
-            const int ca = (int)(us / share), cb = (int)((us + seg_n - 1) / share);
+            const long long us = f0 + unit.first;
+            const int ca = (int)(us / share), cb = (int)((us + unit.n - 1) / share);
             __threadfence();
             __syncthreads();
             if (tid == 0) S.last = atomicAdd(A.ticket + u, 1) == cb - ca;
@@ -642,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
                     __syncwarp();
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                     for (int k = 0; k < runs; ++k) {
                         const float x = wt[k * g + hh];
                         const float4 y =
@@ -649,31 +692,20 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                         acc.x = fmaf(y.x, x, acc.x), acc.y = fmaf(y.y, x, acc.y);
                         acc.z = fmaf(y.z, x, acc.z), acc.w = fmaf(y.w, x, acc.w);
                     }
-                    if (L == L) {
-                        const float inv = L > 0.f ? 1.f / L : 0.f;
-                        acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-                    } else {
-                        acc.x = acc.y = acc.z = acc.w = L;
-                    }
-                    *reinterpret_cast<float4 *>(A.O + (row0 + hh) * kHeadDim + 4 * lane) = acc;
-                    if (A.lse && lane == 0)
-                        A.lse[row0 + hh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+                    put_row(A, row0 + hh, acc, M, L);
                 }
                 if (tid == 0) A.ticket[u] = 0;
             }
         }
-        // ---- the next unit with pages
-        fa = fb;
-        if (fa < run) {
-            while (fa >= seg_us + seg_n) {
-                seg_us += seg_n;
-                seg_n = pages_of(counts_at(++seg_i));
-            }
-        }
+        if (unit.end() >= run) break;
+        __syncthreads();  // the results have been read
+        unit = unit_at(unit.i + 1, unit.end());
     }
-    // copies still in flight (after a wait that gave up)
-    if (dead && !A.fault_skip)
-        for (int k = taken; k < issued; ++k) mbar_wait(&S.full[warp][k % NS], (k / NS) & 1, A.wait_ns);
+    if (dead && !A.fault_skip)  // nothing may be in flight when the CTA ends
+        for (int n = stopped; n < issued; ++n) {
+            const int slot = n & (kSlots - 1);
+            if (pages[n & (2 * kBatch - 1)] != 0) mbar_wait(&S.full[warp][slot], (phase >> slot) & 1u, A.wait_ns);
+        }
 }
 
 int device_sms() {
@@ -713,7 +745,7 @@ cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // every CTA resident at once (no CTA waits for another, but equal runs should start together)
     const long long most = (long long)A.units * ((A.pool ? A.max_sel : 0) + (long long)(A.cache ? A.max_pages : 0));
-    const long long runs = (most + kMinRun - 1) / kMinRun;
+    const long long runs = (most + (long long)A.units * kOver + kMinRun - 1) / kMinRun;
     const int grid = (int)(runs < (long long)sms * Shape<HN>::kCtas ? (runs > 0 ? runs : 1) : sms * Shape<HN>::kCtas);
     return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<HN>), s, A);
 }
