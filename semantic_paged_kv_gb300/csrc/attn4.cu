@@ -15,7 +15,7 @@
 // do not gather in few CTAs.  A unit that a run cuts leaves partial results in
 // the workspace, joined by its last CTA in run order (so the bits do not
 // depend on timing).  Inside a CTA place f of the run goes to warp f % 8, slot f
-// / 8 % 4 of its ring; a warp looks up its pages 16 at a time, one a lane, well
+// / 8 % 4 of its ring; a warp looks up its pages 32 at a time, one a lane, well
 // before their copies start, so that its loop over pages does little else than
 // attend.
 //
@@ -51,10 +51,10 @@ using namespace tc;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSlots = 4;          // pages of a warp's ring
-constexpr int kBatch = 16;         // places looked up at a time
+constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
 constexpr int kOver = 16;          // places that a unit takes beside its pages
-constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
+constexpr int kUnits = 256;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMinRun = kWarps;    // places of a run, at least: one page per warp
 
@@ -80,6 +80,14 @@ template <int HN> struct Shape {
     static constexpr int kCtas = HN == 1 ? 2 : 1;  // per SM
 };
 
+// A unit of a run: index i from u0, first page at place `first` (from the run's start), n pages.
+struct UnitAt {
+    int i, first, n;
+    int2 cnt;
+    int b;  // sequence
+    __device__ __forceinline__ int end() const { return first + n; }
+};
+
 template <int HN> struct Smem {
     unsigned char ring[kWarps][kSlots][q4::kRecord];
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
@@ -87,6 +95,7 @@ template <int HN> struct Smem {
     int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
     unsigned long long full[kWarps][kSlots];
     unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
+    UnitAt look[kWarps];  // a warp's place in its lookups
     long long sum[kWarps];
     long long start0;  // places before unit u0
     int u0, last;
@@ -137,25 +146,30 @@ constexpr float kLazy = 8.f;  // powers of two that a score may pass the running
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
+using pair_t = unsigned long long;  // two fp32 values (common.cuh)
+
 // A warp's running state over the pages of one unit.  Lane (r, c) = (lane / 4,
 // lane % 4); o[hn][t][0..3]: elements of head 8 hn + 2 c + (i & 1), row r of
 // tile t (i < 2) or row r + 8; tile t = 2 j + k, row half i / 2: element
 // 32 j + 4 r + 2 k + i / 2.
 template <int HN> struct State {
     float o[HN][8][4];
-    float m[HN][2], l[HN][2];
-    float off[HN][2][2];         // sum of P (mid - 7.5 step), by group and head (this lane's tokens)
-    float vscale[2], vlimit[2];  // of each group: power of two on step P, and the step that it holds up to
+    pair_t minus_m[HN];          // minus the running maximum (in powers of two), heads 2 c and 2 c + 1
+    float limit[HN][2];          // score (before Queries::factor) above which the maximum moves
+    pair_t l[HN];                // sum of P over this lane's tokens
+    pair_t off[HN][2];           // sum of P (mid - 7.5 step), groups 0 and 1, this lane's tokens
+    pair_t vscale;               // of each group: power of two on step P
+    float vlimit[2];             // and the step that it holds up to
     __device__ __forceinline__ void init() {
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) o[hn][t][0] = o[hn][t][1] = o[hn][t][2] = o[hn][t][3] = 0.f;
-            m[hn][0] = m[hn][1] = -FLT_MAX;
-            l[hn][0] = l[hn][1] = 0.f;
-            off[hn][0][0] = off[hn][0][1] = off[hn][1][0] = off[hn][1][1] = 0.f;
+            minus_m[hn] = pk2(FLT_MAX, FLT_MAX);
+            limit[hn][0] = limit[hn][1] = -INFINITY;
+            l[hn] = off[hn][0] = off[hn][1] = pk2(0.f, 0.f);
         }
-        vscale[0] = vscale[1] = pow2(120);
+        vscale = pk2(pow2(120), pow2(120));
         vlimit[0] = vlimit[1] = 0.f;
     }
 };
@@ -164,8 +178,8 @@ template <int HN> struct State {
 // power of two, and what the scores need of them.
 template <int NQ, int HN> struct Queries {
     uint32_t f[NQ][HN][8][2];
-    float sum[HN][2][2];  // scale log2(e) sum q over a group, for this lane's columns (heads 2 c, 2 c + 1)
-    float factor;         // scale log2(e) over the powers of two of q and of the codes
+    float sum[HN][2][2];  // sum q over a group, in the products' scale, for this lane's columns (heads 2 c, 2 c + 1)
+    float factor;         // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
 };
 
 template <typename T, int NQ, int HN>
@@ -189,8 +203,8 @@ __device__ __forceinline__ void load_queries(const T *Qg, int g, float scale, Qu
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
     const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
-    const float up = pow2(e2);
-    q.factor = sl * pow2(24) * pow2(-e2);
+    const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
+    q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(24) * pow2(-e2);
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn) {
         float s[2] = {0.f, 0.f};
@@ -216,7 +230,8 @@ __device__ __forceinline__ void load_queries(const T *Qg, int g, float scale, Qu
             s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 1);
             s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 2);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) q.sum[hn][gr][e] = sl * __shfl_sync(0xffffffffu, s[gr], 4 * (2 * c + e));
+            for (int e = 0; e < 2; ++e)
+                q.sum[hn][gr][e] = __shfl_sync(0xffffffffu, s[gr], 4 * (2 * c + e)) * up * pow2(-24);
         }
     }
 }
@@ -251,70 +266,74 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
             }
         const float2 g00 = q4::unpack_meta(m0.x), g01 = q4::unpack_meta(m0.y);  // token r
         const float2 g10 = q4::unpack_meta(m1.x), g11 = q4::unpack_meta(m1.y);  // token r + 8
-        const float b00 = fmaf(-7.5f, g00.x, g00.y), b01 = fmaf(-7.5f, g01.x, g01.y);
-        const float b10 = fmaf(-7.5f, g10.x, g10.y), b11 = fmaf(-7.5f, g11.x, g11.y);
+        const float2 b0 = upk2(fma2(pk2(-7.5f, -7.5f), pk2(g00.x, g01.x), pk2(g00.y, g01.y)));
+        const float2 b1 = upk2(fma2(pk2(-7.5f, -7.5f), pk2(g10.x, g11.x), pk2(g10.y, g11.y)));
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float s0 = fmaf(g01.x, acc[hn][1][e], g00.x * acc[hn][0][e]);
-                const float s1 = fmaf(g11.x, acc[hn][1][2 + e], g10.x * acc[hn][0][2 + e]);
-                s[hn][e] = fmaf(s0, q.factor, fmaf(b01, q.sum[hn][1][e], b00 * q.sum[hn][0][e]));
-                s[hn][2 + e] = fmaf(s1, q.factor, fmaf(b11, q.sum[hn][1][e], b10 * q.sum[hn][0][e]));
+                s[hn][e] = fmaf(g00.x, acc[hn][0][e],
+                                fmaf(g01.x, acc[hn][1][e], fmaf(b0.x, q.sum[hn][0][e], b0.y * q.sum[hn][1][e])));
+                s[hn][2 + e] = fmaf(g10.x, acc[hn][0][2 + e],
+                                    fmaf(g11.x, acc[hn][1][2 + e], fmaf(b1.x, q.sum[hn][0][e], b1.y * q.sum[hn][1][e])));
             }
     }
-    const uint2 n0 = lds64(rec + q4::kVMeta + r * 8), n1 = lds64(rec + q4::kVMeta + 64 + r * 8);
-    float2 v0[2] = {q4::unpack_meta(n0.x), q4::unpack_meta(n0.y)};  // token r: (step, mid) of both groups
-    float2 v1[2] = {q4::unpack_meta(n1.x), q4::unpack_meta(n1.y)};  // token r + 8
+    uint2 n0 = lds64(rec + q4::kVMeta + r * 8), n1 = lds64(rec + q4::kVMeta + 64 + r * 8);
     if (len < kPage) {  // slots behind the last token may hold anything
         if (r >= len) {
-            v0[0] = v0[1] = make_float2(0.f, 0.f);
+            n0 = make_uint2(0u, 0u);
 #pragma unroll
             for (int hn = 0; hn < HN; ++hn) s[hn][0] = s[hn][1] = -INFINITY;
         }
         if (r + 8 >= len) {
-            v1[0] = v1[1] = make_float2(0.f, 0.f);
+            n1 = make_uint2(0u, 0u);
 #pragma unroll
             for (int hn = 0; hn < HN; ++hn) s[hn][2] = s[hn][3] = -INFINITY;
         }
     }
+    const float2 v00 = q4::unpack_meta(n0.x), v01 = q4::unpack_meta(n0.y);  // (step, mid): token r, groups 0, 1
+    const float2 v10 = q4::unpack_meta(n1.x), v11 = q4::unpack_meta(n1.y);  // token r + 8
     // ---- the running maxima and the scale of step P, only when one has to move
-    bool move = (v0[0].x > st.vlimit[0]) | (v1[0].x > st.vlimit[0]) | (v0[1].x > st.vlimit[1]) | (v1[1].x > st.vlimit[1]);
+    bool move = (v00.x > st.vlimit[0]) | (v10.x > st.vlimit[0]) | (v01.x > st.vlimit[1]) | (v11.x > st.vlimit[1]);
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            move |= (s[hn][e] > st.m[hn][e] + kLazy) | (s[hn][2 + e] > st.m[hn][e] + kLazy);
+        for (int e = 0; e < 2; ++e) move |= (s[hn][e] > st.limit[hn][e]) | (s[hn][2 + e] > st.limit[hn][e]);
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-        for (int hn = 0; hn < HN; ++hn)
+        for (int hn = 0; hn < HN; ++hn) {
+            const float2 old = upk2(st.minus_m[hn]);
+            float now[2], al[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mx = fmaxf(s[hn][e], s[hn][2 + e]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                mx = fmaxf(mx, st.m[hn][e]);
-                const float al = exp2_fast(st.m[hn][e] - mx);
-                st.m[hn][e] = mx;
-                st.l[hn][e] *= al;
-                st.off[hn][0][e] *= al;
-                st.off[hn][1][e] *= al;
+                const float was = e ? old.y : old.x;
+                now[e] = fminf(was, -mx * q.factor);
+                al[e] = exp2_fast(now[e] - was);
+                st.limit[hn][e] = (kLazy - now[e]) / q.factor;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    st.o[hn][t][e] *= al;
-                    st.o[hn][t][2 + e] *= al;
+                    st.o[hn][t][e] *= al[e];
+                    st.o[hn][t][2 + e] *= al[e];
                 }
+                st.off[hn][e] = mul2(st.off[hn][e], pk2(al[e], al[e]));
             }
+            st.minus_m[hn] = pk2(now[0], now[1]);
+            st.l[hn] = mul2(st.l[hn], pk2(al[0], al[1]));
+        }
+        float2 vs = upk2(st.vscale);
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
-            float mx = fmaxf(v0[gr].x, v1[gr].x);
+            float mx = gr ? fmaxf(v01.x, v11.x) : fmaxf(v00.x, v10.x);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             if (mx > st.vlimit[gr]) {
                 // steps up to [2^5, 2^6) now, up to 2^7 before the scale moves again: with P <= 2^8 below fp16's 2^16
                 const int e = min(5 - exponent_of(mx), 119);  // >= -122
-                const float to = pow2(e), down = to / st.vscale[gr];
-                st.vscale[gr] = to;
+                const float to = pow2(e), down = to / (gr ? vs.y : vs.x);
+                (gr ? vs.y : vs.x) = to;
                 st.vlimit[gr] = pow2(min(7 - e, 127));
 #pragma unroll
                 for (int hn = 0; hn < HN; ++hn)
@@ -324,34 +343,36 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
                         for (int i = 0; i < 4; ++i) st.o[hn][t][i] *= down;
             }
         }
+        st.vscale = pk2(vs.x, vs.y);
     }
-    // ---- P, and step P in hi + lo parts, transposed to B fragments
+    // ---- P, and step P of both groups in hi + lo parts, transposed to B fragments
     uint32_t bh[HN][2][2], bl[HN][2][2];  // [group][token half]
+    const pair_t f[2] = {mul2(pk2(v00.x, v01.x), st.vscale), mul2(pk2(v10.x, v11.x), st.vscale)};
+    const pair_t b[2] = {fma2(pk2(-7.5f, -7.5f), pk2(v00.x, v01.x), pk2(v00.y, v01.y)),
+                         fma2(pk2(-7.5f, -7.5f), pk2(v10.x, v11.x), pk2(v10.y, v11.y))};
 #pragma unroll
-    for (int hn = 0; hn < HN; ++hn) {
-        float p[4];
+    for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = exp2_fast(s[hn][i] - st.m[hn][i & 1]);
-        st.l[hn][0] += p[0] + p[2];
-        st.l[hn][1] += p[1] + p[3];
+        for (int half = 0; half < 2; ++half) {
+            const float2 y = upk2(fma2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), pk2(q.factor, q.factor), st.minus_m[hn]));
+            const float p[2] = {exp2_fast(y.x), exp2_fast(y.y)};
+            st.l[hn] = add2(st.l[hn], pk2(p[0], p[1]));
+            pair_t x[2];
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            const float f0 = v0[gr].x * st.vscale[gr], f1 = v1[gr].x * st.vscale[gr];
-            const float c0 = fmaf(-7.5f, v0[gr].x, v0[gr].y), c1 = fmaf(-7.5f, v1[gr].x, v1[gr].y);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                st.off[hn][gr][e] = fmaf(p[2 + e], c1, fmaf(p[e], c0, st.off[hn][gr][e]));
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const float f = half ? f1 : f0;
-                const float x = p[2 * half] * f, y = p[2 * half + 1] * f;
-                const __half2 hi = __floats2half2_rn(x, y);
-                const float2 back = __half22float2(hi);
-                bh[hn][gr][half] = transpose8(h2_bits(hi));
-                bl[hn][gr][half] = transpose8(h2_bits(__floats2half2_rn(x - back.x, y - back.y)));
+            for (int e = 0; e < 2; ++e) {
+                const pair_t pp = pk2(p[e], p[e]);
+                st.off[hn][e] = fma2(pp, b[half], st.off[hn][e]);
+                x[e] = mul2(pp, f[half]);
             }
+            const float2 x0 = upk2(x[0]), x1 = upk2(x[1]);
+            const __half2 h0 = __floats2half2_rn(x0.x, x1.x), h1 = __floats2half2_rn(x0.y, x1.y);
+            const float2 w0 = __half22float2(h0), w1 = __half22float2(h1);
+            const float2 d0 = upk2(sub2(x[0], pk2(w0.x, w1.x))), d1 = upk2(sub2(x[1], pk2(w0.y, w1.y)));
+            bh[hn][0][half] = transpose8(h2_bits(h0));
+            bh[hn][1][half] = transpose8(h2_bits(h1));
+            bl[hn][0][half] = transpose8(h2_bits(__floats2half2_rn(d0.x, d1.x)));
+            bl[hn][1][half] = transpose8(h2_bits(__floats2half2_rn(d0.y, d1.y)));
         }
-    }
     // ---- O^T += V^T (step P)^T
     {
         const uint4 x0 = lds128(rec + q4::kV + c * 128 + r * 16), x1 = lds128(rec + q4::kV + 512 + c * 128 + r * 16);
@@ -386,13 +407,6 @@ __device__ __forceinline__ int2 unit_counts(const Attn4Args &A, int u) {
 __device__ __forceinline__ int pages_of(int2 n) { return n.x + (n.y + kPage - 1) / kPage; }
 // Places of a unit of n pages: kOver, then the pages; none without pages.
 __device__ __forceinline__ int places_of(int n) { return n > 0 ? n + kOver : 0; }
-
-// A unit of a run: index i from u0, first page at place `first` (from the run's start), n pages.
-struct UnitAt {
-    int i, first, n;
-    int2 cnt;
-    __device__ __forceinline__ int end() const { return first + n; }
-};
 
 // The rest of a wait: true when the phase of the given parity is complete, false after limit_ns.
 __device__ __noinline__ bool wait_more(unsigned long long *bar, uint32_t parity, unsigned long long limit_ns) {
@@ -451,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         if (w < warp) before += S.sum[w];
         total += S.sum[w];
     }
-    long long share = (total + gridDim.x - 1) / gridDim.x;
+    long long share = total < (1ll << 31) ? ((unsigned)total + gridDim.x - 1) / gridDim.x
+                                          : (total + gridDim.x - 1) / gridDim.x;
     if (share < kMinRun) share = kMinRun;
     const long long f0 = (long long)blockIdx.x * share;
     const int run = (int)min(share, total - f0);
@@ -479,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         x.i = i;
         x.cnt = u0 - base + i < kUnits ? S.units[u0 - base + i] : unit_counts(A, u0 + i);
         x.n = pages_of(x.cnt);
+        x.b = (u0 + i) / A.hkv;
         x.first = place + (x.n > 0 ? kOver : 0);
         return x;
     };
@@ -487,8 +503,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     // ---- the warp's pages: places n = 0 .. of the warp are places warp + 8 n of the run
     const int places = run > warp ? (run - warp + kWarps - 1) / kWarps : 0;
     unsigned long long *pages = S.page[warp];
-    UnitAt look = unit;
-    auto look_up = [&](int n) {  // place n of this lane
+    if (lane == 0) S.look[warp] = unit;
+    auto look_up = [&](int n) {  // place n of this lane, in order of the lanes
+        __syncwarp();
+        UnitAt look = S.look[warp];
+        __syncwarp();
         const int f = warp + kWarps * n;
         unsigned long long e = 0;
         if (n < places) {
@@ -510,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     }
                 } else {
                     src = A.cache;
-                    const int b = u / A.hkv, blk = x - look.cnt.x;
+                    const int b = look.b, blk = x - look.cnt.x;
                     const int id = A.table[(size_t)b * A.max_pages + blk];
                     if (id >= 0 && id < A.n_pages) {
                         src += ((size_t)id * A.hkv + (u - b * A.hkv)) * q4::kRecord;
@@ -523,29 +542,29 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             }
         }
         pages[n & (2 * kBatch - 1)] = e;
-    };
-    int looked = 2 * kBatch;
-    look_up(lane);
-    __syncwarp();
-    auto look_further = [&]() {
-        if (lane < kBatch) look_up(looked + lane);
-        looked += kBatch;
+        if (lane == 31) S.look[warp] = look;
         __syncwarp();
     };
-    const uint64_t pol = l2_evict_first();
+    int looked = kBatch;
+    look_up(lane);
+    auto look_further = [&]() {
+        look_up(looked + lane);
+        looked += kBatch;
+    };
     const uint32_t ring = su32(S.ring[warp][0]), full = su32(&S.full[warp][0]);
     const bool copies = lane == 0 && !A.fault_skip;  // fault injection: the waits for pages give up
     auto issue = [&](int n) {                        // the copy of place n, if it is a page
         const unsigned long long e = pages[n & (2 * kBatch - 1)];
         const uint32_t slot = n & (kSlots - 1);
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p;\n\t.reg .b64 once;\n\t"
             "setp.ne.b32 p, %0, 0;\n\t"
+            "createpolicy.fractional.L2::evict_first.b64 once, 1.0;\n\t"
             "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t"
             "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%3], [%4], %2, [%1], "
-            "%5;\n\t}" ::"r"((int)(copies && e != 0)),
+            "once;\n\t}" ::"r"((int)(copies && e != 0)),
             "r"(full + slot * 8), "r"((uint32_t)q4::kRecord), "r"(ring + slot * q4::kRecord),
-            "l"(e & ((1ull << kLenShift) - 1)), "l"(pol)
+            "l"(e & ((1ull << kLenShift) - 1))
             : "memory");
     };
     int issued = 0;  // places whose copy was started
@@ -575,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 issue(issued);
             }
             while (n < n_end) {
-                while (looked - n <= kBatch) look_further();
+                while (looked - n <= kBatch / 2) look_further();
                 const int stop = min(n_end, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
                     const uint32_t slot = n & (kSlots - 1);
@@ -603,21 +622,23 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = st.l[hn][e];
+                const float2 l2 = upk2(st.l[hn]), m2 = upk2(st.minus_m[hn]), off2 = upk2(st.off[hn][e]);
+                const float2 vs = upk2(st.vscale);
+                float l = e ? l2.y : l2.x;
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
                 const int head = 8 * hn + 2 * c + e;
                 if (r == 0) {
-                    S.ml[warp][head][0] = st.m[hn][e];
+                    S.ml[warp][head][0] = -(e ? m2.y : m2.x);
                     S.ml[warp][head][1] = bad ? __int_as_float(0x7fc00000) : l;
                 }
                 if (any) {
 #pragma unroll
                     for (int gr = 0; gr < 2; ++gr) {
-                        float off = st.off[hn][gr][e];
+                        float off = gr ? off2.y : off2.x;
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) off += __shfl_xor_sync(0xffffffffu, off, x);
-                        const float back = 1.f / st.vscale[gr], lo = pow2(24), hi = pow2(20);
+                        const float back = 1.f / (gr ? vs.y : vs.x), lo = pow2(24), hi = pow2(20);
 #pragma unroll
                         for (int j = 2 * gr; j < 2 * gr + 2; ++j)
                             *reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]) =
