@@ -146,7 +146,7 @@ constexpr float kLazy = 8.f;  // powers of two that a score may pass the running
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
-using pair_t = unsigned long long;  // two fp32 values (common.cuh)
+using q4::pair_t;
 
 // A warp's running state over the pages of one unit.  Lane (r, c) = (lane / 4,
 // lane % 4); o[hn][t][0..3]: elements of head 8 hn + 2 c + (i & 1), row r of

@@ -19,24 +19,38 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kVecs = q4::kRecord / 16;
 
-// Rows [n, 128] of one page (n <= 16) into a record in shared memory.
+// A page's rows, the first `len` of them, into a record in shared memory.
 template <typename T>
 __device__ __forceinline__ void page_to_record(const T *kp, const T *vp, int len, unsigned char *rec) {
     const int lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
+    constexpr int kIts = kPage / 4;
+    // bf16: all of the page's loads in flight before the first row is quantised; fp32: K's, then V's
+    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
+    q4::Vec8<T> a[kAhead][kIts], b[kAhead][kIts];
+    auto load = [&](int which, int at) {
+        const T *src = (which ? vp : kp) + l * 8;
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+            const int t = it * 4 + row;
+            a[at][it].zero();
+            b[at][it].zero();
+            if (t < len) {
+                a[at][it].load(src + t * kHeadDim);
+                b[at][it].load(src + t * kHeadDim + 64);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, i);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const T *src = which ? vp : kp;
+        if (which >= kAhead) load(which, 0);
 #pragma unroll
-        for (int it = 0; it < kPage / 4; ++it) {
-            const int t = it * 4 + row;
-            float a[8] = {}, b[8] = {};
-            if (t < len) {
-                load8<T>(src + t * kHeadDim + l * 8, a);
-                load8<T>(src + t * kHeadDim + (l + 8) * 8, b);
-            }
+        for (int it = 0; it < kIts; ++it) {
+            const int t = it * 4 + row, at = which < kAhead ? which : 0;
             uint32_t ca, cb;
             float2 sm[2];
-            q4::quantise_row<T>(a, b, l, l + 8, ca, cb, sm);
+            q4::quantise_row<T>(a[at][it], b[at][it], l, l + 8, ca, cb, sm);
             if (which)
                 q4::put_v(rec, t, l, l + 8, ca, cb);
             else
@@ -93,10 +107,12 @@ __global__ void __launch_bounds__(kWarps * 32) k_pool4_tokens(
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const T *src = (which ? pool_v : pool_k) + (at * kPage + slot) * kHeadDim;
-            float a[8] = {}, b[8] = {};
+            q4::Vec8<T> a, b;
+            a.zero();
+            b.zero();
             if (pg >= 0) {
-                load8<T>(src + l * 8, a);
-                load8<T>(src + (l + 8) * 8, b);
+                a.load(src + l * 8);
+                b.load(src + (l + 8) * 8);
             }
             uint32_t ca, cb;
             float2 sm[2];

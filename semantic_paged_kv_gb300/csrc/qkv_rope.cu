@@ -164,27 +164,24 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
     const int heads = kind == 0 ? A.hq : A.hkv;
     const ice_rows &in = kind == 0 ? A.q : (kind == 1 ? A.k : A.v);
     const ice_rows &out = kind == 0 ? A.qo : (kind == 1 ? A.ko : A.vo);
-    int pos = 0;
-    if (live) {
-        live = i < count_of(A, b);
-        pos = live ? position_of(A, b, i) : 0;
-        if (pos < 0) {
-            set_err(A.err, ICE_ERR_CAPACITY);
-            live = false;
-        }
-    }
+    live = live && i < count_of(A, b);
     const LaneVecs v = lane_vecs(A, l);
     const T *src = static_cast<const T *>(in.data) + (long long)b * in.batch + (long long)i * in.token;
     T *dst = static_cast<T *>(out.data) + (long long)b * out.batch + (long long)i * out.token;
-    float a[kHeads][8], c[kHeads][8];
+    q4::Vec8<T> ra[kHeads], rb[kHeads];
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[j][e] = c[j][e] = 0.f;
+        ra[j].zero();
+        rb[j].zero();
         if (live && h0 + j < heads) {
-            load8<T>(src + (h0 + j) * in.head + v.wa * 8, a[j]);
-            load8<T>(src + (h0 + j) * in.head + v.wb * 8, c[j]);
+            ra[j].load(src + (h0 + j) * in.head + v.wa * 8);
+            rb[j].load(src + (h0 + j) * in.head + v.wb * 8);
         }
+    }
+    const int pos = live ? position_of(A, b, i) : 0;
+    if (pos < 0) {
+        set_err(A.err, ICE_ERR_CAPACITY);
+        live = false;
     }
     const bool turn = live && kind != 2 && A.table;
     float co[8], si[8];
@@ -198,11 +195,14 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
     }
 #pragma unroll
     for (int j = 0; j < kHeads; ++j) {
-        if (A.wq || A.wk) norm_row<T>(a[j], c[j], wa, wb, A.eps, norm);
-        if (turn) rotate<false>(A, v, a[j], c[j], co, si);
+        float a[8], c[8];
+        ra[j].get(a);
+        rb[j].get(c);
+        if (A.wq || A.wk) norm_row<T>(a, c, wa, wb, A.eps, norm);
+        if (turn) rotate<false>(A, v, a, c, co, si);
         if (live && h0 + j < heads) {
-            store8<T>(dst + (h0 + j) * out.head + v.wa * 8, a[j]);
-            store8<T>(dst + (h0 + j) * out.head + v.wb * 8, c[j]);
+            store8<T>(dst + (h0 + j) * out.head + v.wa * 8, a);
+            store8<T>(dst + (h0 + j) * out.head + v.wb * 8, c);
         }
     }
 }
@@ -279,14 +279,17 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (rows >> (8 * r) & 1u) done |= 1u << (it * 4 + r);
-        float a[8] = {}, c[8] = {}, va[8] = {}, vc[8] = {};
+        float a[8] = {}, c[8] = {};
+        q4::Vec8<T> va, vc;
+        va.zero();
+        vc.zero();
         if (live) {
             const T *ks = static_cast<const T *>(A.k.data) + b * A.k.batch + i * A.k.token + h * A.k.head;
             const T *vs = static_cast<const T *>(A.v.data) + b * A.v.batch + i * A.v.token + h * A.v.head;
             load8<T>(ks + v.wa * 8, a);
             load8<T>(ks + v.wb * 8, c);
-            load8<T>(vs + l * 8, va);
-            load8<T>(vs + (l + 8) * 8, vc);
+            va.load(vs + l * 8);
+            vc.load(vs + (l + 8) * 8);
         }
         if (w) norm_row<T>(a, c, wa, wb, A.eps, true);
         if (live && A.table) {
@@ -294,11 +297,12 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
             load_angles(A, v, pos, co, si);
             rotate<sizeof(T) == 4>(A, v, a, c, co, si);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = round_to<T>(a[e]), c[e] = round_to<T>(c[e]);
+        q4::Vec8<T> ka, kc;  // rounded to the storage type
+        ka.set(a);
+        kc.set(c);
         uint32_t ca, cb;
         float2 sm[2];
-        q4::quantise_row<T>(a, c, v.wa, v.wb, ca, cb, sm);
+        q4::quantise_row<T>(ka, kc, v.wa, v.wb, ca, cb, sm);
         q4::put_k(rec, t, v.wa, v.wb, ca, cb);
         if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kKMeta + t * 8) = q4::pack_meta(sm);
         q4::quantise_row<T>(va, vc, l, l + 8, ca, cb, sm);

@@ -12,6 +12,8 @@
 namespace ice {
 namespace q4 {
 
+using pair_t = unsigned long long;  // two fp32 values (common.cuh)
+
 constexpr int kCodeBytes = kPage * kHeadDim / 2;  // K or V codes of a record
 constexpr int kMetaBytes = kPage * 8;             // (step, mid) of two groups a token
 constexpr int kKMeta = kCodeBytes;
@@ -32,18 +34,104 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+// Extremes of values as (min, -max), both taken by min: one exchange serves
+// two values.  bf16 values stay packed, (min, -max) in one word.
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-__device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+// Eight consecutive elements of a row in their storage type.
+template <typename T> struct Vec8;
+template <> struct Vec8<__nv_bfloat16> {
+    uint32_t w[4];
+    using Ends = uint32_t;
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    __device__ __forceinline__ Ends ends() const {
+        const uint32_t mn = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
+        const uint32_t mx = max2_nan(max2_nan(w[0], w[1]), max2_nan(w[2], w[3]));
+        return min2_nan(__byte_perm(mn, mx, 0x5410) ^ 0x80000000u, __byte_perm(mn, mx, 0x7632) ^ 0x80000000u);
+    }
+    __device__ __forceinline__ static Ends none() { return 0x7F807F80u; }
+    __device__ __forceinline__ static Ends join(Ends a, Ends b) { return min2_nan(a, b); }
+    __device__ __forceinline__ static Ends exchange(Ends a, int off) { return __shfl_xor_sync(0xffffffffu, a, off); }
+    __device__ __forceinline__ static float lo(Ends a) { return __uint_as_float(a << 16); }
+    __device__ __forceinline__ static float hi(Ends a) { return -__uint_as_float(a & 0xFFFF0000u); }
+};
+template <> struct Vec8<float> {
+    float v[8];
+    struct Ends {
+        float lo, neg;
+    };
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = v[e];
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = x[e];
+    }
+    __device__ __forceinline__ Ends ends() const {
+        Ends r{v[0], -v[0]};
+#pragma unroll
+        for (int e = 1; e < 8; ++e) r.lo = min_nan(r.lo, v[e]), r.neg = min_nan(r.neg, -v[e]);
+        return r;
+    }
+    __device__ __forceinline__ static Ends none() { return Ends{INFINITY, INFINITY}; }
+    __device__ __forceinline__ static Ends join(Ends a, Ends b) {
+        return Ends{min_nan(a.lo, b.lo), min_nan(a.neg, b.neg)};
+    }
+    __device__ __forceinline__ static Ends exchange(Ends a, int off) {
+        return Ends{__shfl_xor_sync(0xffffffffu, a.lo, off), __shfl_xor_sync(0xffffffffu, a.neg, off)};
+    }
+    __device__ __forceinline__ static float lo(Ends a) { return a.lo; }
+    __device__ __forceinline__ static float hi(Ends a) { return -a.neg; }
+};
 
-// step and mid of a group from its extremes.  T: the storage type of the
-// elements; differences of bf16 values are exact in fp32 (unless their
-// exponents are more than 16 apart, where the rounding is far below a code),
-// those of fp32 values are taken in fp64.
+// step and mid of a group from its extremes.  Differences of bf16 values are
+// exact in fp32 (unless their exponents are more than 16 apart, where the
+// rounding is far below a code); those of fp32 values are taken in fp64.
 template <typename T>
 __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     float step, mid;
@@ -58,71 +146,92 @@ __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     return make_float2(bf16_rn(step), bf16_rn(mid));
 }
 
-// Code of x: rint((x - mid) / step + 7.5), ties to even, decided as if
-// exactly.  The product with the reciprocal is within 2e-6 of the quotient;
-// only values that near a border between two codes (1 in 50 000, and true
-// ties) take the division.
-template <typename T>
-__device__ __forceinline__ uint32_t code_of(float x, float mid, float step, float inv) {
-    const float t = fmaf(x - mid, inv, 7.5f);
-    float c = rintf(t);
-    if (fabsf(t - c) > 0.49999f) {
-        if (sizeof(T) == 2)
-            c = rintf(__fadd_rn(__fdiv_rn(x - mid, step), 7.5f));
-        else
-            c = (float)rint(((double)x - (double)mid) / (double)step + 7.5);
+// The word of a vector's 8 codes, rint((x - mid) / step + 7.5) with ties to
+// even, decided exactly without a division: with k the integer next to (x -
+// mid) / step (from an approximate reciprocal; which of two neighbours it is
+// does not matter), the code is k + 8 where the remainder x - mid - k step is
+// positive, k + 7 where it is negative, and the even one of the two where it
+// is zero.  The remainder's sign is exact (bf16: as far as x - mid is): k step is (4 bits times 8), and a
+// fused multiply-add rounds a nonzero difference to one of the same sign.  fp32
+// values take mid + k step as an unevaluated sum.
+template <typename T, bool kClamp>
+__device__ __forceinline__ uint32_t codes_in(const float (&x)[8], float step, float mid, float inv) {
+    constexpr float kBig = 12582912.f;  // 1.5 * 2^23: integers end up in the low bits
+    const pair_t mid2 = pk2(mid, mid), inv2 = pk2(inv, inv), neg2 = pk2(-step, -step);
+    const pair_t big2 = pk2(kBig, kBig);
+    uint32_t w = kClamp ? 0u : 0x88888888u - 0x4B400000u * 0x11111111u;  // + 8, - the bits of kBig, in every nibble
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const pair_t d = sub2(pk2(x[2 * i], x[2 * i + 1]), mid2);
+        const pair_t t = fma2(d, inv2, big2), k = sub2(t, big2);
+        float2 rem;
+        if (sizeof(T) == 2) {
+            rem = upk2(fma2(k, neg2, d));
+        } else {
+            const float2 kk = upk2(k);
+            float s, e;
+            two_sum(mid, kk.x * step, s, e);
+            rem.x = (x[2 * i] - s) - e;
+            two_sum(mid, kk.y * step, s, e);
+            rem.y = (x[2 * i + 1] - s) - e;
+        }
+        const float2 tt = upk2(t);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int b = __float_as_int(h ? tt.y : tt.x), r = __float_as_int(h ? rem.y : rem.x);
+            const bool below = r < (b & 1);  // negative, or zero and k odd
+            const int sh = 4 * (2 * i + h);
+            if (kClamp) {
+                w |= (uint32_t)min(max(b - 0x4B400000 + 8 - (below ? 1 : 0), 0), 15) << sh;
+            } else {
+                w += (uint32_t)b * (1u << sh);
+                if (below) w -= 1u << sh;
+            }
+        }
     }
-    return (uint32_t)fminf(fmaxf(c, 0.f), 15.f);
+    return w;
 }
 
-// The word of a vector's 8 codes.
+// (lo, hi: the group's extremes)
 template <typename T>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float2 sm) {
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float2 sm, float lo, float hi) {
     if (!(sm.x > 0.f)) return 0u;
-    // below 2^-100 the reciprocal leaves fp32's normal range: scale both sides
-    const bool tiny = sm.x < 7.9e-31f;
+    float step = sm.x, mid = sm.y;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    // codes outside 0 .. 15 come only from the rounding of step and mid; steps below 2^-100 (their reciprocal leaves
+    // fp32's normal range) go the slow way too, scaled
+    const bool tiny = step < 7.9e-31f;
+    if (!tiny && hi - mid < 8.f * step && mid - lo <= 8.f * step) return codes_in<T, false>(x, step, mid, inv);
+    float y[8];
     const float up = tiny ? 1.2676506e30f : 1.f;  // 2^100
-    const float step = sm.x * up, mid = sm.y * up;
-    const float inv = 1.f / step;
-    uint32_t w = 0u;
+    step *= up, mid *= up;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= code_of<T>(tiny ? x[e] * up : x[e], mid, step, inv) << (4 * e);
-    return w;
+    for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(x[e] * up, mid - 9.f * step), mid + 9.f * step);
+    return codes_in<T, true>(y, step, mid, 1.f / step);
 }
 
 // Quantises a row held by 8 lanes (vectors wa and wb of lane l): the words of
 // both vectors, and (step, mid) of both groups in every lane.
 template <typename T>
-__device__ __forceinline__ void quantise_row(const float (&a)[8], const float (&b)[8], int wa, int wb, uint32_t &ca,
+__device__ __forceinline__ void quantise_row(const Vec8<T> &a, const Vec8<T> &b, int wa, int wb, uint32_t &ca,
                                              uint32_t &cb, float2 (&sm)[2]) {
-    float la = a[0], ha = a[0], lb = b[0], hb = b[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        la = min_nan(la, a[e]);
-        ha = max_nan(ha, a[e]);
-        lb = min_nan(lb, b[e]);
-        hb = max_nan(hb, b[e]);
-    }
-    float lo[2] = {INFINITY, INFINITY}, hi[2] = {-INFINITY, -INFINITY};
+    using V = Vec8<T>;
+    const typename V::Ends ea = a.ends(), eb = b.ends();
+    float lo[2], hi[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        if ((wa >> 3) == g) {
-            lo[g] = min_nan(lo[g], la);
-            hi[g] = max_nan(hi[g], ha);
-        }
-        if ((wb >> 3) == g) {
-            lo[g] = min_nan(lo[g], lb);
-            hi[g] = max_nan(hi[g], hb);
-        }
+        typename V::Ends e = V::join((wa >> 3) == g ? ea : V::none(), (wb >> 3) == g ? eb : V::none());
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) {
-            lo[g] = min_nan(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], off));
-            hi[g] = max_nan(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], off));
-        }
+        for (int off = 1; off < 8; off <<= 1) e = V::join(e, V::exchange(e, off));
+        lo[g] = V::lo(e), hi[g] = V::hi(e);
         sm[g] = step_mid<T>(lo[g], hi[g]);
     }
-    ca = codes_of<T>(a, (wa >> 3) ? sm[1] : sm[0]);
-    cb = codes_of<T>(b, (wb >> 3) ? sm[1] : sm[0]);
+    float x[8], y[8];
+    a.get(x);
+    b.get(y);
+    ca = codes_of<T>(x, (wa >> 3) ? sm[1] : sm[0], (wa >> 3) ? lo[1] : lo[0], (wa >> 3) ? hi[1] : hi[0]);
+    cb = codes_of<T>(y, (wb >> 3) ? sm[1] : sm[0], (wb >> 3) ? lo[1] : lo[0], (wb >> 3) ? hi[1] : hi[0]);
 }
 
 // (step, mid) of a token's two groups as stored.
@@ -135,10 +244,18 @@ __device__ __forceinline__ float2 unpack_meta(uint32_t m) {
     return make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
 }
 
-// The values that a vector's codes stand for.
+// The values that a vector's codes stand for: mid + step (code - 7.5), one
+// rounding.  A code at bit 7 of 2^16 adds its value.
 __device__ __forceinline__ void values_of(uint32_t w, float2 sm, float (&x)[8]) {
+    const pair_t step = pk2(sm.x, sm.x), mid = pk2(sm.y, sm.y), off = pk2(65543.5f, 65543.5f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(sm.x, (float)((w >> (4 * e)) & 15u) - 7.5f, sm.y);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = i == 0 ? w << 7 : w >> (i == 0 ? 0 : 8 * i - 7), b = i == 0 ? w << 3 : w >> (i == 0 ? 0 : 8 * i - 3);
+        const pair_t c = sub2(pk2(__uint_as_float((a & 0x780u) | 0x47800000u),
+                                  __uint_as_float((b & 0x780u) | 0x47800000u)), off);
+        const float2 y = upk2(fma2(step, c, mid));
+        x[2 * i] = y.x, x[2 * i + 1] = y.y;
+    }
 }
 
 // Writes a row's codes and (step, mid) into a record (shared or global
@@ -164,30 +281,15 @@ __device__ __forceinline__ uint32_t get_v(const unsigned char *rec, int token, i
 }  // namespace q4
 
 // ------------------------------------------------ rows in 8-element vectors --
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[8]) {
-    Elem<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4 *>(p), x);
+template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+    q4::Vec8<T> v;
+    v.load(p);
+    v.get(x);
 }
-template <> __device__ __forceinline__ void load8<float>(const float *p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+    q4::Vec8<T> v;
+    v.set(x);
+    v.store(p);
 }
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8]);
-template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16 *p, const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <> __device__ __forceinline__ void store8<float>(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-template <typename T> __device__ __forceinline__ float round_to(float x) { return x; }
-template <> __device__ __forceinline__ float round_to<__nv_bfloat16>(float x) { return q4::bf16_rn(x); }
 
 }  // namespace ice
