@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
+#include "tc_common.cuh"
 
 namespace ice {
 namespace {
@@ -19,45 +20,41 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kVecs = q4::kRecord / 16;
 
-// A page's rows, the first `len` of them, into a record in shared memory.
+// A page's rows, the first `len` of them, into a record in shared memory: K's
+// in four turns of four rows, then V's.  The next turn's loads are in flight
+// while one is quantised; the loop is not unrolled, so that it stays in the
+// instruction cache.
 template <typename T>
 __device__ __forceinline__ void page_to_record(const T *kp, const T *vp, int len, unsigned char *rec) {
     const int lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
-    constexpr int kIts = kPage / 4;
-    // bf16: all of the page's loads in flight before the first row is quantised; fp32: K's, then V's
-    constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;
-    q4::Vec8<T> a[kAhead][kIts], b[kAhead][kIts];
-    auto load = [&](int which, int at) {
-        const T *src = (which ? vp : kp) + l * 8;
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-            const int t = it * 4 + row;
-            a[at][it].zero();
-            b[at][it].zero();
-            if (t < len) {
-                a[at][it].load(src + t * kHeadDim);
-                b[at][it].load(src + t * kHeadDim + 64);
-            }
+    q4::Vec8<T> a, b, na, nb;
+    auto load = [&](int turn, q4::Vec8<T> &x, q4::Vec8<T> &y) {
+        const int t = (turn & 3) * 4 + row;
+        const T *src = (turn < 4 ? kp : vp) + t * kHeadDim + l * 8;
+        x.zero();
+        y.zero();
+        if (t < len) {
+            x.load(src);
+            y.load(src + 64);
         }
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(i, i);
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (which >= kAhead) load(which, 0);
-#pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-            const int t = it * 4 + row, at = which < kAhead ? which : 0;
-            uint32_t ca, cb;
-            float2 sm[2];
-            q4::quantise_row<T>(a[at][it], b[at][it], l, l + 8, ca, cb, sm);
-            if (which)
-                q4::put_v(rec, t, l, l + 8, ca, cb);
-            else
-                q4::put_k(rec, t, l, l + 8, ca, cb);
-            if (l == 0)
-                *reinterpret_cast<uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + t * 8) = q4::pack_meta(sm);
-        }
+    load(0, a, b);
+#pragma unroll 1
+    for (int turn = 0; turn < 8; ++turn) {
+        if (turn < 7) load(turn + 1, na, nb);
+        const int t = (turn & 3) * 4 + row;
+        const bool live = t < len;
+        uint32_t ca, cb;
+        uint2 meta;
+        q4::quantise_row<T>(a, b, l, l + 8, live, ca, cb, meta);
+        if (!live) ca = cb = 0u;  // pad slots (their step and mid came out zero)
+        if (turn < 4)
+            q4::put_k(rec, t, l, l + 8, ca, cb);
+        else
+            q4::put_v(rec, t, l, l + 8, ca, cb);
+        if (l == 0) *reinterpret_cast<uint2 *>(rec + (turn < 4 ? q4::kKMeta : q4::kVMeta) + t * 8) = meta;
+        a = na;
+        b = nb;
     }
 }
 
@@ -74,10 +71,13 @@ __global__ void __launch_bounds__(kWarps * 32) k_pool4_pack(const T *__restrict_
     const size_t at = (size_t)u * page_cap + pg;
     const int len = min(max(page_len[at], 0), kPage);
     page_to_record<T>(pool_k + at * kPage * kHeadDim, pool_v + at * kPage * kHeadDim, len, s_rec[warp]);
+    tc::fence_proxy_async();
     __syncwarp();
-    uint4 *dst = reinterpret_cast<uint4 *>(records + at * q4::kRecord);
-    const uint4 *src = reinterpret_cast<const uint4 *>(s_rec[warp]);
-    for (int i = lane; i < kVecs; i += 32) dst[i] = src[i];
+    if (lane == 0) {  // one bulk store a record; the buffer has been read before the CTA ends
+        tc::bulk_store(records + at * q4::kRecord, s_rec[warp], q4::kRecord);
+        tc::bulk_commit();
+        tc::bulk_wait_read_all();
+    }
 }
 
 // Tokens first .. n_indexed - 1 of every unit, one row of 8 lanes each.
@@ -115,15 +115,15 @@ __global__ void __launch_bounds__(kWarps * 32) k_pool4_tokens(
                 b.load(src + (l + 8) * 8);
             }
             uint32_t ca, cb;
-            float2 sm[2];
-            q4::quantise_row<T>(a, b, l, l + 8, ca, cb, sm);
+            uint2 meta;
+            q4::quantise_row<T>(a, b, l, l + 8, pg >= 0, ca, cb, meta);
             if (pg < 0) continue;
             if (which)
                 q4::put_v(rec, slot, l, l + 8, ca, cb);
             else
                 q4::put_k(rec, slot, l, l + 8, ca, cb);
             if (l == 0)
-                *reinterpret_cast<uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + slot * 8) = q4::pack_meta(sm);
+                *reinterpret_cast<uint2 *>(rec + (which ? q4::kVMeta : q4::kKMeta) + slot * 8) = meta;
         }
     }
 }

@@ -301,13 +301,13 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
         ka.set(a);
         kc.set(c);
         uint32_t ca, cb;
-        float2 sm[2];
-        q4::quantise_row<T>(ka, kc, v.wa, v.wb, ca, cb, sm);
+        uint2 meta;
+        q4::quantise_row<T>(ka, kc, v.wa, v.wb, live, ca, cb, meta);
         q4::put_k(rec, t, v.wa, v.wb, ca, cb);
-        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kKMeta + t * 8) = q4::pack_meta(sm);
-        q4::quantise_row<T>(va, vc, l, l + 8, ca, cb, sm);
+        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kKMeta + t * 8) = meta;
+        q4::quantise_row<T>(va, vc, l, l + 8, live, ca, cb, meta);
         q4::put_v(rec, t, l, l + 8, ca, cb);
-        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kVMeta + t * 8) = q4::pack_meta(sm);
+        if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kVMeta + t * 8) = meta;
     }
     __syncwarp();
     unsigned char *out = records + ((size_t)pg * A.hkv + h) * q4::kRecord;

@@ -131,19 +131,25 @@ template <> struct Vec8<float> {
 
 // step and mid of a group from its extremes.  Differences of bf16 values are
 // exact in fp32 (unless their exponents are more than 16 apart, where the
-// rounding is far below a code); those of fp32 values are taken in fp64.
+// rounding is far below a code); those of fp32 values are taken in fp64.  The
+// quotient by 15 is corrected by its remainder, which rounds it correctly
+// (Markstein 1990: a quotient within an ulp and a correctly rounded
+// reciprocal); differences below 1e-30, whose remainder could underflow, are
+// divided.
 template <typename T>
 __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     float step, mid;
     if (sizeof(T) == 2) {
-        step = (hi - lo) / 15.f;
+        const float d = hi - lo, q = d * (1.f / 15.f);
+        step = fmaf(fmaf(-15.f, q, d), 1.f / 15.f, q);
+        if (d < 1e-30f) step = d / 15.f;
         mid = (hi + lo) * 0.5f;
     } else {
         step = (float)(((double)hi - (double)lo) / 15.0);
         mid = (float)(((double)hi + (double)lo) * 0.5);
     }
     if (!(hi - lo < INFINITY)) return make_float2(0.f, __int_as_float(0x7fc00000));
-    return make_float2(bf16_rn(step), bf16_rn(mid));
+    return make_float2(step, mid);
 }
 
 // The word of a vector's 8 codes, rint((x - mid) / step + 7.5) with ties to
@@ -192,56 +198,63 @@ __device__ __forceinline__ uint32_t codes_in(const float (&x)[8], float step, fl
     return w;
 }
 
-// (lo, hi: the group's extremes)
+// Codes of a group whose step is outside [2^-100, ...) (the reciprocal leaves
+// fp32's normal range) or whose extremes lie outside the codes' range by the
+// rounding of step and mid.
 template <typename T>
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], float2 sm, float lo, float hi) {
-    if (!(sm.x > 0.f)) return 0u;
-    float step = sm.x, mid = sm.y;
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
-    // codes outside 0 .. 15 come only from the rounding of step and mid; steps below 2^-100 (their reciprocal leaves
-    // fp32's normal range) go the slow way too, scaled
-    const bool tiny = step < 7.9e-31f;
-    if (!tiny && hi - mid < 8.f * step && mid - lo <= 8.f * step) return codes_in<T, false>(x, step, mid, inv);
-    float y[8];
-    const float up = tiny ? 1.2676506e30f : 1.f;  // 2^100
+__device__ __noinline__ uint32_t codes_slow(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                            float x7, float step, float mid) {
+    if (!(step > 0.f)) return 0u;
+    const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+    const float up = step < 7.9e-31f ? 1.2676506e30f : 1.f;  // 2^100
     step *= up, mid *= up;
+    float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(x[e] * up, mid - 9.f * step), mid + 9.f * step);
     return codes_in<T, true>(y, step, mid, 1.f / step);
 }
 
+// (step, mid) as stored: one word a group.
+__device__ __forceinline__ float2 unpack_meta(uint32_t m) {
+    return make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+}
+
 // Quantises a row held by 8 lanes (vectors wa and wb of lane l): the words of
-// both vectors, and (step, mid) of both groups in every lane.
+// both vectors, and in every lane both groups' (step, mid) as stored.  Lanes 0
+// .. 3 find group 0's step and mid, lanes 4 .. 7 group 1's.  live: false for
+// lanes without a row, whose results mean nothing.
 template <typename T>
-__device__ __forceinline__ void quantise_row(const Vec8<T> &a, const Vec8<T> &b, int wa, int wb, uint32_t &ca,
-                                             uint32_t &cb, float2 (&sm)[2]) {
+__device__ __forceinline__ void quantise_row(const Vec8<T> &a, const Vec8<T> &b, int wa, int wb, bool live,
+                                             uint32_t &ca, uint32_t &cb, uint2 &meta) {
     using V = Vec8<T>;
+    const bool upper = threadIdx.x & 4;
     const typename V::Ends ea = a.ends(), eb = b.ends();
-    float lo[2], hi[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        typename V::Ends e = V::join((wa >> 3) == g ? ea : V::none(), (wb >> 3) == g ? eb : V::none());
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1) e = V::join(e, V::exchange(e, off));
-        lo[g] = V::lo(e), hi[g] = V::hi(e);
-        sm[g] = step_mid<T>(lo[g], hi[g]);
-    }
+    const typename V::Ends e0 = V::join((wa >> 3) == 0 ? ea : V::none(), (wb >> 3) == 0 ? eb : V::none());
+    const typename V::Ends e1 = V::join((wa >> 3) == 1 ? ea : V::none(), (wb >> 3) == 1 ? eb : V::none());
+    typename V::Ends e = V::join(upper ? e1 : e0, V::exchange(upper ? e0 : e1, 4));
+    e = V::join(e, V::exchange(e, 1));
+    e = V::join(e, V::exchange(e, 2));
+    const float lo = V::lo(e), hi = V::hi(e);
+    const float2 exact = step_mid<T>(lo, hi);
+    const __nv_bfloat162 held = __floats2bfloat162_rn(exact.x, exact.y);
+    const uint32_t own = *reinterpret_cast<const uint32_t *>(&held), other = __shfl_xor_sync(0xffffffffu, own, 4);
+    const float2 sm = unpack_meta(own);
+    meta = upper ? make_uint2(other, own) : make_uint2(own, other);
+    const bool plain = (sm.x >= 7.9e-31f) & (hi - sm.y < 8.f * sm.x) & (sm.y - lo <= 8.f * sm.x);
+    const float2 ga = unpack_meta((wa >> 3) ? meta.y : meta.x), gb = unpack_meta((wb >> 3) ? meta.y : meta.x);
     float x[8], y[8];
     a.get(x);
     b.get(y);
-    ca = codes_of<T>(x, (wa >> 3) ? sm[1] : sm[0], (wa >> 3) ? lo[1] : lo[0], (wa >> 3) ? hi[1] : hi[0]);
-    cb = codes_of<T>(y, (wb >> 3) ? sm[1] : sm[0], (wb >> 3) ? lo[1] : lo[0], (wb >> 3) ? hi[1] : hi[0]);
-}
-
-// (step, mid) of a token's two groups as stored.
-__device__ __forceinline__ uint2 pack_meta(const float2 (&sm)[2]) {
-    const __nv_bfloat162 g0 = __floats2bfloat162_rn(sm[0].x, sm[0].y);
-    const __nv_bfloat162 g1 = __floats2bfloat162_rn(sm[1].x, sm[1].y);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&g0), *reinterpret_cast<const uint32_t *>(&g1));
-}
-__device__ __forceinline__ float2 unpack_meta(uint32_t m) {
-    return make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    if (__all_sync(0xffffffffu, plain | !live)) {
+        float ia, ib;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ia) : "f"(ga.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ib) : "f"(gb.x));
+        ca = codes_in<T, false>(x, ga.x, ga.y, ia);
+        cb = codes_in<T, false>(y, gb.x, gb.y, ib);
+    } else {
+        ca = codes_slow<T>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], ga.x, ga.y);
+        cb = codes_slow<T>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], gb.x, gb.y);
+    }
 }
 
 // The values that a vector's codes stand for: mid + step (code - 7.5), one
