@@ -27,34 +27,29 @@ constexpr int kVecs = q4::kRecord / 16;
 template <typename T>
 __device__ __forceinline__ void page_to_record(const T *kp, const T *vp, int len, unsigned char *rec) {
     const int lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
-    q4::Vec8<T> a, b, na, nb;
-    auto load = [&](int turn, q4::Vec8<T> &x, q4::Vec8<T> &y) {
-        const int t = (turn & 3) * 4 + row;
-        const T *src = (turn < 4 ? kp : vp) + t * kHeadDim + l * 8;
-        x.zero();
-        y.zero();
-        if (t < len) {
-            x.load(src);
-            y.load(src + 64);
-        }
+    q4::Vec8<T> a[2], b[2];
+    auto load = [&](int turn, q4::Vec8<T> &x, q4::Vec8<T> &y) {  // (rows behind the last one: the last one)
+        const T *src = (turn < 4 ? kp : vp) + min((turn & 3) * 4 + row, len - 1) * kHeadDim + l * 8;
+        x.load(src);
+        y.load(src + 64);
     };
-    load(0, a, b);
+    load(0, a[0], b[0]);
 #pragma unroll 1
-    for (int turn = 0; turn < 8; ++turn) {
-        if (turn < 7) load(turn + 1, na, nb);
-        const int t = (turn & 3) * 4 + row;
-        const bool live = t < len;
-        uint32_t ca, cb;
-        uint2 meta;
-        q4::quantise_row<T>(a, b, l, l + 8, live, ca, cb, meta);
-        if (!live) ca = cb = 0u;  // pad slots (their step and mid came out zero)
-        if (turn < 4)
-            q4::put_k(rec, t, l, l + 8, ca, cb);
-        else
-            q4::put_v(rec, t, l, l + 8, ca, cb);
-        if (l == 0) *reinterpret_cast<uint2 *>(rec + (turn < 4 ? q4::kKMeta : q4::kVMeta) + t * 8) = meta;
-        a = na;
-        b = nb;
+    for (int pair = 0; pair < 4; ++pair) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int turn = 2 * pair + i, t = (turn & 3) * 4 + row;
+            if (i == 0 || pair < 3) load(turn + 1, a[i ^ 1], b[i ^ 1]);
+            uint32_t ca, cb;
+            uint2 meta;
+            q4::quantise_row<T>(a[i], b[i], l, l + 8, true, ca, cb, meta);
+            if (t >= len) ca = cb = meta.x = meta.y = 0u;  // pad slots
+            if (pair < 2)
+                q4::put_k(rec, t, l, l + 8, ca, cb);
+            else
+                q4::put_v(rec, t, l, l + 8, ca, cb);
+            if (l == 0) *reinterpret_cast<uint2 *>(rec + (pair < 2 ? q4::kKMeta : q4::kVMeta) + t * 8) = meta;
+        }
     }
 }
 
@@ -70,7 +65,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_pool4_pack(const T *__restrict_
     if (pg >= min(n_pages[u], page_cap)) return;
     const size_t at = (size_t)u * page_cap + pg;
     const int len = min(max(page_len[at], 0), kPage);
-    page_to_record<T>(pool_k + at * kPage * kHeadDim, pool_v + at * kPage * kHeadDim, len, s_rec[warp]);
+    if (len > 0)
+        page_to_record<T>(pool_k + at * kPage * kHeadDim, pool_v + at * kPage * kHeadDim, len, s_rec[warp]);
+    else
+        for (int i = lane; i < kVecs; i += 32) reinterpret_cast<uint4 *>(s_rec[warp])[i] = make_uint4(0u, 0u, 0u, 0u);
     tc::fence_proxy_async();
     __syncwarp();
     if (lane == 0) {  // one bulk store a record; the buffer has been read before the CTA ends

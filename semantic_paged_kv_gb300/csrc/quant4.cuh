@@ -160,49 +160,64 @@ __device__ __forceinline__ float2 step_mid(float lo, float hi) {
 // is zero.  The remainder's sign is exact (bf16: as far as x - mid is): k step is (4 bits times 8), and a
 // fused multiply-add rounds a nonzero difference to one of the same sign.  fp32
 // values take mid + k step as an unevaluated sum.
-template <typename T, bool kClamp>
+template <typename T>
 __device__ __forceinline__ uint32_t codes_in(const float (&x)[8], float step, float mid, float inv) {
     constexpr float kBig = 12582912.f;  // 1.5 * 2^23: integers end up in the low bits
-    const pair_t mid2 = pk2(mid, mid), inv2 = pk2(inv, inv), neg2 = pk2(-step, -step);
-    const pair_t big2 = pk2(kBig, kBig);
-    uint32_t w = kClamp ? 0u : 0x88888888u - 0x4B400000u * 0x11111111u;  // + 8, - the bits of kBig, in every nibble
+    uint32_t w = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const pair_t d = sub2(pk2(x[2 * i], x[2 * i + 1]), mid2);
-        const pair_t t = fma2(d, inv2, big2), k = sub2(t, big2);
-        float2 rem;
+    for (int e = 0; e < 8; ++e) {
+        const float d = x[e] - mid, t = fmaf(d, inv, kBig), k = t - kBig;
+        float rem;
         if (sizeof(T) == 2) {
-            rem = upk2(fma2(k, neg2, d));
+            rem = fmaf(-k, step, d);
         } else {
-            const float2 kk = upk2(k);
-            float s, e;
-            two_sum(mid, kk.x * step, s, e);
-            rem.x = (x[2 * i] - s) - e;
-            two_sum(mid, kk.y * step, s, e);
-            rem.y = (x[2 * i + 1] - s) - e;
+            float s, er;
+            two_sum(mid, k * step, s, er);
+            rem = (x[e] - s) - er;
         }
-        const float2 tt = upk2(t);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int b = __float_as_int(h ? tt.y : tt.x), r = __float_as_int(h ? rem.y : rem.x);
-            const bool below = r < (b & 1);  // negative, or zero and k odd
-            const int sh = 4 * (2 * i + h);
-            if (kClamp) {
-                w |= (uint32_t)min(max(b - 0x4B400000 + 8 - (below ? 1 : 0), 0), 15) << sh;
-            } else {
-                w += (uint32_t)b * (1u << sh);
-                if (below) w -= 1u << sh;
-            }
-        }
+        const int b = __float_as_int(t);
+        const bool below = __float_as_int(rem) < (b & 1);  // negative, or zero and k odd
+        w |= (uint32_t)min(max(b - 0x4B400000 + 8 - (below ? 1 : 0), 0), 15) << (4 * e);
     }
     return w;
 }
 
-// Codes of a group whose step is outside [2^-100, ...) (the reciprocal leaves
-// fp32's normal range) or whose extremes lie outside the codes' range by the
-// rounding of step and mid.
+// The same for bf16 values of an ordinary group, in three operations a pair:
+// t = (x - mid) / step + 7.5 rounded to a multiple of 2^-18 (by an addition
+// near 48), then to an integer, ties to even.  A true tie survives the first
+// rounding: the reciprocal's error leaves (x - mid) inv within 2^-20 of the
+// quotient.  Nothing else becomes a tie: with step in [2^s, 2^(s+1)) and mid at
+// least 2^-9 step from every multiple of step (ordinary), x - mid - n step is
+// either 0, or above 2^-10 step (|x| < 2^-10 step), or a multiple of 2^(s-17)
+// (the last bits of x, mid and step), which is 2^-18 step or more.
+__device__ __forceinline__ uint32_t codes_ordinary(const float (&x)[8], float mid, float inv) {
+    constexpr float kBig = 12582912.f - 48.f;  // 1.5 * 2^23 - 48
+    const pair_t mid2 = pk2(mid, mid), inv2 = pk2(inv, inv), snap2 = pk2(55.5f, 55.5f), big2 = pk2(kBig, kBig);
+    uint32_t w = 0u - 0x4B400000u * 0x11111111u;  // the bits of 1.5 * 2^23 in every nibble
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = upk2(add2(fma2(sub2(pk2(x[2 * i], x[2 * i + 1]), mid2), inv2, snap2), big2));
+        w += __float_as_uint(t.x) * (1u << (8 * i));
+        w += __float_as_uint(t.y) * (16u << (8 * i));
+    }
+    return w;
+}
+// Whether codes_ordinary() holds for a group: its codes lie in 0 .. 15 without
+// clamping, step's reciprocal is normal, and mid keeps its distance (above).
+__device__ __forceinline__ bool ordinary(float step, float mid, float lo, float hi) {
+    constexpr float kBig = 12582912.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+    const float n = fmaf(mid, inv, kBig) - kBig, off = fmaf(-n, step, mid);
+    return (step >= 7.9e-31f) & (hi - mid < 8.f * step) & (mid - lo <= 8.f * step) & (fabsf(mid) < 4096.f * step) &
+           (fabsf(off) >= 0.001953125f * step);
+}
+
+// Codes of any group: also steps below 2^-100 (the reciprocal leaves fp32's
+// normal range; both sides scaled) and extremes outside the codes' range by
+// the rounding of step and mid.
 template <typename T>
-__device__ __noinline__ uint32_t codes_slow(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+__device__ __noinline__ uint32_t codes_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
                                             float x7, float step, float mid) {
     if (!(step > 0.f)) return 0u;
     const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
@@ -211,7 +226,7 @@ __device__ __noinline__ uint32_t codes_slow(float x0, float x1, float x2, float 
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(x[e] * up, mid - 9.f * step), mid + 9.f * step);
-    return codes_in<T, true>(y, step, mid, 1.f / step);
+    return codes_in<T>(y, step, mid, 1.f / step);
 }
 
 // (step, mid) as stored: one word a group.
@@ -240,20 +255,19 @@ __device__ __forceinline__ void quantise_row(const Vec8<T> &a, const Vec8<T> &b,
     const uint32_t own = *reinterpret_cast<const uint32_t *>(&held), other = __shfl_xor_sync(0xffffffffu, own, 4);
     const float2 sm = unpack_meta(own);
     meta = upper ? make_uint2(other, own) : make_uint2(own, other);
-    const bool plain = (sm.x >= 7.9e-31f) & (hi - sm.y < 8.f * sm.x) & (sm.y - lo <= 8.f * sm.x);
     const float2 ga = unpack_meta((wa >> 3) ? meta.y : meta.x), gb = unpack_meta((wb >> 3) ? meta.y : meta.x);
     float x[8], y[8];
     a.get(x);
     b.get(y);
-    if (__all_sync(0xffffffffu, plain | !live)) {
+    if (sizeof(T) == 2 && __all_sync(0xffffffffu, ordinary(sm.x, sm.y, lo, hi) | !live)) {
         float ia, ib;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ia) : "f"(ga.x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ib) : "f"(gb.x));
-        ca = codes_in<T, false>(x, ga.x, ga.y, ia);
-        cb = codes_in<T, false>(y, gb.x, gb.y, ib);
+        ca = codes_ordinary(x, ga.y, ia);
+        cb = codes_ordinary(y, gb.y, ib);
     } else {
-        ca = codes_slow<T>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], ga.x, ga.y);
-        cb = codes_slow<T>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], gb.x, gb.y);
+        ca = codes_any<T>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], ga.x, ga.y);
+        cb = codes_any<T>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], gb.x, gb.y);
     }
 }
 
