@@ -22,9 +22,12 @@
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
+#include "tc_common.cuh"
 
 namespace ice {
 namespace {
+
+using q4::pair_t;
 
 constexpr int kThreads = 128;
 constexpr int kGroups = kThreads / 8;  // rows in flight per CTA
@@ -42,13 +45,22 @@ struct RopeArgs {
     int32_t *err;
 };
 
+// The kernels' layouts: bf16 rows rotated as a whole in halves (what the
+// models here do), compiled apart from the rest so that its loops are short.
+constexpr int kHalves = 0, kAny = 1;
+
 // Which vectors of a row a lane holds, and which of them are rotated.
 struct LaneVecs {
     int wa, wb;
     bool ra, rb;
 };
+template <int kLayout>
 __device__ __forceinline__ LaneVecs lane_vecs(const RopeArgs &A, int l) {
     LaneVecs v;
+    if (kLayout == kHalves) {
+        v.wa = l, v.wb = l + 8, v.ra = v.rb = true;
+        return v;
+    }
     const int rd = A.table ? A.rotary : 0;
     if (A.interleaved || rd == 0) {
         v.wa = l, v.wb = l + 8;
@@ -64,16 +76,18 @@ __device__ __forceinline__ LaneVecs lane_vecs(const RopeArgs &A, int l) {
 }
 
 // cos and sin of a lane's 8 pairs.
+template <int kLayout>
 __device__ __forceinline__ void load_angles(const RopeArgs &A, const LaneVecs &v, int pos, float (&c)[8],
                                             float (&s)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
-    const float *row = A.table + (size_t)pos * A.rotary;
+    const bool inter = kLayout == kAny && A.interleaved;
+    const float *row = A.table + (size_t)pos * (kLayout == kHalves ? kHeadDim : A.rotary);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         // pairs 8 wa ..; interleaved: pairs 4 wa .. of vector A, then 4 wb .. of B
-        const bool on = A.interleaved ? (i < 2 ? v.ra : v.rb) : v.ra;
-        const int pair = A.interleaved ? (i < 2 ? 4 * v.wa + 2 * i : 4 * v.wb + 2 * (i - 2)) : 8 * v.wa + 2 * i;
+        const bool on = inter ? (i < 2 ? v.ra : v.rb) : v.ra;
+        const int pair = inter ? (i < 2 ? 4 * v.wa + 2 * i : 4 * v.wb + 2 * (i - 2)) : 8 * v.wa + 2 * i;
         if (on) {
             const float4 f = *reinterpret_cast<const float4 *>(row + 2 * pair);
             c[2 * i] = f.x, s[2 * i] = f.y, c[2 * i + 1] = f.z, s[2 * i + 1] = f.w;
@@ -93,10 +107,18 @@ __device__ __forceinline__ void rotate_pair(float &a, float &b, float c, float s
     }
 }
 
-template <bool kWide>
+template <int kLayout, bool kWide>
 __device__ __forceinline__ void rotate(const RopeArgs &A, const LaneVecs &v, float (&a)[8], float (&b)[8],
                                        const float (&c)[8], const float (&s)[8]) {
-    if (A.interleaved) {
+    if (kLayout == kHalves && !kWide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const pair_t x = pk2(a[2 * i], a[2 * i + 1]), y = pk2(b[2 * i], b[2 * i + 1]);
+            const pair_t co = pk2(c[2 * i], c[2 * i + 1]), si = pk2(s[2 * i], s[2 * i + 1]);
+            const float2 p = upk2(sub2(mul2(x, co), mul2(y, si))), q = upk2(add2(mul2(y, co), mul2(x, si)));
+            a[2 * i] = p.x, a[2 * i + 1] = p.y, b[2 * i] = q.x, b[2 * i + 1] = q.y;
+        }
+    } else if (A.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (v.ra) rotate_pair<kWide>(a[2 * i], a[2 * i + 1], c[i], s[i]);
@@ -112,16 +134,20 @@ __device__ __forceinline__ void rotate(const RopeArgs &A, const LaneVecs &v, flo
 template <typename T>
 __device__ __forceinline__ void norm_row(float (&a)[8], float (&b)[8], const float (&wa)[8], const float (&wb)[8],
                                          float eps, bool on) {
-    float hi = 0.f, lo = 0.f;
+    pair_t hi2 = pk2(0.f, 0.f), lo2 = hi2;  // two sums, of the even and the odd elements
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        const float f = e < 8 ? a[e & 7] : b[e & 7];
-        const float t = __fmul_rn(f, f);
-        float sum, er;
-        two_sum(hi, t, sum, er);
-        hi = sum;
-        lo += sizeof(T) == 2 ? er : er + fmaf(f, f, -t);  // bf16 squares are exact
+    for (int i = 0; i < 8; ++i) {
+        const pair_t f = i < 4 ? pk2(a[2 * (i & 3)], a[2 * (i & 3) + 1]) : pk2(b[2 * (i & 3)], b[2 * (i & 3) + 1]);
+        const pair_t t = mul2(f, f);
+        pair_t er;
+        two_sum2(hi2, t, hi2, er);
+        lo2 = add2(lo2, er);
+        if (sizeof(T) == 4) lo2 = add2(lo2, fma2(f, f, sub2(pk2(0.f, 0.f), t)));  // bf16 squares are exact
     }
+    const float2 hh = upk2(hi2), ll = upk2(lo2);
+    float hi, lo;
+    two_sum(hh.x, hh.y, hi, lo);
+    lo += ll.x + ll.y;
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) {
         const float ohi = __shfl_xor_sync(0xffffffffu, hi, off), olo = __shfl_xor_sync(0xffffffffu, lo, off);
@@ -134,10 +160,12 @@ __device__ __forceinline__ void norm_row(float (&a)[8], float (&b)[8], const flo
     const float total = isfinite(hi) ? hi + lo : hi;
     const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(total, 1.f / kHeadDim), eps));
     if (on) {
+        const pair_t r2 = pk2(r, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            a[e] = __fmul_rn(__fmul_rn(a[e], r), wa[e]);
-            b[e] = __fmul_rn(__fmul_rn(b[e], r), wb[e]);
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = upk2(mul2(mul2(pk2(a[2 * i], a[2 * i + 1]), r2), pk2(wa[2 * i], wa[2 * i + 1])));
+            const float2 y = upk2(mul2(mul2(pk2(b[2 * i], b[2 * i + 1]), r2), pk2(wb[2 * i], wb[2 * i + 1])));
+            a[2 * i] = x.x, a[2 * i + 1] = x.y, b[2 * i] = y.x, b[2 * i + 1] = y.y;
         }
     }
 }
@@ -156,7 +184,7 @@ __device__ __forceinline__ int count_of(const RopeArgs &A, int b) {
 
 // Heads chunk * kHeads .. of token (b, i): q, then k, then v.  Every lane of
 // the warp calls it (the norm shuffles); `live` lanes have a token.
-template <typename T>
+template <typename T, int kLayout, bool kNorm>
 __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int chunk, bool live) {
     const int l = threadIdx.x & 7;
     const int kind = chunk < A.nq ? 0 : (chunk < A.nq + A.nk ? 1 : 2);
@@ -165,7 +193,7 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
     const ice_rows &in = kind == 0 ? A.q : (kind == 1 ? A.k : A.v);
     const ice_rows &out = kind == 0 ? A.qo : (kind == 1 ? A.ko : A.vo);
     live = live && i < count_of(A, b);
-    const LaneVecs v = lane_vecs(A, l);
+    const LaneVecs v = lane_vecs<kLayout>(A, l);
     const T *src = static_cast<const T *>(in.data) + (long long)b * in.batch + (long long)i * in.token;
     T *dst = static_cast<T *>(out.data) + (long long)b * out.batch + (long long)i * out.token;
     q4::Vec8<T> ra[kHeads], rb[kHeads];
@@ -183,11 +211,11 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
         set_err(A.err, ICE_ERR_CAPACITY);
         live = false;
     }
-    const bool turn = live && kind != 2 && A.table;
+    const bool turn = live && kind != 2 && (kLayout == kHalves || A.table);
     float co[8], si[8];
-    if (turn) load_angles(A, v, pos, co, si);
+    if (turn) load_angles<kLayout>(A, v, pos, co, si);
     const T *w = static_cast<const T *>(kind == 0 ? A.wq : A.wk);
-    const bool norm = kind != 2 && w;
+    const bool norm = kNorm && kind != 2 && w;
     float wa[8] = {}, wb[8] = {};
     if (norm) {
         load8<T>(w + v.wa * 8, wa);
@@ -198,8 +226,8 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
         float a[8], c[8];
         ra[j].get(a);
         rb[j].get(c);
-        if (A.wq || A.wk) norm_row<T>(a, c, wa, wb, A.eps, norm);
-        if (turn) rotate<false>(A, v, a, c, co, si);
+        if (kNorm) norm_row<T>(a, c, wa, wb, A.eps, norm);
+        if (turn) rotate<kLayout, false>(A, v, a, c, co, si);
         if (live && h0 + j < heads) {
             store8<T>(dst + (h0 + j) * out.head + v.wa * 8, a);
             store8<T>(dst + (h0 + j) * out.head + v.wb * 8, c);
@@ -207,7 +235,7 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
     }
 }
 
-template <typename T>
+template <typename T, int kLayout, bool kNorm>
 __global__ void __launch_bounds__(kThreads) k_qkv_rope(const __grid_constant__ RopeArgs A, long long n_items,
                                                        int n_chunks) {
     dep_wait();
@@ -215,10 +243,10 @@ __global__ void __launch_bounds__(kThreads) k_qkv_rope(const __grid_constant__ R
     const bool live = item < n_items;
     const long long at = live ? item : 0;
     const long long tok = at / n_chunks;
-    dense_chunk<T>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % n_chunks), live);
+    dense_chunk<T, kLayout, kNorm>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % n_chunks), live);
 }
 
-template <typename T>
+template <typename T, int kLayout, bool kNorm>
 __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constant__ RopeArgs A, long long q_items,
                                                             int q_blocks, long long n_items, int blocks,
                                                             unsigned char *__restrict__ records,
@@ -231,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
         const bool live = item < q_items;
         const long long at = live ? item : 0;
         const long long tok = at / A.nq;
-        dense_chunk<T>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % A.nq), live);
+        dense_chunk<T, kLayout, kNorm>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % A.nq), live);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
@@ -253,67 +281,76 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
         return;
     }
     unsigned char *rec = s_rec[warp];
-    const LaneVecs v = lane_vecs(A, l);
+    const LaneVecs v = lane_vecs<kLayout>(A, l);
     const T *w = static_cast<const T *>(A.wk);
     float wa[8] = {}, wb[8] = {};
-    if (w) {
+    if (kNorm && w) {
         load8<T>(w + v.wa * 8, wa);
         load8<T>(w + v.wb * 8, wb);
     }
     unsigned done = 0;  // tokens of the block that are written
-#pragma unroll
-    for (int it = 0; it < kPage / 4; ++it) {
+    const T *kb = static_cast<const T *>(A.k.data) + b * A.k.batch + h * A.k.head;
+    const T *vb = static_cast<const T *>(A.v.data) + b * A.v.batch + h * A.v.head;
+    struct Rows {
+        q4::Vec8<T> ka, kb, va, vb;
+    };
+    auto load = [&](int it, Rows &x) {  // (lanes without a new token: the nearest one's rows)
+        const long long t = t0 + it * 4 + row;
+        const long long i = (t < ta ? ta : (t < tb ? t : tb - 1)) - s0;
+        const T *ks = kb + i * A.k.token, *vs = vb + i * A.v.token;
+        x.ka.load(ks + v.wa * 8);
+        x.kb.load(ks + v.wb * 8);
+        x.va.load(vs + l * 8);
+        x.vb.load(vs + (l + 8) * 8);
+    };
+    // four rows a turn, the next turn's in flight; rolled, to stay in the instruction cache
+    const int last = (int)(tb - 1 - t0) >> 2;
+    Rows cur, next;
+    load((int)(ta - t0) >> 2, cur);
+#pragma unroll 1
+    for (int it = (int)(ta - t0) >> 2; it <= last; ++it) {
         const int t = it * 4 + row;
         bool live = t0 + t >= ta && t0 + t < tb;
-        const int i = live ? (int)(t0 + t - s0) : 0;
-        int pos = 0;
-        if (live) {
-            pos = position_of(A, b, i);
-            if (pos < 0) {
-                set_err(A.err, ICE_ERR_CAPACITY);
-                live = false;
-            }
+        const int pos = live ? position_of(A, b, (int)(t0 + t - s0)) : 0;
+        if (it < last) load(it + 1, next);
+        if (pos < 0) {
+            set_err(A.err, ICE_ERR_CAPACITY);
+            live = false;
         }
-        const unsigned rows = __ballot_sync(0xffffffffu, live);
-        if (!rows) continue;
+        const unsigned rows = __ballot_sync(0xffffffffu, live && l == 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (rows >> (8 * r) & 1u) done |= 1u << (it * 4 + r);
-        float a[8] = {}, c[8] = {};
-        q4::Vec8<T> va, vc;
-        va.zero();
-        vc.zero();
-        if (live) {
-            const T *ks = static_cast<const T *>(A.k.data) + b * A.k.batch + i * A.k.token + h * A.k.head;
-            const T *vs = static_cast<const T *>(A.v.data) + b * A.v.batch + i * A.v.token + h * A.v.head;
-            load8<T>(ks + v.wa * 8, a);
-            load8<T>(ks + v.wb * 8, c);
-            va.load(vs + l * 8);
-            vc.load(vs + (l + 8) * 8);
-        }
-        if (w) norm_row<T>(a, c, wa, wb, A.eps, true);
-        if (live && A.table) {
+        for (int r = 0; r < 4; ++r) done |= (rows >> (8 * r) & 1u) << (it * 4 + r);
+        float a[8], c[8];
+        cur.ka.get(a);
+        cur.kb.get(c);
+        if (kNorm && w) norm_row<T>(a, c, wa, wb, A.eps, true);
+        if (kLayout == kHalves || A.table) {
             float co[8], si[8];
-            load_angles(A, v, pos, co, si);
-            rotate<sizeof(T) == 4>(A, v, a, c, co, si);
+            load_angles<kLayout>(A, v, max(pos, 0), co, si);
+            rotate<kLayout, sizeof(T) == 4>(A, v, a, c, co, si);
         }
-        q4::Vec8<T> ka, kc;  // rounded to the storage type
-        ka.set(a);
-        kc.set(c);
+        cur.ka.set(a);  // rounded to the storage type
+        cur.kb.set(c);
         uint32_t ca, cb;
         uint2 meta;
-        q4::quantise_row<T>(ka, kc, v.wa, v.wb, live, ca, cb, meta);
+        q4::quantise_row<T>(cur.ka, cur.kb, v.wa, v.wb, live, ca, cb, meta);
         q4::put_k(rec, t, v.wa, v.wb, ca, cb);
         if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kKMeta + t * 8) = meta;
-        q4::quantise_row<T>(va, vc, l, l + 8, live, ca, cb, meta);
+        q4::quantise_row<T>(cur.va, cur.vb, l, l + 8, live, ca, cb, meta);
         q4::put_v(rec, t, l, l + 8, ca, cb);
         if (l == 0) *reinterpret_cast<uint2 *>(rec + q4::kVMeta + t * 8) = meta;
+        cur = next;
     }
     __syncwarp();
     unsigned char *out = records + ((size_t)pg * A.hkv + h) * q4::kRecord;
     if (done == 0xFFFFu) {
-        for (int i = lane; i < q4::kRecord / 16; i += 32)
-            reinterpret_cast<uint4 *>(out)[i] = reinterpret_cast<const uint4 *>(rec)[i];
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {  // one bulk store; the buffer has been read before the CTA ends
+            tc::bulk_store(out, rec, q4::kRecord);
+            tc::bulk_commit();
+            tc::bulk_wait_read_all();
+        }
         return;
     }
     // only the new tokens: K rows of four 16-byte vectors, the (step, mid) pairs, V in 2-byte pieces
@@ -367,6 +404,14 @@ RopeArgs rope_args(const ice_params &p, int n_new, const ice_rows *q, const ice_
     return A;
 }
 
+// The instantiation for a call: bf16 in halves without or with norms, bf16 with
+// any other rotation, fp32.
+template <typename K> K pick(const ice_params &p, const RopeArgs &A, K halves, K halves_norm, K any, K fp32) {
+    if (p.dtype != ICE_BF16) return fp32;
+    if (!A.table || A.interleaved || A.rotary != kHeadDim) return any;
+    return A.wq || A.wk ? halves_norm : halves;
+}
+
 }  // namespace
 
 cudaError_t launch_rope_table(const double *inv_freq, int rotary_dim, int n_positions, float *table, cudaStream_t s) {
@@ -388,9 +433,9 @@ cudaError_t launch_qkv_rope(const ice_params &p, int n_new, const ice_rows *q, c
     if (!n_chunks) return cudaSuccess;
     const long long items = (long long)p.batch * n_new * n_chunks;
     const dim3 grid((unsigned)ceil_div(items, kGroups));
-    if (p.dtype == ICE_BF16)
-        return launch_dependent(k_qkv_rope<__nv_bfloat16>, grid, dim3(kThreads), 0, s, A, items, n_chunks);
-    return launch_dependent(k_qkv_rope<float>, grid, dim3(kThreads), 0, s, A, items, n_chunks);
+    auto kern = pick(p, A, k_qkv_rope<__nv_bfloat16, kHalves, false>, k_qkv_rope<__nv_bfloat16, kHalves, true>,
+                     k_qkv_rope<__nv_bfloat16, kAny, true>, k_qkv_rope<float, kAny, true>);
+    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, items, n_chunks);
 }
 
 cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k,
@@ -405,11 +450,10 @@ cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows 
     const long long items = (long long)p.batch * blocks * p.n_kv_heads;
     const dim3 grid((unsigned)(q_blocks + ceil_div(items, kThreads / 32)));
     unsigned char *r = static_cast<unsigned char *>(cache.records);
-    if (p.dtype == ICE_BF16)
-        return launch_dependent(k_cache4_append<__nv_bfloat16>, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items,
-                                blocks, r, cache.table, cache.n_pages, cache.max_pages);
-    return launch_dependent(k_cache4_append<float>, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items, blocks, r,
-                            cache.table, cache.n_pages, cache.max_pages);
+    auto kern = pick(p, A, k_cache4_append<__nv_bfloat16, kHalves, false>, k_cache4_append<__nv_bfloat16, kHalves, true>,
+                     k_cache4_append<__nv_bfloat16, kAny, true>, k_cache4_append<float, kAny, true>);
+    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items, blocks, r, cache.table,
+                            cache.n_pages, cache.max_pages);
 }
 
 }  // namespace ice
