@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(kWarps * 32) k_cache4_read(const unsigned char
                                                              const int32_t *__restrict__ start,
                                                              const int32_t *__restrict__ counts, ice_rows k_out,
                                                              ice_rows v_out, int32_t *__restrict__ err,
-                                                             long long n_items) {
+                                                             unsigned n_items) {
     __shared__ __align__(16) unsigned char s_rec[kWarps][q4::kRecord];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
-    const long long item = (long long)blockIdx.x * kWarps + warp;
+    const unsigned item = blockIdx.x * kWarps + warp;
     dep_wait();
     if (item >= n_items) return;
     const int h = (int)(item % n_kv_heads);
@@ -239,7 +239,7 @@ template <typename T>
 cudaError_t read_t(const ice_params &p, int n_new, const ice_cache4 &c, const int32_t *start, const int32_t *counts,
                    const ice_rows &k_out, const ice_rows &v_out, int32_t *err, cudaStream_t s) {
     const int blocks = cache4_blocks(n_new);
-    const long long items = (long long)p.batch * blocks * p.n_kv_heads;
+    const unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
     return launch_dependent(k_cache4_read<T>, dim3((unsigned)ceil_div(items, kWarps)), dim3(kWarps * 32), 0, s,
                             static_cast<const unsigned char *>(c.records), c.table, c.n_pages, c.max_pages,
                             p.n_kv_heads, blocks, n_new, start, counts, k_out, v_out, err, items);

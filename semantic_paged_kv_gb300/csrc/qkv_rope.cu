@@ -35,7 +35,6 @@ constexpr int kHeads = 4;              // heads per lane group
 
 struct RopeArgs {
     ice_rows q, k, v, qo, ko, vo;
-    int nq, nk;  // chunks of kHeads heads of q and of k (v's come after them)
     int hq, hkv, n_new;
     const int32_t *positions, *start, *counts;
     const float *table;
@@ -131,42 +130,55 @@ __device__ __forceinline__ void rotate(const RopeArgs &A, const LaneVecs &v, flo
 }
 
 // x <- (x r) w over the 8 lanes of a row (every lane of the warp calls it).
-template <typename T>
+// Keys take the error-free sum (their 4-bit codes may hang on its last bit),
+// queries a plain fp32 sum.
+template <typename T, bool kExact>
 __device__ __forceinline__ void norm_row(float (&a)[8], float (&b)[8], const float (&wa)[8], const float (&wb)[8],
-                                         float eps, bool on) {
-    pair_t hi2 = pk2(0.f, 0.f), lo2 = hi2;  // two sums, of the even and the odd elements
+                                         float eps) {
+    pair_t sum2 = pk2(0.f, 0.f), lo2 = sum2;  // two sums, of the even and the odd elements
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const pair_t f = i < 4 ? pk2(a[2 * (i & 3)], a[2 * (i & 3) + 1]) : pk2(b[2 * (i & 3)], b[2 * (i & 3) + 1]);
-        const pair_t t = mul2(f, f);
-        pair_t er;
-        two_sum2(hi2, t, hi2, er);
-        lo2 = add2(lo2, er);
-        if (sizeof(T) == 4) lo2 = add2(lo2, fma2(f, f, sub2(pk2(0.f, 0.f), t)));  // bf16 squares are exact
+        if (kExact) {
+            const pair_t t = mul2(f, f);
+            pair_t er;
+            two_sum2(sum2, t, sum2, er);
+            lo2 = add2(lo2, er);
+            if (sizeof(T) == 4) lo2 = add2(lo2, fma2(f, f, sub2(pk2(0.f, 0.f), t)));  // bf16 squares are exact
+        } else {
+            sum2 = fma2(f, f, sum2);
+        }
     }
-    const float2 hh = upk2(hi2), ll = upk2(lo2);
-    float hi, lo;
-    two_sum(hh.x, hh.y, hi, lo);
-    lo += ll.x + ll.y;
+    const float2 hh = upk2(sum2), ll = upk2(lo2);
+    float sum, lo = 0.f;
+    if (kExact) {
+        two_sum(hh.x, hh.y, sum, lo);
+        lo += ll.x + ll.y;
+    } else {
+        sum = hh.x + hh.y;
+    }
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) {
-        const float ohi = __shfl_xor_sync(0xffffffffu, hi, off), olo = __shfl_xor_sync(0xffffffffu, lo, off);
-        float sum, er;
-        two_sum(hi, ohi, sum, er);
-        hi = sum;
-        lo += olo + er;
+        const float other = __shfl_xor_sync(0xffffffffu, sum, off);
+        if (kExact) {
+            const float olo = __shfl_xor_sync(0xffffffffu, lo, off);
+            float t, er;
+            two_sum(sum, other, t, er);
+            sum = t;
+            lo += olo + er;
+        } else {
+            sum += other;
+        }
     }
     // an overflowed sum is infinite (its error terms are not numbers): r = 0, as in plain fp32
-    const float total = isfinite(hi) ? hi + lo : hi;
-    const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(total, 1.f / kHeadDim), eps));
-    if (on) {
-        const pair_t r2 = pk2(r, r);
+    if (kExact && isfinite(sum)) sum += lo;
+    const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.f / kHeadDim), eps));
+    const pair_t r2 = pk2(r, r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = upk2(mul2(mul2(pk2(a[2 * i], a[2 * i + 1]), r2), pk2(wa[2 * i], wa[2 * i + 1])));
-            const float2 y = upk2(mul2(mul2(pk2(b[2 * i], b[2 * i + 1]), r2), pk2(wb[2 * i], wb[2 * i + 1])));
-            a[2 * i] = x.x, a[2 * i + 1] = x.y, b[2 * i] = y.x, b[2 * i + 1] = y.y;
-        }
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = upk2(mul2(mul2(pk2(a[2 * i], a[2 * i + 1]), r2), pk2(wa[2 * i], wa[2 * i + 1])));
+        const float2 y = upk2(mul2(mul2(pk2(b[2 * i], b[2 * i + 1]), r2), pk2(wb[2 * i], wb[2 * i + 1])));
+        a[2 * i] = x.x, a[2 * i + 1] = x.y, b[2 * i] = y.x, b[2 * i + 1] = y.y;
     }
 }
 
@@ -182,16 +194,21 @@ __device__ __forceinline__ int count_of(const RopeArgs &A, int b) {
     return A.counts ? min(max(A.counts[b], 0), A.n_new) : A.n_new;
 }
 
-// Heads chunk * kHeads .. of token (b, i): q, then k, then v.  Every lane of
-// the warp calls it (the norm shuffles); `live` lanes have a token.
-template <typename T, int kLayout, bool kNorm>
-__device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int chunk, bool live) {
+// What a CTA's rows are.
+constexpr int kQ = 0, kK = 1, kV = 2;
+
+// Item `item` of `items`: kHeads heads of one token of q, k or v.
+template <typename T, int kLayout, bool kNorm, int kKind>
+__device__ __forceinline__ void dense_chunk(const RopeArgs &A, unsigned item, unsigned items) {
     const int l = threadIdx.x & 7;
-    const int kind = chunk < A.nq ? 0 : (chunk < A.nq + A.nk ? 1 : 2);
-    const int h0 = (kind == 0 ? chunk : (kind == 1 ? chunk - A.nq : chunk - A.nq - A.nk)) * kHeads;
-    const int heads = kind == 0 ? A.hq : A.hkv;
-    const ice_rows &in = kind == 0 ? A.q : (kind == 1 ? A.k : A.v);
-    const ice_rows &out = kind == 0 ? A.qo : (kind == 1 ? A.ko : A.vo);
+    const ice_rows &in = kKind == kQ ? A.q : (kKind == kK ? A.k : A.v);
+    const ice_rows &out = kKind == kQ ? A.qo : (kKind == kK ? A.ko : A.vo);
+    const int heads = kKind == kQ ? A.hq : A.hkv;
+    const unsigned chunks = (heads + kHeads - 1) / kHeads;
+    bool live = item < items;  // (every lane stays: the norm shuffles)
+    if (!live) item = 0;
+    const unsigned tok = item / chunks;
+    const int b = tok / A.n_new, i = tok % A.n_new, h0 = (int)(item % chunks) * kHeads;
     live = live && i < count_of(A, b);
     const LaneVecs v = lane_vecs<kLayout>(A, l);
     const T *src = static_cast<const T *>(in.data) + (long long)b * in.batch + (long long)i * in.token;
@@ -211,11 +228,11 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
         set_err(A.err, ICE_ERR_CAPACITY);
         live = false;
     }
-    const bool turn = live && kind != 2 && (kLayout == kHalves || A.table);
+    const bool turn = live && kKind != kV && (kLayout == kHalves || A.table);
     float co[8], si[8];
     if (turn) load_angles<kLayout>(A, v, pos, co, si);
-    const T *w = static_cast<const T *>(kind == 0 ? A.wq : A.wk);
-    const bool norm = kNorm && kind != 2 && w;
+    const T *w = static_cast<const T *>(kKind == kQ ? A.wq : A.wk);
+    const bool norm = kNorm && kKind != kV && w;
     float wa[8] = {}, wb[8] = {};
     if (norm) {
         load8<T>(w + v.wa * 8, wa);
@@ -226,7 +243,7 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
         float a[8], c[8];
         ra[j].get(a);
         rb[j].get(c);
-        if (kNorm) norm_row<T>(a, c, wa, wb, A.eps, norm);
+        if (norm) norm_row<T, kKind == kK>(a, c, wa, wb, A.eps);
         if (turn) rotate<kLayout, false>(A, v, a, c, co, si);
         if (live && h0 + j < heads) {
             store8<T>(dst + (h0 + j) * out.head + v.wa * 8, a);
@@ -235,35 +252,33 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, int b, int i, int
     }
 }
 
+// CTAs [0, q_blocks) take the queries, the next k_blocks the keys, the rest the values.
 template <typename T, int kLayout, bool kNorm>
-__global__ void __launch_bounds__(kThreads) k_qkv_rope(const __grid_constant__ RopeArgs A, long long n_items,
-                                                       int n_chunks) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : (kNorm ? 5 : 6)) k_qkv_rope(
+    const __grid_constant__ RopeArgs A, unsigned q_items, unsigned kv_items, int q_blocks, int k_blocks) {
     dep_wait();
-    const long long item = (long long)blockIdx.x * kGroups + threadIdx.x / 8;
-    const bool live = item < n_items;
-    const long long at = live ? item : 0;
-    const long long tok = at / n_chunks;
-    dense_chunk<T, kLayout, kNorm>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % n_chunks), live);
+    const int block = blockIdx.x;
+    const unsigned group = threadIdx.x / 8;
+    if (block < q_blocks)
+        dense_chunk<T, kLayout, kNorm, kQ>(A, block * kGroups + group, q_items);
+    else if (block < q_blocks + k_blocks)
+        dense_chunk<T, kLayout, kNorm, kK>(A, (block - q_blocks) * kGroups + group, kv_items);
+    else
+        dense_chunk<T, kLayout, kNorm, kV>(A, (block - q_blocks - k_blocks) * kGroups + group, kv_items);
 }
 
 template <typename T, int kLayout, bool kNorm>
-__global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constant__ RopeArgs A, long long q_items,
-                                                            int q_blocks, long long n_items, int blocks,
-                                                            unsigned char *__restrict__ records,
-                                                            const int32_t *__restrict__ table, int n_pages,
-                                                            int max_pages) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : (kNorm ? 5 : 6)) k_cache4_append(
+    const __grid_constant__ RopeArgs A, unsigned q_items, int q_blocks, unsigned n_items, int blocks,
+    unsigned char *__restrict__ records, const int32_t *__restrict__ table, int n_pages, int max_pages) {
     __shared__ __align__(16) unsigned char s_rec[kThreads / 32][q4::kRecord];
     dep_wait();
     if ((int)blockIdx.x < q_blocks) {  // the queries
-        const long long item = (long long)blockIdx.x * kGroups + threadIdx.x / 8;
-        const bool live = item < q_items;
-        const long long at = live ? item : 0;
-        const long long tok = at / A.nq;
-        dense_chunk<T, kLayout, kNorm>(A, (int)(tok / A.n_new), (int)(tok % A.n_new), (int)(at % A.nq), live);
+        dense_chunk<T, kLayout, kNorm, kQ>(A, blockIdx.x * kGroups + threadIdx.x / 8, q_items);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
-    const long long item = (long long)(blockIdx.x - q_blocks) * (kThreads / 32) + warp;
+    const unsigned item = (blockIdx.x - q_blocks) * (kThreads / 32) + warp;
     if (item >= n_items) return;
     const int h = (int)(item % A.hkv);
     const int x = (int)(item / A.hkv % blocks);
@@ -323,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) k_cache4_append(const __grid_constan
         float a[8], c[8];
         cur.ka.get(a);
         cur.kb.get(c);
-        if (kNorm && w) norm_row<T>(a, c, wa, wb, A.eps, true);
+        if (kNorm && w) norm_row<T, true>(a, c, wa, wb, A.eps);
         if (kLayout == kHalves || A.table) {
             float co[8], si[8];
             load_angles<kLayout>(A, v, max(pos, 0), co, si);
@@ -426,16 +441,15 @@ cudaError_t launch_qkv_rope(const ice_params &p, int n_new, const ice_rows *q, c
                             const ice_rope *rope, const ice_rows *q_out, const ice_rows *k_out, const ice_rows *v_out,
                             int32_t *err, cudaStream_t s) {
     RopeArgs A = rope_args(p, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out, err);
-    const int per = ceil_div(p.n_kv_heads, kHeads);
-    A.nq = q ? ceil_div(p.n_q_heads, kHeads) : 0;
-    A.nk = k ? per : 0;
-    const int n_chunks = A.nq + A.nk + (v ? per : 0);
-    if (!n_chunks) return cudaSuccess;
-    const long long items = (long long)p.batch * n_new * n_chunks;
-    const dim3 grid((unsigned)ceil_div(items, kGroups));
+    const long long toks = (long long)p.batch * n_new;
+    const unsigned q_items = (unsigned)(q ? toks * ceil_div(p.n_q_heads, kHeads) : 0);
+    const unsigned kv_items = (unsigned)(toks * ceil_div(p.n_kv_heads, kHeads));
+    const int q_blocks = ceil_div(q_items, kGroups), k_blocks = k ? ceil_div(kv_items, kGroups) : 0;
+    const dim3 grid(q_blocks + k_blocks + (v ? ceil_div(kv_items, kGroups) : 0));
+    if (grid.x == 0) return cudaSuccess;
     auto kern = pick(p, A, k_qkv_rope<__nv_bfloat16, kHalves, false>, k_qkv_rope<__nv_bfloat16, kHalves, true>,
                      k_qkv_rope<__nv_bfloat16, kAny, true>, k_qkv_rope<float, kAny, true>);
-    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, items, n_chunks);
+    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, q_items, kv_items, q_blocks, k_blocks);
 }
 
 cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows *q, const ice_rows *k,
@@ -443,11 +457,10 @@ cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows 
                                  const int32_t *counts, const ice_rope *rope, const ice_rows *q_out,
                                  const ice_cache4 &cache, int32_t *err, cudaStream_t s) {
     RopeArgs A = rope_args(p, n_new, q, k, v, positions, start, counts, rope, q_out, nullptr, nullptr, err);
-    A.nq = q ? ceil_div(p.n_q_heads, kHeads) : 0;
-    const long long q_items = (long long)p.batch * n_new * A.nq;
+    const unsigned q_items = (unsigned)(q ? (long long)p.batch * n_new * ceil_div(p.n_q_heads, kHeads) : 0);
     const int q_blocks = ceil_div(q_items, kGroups);
     const int blocks = cache4_blocks(n_new);
-    const long long items = (long long)p.batch * blocks * p.n_kv_heads;
+    const unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
     const dim3 grid((unsigned)(q_blocks + ceil_div(items, kThreads / 32)));
     unsigned char *r = static_cast<unsigned char *>(cache.records);
     auto kern = pick(p, A, k_cache4_append<__nv_bfloat16, kHalves, false>, k_cache4_append<__nv_bfloat16, kHalves, true>,
