@@ -34,7 +34,10 @@
 //   O^T += V^T (step P)^T: V codes as operands the same way (the record pairs
 //     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
 //     by a power of two that follows the largest step; the 8 x 8 transposes of
-//     P by movmatrix.  sum (mid - 7.5 step) P joins at the end of the unit.
+//     P by movmatrix.  The codes go in as 2 c - 15 (a mean over many
+//     values cancels down to the noise of its sums; sum mid P joins at the end
+//     of the unit), and every 16 pages the sums leave the tensor core's
+//     accumulators, which truncate, for fp32 sums in shared memory.
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -131,10 +134,29 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// a > l or b > l or c > m or d > m.
+__device__ __forceinline__ bool exceeds(float a, float b, float c, float d, float l, float m) {
+    int r;
+    asm("{\n\t.reg .pred p;\n\t"
+        "setp.gt.f32 p, %1, %5;\n\t"
+        "setp.gt.or.f32 p, %2, %5, p;\n\t"
+        "setp.gt.or.f32 p, %3, %6, p;\n\t"
+        "setp.gt.or.f32 p, %4, %6, p;\n\t"
+        "selp.s32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d), "f"(l), "f"(m));
+    return r != 0;
+}
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// (code - 7.5) 2^-10 of two codes at bit 0 (c 2^-24 as fp16) or bit 4 (c 2^-20) of the halves: exact.
+__device__ __forceinline__ uint32_t centred(uint32_t x, bool high) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(high ? 0x64006400u : 0x74007400u), "r"(0x9F809F80u));
+    return d;
 }
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 // 2^e as a float, -126 <= e <= 127.
@@ -145,6 +167,7 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_u
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+constexpr int kFlush = 16;  // pages after which a warp's sums leave the tensor core's accumulators
 
 using q4::pair_t;
 
@@ -157,7 +180,7 @@ template <int HN> struct State {
     pair_t minus_m[HN];          // minus the running maximum (in powers of two), heads 2 c and 2 c + 1
     float limit[HN][2];          // score (before Queries::factor) above which the maximum moves
     pair_t l[HN];                // sum of P over this lane's tokens
-    pair_t off[HN][2];           // sum of P (mid - 7.5 step), groups 0 and 1, this lane's tokens
+    pair_t off[HN][2];           // sum of P mid, groups 0 and 1, this lane's tokens
     pair_t vscale;               // of each group: power of two on step P
     float vlimit[2];             // and the step that it holds up to
     __device__ __forceinline__ void init() {
@@ -294,11 +317,10 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     const float2 v00 = q4::unpack_meta(n0.x), v01 = q4::unpack_meta(n0.y);  // (step, mid): token r, groups 0, 1
     const float2 v10 = q4::unpack_meta(n1.x), v11 = q4::unpack_meta(n1.y);  // token r + 8
     // ---- the running maxima and the scale of step P, only when one has to move
-    bool move = (v00.x > st.vlimit[0]) | (v10.x > st.vlimit[0]) | (v01.x > st.vlimit[1]) | (v11.x > st.vlimit[1]);
+    bool move = exceeds(v00.x, v10.x, v01.x, v11.x, st.vlimit[0], st.vlimit[1]);
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) move |= (s[hn][e] > st.limit[hn][e]) | (s[hn][2 + e] > st.limit[hn][e]);
+        move |= exceeds(s[hn][0], s[hn][2], s[hn][1], s[hn][3], st.limit[hn][0], st.limit[hn][1]);
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
@@ -348,8 +370,7 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     // ---- P, and step P of both groups in hi + lo parts, transposed to B fragments
     uint32_t bh[HN][2][2], bl[HN][2][2];  // [group][token half]
     const pair_t f[2] = {mul2(pk2(v00.x, v01.x), st.vscale), mul2(pk2(v10.x, v11.x), st.vscale)};
-    const pair_t b[2] = {fma2(pk2(-7.5f, -7.5f), pk2(v00.x, v01.x), pk2(v00.y, v01.y)),
-                         fma2(pk2(-7.5f, -7.5f), pk2(v10.x, v11.x), pk2(v10.y, v11.y))};
+    const pair_t b[2] = {pk2(v00.y, v01.y), pk2(v10.y, v11.y)};
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
@@ -382,7 +403,8 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t y0 = w0[j] >> (8 * k), y1 = w1[j] >> (8 * k);
-                const uint32_t a[4] = {y0 & kLow, y0 & kHigh, y1 & kLow, y1 & kHigh};
+                const uint32_t a[4] = {centred(y0 & kLow, false), centred(y0 & kHigh, true),
+                                       centred(y1 & kLow, false), centred(y1 & kHigh, true)};
 #pragma unroll
                 for (int hn = 0; hn < HN; ++hn) {
                     float(&o)[4] = st.o[hn][2 * j + k];
@@ -553,16 +575,19 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     };
     const uint32_t ring = su32(S.ring[warp][0]), full = su32(&S.full[warp][0]);
     const bool copies = lane == 0 && !A.fault_skip;  // fault injection: the waits for pages give up
-    auto issue = [&](int n) {                        // the copy of place n, if it is a page
+    // The copy of place n; a place without a page completes its slot's phase as well, so that phases follow n.
+    auto issue = [&](int n) {
         const unsigned long long e = pages[n & (2 * kBatch - 1)];
         const uint32_t slot = n & (kSlots - 1);
         asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 once;\n\t"
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 once;\n\t.reg .b32 bytes;\n\t"
             "setp.ne.b32 p, %0, 0;\n\t"
+            "setp.ne.and.b64 q, %4, 0, p;\n\t"
+            "selp.b32 bytes, %2, 0, q;\n\t"
             "createpolicy.fractional.L2::evict_first.b64 once, 1.0;\n\t"
-            "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], %2;\n\t"
-            "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%3], [%4], %2, [%1], "
-            "once;\n\t}" ::"r"((int)(copies && e != 0)),
+            "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], bytes;\n\t"
+            "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%3], [%4], %2, [%1], "
+            "once;\n\t}" ::"r"((int)copies),
             "r"(full + slot * 8), "r"((uint32_t)q4::kRecord), "r"(ring + slot * q4::kRecord),
             "l"(e & ((1ull << kLenShift) - 1))
             : "memory");
@@ -575,7 +600,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     Queries<NQ, HN> q;
     bool dead = false;  // a wait gave up, for place `stopped`
     int stopped = 0;
-    uint32_t phase = 0;  // of the warp's slots
     for (;;) {
         // the next unit with pages in the run
         while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end());
@@ -588,67 +612,86 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
         const bool any = n < n_end;
         if (any) load_queries<T, NQ, HN>(static_cast<const T *>(A.Q) + row0 * kHeadDim, g, A.scale, q);
-        if (any && !dead) {
+        bool flushed = false;
+        if (any && !dead)
             for (; issued < n + kSlots - 1; ++issued) {  // (after places without a page)
                 if (issued >= looked) look_further();
                 issue(issued);
             }
-            while (n < n_end) {
+        while (n < n_end && !dead) {
+            const int until = min(n_end, n + kFlush);
+            while (n < until) {
                 while (looked - n <= kBatch / 2) look_further();
-                const int stop = min(n_end, looked - (kSlots - 1));
+                const int stop = min(until, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
-                    const uint32_t slot = n & (kSlots - 1);
+                    const uint32_t slot = n & (kSlots - 1), parity = (n / kSlots) & 1;
                     issue(n + kSlots - 1);
-                    if (!__all_sync(0xffffffffu, mbar_test(&S.full[warp][slot], (phase >> slot) & 1u)))
-                        if (!wait_more(&S.full[warp][slot], (phase >> slot) & 1u, A.wait_ns)) {
+                    if (!__all_sync(0xffffffffu, mbar_test(&S.full[warp][slot], parity)))
+                        if (!wait_more(&S.full[warp][slot], parity, A.wait_ns)) {
                             dead = true;
                             break;
                         }
-                    phase ^= 1u << slot;
                     attend_page4<NQ, HN>(q, ring + slot * q4::kRecord,
                                          (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
                     __syncwarp();
                 }
-                issued = n + kSlots - 1 + (dead ? 1 : 0);
                 if (dead) break;
             }
+            issued = n + kSlots - 1 + (dead ? 1 : 0);
             stopped = n;
-        }
-        const bool bad = any && dead;
-        if (bad) set_err(A.err, ICE_ERR_TIMEOUT);
-
-        // ---- the warps' results to shared memory
+            // ---- the warp's sums to shared memory, in the scale of the running maximum
 #pragma unroll
-        for (int hn = 0; hn < HN; ++hn)
+            for (int hn = 0; hn < HN; ++hn) {
+                const float2 l2 = upk2(st.l[hn]), m2 = upk2(st.minus_m[hn]), vs = upk2(st.vscale);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float2 l2 = upk2(st.l[hn]), m2 = upk2(st.minus_m[hn]), off2 = upk2(st.off[hn][e]);
-                const float2 vs = upk2(st.vscale);
-                float l = e ? l2.y : l2.x;
+                for (int e = 0; e < 2; ++e) {
+                    const int head = 8 * hn + 2 * c + e;
+                    const float m = -(e ? m2.y : m2.x);
+                    const float before = flushed ? exp2_fast(S.ml[warp][head][0] - m) : 0.f;
+                    __syncwarp();
+                    float l = e ? l2.y : l2.x;
+                    float2 off = upk2(st.off[hn][e]);
+                    if (n == n_end) {
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-                const int head = 8 * hn + 2 * c + e;
-                if (r == 0) {
-                    S.ml[warp][head][0] = -(e ? m2.y : m2.x);
-                    S.ml[warp][head][1] = bad ? __int_as_float(0x7fc00000) : l;
-                }
-                if (any) {
+                        for (int x = 4; x < 32; x <<= 1) {
+                            l += __shfl_xor_sync(0xffffffffu, l, x);
+                            off.x += __shfl_xor_sync(0xffffffffu, off.x, x);
+                            off.y += __shfl_xor_sync(0xffffffffu, off.y, x);
+                        }
+                    } else {
+                        off = make_float2(0.f, 0.f);
+                    }
+                    if (r == 0) {
+                        S.ml[warp][head][0] = m;
+                        S.ml[warp][head][1] = l;
+                    }
 #pragma unroll
-                    for (int gr = 0; gr < 2; ++gr) {
-                        float off = gr ? off2.y : off2.x;
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) off += __shfl_xor_sync(0xffffffffu, off, x);
-                        const float back = 1.f / (gr ? vs.y : vs.x), lo = pow2(24), hi = pow2(20);
-#pragma unroll
-                        for (int j = 2 * gr; j < 2 * gr + 2; ++j)
-                            *reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]) =
-                                make_float4(fmaf(st.o[hn][2 * j][e] * lo, back, off),
-                                            fmaf(st.o[hn][2 * j][2 + e] * hi, back, off),
-                                            fmaf(st.o[hn][2 * j + 1][e] * lo, back, off),
-                                            fmaf(st.o[hn][2 * j + 1][2 + e] * hi, back, off));
+                    for (int j = 0; j < 4; ++j) {
+                        const float back = 1.f / (j < 2 ? vs.x : vs.y), up = pow2(10);
+                        float4 *at = reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]);
+                        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (flushed) sum = *at;
+                        const float add = j < 2 ? off.x : off.y;
+                        float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
+                        *at = make_float4(fmaf(sum.x, before, fmaf(o0[e] * up, back, add)),
+                                          fmaf(sum.y, before, fmaf(o0[2 + e] * up, back, add)),
+                                          fmaf(sum.z, before, fmaf(o1[e] * up, back, add)),
+                                          fmaf(sum.w, before, fmaf(o1[2 + e] * up, back, add)));
+                        o0[e] = o0[2 + e] = o1[e] = o1[2 + e] = 0.f;
                     }
                 }
             }
+            flushed = true;
+        }
+        if (n < n_end || !any) {  // no page here, or a wait gave up
+            const bool bad = any;
+            if (bad) set_err(A.err, ICE_ERR_TIMEOUT);
+            __syncwarp();
+            for (int i = lane; i < Shape<HN>::kHeads; i += 32) {
+                S.ml[warp][i][0] = -FLT_MAX;
+                S.ml[warp][i][1] = bad ? __int_as_float(0x7fc00000) : 0.f;
+            }
+        }
         __syncthreads();
         // ---- joined: 32 threads a head, 4 elements each
         const bool whole = unit.first >= 0 && unit.end() <= run;
@@ -663,6 +706,10 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 const float l = S.ml[w][hh][1];
                 if (l == 0.f) continue;
                 const float wt = exp2_fast(S.ml[w][hh][0] - M);
+                if (l != l) {  // a wait gave up, or a value that is not a number
+                    L = acc.x = acc.y = acc.z = acc.w = l;
+                    break;
+                }
                 const float4 x = *reinterpret_cast<const float4 *>(&S.o[w][hh][4 * lane]);
                 L = fmaf(l, wt, L);
                 acc.x = fmaf(x.x, wt, acc.x), acc.y = fmaf(x.y, wt, acc.y);
@@ -724,8 +771,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     }
     if (dead && !A.fault_skip)  // nothing may be in flight when the CTA ends
         for (int n = stopped; n < issued; ++n) {
-            const int slot = n & (kSlots - 1);
-            if (pages[n & (2 * kBatch - 1)] != 0) mbar_wait(&S.full[warp][slot], (phase >> slot) & 1u, A.wait_ns);
+            mbar_wait(&S.full[warp][n & (kSlots - 1)], (n / kSlots) & 1, A.wait_ns);
         }
 }
 

@@ -6,8 +6,8 @@
 //             is an error-free double-float sum, so r is the correctly
 //             rounded value;
 //   rotation  (a, b) <- (a cos - b sin, b cos + a sin), each product rounded
-//             once (no contraction).  Keys of an fp32 cache take fp64
-//             products: their codes are decided as if exactly.
+//             once (no contraction).  Keys of an fp32 cache take the products
+//             with their rounding errors: their codes hang on the last bit.
 //
 // Both are bound by HBM for prompts (each row read and written once) and by
 // latency for single tokens.  8 lanes hold a row as two 8-element vectors: for
@@ -94,16 +94,25 @@ __device__ __forceinline__ void load_angles(const RopeArgs &A, const LaneVecs &v
     }
 }
 
+// x y + z w, its products and their sum with their rounding errors: within
+// 2^-44 of the exact value before the one rounding.
+__device__ __forceinline__ float dot2_wide(float x, float y, float z, float w) {
+    const float p = __fmul_rn(x, y), q = __fmul_rn(z, w);
+    float s, e;
+    two_sum(p, q, s, e);
+    return s + (e + (fmaf(x, y, -p) + fmaf(z, w, -q)));
+}
+
 template <bool kWide>
 __device__ __forceinline__ void rotate_pair(float &a, float &b, float c, float s) {
+    float x, y;
     if (kWide) {
-        const double x = (double)a * c - (double)b * s, y = (double)b * c + (double)a * s;
-        a = (float)x, b = (float)y;
+        x = dot2_wide(a, c, -b, s), y = dot2_wide(b, c, a, s);
     } else {
-        const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-        const float y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-        a = x, b = y;
+        x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
     }
+    a = x, b = y;
 }
 
 template <int kLayout, bool kWide>

@@ -131,25 +131,23 @@ template <> struct Vec8<float> {
 
 // step and mid of a group from its extremes.  Differences of bf16 values are
 // exact in fp32 (unless their exponents are more than 16 apart, where the
-// rounding is far below a code); those of fp32 values are taken in fp64.  The
-// quotient by 15 is corrected by its remainder, which rounds it correctly
-// (Markstein 1990: a quotient within an ulp and a correctly rounded
-// reciprocal); differences below 1e-30, whose remainder could underflow, are
-// divided.
+// rounding is far below a code); those of fp32 values are kept with their
+// rounding error.  The quotient by 15 is corrected by its remainder, which
+// rounds it correctly (Markstein 1990: a quotient within an ulp and a correctly
+// rounded reciprocal); differences below 1e-30, whose remainder could
+// underflow, are divided.
 template <typename T>
 __device__ __forceinline__ float2 step_mid(float lo, float hi) {
-    float step, mid;
-    if (sizeof(T) == 2) {
-        const float d = hi - lo, q = d * (1.f / 15.f);
-        step = fmaf(fmaf(-15.f, q, d), 1.f / 15.f, q);
-        if (d < 1e-30f) step = d / 15.f;
-        mid = (hi + lo) * 0.5f;
-    } else {
-        step = (float)(((double)hi - (double)lo) / 15.0);
-        mid = (float)(((double)hi + (double)lo) * 0.5);
-    }
-    if (!(hi - lo < INFINITY)) return make_float2(0.f, __int_as_float(0x7fc00000));
-    return make_float2(step, mid);
+    float d, er = 0.f;
+    if (sizeof(T) == 2)
+        d = hi - lo;
+    else
+        two_sum(hi, -lo, d, er);
+    const float q = d * (1.f / 15.f);
+    float step = fmaf(fmaf(-15.f, q, d) + er, 1.f / 15.f, q);
+    if (d < 1e-30f) step = d / 15.f;
+    if (!(d < INFINITY)) return make_float2(0.f, __int_as_float(0x7fc00000));
+    return make_float2(step, (hi + lo) * 0.5f);
 }
 
 // The word of a vector's 8 codes, rint((x - mid) / step + 7.5) with ties to
