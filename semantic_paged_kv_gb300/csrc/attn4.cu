@@ -34,10 +34,12 @@
 //   O^T += V^T (step P)^T: V codes as operands the same way (the record pairs
 //     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
 //     by a power of two that follows the largest step; the 8 x 8 transposes of
-//     P by movmatrix.  The codes go in as 2 c - 15 (a mean over many
-//     values cancels down to the noise of its sums; sum mid P joins at the end
-//     of the unit), and every 16 pages the sums leave the tensor core's
-//     accumulators, which truncate, for fp32 sums in shared memory.
+//     P by movmatrix.  The codes go in centred and as normal numbers, (code -
+//     7.5) 2^-10: a mean over many values cancels down to the noise of its
+//     sums, and the tensor core aligns subnormal operands by their nominal
+//     exponent, which costs six of its bits (relative error of O: 1e-5 with
+//     plain codes, 1.2e-6 with centred subnormals, 4e-7 so).  sum mid P joins
+//     at the end of the unit.
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -57,8 +59,9 @@ constexpr int kSlots = 4;          // pages of a warp's ring
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
 constexpr int kOver = 16;          // places that a unit takes beside its pages
-constexpr int kUnits = 256;        // units whose page counts a CTA keeps at hand
+constexpr int kUnits = 192;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
+constexpr int kMaxRuns = 384;      // CTAs, at most
 constexpr int kMinRun = kWarps;    // places of a run, at least: one page per warp
 
 struct Attn4Args {
@@ -94,7 +97,7 @@ struct UnitAt {
 template <int HN> struct Smem {
     unsigned char ring[kWarps][kSlots][q4::kRecord];
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
-    float ml[kWarps][Shape<HN>::kHeads][2];
+    float4 ml[kWarps][Shape<HN>::kHeads];  // maximum, sum, and each group's sum P mid
     int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
     unsigned long long full[kWarps][kSlots];
     unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
@@ -167,7 +170,6 @@ __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_u
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
-constexpr int kFlush = 16;  // pages after which a warp's sums leave the tensor core's accumulators
 
 using q4::pair_t;
 
@@ -205,58 +207,84 @@ template <int NQ, int HN> struct Queries {
     float factor;         // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
 };
 
+// What the CTA's threads share to prepare the queries of a unit.
+template <int NQ, int HN> struct QueryScratch {
+    uint2 f[NQ][HN][8][32];  // fragments by lane
+    float sum[8 * HN][2];
+    float big[kWarps];
+};
+
+// This thread's 8 elements of the group's queries: head tid / 16, elements 8 (tid % 16) ...
+template <typename T>
+__device__ __forceinline__ q4::Vec8<T> query_part(const T *Qg, int g) {
+    q4::Vec8<T> v;
+    v.zero();
+    if ((int)threadIdx.x < g * (kHeadDim / 8)) v.load(Qg + threadIdx.x * 8);
+    return v;
+}
+
+// The queries from every thread's part: the CTA's threads convert one vector
+// each, every warp then reads its fragments (all of the CTA's threads call it).
 template <typename T, int NQ, int HN>
-__device__ __forceinline__ void load_queries(const T *Qg, int g, float scale, Queries<NQ, HN> &q) {
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+__device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float scale, QueryScratch<NQ, HN> &X,
+                                                Queries<NQ, HN> &q) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
     const float sl = scale * 1.4426950408889634f;
-    float x[HN][4][8];
-    float big = 0.f;
+    float x[8];
+    part.get(x);
+    float big = 0.f, s = 0.f;
 #pragma unroll
-    for (int hn = 0; hn < HN; ++hn) {
-        const int head = 8 * hn + r;
+    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e])), s += x[e];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[hn][i][e] = 0.f;
-            if (head < g) load8<T>(Qg + (size_t)head * kHeadDim + 32 * i + 8 * c, x[hn][i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[hn][i][e]));
-        }
-    }
+    for (int off = 1; off < 8; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    const int head = tid >> 4, vec = tid & 15;
+    if (head < 8 * HN && (tid & 7) == 0) X.sum[head][vec >> 3] = s;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    if (lane == 0) X.big[warp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, X.big[w]);
     const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
     const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
     q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(24) * pow2(-e2);
+    if (head < 8 * HN) {
+        // element 8 vec + e is code e of word vec: half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
+        uint32_t f[NQ][4];
 #pragma unroll
-    for (int hn = 0; hn < HN; ++hn) {
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[i >> 1] += x[hn][i][e];
-            // code e of a word is in half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float w = (p & 1) ? 0.0625f * up : up;
-                const float a = x[hn][i][p] * w, b = x[hn][i][p + 4] * w;
-                const __half2 hi = __floats2half2_rn(a, b);
-                q.f[0][hn][2 * i + (p >> 1)][p & 1] = h2_bits(hi);
-                if (NQ > 1) {  // fp32 queries: the remainder
-                    const float2 back = __half22float2(hi);
-                    q.f[NQ - 1][hn][2 * i + (p >> 1)][p & 1] = h2_bits(__floats2half2_rn(a - back.x, b - back.y));
-                }
+        for (int p = 0; p < 4; ++p) {
+            const float w = (p & 1) ? 0.0625f * up : up;
+            const float a = x[p] * w, b = x[p + 4] * w;
+            const __half2 hi = __floats2half2_rn(a, b);
+            f[0][p] = h2_bits(hi);
+            if (NQ > 1) {  // fp32 queries: the remainder
+                const float2 back = __half22float2(hi);
+                f[NQ - 1][p] = h2_bits(__floats2half2_rn(a - back.x, b - back.y));
             }
         }
+        const int i = vec >> 2, to = (head & 7) * 4 + (vec & 3);
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 1);
-            s[gr] += __shfl_xor_sync(0xffffffffu, s[gr], 2);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                q.sum[hn][gr][e] = __shfl_sync(0xffffffffu, s[gr], 4 * (2 * c + e)) * up * pow2(-24);
+        for (int n = 0; n < NQ; ++n) {
+            X.f[n][head >> 3][2 * i][to] = make_uint2(f[n][0], f[n][1]);
+            X.f[n][head >> 3][2 * i + 1][to] = make_uint2(f[n][2], f[n][3]);
         }
     }
+    __syncthreads();
+#pragma unroll
+    for (int hn = 0; hn < HN; ++hn) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint2 v = X.f[n][hn][k][lane];
+                q.f[n][hn][k][0] = v.x, q.f[n][hn][k][1] = v.y;
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-24);
+    }
+    __syncthreads();  // the scratch lies where the results go
 }
 
 // Folds one page (record at shared address `rec`, its first `len` slots; whatever the others hold).
@@ -521,6 +549,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         return x;
     };
     UnitAt unit = unit_at(0, (int)(S.start0 - f0));
+    auto queries_of = [&](const UnitAt &x) {
+        const int u = u0 + x.i;
+        return query_part<T>(static_cast<const T *>(A.Q) + ((size_t)x.b * A.hq + (size_t)(u - x.b * A.hkv) * g) * kHeadDim, g);
+    };
+    q4::Vec8<T> qpart = queries_of(unit);  // in flight during the lookups
 
     // ---- the warp's pages: places n = 0 .. of the warp are places warp + 8 n of the run
     const int places = run > warp ? (run - warp + kWarps - 1) / kWarps : 0;
@@ -600,29 +633,28 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     Queries<NQ, HN> q;
     bool dead = false;  // a wait gave up, for place `stopped`
     int stopped = 0;
-    for (;;) {
+    for (bool first = true;; first = false) {
         // the next unit with pages in the run
-        while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end());
+        while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end()), first = false;
         if (unit.first >= run) break;
+        if (!first) qpart = queries_of(unit);
         const int pa = max(unit.first, 0), pb = min(unit.end(), run);
-        const int u = u0 + unit.i, b = u / A.hkv;
+        const int u = u0 + unit.i, b = unit.b;
         const size_t row0 = (size_t)b * A.hq + (size_t)(u - b * A.hkv) * g;
         st.init();
         int n = (pa + ((warp - pa) & (kWarps - 1))) / kWarps;
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
         const bool any = n < n_end;
-        if (any) load_queries<T, NQ, HN>(static_cast<const T *>(A.Q) + row0 * kHeadDim, g, A.scale, q);
-        bool flushed = false;
         if (any && !dead)
             for (; issued < n + kSlots - 1; ++issued) {  // (after places without a page)
                 if (issued >= looked) look_further();
                 issue(issued);
             }
-        while (n < n_end && !dead) {
-            const int until = min(n_end, n + kFlush);
-            while (n < until) {
+        prepare_queries<T, NQ, HN>(qpart, A.scale, *reinterpret_cast<QueryScratch<NQ, HN> *>(&S.o[0][0][0]), q);
+        if (any && !dead) {
+            while (n < n_end) {
                 while (looked - n <= kBatch / 2) look_further();
-                const int stop = min(until, looked - (kSlots - 1));
+                const int stop = min(n_end, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
                     const uint32_t slot = n & (kSlots - 1), parity = (n / kSlots) & 1;
                     issue(n + kSlots - 1);
@@ -639,57 +671,41 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             }
             issued = n + kSlots - 1 + (dead ? 1 : 0);
             stopped = n;
-            // ---- the warp's sums to shared memory, in the scale of the running maximum
+        }
+        if (any && dead) set_err(A.err, ICE_ERR_TIMEOUT);
+
+        // ---- the warps' sums to shared memory
 #pragma unroll
-            for (int hn = 0; hn < HN; ++hn) {
-                const float2 l2 = upk2(st.l[hn]), m2 = upk2(st.minus_m[hn]), vs = upk2(st.vscale);
+        for (int hn = 0; hn < HN; ++hn) {
+            const float2 m2 = upk2(st.minus_m[hn]), vs = upk2(st.vscale);
+            pair_t l2 = st.l[hn], off2[2] = {st.off[hn][0], st.off[hn][1]};
+            auto other = [](pair_t x, int by) {
+                const float2 y = upk2(x);
+                return pk2(__shfl_xor_sync(0xffffffffu, y.x, by), __shfl_xor_sync(0xffffffffu, y.y, by));
+            };
+            if (any) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int head = 8 * hn + 2 * c + e;
-                    const float m = -(e ? m2.y : m2.x);
-                    const float before = flushed ? exp2_fast(S.ml[warp][head][0] - m) : 0.f;
-                    __syncwarp();
-                    float l = e ? l2.y : l2.x;
-                    float2 off = upk2(st.off[hn][e]);
-                    if (n == n_end) {
+                for (int by = 4; by < 32; by <<= 1) {
+                    l2 = add2(l2, other(l2, by));
+                    off2[0] = add2(off2[0], other(off2[0], by));
+                    off2[1] = add2(off2[1], other(off2[1], by));
+                }
+                const float back[2] = {1024.f / vs.x, 1024.f / vs.y};  // codes went in times 2^-10 (both factors normal)
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) {
-                            l += __shfl_xor_sync(0xffffffffu, l, x);
-                            off.x += __shfl_xor_sync(0xffffffffu, off.x, x);
-                            off.y += __shfl_xor_sync(0xffffffffu, off.y, x);
-                        }
-                    } else {
-                        off = make_float2(0.f, 0.f);
-                    }
-                    if (r == 0) {
-                        S.ml[warp][head][0] = m;
-                        S.ml[warp][head][1] = l;
-                    }
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float back = 1.f / (j < 2 ? vs.x : vs.y), up = pow2(10);
-                        float4 *at = reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]);
-                        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (flushed) sum = *at;
-                        const float add = j < 2 ? off.x : off.y;
-                        float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
-                        *at = make_float4(fmaf(sum.x, before, fmaf(o0[e] * up, back, add)),
-                                          fmaf(sum.y, before, fmaf(o0[2 + e] * up, back, add)),
-                                          fmaf(sum.z, before, fmaf(o1[e] * up, back, add)),
-                                          fmaf(sum.w, before, fmaf(o1[2 + e] * up, back, add)));
-                        o0[e] = o0[2 + e] = o1[e] = o1[2 + e] = 0.f;
+                        const float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
+                        const float f = back[j >> 1];
+                        *reinterpret_cast<float4 *>(&S.o[warp][8 * hn + 2 * c + e][32 * j + 4 * r]) =
+                            make_float4(o0[e] * f, o0[2 + e] * f, o1[e] * f, o1[2 + e] * f);
                     }
-                }
             }
-            flushed = true;
-        }
-        if (n < n_end || !any) {  // no page here, or a wait gave up
-            const bool bad = any;
-            if (bad) set_err(A.err, ICE_ERR_TIMEOUT);
-            __syncwarp();
-            for (int i = lane; i < Shape<HN>::kHeads; i += 32) {
-                S.ml[warp][i][0] = -FLT_MAX;
-                S.ml[warp][i][1] = bad ? __int_as_float(0x7fc00000) : 0.f;
+            if (r == 0) {
+                const float2 l = upk2(l2), x = upk2(off2[0]), y = upk2(off2[1]);
+                const float bad = __int_as_float(0x7fc00000);
+                S.ml[warp][8 * hn + 2 * c] = make_float4(-m2.x, any && dead ? bad : l.x, x.x, x.y);
+                S.ml[warp][8 * hn + 2 * c + 1] = make_float4(-m2.y, any && dead ? bad : l.y, y.x, y.y);
             }
         }
         __syncthreads();
@@ -699,21 +715,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         for (int hh = warp; hh < g; hh += kWarps) {
             float M = -FLT_MAX, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, S.ml[w][hh][0]);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, S.ml[w][hh].x);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float l = S.ml[w][hh][1];
-                if (l == 0.f) continue;
-                const float wt = exp2_fast(S.ml[w][hh][0] - M);
-                if (l != l) {  // a wait gave up, or a value that is not a number
-                    L = acc.x = acc.y = acc.z = acc.w = l;
-                    break;
-                }
+                const float4 ml = S.ml[w][hh];
+                if (ml.y == 0.f) continue;  // no page
+                const float wt = ml.y == ml.y ? exp2_fast(ml.x - M) : ml.y;  // a sum that is not a number spreads
                 const float4 x = *reinterpret_cast<const float4 *>(&S.o[w][hh][4 * lane]);
-                L = fmaf(l, wt, L);
-                acc.x = fmaf(x.x, wt, acc.x), acc.y = fmaf(x.y, wt, acc.y);
-                acc.z = fmaf(x.z, wt, acc.z), acc.w = fmaf(x.w, wt, acc.w);
+                const float off = lane < 16 ? ml.z : ml.w;
+                L = fmaf(ml.y, wt, L);
+                acc.x = fmaf(x.x + off, wt, acc.x), acc.y = fmaf(x.y + off, wt, acc.y);
+                acc.z = fmaf(x.z + off, wt, acc.z), acc.w = fmaf(x.w + off, wt, acc.w);
             }
             if (whole) {
                 put_row(A, row0 + hh, acc, M, L);
@@ -732,35 +745,57 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             __syncthreads();
             if (S.last) {
                 __threadfence();
-                float *wt = &S.o[0][0][0];  // [runs][g] weights: at most kHeads * kWarps * kRow
-                auto part_at = [&](int k) {
-                    return ((size_t)(ca + k) * 2 + (us > (long long)(ca + k) * share ? 1 : 0)) * g;
-                };
-                const int runs = cb - ca + 1;
-                for (int hh = warp; hh < g; hh += kWarps) {
-                    float M = -FLT_MAX, L = 0.f;
-                    for (int k = lane; k < runs; k += 32) M = fmaxf(M, __ldcg(A.part_ml + (part_at(k) + hh) * 2));
+                // a head's runs go to 1, 2, 4 or 8 warps, whose sums meet in shared memory
+                const int runs = cb - ca + 1, split = g == 1 ? 8 : (g == 2 ? 4 : (g <= 4 ? 2 : 1));
+                float2 *wt = reinterpret_cast<float2 *>(&S.o[0][0][0]) + warp * kMaxRuns;  // of this warp's head
+                float *sums = reinterpret_cast<float *>(&S.o[0][0][0]) + 2 * kWarps * kMaxRuns;
+                const float2 *ml = reinterpret_cast<const float2 *>(A.part_ml) + (size_t)ca * 2 * g;
+                const float *po = A.part_o + (size_t)ca * 2 * g * kHeadDim;
+                // (the first run's part is its second one when the unit starts inside it)
+                const int skip = us > (long long)ca * share ? g : 0;
+                float M, L;
+                float4 acc;
+                for (int hh = warp / split; hh < g; hh += kWarps / split) {
+                    M = -FLT_MAX, L = 0.f;
+                    for (int k = lane; k < runs; k += 32) {
+                        const float2 x = __ldcg(ml + 2 * k * g + (k ? 0 : skip) + hh);
+                        M = fmaxf(M, x.x);
+                        wt[k] = x;
+                    }
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
                     for (int k = lane; k < runs; k += 32) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(A.part_ml + (part_at(k) + hh) * 2));
-                        const float x = ml.y == 0.f ? 0.f : exp2_fast(ml.x - M);
-                        wt[k * g + hh] = x;
-                        L = fmaf(ml.y, x, L);
+                        const float2 x = wt[k];
+                        const float w = x.y == 0.f ? 0.f : (x.y == x.y ? exp2_fast(x.x - M) : x.y);
+                        L = fmaf(x.y, w, L);
+                        wt[k].x = w;
                     }
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
                     __syncwarp();
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = 0; k < runs; ++k) {
-                        const float x = wt[k * g + hh];
-                        const float4 y =
-                            __ldcg(reinterpret_cast<const float4 *>(A.part_o + (part_at(k) + hh) * kHeadDim + 4 * lane));
-                        acc.x = fmaf(y.x, x, acc.x), acc.y = fmaf(y.y, x, acc.y);
-                        acc.z = fmaf(y.z, x, acc.z), acc.w = fmaf(y.w, x, acc.w);
+                    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
+#pragma unroll 8
+                    for (int k = warp % split; k < runs; k += split) {
+                        const float w = wt[k].x;
+                        const float4 y = __ldcg(row + (size_t)(2 * k * g + (k ? 0 : skip)) * (kHeadDim / 4));
+                        acc.x = fmaf(y.x, w, acc.x), acc.y = fmaf(y.y, w, acc.y);
+                        acc.z = fmaf(y.z, w, acc.z), acc.w = fmaf(y.w, w, acc.w);
                     }
-                    put_row(A, row0 + hh, acc, M, L);
+                    if (split == 1)
+                        put_row(A, row0 + hh, acc, M, L);
+                    else
+                        *reinterpret_cast<float4 *>(sums + warp * kHeadDim + 4 * lane) = acc;
+                }
+                if (split > 1) {  // (at most one head a warp: g <= kWarps / split)
+                    __syncthreads();
+                    if (warp % split == 0 && warp / split < g) {
+                        for (int w = 1; w < split; ++w) {
+                            const float4 y = *reinterpret_cast<const float4 *>(sums + (warp + w) * kHeadDim + 4 * lane);
+                            acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+                        }
+                        put_row(A, row0 + warp / split, acc, M, L);
+                    }
                 }
                 if (tid == 0) A.ticket[u] = 0;
             }
@@ -805,6 +840,11 @@ Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
     return w;
 }
 
+static_assert(kWarps * (2 * kMaxRuns + kHeadDim) <= kWarps * 8 * kRow, "the joining weights and sums lie in Smem::o");
+static_assert(sizeof(QueryScratch<2, 1>) <= sizeof(Smem<1>::o) && sizeof(QueryScratch<2, 2>) <= sizeof(Smem<2>::o),
+              "the queries' scratch lies in Smem::o");
+static_assert(2 * (sizeof(Smem<1>) + 1024) <= 227 * 1024, "two CTAs an SM");
+
 template <typename T, int NQ, int HN>
 cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     auto kern = k_attn4<T, NQ, HN>;
@@ -813,7 +853,8 @@ cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     // every CTA resident at once (no CTA waits for another, but equal runs should start together)
     const long long most = (long long)A.units * ((A.pool ? A.max_sel : 0) + (long long)(A.cache ? A.max_pages : 0));
     const long long runs = (most + (long long)A.units * kOver + kMinRun - 1) / kMinRun;
-    const int grid = (int)(runs < (long long)sms * Shape<HN>::kCtas ? (runs > 0 ? runs : 1) : sms * Shape<HN>::kCtas);
+    const int ctas = sms * Shape<HN>::kCtas < kMaxRuns ? sms * Shape<HN>::kCtas : kMaxRuns;
+    const int grid = (int)(runs < ctas ? (runs > 0 ? runs : 1) : ctas);
     return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<HN>), s, A);
 }
 
