@@ -77,8 +77,6 @@ struct Attn4Args {
     float *O, *lse;
     float *part_o, *part_ml;
     int32_t *ticket, *err;
-    unsigned long long wait_ns;
-    int fault_skip;
 };
 
 template <int HN> struct Shape {
@@ -99,7 +97,6 @@ template <int HN> struct Smem {
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
     float4 ml[kWarps][Shape<HN>::kHeads];  // maximum, sum, and each group's sum P mid
     int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
-    unsigned long long full[kWarps][kSlots];
     unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
     UnitAt look[kWarps];  // a warp's place in its lookups
     long long sum[kWarps];
@@ -458,9 +455,22 @@ __device__ __forceinline__ int pages_of(int2 n) { return n.x + (n.y + kPage - 1)
 // Places of a unit of n pages: kOver, then the pages; none without pages.
 __device__ __forceinline__ int places_of(int n) { return n > 0 ? n + kOver : 0; }
 
-// The rest of a wait: true when the phase of the given parity is complete, false after limit_ns.
-__device__ __noinline__ bool wait_more(unsigned long long *bar, uint32_t parity, unsigned long long limit_ns) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit_ns));
+// One record (address behind the length bits) into shared memory, by the
+// lanes of a warp in 16-byte pieces, as one group; nothing for place entry 0.
+__device__ __forceinline__ void copy_record(uint32_t dst, unsigned long long entry) {
+    const int lane = threadIdx.x & 31;
+    if (entry != 0) {
+        const unsigned char *src = reinterpret_cast<const unsigned char *>(entry & ((1ull << kLenShift) - 1)) + lane * 16;
+        dst += lane * 16;
+#pragma unroll
+        for (int i = 0; i < q4::kRecord / 512; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * i), "l"(src + 512 * i) : "memory");
+        if (lane < q4::kRecord % 512 / 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + q4::kRecord / 512 * 512),
+                         "l"(src + q4::kRecord / 512 * 512)
+                         : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // Row of O and lse from the sums over all pages (this lane's 4 elements).
@@ -479,8 +489,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     Smem<HN> &S = *reinterpret_cast<Smem<HN> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = A.g;
-    if (tid < kWarps * kSlots) mbar_init(&S.full[0][0] + tid, 1);
-    mbar_init_fence();
     dep_wait();
 
     // ---- the CTA's run of places: a prefix sum over the units
@@ -606,24 +614,9 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         look_up(looked + lane);
         looked += kBatch;
     };
-    const uint32_t ring = su32(S.ring[warp][0]), full = su32(&S.full[warp][0]);
-    const bool copies = lane == 0 && !A.fault_skip;  // fault injection: the waits for pages give up
-    // The copy of place n; a place without a page completes its slot's phase as well, so that phases follow n.
-    auto issue = [&](int n) {
-        const unsigned long long e = pages[n & (2 * kBatch - 1)];
-        const uint32_t slot = n & (kSlots - 1);
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .b64 once;\n\t.reg .b32 bytes;\n\t"
-            "setp.ne.b32 p, %0, 0;\n\t"
-            "setp.ne.and.b64 q, %4, 0, p;\n\t"
-            "selp.b32 bytes, %2, 0, q;\n\t"
-            "createpolicy.fractional.L2::evict_first.b64 once, 1.0;\n\t"
-            "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%1], bytes;\n\t"
-            "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%3], [%4], %2, [%1], "
-            "once;\n\t}" ::"r"((int)copies),
-            "r"(full + slot * 8), "r"((uint32_t)q4::kRecord), "r"(ring + slot * q4::kRecord),
-            "l"(e & ((1ull << kLenShift) - 1))
-            : "memory");
+    const uint32_t ring = su32(S.ring[warp][0]);
+    auto issue = [&](int n) {  // the copy of place n: one group a place, also where there is no page
+        copy_record(ring + (n & (kSlots - 1)) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
     };
     int issued = 0;  // places whose copy was started
     for (; issued < kSlots - 1; ++issued) issue(issued);
@@ -631,8 +624,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     const int r = lane >> 2, c = lane & 3;
     State<HN> st;
     Queries<NQ, HN> q;
-    bool dead = false;  // a wait gave up, for place `stopped`
-    int stopped = 0;
     for (bool first = true;; first = false) {
         // the next unit with pages in the run
         while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end()), first = false;
@@ -645,34 +636,28 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         int n = (pa + ((warp - pa) & (kWarps - 1))) / kWarps;
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
         const bool any = n < n_end;
-        if (any && !dead)
+        if (any)
             for (; issued < n + kSlots - 1; ++issued) {  // (after places without a page)
                 if (issued >= looked) look_further();
                 issue(issued);
             }
         prepare_queries<T, NQ, HN>(qpart, A.scale, *reinterpret_cast<QueryScratch<NQ, HN> *>(&S.o[0][0][0]), q);
-        if (any && !dead) {
+        if (any) {
             while (n < n_end) {
                 while (looked - n <= kBatch / 2) look_further();
                 const int stop = min(n_end, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
-                    const uint32_t slot = n & (kSlots - 1), parity = (n / kSlots) & 1;
-                    issue(n + kSlots - 1);
-                    if (!__all_sync(0xffffffffu, mbar_test(&S.full[warp][slot], parity)))
-                        if (!wait_more(&S.full[warp][slot], parity, A.wait_ns)) {
-                            dead = true;
-                            break;
-                        }
-                    attend_page4<NQ, HN>(q, ring + slot * q4::kRecord,
-                                         (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
+                    // place n has arrived (n + 1 and n + 2 may be on their way), and every lane is done with n - 1
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
                     __syncwarp();
+                    issue(n + kSlots - 1);
+                    attend_page4<NQ, HN>(q, ring + (n & (kSlots - 1)) * q4::kRecord,
+                                         (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
                 }
-                if (dead) break;
             }
-            issued = n + kSlots - 1 + (dead ? 1 : 0);
-            stopped = n;
+            issued = n + kSlots - 1;
+            __syncwarp();
         }
-        if (any && dead) set_err(A.err, ICE_ERR_TIMEOUT);
 
         // ---- the warps' sums to shared memory
 #pragma unroll
@@ -703,9 +688,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             }
             if (r == 0) {
                 const float2 l = upk2(l2), x = upk2(off2[0]), y = upk2(off2[1]);
-                const float bad = __int_as_float(0x7fc00000);
-                S.ml[warp][8 * hn + 2 * c] = make_float4(-m2.x, any && dead ? bad : l.x, x.x, x.y);
-                S.ml[warp][8 * hn + 2 * c + 1] = make_float4(-m2.y, any && dead ? bad : l.y, y.x, y.y);
+                S.ml[warp][8 * hn + 2 * c] = make_float4(-m2.x, l.x, x.x, x.y);
+                S.ml[warp][8 * hn + 2 * c + 1] = make_float4(-m2.y, l.y, y.x, y.y);
             }
         }
         __syncthreads();
@@ -804,10 +788,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         __syncthreads();  // the results have been read
         unit = unit_at(unit.i + 1, unit.end());
     }
-    if (dead && !A.fault_skip)  // nothing may be in flight when the CTA ends
-        for (int n = stopped; n < issued; ++n) {
-            mbar_wait(&S.full[warp][n & (kSlots - 1)], (n / kSlots) & 1, A.wait_ns);
-        }
 }
 
 int device_sms() {
@@ -882,9 +862,6 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
     const int sms = device_sms();
     const Attn4Ws w = ws_layout(p, sms, ws);
     A.ticket = w.ticket, A.part_ml = w.part_ml, A.part_o = w.part_o;
-    const bool fault = fault_armed("timeout");
-    A.wait_ns = fault ? kFaultWaitNs : kWaitNs;
-    A.fault_skip = fault ? 1 : 0;
     if (p.dtype == ICE_BF16)
         return A.g <= 8 ? launch_t<__nv_bfloat16, 1, 1>(A, sms, s) : launch_t<__nv_bfloat16, 1, 2>(A, sms, s);
     return A.g <= 8 ? launch_t<float, 2, 1>(A, sms, s) : launch_t<float, 2, 2>(A, sms, s);
