@@ -156,8 +156,14 @@ def _ptr(x) -> int | None:
     return int(x)
 
 
+# The current stream's handle without building a torch.cuda.Stream (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -482,7 +488,7 @@ def rows(t: torch.Tensor) -> IceRows:
     return r
 
 
-class Rope:
+class Rope(IceRope):
     """ice_rope: cos/sin table [n_positions, rotary_dim / 2, 2] (fp32, see ice_rope_table) or None, and norm weights
     [d] of q and k or None."""
 
@@ -494,11 +500,11 @@ class Rope:
             if w is not None and (tuple(w.shape) != (HEAD_DIM,) or not w.is_contiguous()):
                 raise IceError(ICE_ERR_INVALID_ARG, f"norm weights are contiguous [{HEAD_DIM}]")
         n, half = (table.shape[0], table.shape[1]) if table is not None else (0, 0)
+        super().__init__(_ptr(table), n, 2 * half, int(interleaved), eps, _ptr(q_norm), _ptr(k_norm))
         self.keep = (table, q_norm, k_norm)
-        self.struct = IceRope(_ptr(table), n, 2 * half, int(interleaved), eps, _ptr(q_norm), _ptr(k_norm))
 
 
-class Cache4:
+class Cache4(IceCache4):
     """ice_cache4: records [n_pages, Hkv, ICE_RECORD4_BYTES] (uint8) and the block table [B, max_pages] (int32)."""
 
     def __init__(self, records: torch.Tensor, table: torch.Tensor):
@@ -507,15 +513,8 @@ class Cache4:
             raise IceError(ICE_ERR_INVALID_ARG, f"records are contiguous uint8 [n_pages, Hkv, {ICE_RECORD4_BYTES}]")
         if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous():
             raise IceError(ICE_ERR_INVALID_ARG, "a block table is contiguous int32 [B, max_pages]")
+        super().__init__(records.data_ptr(), table.data_ptr(), records.shape[0], table.shape[1])
         self.keep = (records, table)
-        self.struct = IceCache4(records.data_ptr(), table.data_ptr(), records.shape[0], table.shape[1])
-
-
-def _ref(x):
-    """A struct (or its holder) by reference; None stays NULL."""
-    if x is None:
-        return None
-    return ctypes.byref(getattr(x, "struct", x))
 
 
 def ice_rope_table(inv_freq, n_positions: int, table, stream=None):
@@ -530,52 +529,52 @@ def ice_rope_table(inv_freq, n_positions: int, table, stream=None):
 
 def ice_qkv_rope(params, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out, err, stream=None):
     """q, k, v and the outputs are ``rows(...)`` views (or None), rope a Rope (or None)."""
-    _check(load().ice_qkv_rope(ctypes.byref(params), n_new, _ref(q), _ref(k), _ref(v), _ptr(positions), _ptr(start),
-                               _ptr(counts), _ref(rope), _ref(q_out), _ref(k_out), _ref(v_out), _ptr(err),
+    _check(load().ice_qkv_rope(params, n_new, q, k, v, _ptr(positions), _ptr(start),
+                               _ptr(counts), rope, q_out, k_out, v_out, _ptr(err),
                                _stream(stream)))
 
 
 def ice_cache4_append(params, n_new, q, k, v, positions, start, counts, rope, q_out, cache, err, stream=None):
-    _check(load().ice_cache4_append(ctypes.byref(params), n_new, _ref(q), _ref(k), _ref(v), _ptr(positions),
-                                    _ptr(start), _ptr(counts), _ref(rope), _ref(q_out), _ref(cache), _ptr(err),
+    _check(load().ice_cache4_append(params, n_new, q, k, v, _ptr(positions),
+                                    _ptr(start), _ptr(counts), rope, q_out, cache, _ptr(err),
                                     _stream(stream)))
 
 
 def ice_cache4_read(params, n_new, cache, start, counts, k_out, v_out, err, stream=None):
-    _check(load().ice_cache4_read(ctypes.byref(params), n_new, _ref(cache), _ptr(start), _ptr(counts), _ref(k_out),
-                                  _ref(v_out), _ptr(err), _stream(stream)))
+    _check(load().ice_cache4_read(params, n_new, cache, _ptr(start), _ptr(counts), k_out,
+                                  v_out, _ptr(err), _stream(stream)))
 
 
 def ice_pool4_bytes(params: IceParams) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().ice_pool4_bytes(ctypes.byref(params), ctypes.byref(n)))
+    _check(load().ice_pool4_bytes(params, ctypes.byref(n)))
     return n.value
 
 
 def ice_pool4_pack(params, index, first_token: int, records, err, stream=None):
-    _check(load().ice_pool4_pack(ctypes.byref(params), _ref(index), first_token, _ptr(records), _ptr(err),
+    _check(load().ice_pool4_pack(params, index.struct if isinstance(index, Index) else index, first_token, _ptr(records), _ptr(err),
                                  _stream(stream)))
 
 
 def ice_pool4_unpack(params, index, records, err, stream=None):
-    _check(load().ice_pool4_unpack(ctypes.byref(params), _ref(index), _ptr(records), _ptr(err), _stream(stream)))
+    _check(load().ice_pool4_unpack(params, index.struct if isinstance(index, Index) else index, _ptr(records), _ptr(err), _stream(stream)))
 
 
 def ice_attn4_workspace_bytes(params: IceParams) -> int:
     n = ctypes.c_size_t(0)
-    _check(load().ice_attn4_workspace_bytes(ctypes.byref(params), ctypes.byref(n)))
+    _check(load().ice_attn4_workspace_bytes(params, ctypes.byref(n)))
     return n.value
 
 
 def ice_cache4_attn_decode(params, Q, cache, lens, scale, O, lse, ws, err, stream=None):
-    _check(load().ice_cache4_attn_decode(ctypes.byref(params), _ptr(Q), _ref(cache), _ptr(lens), float(scale), _ptr(O),
+    _check(load().ice_cache4_attn_decode(params, _ptr(Q), cache, _ptr(lens), float(scale), _ptr(O),
                                          _ptr(lse), _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)))
 
 
 def ice_sparse_attn_decode4(params, Q, records, page_len, sel_pages, sel_count, cache, lens, scale, O, lse, ws, err,
                             stream=None):
-    _check(load().ice_sparse_attn_decode4(ctypes.byref(params), _ptr(Q), _ptr(records), _ptr(page_len),
-                                          _ptr(sel_pages), _ptr(sel_count), sel_pages.shape[-1], _ref(cache),
+    _check(load().ice_sparse_attn_decode4(params, _ptr(Q), _ptr(records), _ptr(page_len),
+                                          _ptr(sel_pages), _ptr(sel_count), sel_pages.shape[-1], cache,
                                           _ptr(lens), float(scale), _ptr(O), _ptr(lse), _ptr(ws), _nbytes(ws),
                                           _ptr(err), _stream(stream)))
 

@@ -43,6 +43,8 @@
 #include <cuda_fp16.h>
 #include <float.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
@@ -790,11 +792,16 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     }
 }
 
+// SMs of the current device (asked of the driver once a device).
 int device_sms() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 1;
+    n = n > 0 ? n : 1;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 struct Attn4Ws {
