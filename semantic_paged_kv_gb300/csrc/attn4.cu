@@ -60,7 +60,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSlots = 4;          // pages of a warp's ring
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
-constexpr int kOver = 16;          // places that a unit takes beside its pages
+constexpr int kOver = 24;          // places that a unit takes beside its pages
 constexpr int kUnits = 192;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
@@ -525,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         if (w < warp) before += S.sum[w];
         total += S.sum[w];
     }
-    long long share = total < (1ll << 31) ? ((unsigned)total + gridDim.x - 1) / gridDim.x
-                                          : (total + gridDim.x - 1) / gridDim.x;
+    int share = (int)(total < (1ll << 31) ? ((unsigned)total + gridDim.x - 1) / gridDim.x
+                                          : (total + gridDim.x - 1) / gridDim.x);
     if (share < kMinRun) share = kMinRun;
     const long long f0 = (long long)blockIdx.x * share;
-    const int run = (int)min(share, total - f0);
+    const int run = (int)min((long long)share, total - f0);
     if (run <= 0) return;  // the whole CTA
     if (f0 >= before && f0 < before + mine) {
         long long at = before;
@@ -569,26 +569,29 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     const int places = run > warp ? (run - warp + kWarps - 1) / kWarps : 0;
     unsigned long long *pages = S.page[warp];
     if (lane == 0) S.look[warp] = unit;
-    auto look_up = [&](int n) {  // place n of this lane, in order of the lanes
+    const uint32_t ring = su32(S.ring[warp][0]);
+    auto issue = [&](int n) {  // the copy of place n: one group a place, also where there is no page
+        copy_record(ring + (n & (kSlots - 1)) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
+    };
+    int looked = 0, issued = 0;  // places looked up, and those whose copy was started
+    auto look_further = [&]() {
         __syncwarp();
         UnitAt look = S.look[warp];
-        __syncwarp();
-        const int f = warp + kWarps * n;
-        unsigned long long e = 0;
+        const int n = looked + lane, f = warp + kWarps * n;
+        const unsigned char *src = nullptr;
+        int len = 0;
         if (n < places) {
             while (f >= look.end()) look = unit_at(look.i + 1, look.end());
             if (f >= look.first) {
                 const int x = f - look.first, u = u0 + look.i;
                 // a page that does not exist is copied from the first one and attended with length 0
-                const unsigned char *src;
-                int len = 0;
                 if (x < look.cnt.x) {
                     src = A.pool;
                     const int id = A.sel_pages[(size_t)u * A.max_sel + x];
                     if (id >= 0 && id < A.page_cap) {
                         const size_t at = (size_t)u * A.page_cap + id;
                         src += at * q4::kRecord;
-                        len = min(max(A.page_len[at], 0), kPage);
+                        len = A.page_len[at];
                     } else {
                         set_err(A.err, ICE_ERR_CAPACITY);
                     }
@@ -598,30 +601,27 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     const int id = A.table[(size_t)b * A.max_pages + blk];
                     if (id >= 0 && id < A.n_pages) {
                         src += ((size_t)id * A.hkv + (u - b * A.hkv)) * q4::kRecord;
-                        len = min(kPage, look.cnt.y - blk * kPage);
+                        len = look.cnt.y - blk * kPage;
                     } else {
                         set_err(A.err, ICE_ERR_CAPACITY);
                     }
                 }
-                e = reinterpret_cast<unsigned long long>(src) | (unsigned long long)len << kLenShift;
             }
         }
-        pages[n & (2 * kBatch - 1)] = e;
+        unsigned long long *entry = &pages[n & (2 * kBatch - 1)];
+        if (looked == 0) {  // the first copies start while the lengths are on their way
+            *entry = reinterpret_cast<unsigned long long>(src);
+            __syncwarp();
+            for (; issued < kSlots - 1; ++issued) issue(issued);
+            __syncwarp();
+        }
+        *entry = reinterpret_cast<unsigned long long>(src) | (unsigned long long)min(max(len, 0), kPage) << kLenShift;
+        __syncwarp();
         if (lane == 31) S.look[warp] = look;
+        looked += kBatch;
         __syncwarp();
     };
-    int looked = kBatch;
-    look_up(lane);
-    auto look_further = [&]() {
-        look_up(looked + lane);
-        looked += kBatch;
-    };
-    const uint32_t ring = su32(S.ring[warp][0]);
-    auto issue = [&](int n) {  // the copy of place n: one group a place, also where there is no page
-        copy_record(ring + (n & (kSlots - 1)) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
-    };
-    int issued = 0;  // places whose copy was started
-    for (; issued < kSlots - 1; ++issued) issue(issued);
+    look_further();
 
     const int r = lane >> 2, c = lane & 3;
     State<HN> st;
@@ -725,9 +725,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             // the unit's runs: CTAs ca .. cb; a run's part is its second one when the unit starts inside the run
             const long long us = f0 + unit.first;
             const int ca = (int)(us / share), cb = (int)((us + unit.n - 1) / share);
-            __threadfence();
             __syncthreads();
-            if (tid == 0) S.last = atomicAdd(A.ticket + u, 1) == cb - ca;
+            if (tid == 0) {
+                __threadfence();  // (the whole CTA's stores: they come before the barrier)
+                S.last = atomicAdd(A.ticket + u, 1) == cb - ca;
+            }
             __syncthreads();
             if (S.last) {
                 __threadfence();
@@ -742,6 +744,17 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 float M, L;
                 float4 acc;
                 for (int hh = warp / split; hh < g; hh += kWarps / split) {
+                    // the first rows are on their way while the weights are found
+                    constexpr int kAhead = 8;
+                    const int k0 = warp % split;
+                    const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
+                    auto row_of = [&](int k) {
+                        return k < runs ? __ldcg(row + (size_t)(2 * k * g + (k ? 0 : skip)) * (kHeadDim / 4))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    };
+                    float4 y[kAhead];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) y[i] = row_of(k0 + i * split);
                     M = -FLT_MAX, L = 0.f;
                     for (int k = lane; k < runs; k += 32) {
                         const float2 x = __ldcg(ml + 2 * k * g + (k ? 0 : skip) + hh);
@@ -760,13 +773,18 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
                     __syncwarp();
                     acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
-#pragma unroll 8
-                    for (int k = warp % split; k < runs; k += split) {
-                        const float w = wt[k].x;
-                        const float4 y = __ldcg(row + (size_t)(2 * k * g + (k ? 0 : skip)) * (kHeadDim / 4));
-                        acc.x = fmaf(y.x, w, acc.x), acc.y = fmaf(y.y, w, acc.y);
-                        acc.z = fmaf(y.z, w, acc.z), acc.w = fmaf(y.w, w, acc.w);
+                    for (int k = k0; k < runs; k += kAhead * split) {
+                        float4 z[kAhead];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) z[i] = y[i];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) y[i] = row_of(k + (kAhead + i) * split);
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const float w = k + i * split < runs ? wt[k + i * split].x : 0.f;
+                            acc.x = fmaf(z[i].x, w, acc.x), acc.y = fmaf(z[i].y, w, acc.y);
+                            acc.z = fmaf(z[i].z, w, acc.z), acc.w = fmaf(z[i].w, w, acc.w);
+                        }
                     }
                     if (split == 1)
                         put_row(A, row0 + hh, acc, M, L);
