@@ -166,6 +166,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent of a positive finite float (-127 for subnormals).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
+constexpr int kFlush = 32;  // pages after which a warp's sums leave the tensor core's accumulators (they truncate)
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
@@ -205,6 +206,10 @@ template <int NQ, int HN> struct Queries {
     float sum[HN][2][2];  // sum q over a group, in the products' scale, for this lane's columns (heads 2 c, 2 c + 1)
     float factor;         // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
 };
+
+// Codes of K as operands: c 2^-24 (kLow; kHigh times 16, and its queries over 16), or with fp32 queries centred() ones,
+// whose products keep the bits that those queries have.
+template <int NQ> constexpr int kCodeScale = NQ > 1 ? 10 : 24;
 
 // What the CTA's threads share to prepare the queries of a unit.
 template <int NQ, int HN> struct QueryScratch {
@@ -246,13 +251,13 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
     for (int w = 0; w < kWarps; ++w) big = fmaxf(big, X.big[w]);
     const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
     const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
-    q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(24) * pow2(-e2);
+    q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(kCodeScale<NQ>) * pow2(-e2);
     if (head < 8 * HN) {
         // element 8 vec + e is code e of word vec: half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
         uint32_t f[NQ][4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const float w = (p & 1) ? 0.0625f * up : up;
+            const float w = NQ == 1 && (p & 1) ? 0.0625f * up : up;
             const float a = x[p] * w, b = x[p + 4] * w;
             const __half2 hi = __floats2half2_rn(a, b);
             f[0][p] = h2_bits(hi);
@@ -281,7 +286,7 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr) q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-24);
+            for (int gr = 0; gr < 2; ++gr) q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-kCodeScale<NQ>);
     }
     __syncthreads();  // the scratch lies where the results go
 }
@@ -302,7 +307,10 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t x0 = w0[i] >> (8 * k), x1 = w1[i] >> (8 * k);
-                const uint32_t a[4] = {x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh};
+                uint32_t a[4] = {x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh};
+                if (NQ > 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = centred(a[e], e > 1);
 #pragma unroll
                 for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
@@ -316,8 +324,9 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
             }
         const float2 g00 = q4::unpack_meta(m0.x), g01 = q4::unpack_meta(m0.y);  // token r
         const float2 g10 = q4::unpack_meta(m1.x), g11 = q4::unpack_meta(m1.y);  // token r + 8
-        const float2 b0 = upk2(fma2(pk2(-7.5f, -7.5f), pk2(g00.x, g01.x), pk2(g00.y, g01.y)));
-        const float2 b1 = upk2(fma2(pk2(-7.5f, -7.5f), pk2(g10.x, g11.x), pk2(g10.y, g11.y)));
+        constexpr float kOff = NQ > 1 ? 0.f : -7.5f;
+        const float2 b0 = upk2(fma2(pk2(kOff, kOff), pk2(g00.x, g01.x), pk2(g00.y, g01.y)));
+        const float2 b1 = upk2(fma2(pk2(kOff, kOff), pk2(g10.x, g11.x), pk2(g10.y, g11.y)));
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
@@ -644,10 +653,11 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 issue(issued);
             }
         prepare_queries<T, NQ, HN>(qpart, A.scale, *reinterpret_cast<QueryScratch<NQ, HN> *>(&S.o[0][0][0]), q);
-        if (any) {
-            while (n < n_end) {
+        for (bool flushed = false; n < n_end; flushed = true) {
+            const int until = min(n_end, n + kFlush);
+            while (n < until) {
                 while (looked - n <= kBatch / 2) look_further();
-                const int stop = min(n_end, looked - (kSlots - 1));
+                const int stop = min(until, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
                     // place n has arrived (n + 1 and n + 2 may be on their way), and every lane is done with n - 1
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
@@ -659,12 +669,40 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             }
             issued = n + kSlots - 1;
             __syncwarp();
+            // ---- the warp's sums of V to shared memory, in the scale of the running maximum
+            const float2 vs = upk2(st.vscale);
+            const float back[2] = {1024.f / vs.x, 1024.f / vs.y};  // codes went in times 2^-10 (both factors normal)
+#pragma unroll
+            for (int hn = 0; hn < HN; ++hn) {
+                const float2 m2 = upk2(st.minus_m[hn]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int head = 8 * hn + 2 * c + e;
+                    const float m = -(e ? m2.y : m2.x);
+                    const float before = flushed ? exp2_fast(S.ml[warp][head].x - m) : 0.f;
+                    __syncwarp();
+                    if (r == 0) S.ml[warp][head].x = m;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
+                        const float f = back[j >> 1];
+                        float4 *at = reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]);
+                        float4 x = make_float4(o0[e] * f, o0[2 + e] * f, o1[e] * f, o1[2 + e] * f);
+                        if (flushed) {
+                            const float4 y = *at;
+                            x.x = fmaf(y.x, before, x.x), x.y = fmaf(y.y, before, x.y);
+                            x.z = fmaf(y.z, before, x.z), x.w = fmaf(y.w, before, x.w);
+                        }
+                        *at = x;
+                        o0[e] = o0[2 + e] = o1[e] = o1[2 + e] = 0.f;
+                    }
+                }
+            }
         }
-
-        // ---- the warps' sums to shared memory
+        // ---- and its softmax sums
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
-            const float2 m2 = upk2(st.minus_m[hn]), vs = upk2(st.vscale);
+            const float2 m2 = upk2(st.minus_m[hn]);
             pair_t l2 = st.l[hn], off2[2] = {st.off[hn][0], st.off[hn][1]};
             auto other = [](pair_t x, int by) {
                 const float2 y = upk2(x);
@@ -677,16 +715,6 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     off2[0] = add2(off2[0], other(off2[0], by));
                     off2[1] = add2(off2[1], other(off2[1], by));
                 }
-                const float back[2] = {1024.f / vs.x, 1024.f / vs.y};  // codes went in times 2^-10 (both factors normal)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
-                        const float f = back[j >> 1];
-                        *reinterpret_cast<float4 *>(&S.o[warp][8 * hn + 2 * c + e][32 * j + 4 * r]) =
-                            make_float4(o0[e] * f, o0[2 + e] * f, o1[e] * f, o1[2 + e] * f);
-                    }
             }
             if (r == 0) {
                 const float2 l = upk2(l2), x = upk2(off2[0]), y = upk2(off2[1]);

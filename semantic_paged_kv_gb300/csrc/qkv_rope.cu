@@ -123,8 +123,10 @@ __device__ __forceinline__ void rotate(const RopeArgs &A, const LaneVecs &v, flo
         for (int i = 0; i < 4; ++i) {
             const pair_t x = pk2(a[2 * i], a[2 * i + 1]), y = pk2(b[2 * i], b[2 * i + 1]);
             const pair_t co = pk2(c[2 * i], c[2 * i + 1]), si = pk2(s[2 * i], s[2 * i + 1]);
-            const float2 p = upk2(sub2(mul2(x, co), mul2(y, si))), q = upk2(add2(mul2(y, co), mul2(x, si)));
-            a[2 * i] = p.x, a[2 * i + 1] = p.y, b[2 * i] = q.x, b[2 * i + 1] = q.y;
+            // (packed sums of packed products come out fused: the sums stay scalar)
+            const float2 p = upk2(mul2(x, co)), q = upk2(mul2(y, si)), u = upk2(mul2(y, co)), w = upk2(mul2(x, si));
+            a[2 * i] = __fsub_rn(p.x, q.x), a[2 * i + 1] = __fsub_rn(p.y, q.y);
+            b[2 * i] = __fadd_rn(u.x, w.x), b[2 * i + 1] = __fadd_rn(u.y, w.y);
         }
     } else if (A.interleaved) {
 #pragma unroll
