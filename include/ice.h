@@ -658,9 +658,10 @@ ice_status ice_cache4_read(const ice_params *p, int32_t n_new, const ice_cache4 
                            const int32_t *counts, const ice_rows *k_out, const ice_rows *v_out, int32_t *err_dev,
                            void *stream);
 
-/* Workspace bytes of the two attention calls below (zero-filled once before
- * its first use and left so by every call, like a decode workspace; calls
- * that share one must not overlap on the GPU). */
+/* Workspace bytes of the two attention calls below.  It must be zero-filled
+ * once before its first use; every call that completes leaves it fit for the
+ * next one, of these or of other shapes (whose bytes it must have).  Calls
+ * that share one must not overlap on the GPU. */
 ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes);
 
 /*
@@ -673,8 +674,7 @@ ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes);
  * token gives O = 0 and lse = -inf.  The pages are split evenly over the GPU,
  * whatever the lengths; every run of a call gives the same bits.
  * A page outside [0, n_pages) sets ICE_ERR_CAPACITY in err_dev and its tokens
- * are left out.  A bounded wait that gives up sets ICE_ERR_TIMEOUT and leaves
- * NaN in the rows it concerns.
+ * are left out.
  */
 ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_cache4 *cache, const int32_t *lens,
                                   float scale, float *O, float *lse, void *ws, size_t ws_bytes, int32_t *err_dev,

@@ -850,10 +850,15 @@ int device_sms() {
     return n;
 }
 
+int max_ctas(int sms) { return 2 * sms < kMaxRuns ? 2 * sms : kMaxRuns; }
+
+// The partial results lie before the tickets, at sizes that no shape changes:
+// calls of different shapes can share a workspace (one after the other) without
+// writing over each other's tickets.
 struct Attn4Ws {
-    int32_t *ticket;  // [units] zero between calls
     float *part_ml;   // [2 runs, g, 2]
     float *part_o;    // [2 runs, g, 128]
+    int32_t *ticket;  // [units] zero between calls
     size_t bytes;
 };
 Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
@@ -865,10 +870,10 @@ Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
         off += (bytes + 255) & ~(size_t)255;
         return r;
     };
-    const size_t g = p.n_q_heads / p.n_kv_heads, parts = 2 * 2 * (size_t)sms * g;
-    w.ticket = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * units_of(p)));
+    const size_t parts = 2 * (size_t)max_ctas(sms) * 16;  // (g <= 16)
     w.part_ml = reinterpret_cast<float *>(take(sizeof(float) * parts * 2));
     w.part_o = reinterpret_cast<float *>(take(sizeof(float) * parts * kHeadDim));
+    w.ticket = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * units_of(p)));
     w.bytes = off;
     return w;
 }
@@ -886,7 +891,7 @@ cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     // every CTA resident at once (no CTA waits for another, but equal runs should start together)
     const long long most = (long long)A.units * ((A.pool ? A.max_sel : 0) + (long long)(A.cache ? A.max_pages : 0));
     const long long runs = (most + (long long)A.units * kOver + kMinRun - 1) / kMinRun;
-    const int ctas = sms * Shape<HN>::kCtas < kMaxRuns ? sms * Shape<HN>::kCtas : kMaxRuns;
+    const int ctas = Shape<HN>::kCtas * sms < max_ctas(sms) ? Shape<HN>::kCtas * sms : max_ctas(sms);
     const int grid = (int)(runs < ctas ? (runs > 0 ? runs : 1) : ctas);
     return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<HN>), s, A);
 }

@@ -590,3 +590,157 @@ def test_pack_of_inserted_tokens():
     before = recs.clone()
     ice.ice_pool4_pack(p, idx, N + steps - 1, recs, err)
     assert ice.ice_check(err) == ice.ICE_ERR_CAPACITY and torch.equal(recs, before)
+
+
+# --------------------------------------------------------- what tests miss --
+def test_codes_on_borders():
+    """Values on a coarse grid: true ties between two codes, mid a multiple of step or next to one, tiny values beside
+    large ones."""
+    g = _gen(111)
+    n = 4000
+
+    def ints(lo, hi):
+        return torch.randint(lo, hi, (n, S, D), generator=g, device="cuda").float()
+
+    rows = [ints(-15, 16), ints(0, 16) * 0.5, ints(-128, 128) / 16, ints(-7, 8) * 0.75 + 1.5,
+            ints(-30, 31) * torch.exp2(torch.randint(-12, 3, (n, S, D), generator=g, device="cuda").float()),
+            ints(-3, 4) * 1e-30, (ints(0, 31) + 100) * 2]
+    rows[0][:, :, ::7] *= 1e-6
+    for x in rows:
+        k = x.bfloat16()
+        v = k.flip(-1)
+        pool = lambda t: t.view(1, n, S, D).contiguous()  # noqa: E731
+        lens = torch.full((1, n), 16, dtype=torch.int32, device="cuda")
+        cnt = torch.full((1,), n, dtype=torch.int32, device="cuda")
+        recs, err = torch.empty((1, n, R), dtype=torch.uint8, device="cuda"), _err()
+        ice.ice_pool4_pack(_params(1, 1, 1, "bf16", page_cap=n), _ix(n_pages=cnt, page_len=lens, pool_k=pool(k),
+                                                                      pool_v=pool(v)), 0, recs, err)
+        assert ice.ice_check(err) == ice.ICE_OK and torch.equal(recs[0], ref.encode(k, v))
+
+
+def test_long_context_of_shared_pages():
+    """100k tokens a sequence (the warps' sums are flushed on the way), sequences sharing the pages of a small cache."""
+    B, hq, hkv, n = 2, 64, 8, 100003
+    p = _params(B, hq, hkv, "bf16")
+    recs = _random_records(600, hkv, 121)
+    bt = torch.randint(0, 600, (B, -(-n // S)), generator=_gen(122), device="cuda").int()
+    Q = torch.randn((B, hq, D), generator=_gen(123), device="cuda").bfloat16()
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    ln = torch.tensor([n, n - 40000], dtype=torch.int32, device="cuda")
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), ln, 0.088, O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    for b, h in ((0, 0), (0, 7), (1, 3)):
+        k, v = (x.reshape(-1, D)[:int(ln[b])] for x in ref.decode(recs[bt[b].long(), h]))
+        o, l = ref.attention(Q[b, 8 * h:8 * h + 8].double(), k, v, 0.088)
+        got = O[b, 8 * h:8 * h + 8].double()
+        # a mean over 1e5 values: relative to its own size, as fp32 sums of that many terms leave it
+        assert float((got - o).norm() / o.norm()) < 1e-5
+        assert float((lse[b, 8 * h:8 * h + 8].double() - l).abs().max()) < 1e-5
+
+
+def test_records_beyond_4_gb():
+    """Pages whose bytes start behind 2^32."""
+    n, B, hq, hkv, T = 1_900_000, 1, 4, 1, 40
+    p = _params(B, hq, hkv, "bf16")
+    recs = torch.zeros((n, hkv, R), dtype=torch.uint8, device="cuda")
+    bt = torch.tensor([[n - 1, 5, n - 2]], dtype=torch.int32, device="cuda")
+    cache, err, r = ice.Cache4(recs, bt), _err(), ice.rows
+    _, q, k, v = _qkv(B, T, hq, hkv, "bf16", 131)
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    ice.ice_cache4_append(p, T, None, r(k), r(v), None, start, None, None, None, cache, err)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    ice.ice_cache4_read(p, T, cache, start, None, r(ko), r(vo), err)
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    Q = q[:, 0].contiguous()
+    ice.ice_cache4_attn_decode(p, Q, cache, start + T, 0.088, O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    hk, hv = ref.held(k[0, :, 0]), ref.held(v[0, :, 0])
+    assert torch.equal(ko[0, :, 0], hk.bfloat16()) and torch.equal(vo[0, :, 0], hv.bfloat16())
+    _check_attn(O, lse, Q, lambda b, h: (hk, hv), B, hkv, 0.088)
+    # the same records as a pool: unit 0 of one, page n - 1 selected
+    pl = torch.full((1, n), 16, dtype=torch.int32, device="cuda")
+    sel = torch.tensor([[5, n - 1]], dtype=torch.int32, device="cuda")
+    cnt = torch.full((1,), 2, dtype=torch.int32, device="cuda")
+    ice.ice_sparse_attn_decode4(_params(B, hq, hkv, "bf16", page_cap=n), Q, recs, pl, sel, cnt, None, None, 0.088, O,
+                                lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    order = list(range(16, 32)) + list(range(16))
+    _check_attn(O, lse, Q, lambda b, h: (hk[order], hv[order]), B, hkv, 0.088)
+
+
+def test_one_workspace_for_several_shapes_and_two_streams():
+    """One workspace for calls of different shapes, one after the other; two calls at once, a workspace each."""
+    shapes = [(1, 8, 8, [3000]), (40, 32, 8, [70] * 40), (1, 16, 1, [2000]), (3, 4, 1, [500, 0, 33])]
+    calls = []
+    for i, (B, hq, hkv, lens) in enumerate(shapes):
+        blocks = -(-max(lens) // S)
+        recs = _random_records(B * blocks, hkv, 141 + i)
+        bt = torch.arange(B * blocks, dtype=torch.int32, device="cuda").view(B, blocks)
+        Q = torch.randn((B, hq, D), generator=_gen(150 + i), device="cuda").bfloat16()
+        calls.append((_params(B, hq, hkv, "bf16"), Q, ice.Cache4(recs, bt),
+                      torch.tensor(lens, dtype=torch.int32, device="cuda"), B, hq))
+    ws = ice.workspace(max(ice.ice_attn4_workspace_bytes(c[0]) for c in calls))
+    err, want = _err(), []
+
+    def call(c, w, stream=None):
+        O = torch.empty((c[4], c[5], D), device="cuda")
+        ice.ice_cache4_attn_decode(c[0], c[1], c[2], c[3], 0.088, O, None, w, err, stream)
+        return O
+
+    for c in calls:
+        want.append(call(c, ice.workspace(ice.ice_attn4_workspace_bytes(c[0]))))
+    for _ in range(3):
+        for c, x in zip(calls, want):
+            assert torch.equal(call(c, ws), x)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    own = [ice.workspace(ws.numel()) for _ in streams]
+    torch.cuda.synchronize()
+    got = [[call(calls[(i + j) % 4], own[j], s) for j, s in enumerate(streams)] for i in range(8)]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for j in range(2):
+            assert torch.equal(got[i][j], want[(i + j) % 4])
+    assert ice.ice_check(err) == ice.ICE_OK
+
+
+def test_host_pool_in_4_bits():
+    """A pool in pinned host memory packed from there: the records of the same pool in device memory."""
+    kw = dict(batch=1, n_q_heads=8, n_kv_heads=2, n_tokens=600, seed=9)
+    K, V = (torch.randn((1, 2, 600, D), generator=_gen(s), device="cuda").bfloat16() for s in (1, 2))
+    cfg = ice.Config(**kw)
+    p, got, err = cfg.params(), [], _err()
+    hp = ice.HostPool(cfg, 64, n_threads=2)
+    try:
+        for pool in (None, hp):
+            idx = ice.Index(cfg, host_pool=pool)
+            ice.ice_build_index(p, K, V, idx, ice.workspace(ice.ice_build_workspace_bytes(p)), err)
+            recs = torch.zeros((2, cfg.page_cap, R), dtype=torch.uint8, device="cuda")
+            ice.ice_pool4_pack(p, idx, 0, recs, err)
+            assert ice.ice_check(err) == ice.ICE_OK
+            got.append((idx.n_pages.clone(), recs))
+    finally:
+        hp.close()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3.0])
+def test_attention_scales_and_values_that_are_not_numbers(scale):
+    p = _params(1, 8, 1, "bf16")
+    n = 100
+    recs = _random_records(7, 1, 161)
+    bt = torch.arange(7, dtype=torch.int32, device="cuda").view(1, 7)
+    Q = torch.randn((1, 8, D), generator=_gen(162), device="cuda").bfloat16()
+    O, lse, ws, err = _attn_buffers(1, 8, p)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), ln, scale, O, lse, ws, err)
+    K, V = _rows_of(recs, bt, 0)
+    sign = -1 if scale < 0 else 1
+    _check_attn(O, lse, sign * Q, lambda b, h: (K[b, h, :n], V[b, h, :n]), 1, 1, abs(scale))
+    # one value group that is not a number: its half of O; one key: the whole row of every head
+    recs[2, 0, 2176 + 8 * 5:2176 + 8 * 5 + 4] = 0xFF
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), ln, scale, O, lse, ws, err)
+    assert bool(O[..., :64].isnan().all()) and bool(O[..., 64:].isfinite().all())
+    recs[2, 0, 1024:1028] = 0xFF
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), ln, scale, O, lse, ws, err)
+    assert bool(O.isnan().all()) and bool(lse.isnan().all())
+    assert ice.ice_check(err) == ice.ICE_OK
