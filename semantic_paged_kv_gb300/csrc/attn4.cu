@@ -57,7 +57,7 @@ using namespace tc;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSlots = 4;          // pages of a warp's ring
+constexpr int kSlots = 3;          // pages of a warp's ring
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
 constexpr int kOver = 24;          // places that a unit takes beside its pages
@@ -94,9 +94,17 @@ struct UnitAt {
     __device__ __forceinline__ int end() const { return first + n; }
 };
 
-template <int HN> struct Smem {
+// What the CTA's threads share to prepare the queries of a unit.
+template <int NQ, int HN> struct QueryScratch {
+    uint2 f[NQ][HN][8][32];  // fragments by lane
+    float sum[8 * HN][2];
+    float big[kWarps];
+};
+
+template <int NQ, int HN> struct Smem {
     unsigned char ring[kWarps][kSlots][q4::kRecord];
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
+    QueryScratch<NQ, HN> q;
     float4 ml[kWarps][Shape<HN>::kHeads];  // maximum, sum, and each group's sum P mid
     int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
     unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
@@ -202,7 +210,7 @@ template <int HN> struct State {
 // The group's queries as B fragments (columns = heads), in fp16 after a common
 // power of two, and what the scores need of them.
 template <int NQ, int HN> struct Queries {
-    uint32_t f[NQ][HN][8][2];
+    uint32_t f;           // shared address of this lane's fragments (QueryScratch::f)
     float sum[HN][2][2];  // sum q over a group, in the products' scale, for this lane's columns (heads 2 c, 2 c + 1)
     float factor;         // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
 };
@@ -210,13 +218,6 @@ template <int NQ, int HN> struct Queries {
 // Codes of K as operands: c 2^-24 (kLow; kHigh times 16, and its queries over 16), or with fp32 queries centred() ones,
 // whose products keep the bits that those queries have.
 template <int NQ> constexpr int kCodeScale = NQ > 1 ? 10 : 24;
-
-// What the CTA's threads share to prepare the queries of a unit.
-template <int NQ, int HN> struct QueryScratch {
-    uint2 f[NQ][HN][8][32];  // fragments by lane
-    float sum[8 * HN][2];
-    float big[kWarps];
-};
 
 // This thread's 8 elements of the group's queries: head tid / 16, elements 8 (tid % 16) ...
 template <typename T>
@@ -274,21 +275,14 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
         }
     }
     __syncthreads();
+    q.f = su32(&X.f[0][0][0][lane]);
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint2 v = X.f[n][hn][k][lane];
-                q.f[n][hn][k][0] = v.x, q.f[n][hn][k][1] = v.y;
-            }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-kCodeScale<NQ>);
     }
-    __syncthreads();  // the scratch lies where the results go
 }
 
 // Folds one page (record at shared address `rec`, its first `len` slots; whatever the others hold).
@@ -316,10 +310,11 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         float(&d)[4] = acc[hn][i >> 1];
+                        const uint2 f = lds64(q.f + ((n * HN + hn) * 8 + 2 * i + k) * 256);
                         if ((i & 1) | k | n)
-                            mma_add(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1]);
+                            mma_add(d, a, f.x, f.y);
                         else
-                            mma_first(d, a, q.f[n][hn][2 * i + k][0], q.f[n][hn][2 * i + k][1]);
+                            mma_first(d, a, f.x, f.y);
                     }
             }
         const float2 g00 = q4::unpack_meta(m0.x), g01 = q4::unpack_meta(m0.y);  // token r
@@ -497,7 +492,7 @@ __device__ __forceinline__ void put_row(const Attn4Args &A, size_t row, float4 a
 template <typename T, int NQ, int HN>
 __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __grid_constant__ Attn4Args A) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    Smem<HN> &S = *reinterpret_cast<Smem<HN> *>(smem_raw);
+    Smem<NQ, HN> &S = *reinterpret_cast<Smem<NQ, HN> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = A.g;
     dep_wait();
@@ -580,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
     if (lane == 0) S.look[warp] = unit;
     const uint32_t ring = su32(S.ring[warp][0]);
     auto issue = [&](int n) {  // the copy of place n: one group a place, also where there is no page
-        copy_record(ring + (n & (kSlots - 1)) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
+        copy_record(ring + (n % kSlots) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
     };
     int looked = 0, issued = 0;  // places looked up, and those whose copy was started
     auto look_further = [&]() {
@@ -652,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 if (issued >= looked) look_further();
                 issue(issued);
             }
-        prepare_queries<T, NQ, HN>(qpart, A.scale, *reinterpret_cast<QueryScratch<NQ, HN> *>(&S.o[0][0][0]), q);
+        prepare_queries<T, NQ, HN>(qpart, A.scale, S.q, q);
         for (bool flushed = false; n < n_end; flushed = true) {
             const int until = min(n_end, n + kFlush);
             while (n < until) {
@@ -663,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
                     __syncwarp();
                     issue(n + kSlots - 1);
-                    attend_page4<NQ, HN>(q, ring + (n & (kSlots - 1)) * q4::kRecord,
+                    attend_page4<NQ, HN>(q, ring + (n % kSlots) * q4::kRecord,
                                          (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
                 }
             }
@@ -879,21 +874,20 @@ Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
 }
 
 static_assert(kWarps * (2 * kMaxRuns + kHeadDim) <= kWarps * 8 * kRow, "the joining weights and sums lie in Smem::o");
-static_assert(sizeof(QueryScratch<2, 1>) <= sizeof(Smem<1>::o) && sizeof(QueryScratch<2, 2>) <= sizeof(Smem<2>::o),
-              "the queries' scratch lies in Smem::o");
-static_assert(2 * (sizeof(Smem<1>) + 1024) <= 227 * 1024, "two CTAs an SM");
+static_assert(2 * (sizeof(Smem<2, 1>) + 1024) <= 227 * 1024 && sizeof(Smem<2, 2>) <= 227 * 1024 - 1024,
+              "two CTAs an SM, one with more than 8 heads a group");
 
 template <typename T, int NQ, int HN>
 cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     auto kern = k_attn4<T, NQ, HN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<HN>));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<NQ, HN>));
     if (e != cudaSuccess) return e;
     // every CTA resident at once (no CTA waits for another, but equal runs should start together)
     const long long most = (long long)A.units * ((A.pool ? A.max_sel : 0) + (long long)(A.cache ? A.max_pages : 0));
     const long long runs = (most + (long long)A.units * kOver + kMinRun - 1) / kMinRun;
     const int ctas = Shape<HN>::kCtas * sms < max_ctas(sms) ? Shape<HN>::kCtas * sms : max_ctas(sms);
     const int grid = (int)(runs < ctas ? (runs > 0 ? runs : 1) : ctas);
-    return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<HN>), s, A);
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<NQ, HN>), s, A);
 }
 
 }  // namespace
