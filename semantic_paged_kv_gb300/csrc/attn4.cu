@@ -14,8 +14,8 @@
 // than it has (what starting and ending one costs), so that many short units
 // do not gather in few CTAs.  A unit that a run cuts leaves partial results in
 // the workspace, joined by its last CTA in run order (so the bits do not
-// depend on timing).  Inside a CTA place f of the run goes to warp f % 8, slot f
-// / 8 % 4 of its ring; a warp looks up its pages 32 at a time, one a lane, well
+// depend on timing).  Inside a CTA place f of the run goes to warp f % 8; a
+// warp looks up its pages 32 at a time, one a lane, well
 // before their copies start, so that its loop over pages does little else than
 // attend.
 //
@@ -55,16 +55,14 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSlots = 3;          // pages of a warp's ring
+constexpr int kSlots = 2;          // pages of a warp's ring: one attended, one on its way
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
 constexpr int kOver = 24;          // places that a unit takes beside its pages
-constexpr int kUnits = 192;        // units whose page counts a CTA keeps at hand
+constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
-constexpr int kMinRun = kWarps;    // places of a run, at least: one page per warp
+constexpr int kMinRun = 8;    // places of a run, at least: one page per warp
 
 struct Attn4Args {
     const void *Q;
@@ -83,7 +81,9 @@ struct Attn4Args {
 
 template <int HN> struct Shape {
     static constexpr int kHeads = 8 * HN;
-    static constexpr int kCtas = HN == 1 ? 2 : 1;  // per SM
+    static constexpr int kCtas = HN == 1 ? 2 : 1;    // per SM
+    static constexpr int kWarps = 8;
+    static constexpr int kThreads = 32 * kWarps;
 };
 
 // A unit of a run: index i from u0, first page at place `first` (from the run's start), n pages.
@@ -98,10 +98,11 @@ struct UnitAt {
 template <int NQ, int HN> struct QueryScratch {
     uint2 f[NQ][HN][8][32];  // fragments by lane
     float sum[8 * HN][2];
-    float big[kWarps];
+    float big[Shape<HN>::kWarps];
 };
 
 template <int NQ, int HN> struct Smem {
+    static constexpr int kWarps = Shape<HN>::kWarps;
     unsigned char ring[kWarps][kSlots][q4::kRecord];
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
     QueryScratch<NQ, HN> q;
@@ -249,7 +250,7 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
     if (lane == 0) X.big[warp] = big;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) big = fmaxf(big, X.big[w]);
+    for (int w = 0; w < Shape<HN>::kWarps; ++w) big = fmaxf(big, X.big[w]);
     const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
     const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
     q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(kCodeScale<NQ>) * pow2(-e2);
@@ -490,7 +491,9 @@ __device__ __forceinline__ void put_row(const Attn4Args &A, size_t row, float4 a
 }
 
 template <typename T, int NQ, int HN>
-__global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __grid_constant__ Attn4Args A) {
+__global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
+    k_attn4(const __grid_constant__ Attn4Args A) {
+    constexpr int kWarps = Shape<HN>::kWarps, kThreads = Shape<HN>::kThreads;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem<NQ, HN> &S = *reinterpret_cast<Smem<NQ, HN> *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -639,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
         const int u = u0 + unit.i, b = unit.b;
         const size_t row0 = (size_t)b * A.hq + (size_t)(u - b * A.hkv) * g;
         st.init();
-        int n = (pa + ((warp - pa) & (kWarps - 1))) / kWarps;
+        int n = pa > warp ? (pa - warp + kWarps - 1) / kWarps : 0;
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
         const bool any = n < n_end;
         if (any)
@@ -756,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
             __syncthreads();
             if (S.last) {
                 __threadfence();
-                // a head's runs go to 1, 2, 4 or 8 warps, whose sums meet in shared memory
-                const int runs = cb - ca + 1, split = g == 1 ? 8 : (g == 2 ? 4 : (g <= 4 ? 2 : 1));
+                // a head's runs go to as many warps as there are for it, whose sums meet in shared memory
+                const int runs = cb - ca + 1, split = g >= kWarps ? 1 : kWarps / g;
                 float2 *wt = reinterpret_cast<float2 *>(&S.o[0][0][0]) + warp * kMaxRuns;  // of this warp's head
                 float *sums = reinterpret_cast<float *>(&S.o[0][0][0]) + 2 * kWarps * kMaxRuns;
                 const float2 *ml = reinterpret_cast<const float2 *>(A.part_ml) + (size_t)ca * 2 * g;
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, Shape<HN>::kCtas) k_attn4(const __gr
                 const int skip = us > (long long)ca * share ? g : 0;
                 float M, L;
                 float4 acc;
-                for (int hh = warp / split; hh < g; hh += kWarps / split) {
+                for (int hh = warp / split; hh < g; hh += split == 1 ? kWarps : g) {
                     // the first rows are on their way while the weights are found
                     constexpr int kAhead = 8;
                     const int k0 = warp % split;
@@ -873,7 +876,7 @@ Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
     return w;
 }
 
-static_assert(kWarps * (2 * kMaxRuns + kHeadDim) <= kWarps * 8 * kRow, "the joining weights and sums lie in Smem::o");
+static_assert(2 * kMaxRuns + kHeadDim <= 8 * kRow, "the joining weights and sums (a part a warp) lie in Smem::o");
 static_assert(2 * (sizeof(Smem<2, 1>) + 1024) <= 227 * 1024 && sizeof(Smem<2, 2>) <= 227 * 1024 - 1024,
               "two CTAs an SM, one with more than 8 heads a group");
 
@@ -887,7 +890,7 @@ cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
     const long long runs = (most + (long long)A.units * kOver + kMinRun - 1) / kMinRun;
     const int ctas = Shape<HN>::kCtas * sms < max_ctas(sms) ? Shape<HN>::kCtas * sms : max_ctas(sms);
     const int grid = (int)(runs < ctas ? (runs > 0 ? runs : 1) : ctas);
-    return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem<NQ, HN>), s, A);
+    return launch_dependent(kern, dim3(grid), dim3(Shape<HN>::kThreads), sizeof(Smem<NQ, HN>), s, A);
 }
 
 }  // namespace
