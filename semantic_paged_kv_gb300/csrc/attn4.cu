@@ -34,7 +34,10 @@
 //   O^T += V^T (step P)^T: V codes as operands the same way (the record pairs
 //     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
 //     by a power of two that follows the largest step; the 8 x 8 transposes of
-//     P by movmatrix.  The codes go in centred and as normal numbers, (code -
+//     P by movmatrix.  A product blocks the scheduler for 8 clocks (24 of them
+//     are 43% of the measured 111 clocks a page and SM with g = 8 and no copy),
+//     so with g <= 4 the columns 4 .. 7 hold heads 0 .. 3 again and take the lo
+//     parts: one product a tile instead of two.  The codes go in centred and as normal numbers, (code -
 //     7.5) 2^-10: a mean over many values cancels down to the noise of its
 //     sums, and the tensor core aligns subnormal operands by their nominal
 //     exponent, which costs six of its bits (relative error of O: 1e-5 with
@@ -220,12 +223,14 @@ template <int NQ, int HN> struct Queries {
 // whose products keep the bits that those queries have.
 template <int NQ> constexpr int kCodeScale = NQ > 1 ? 10 : 24;
 
-// This thread's 8 elements of the group's queries: head tid / 16, elements 8 (tid % 16) ...
-template <typename T>
+// This thread's 8 elements of the group's queries: head tid / 16 (kTwice: heads 4 .. 7 are heads 0 .. 3 again),
+// elements 8 (tid % 16) ...
+template <typename T, bool kTwice>
 __device__ __forceinline__ q4::Vec8<T> query_part(const T *Qg, int g) {
     q4::Vec8<T> v;
     v.zero();
-    if ((int)threadIdx.x < g * (kHeadDim / 8)) v.load(Qg + threadIdx.x * 8);
+    const int head = kTwice ? (threadIdx.x >> 4) & 3 : threadIdx.x >> 4;
+    if (head < g) v.load(Qg + head * kHeadDim + (threadIdx.x & 15) * 8);
     return v;
 }
 
@@ -287,7 +292,7 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
 }
 
 // Folds one page (record at shared address `rec`, its first `len` slots; whatever the others hold).
-template <int NQ, int HN>
+template <int NQ, int HN, bool kTwice>
 __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t rec, int len, State<HN> &st) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     // ---- S^T = K Q^T, an accumulator per group
@@ -421,10 +426,16 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
             const __half2 h0 = __floats2half2_rn(x0.x, x1.x), h1 = __floats2half2_rn(x0.y, x1.y);
             const float2 w0 = __half22float2(h0), w1 = __half22float2(h1);
             const float2 d0 = upk2(sub2(x[0], pk2(w0.x, w1.x))), d1 = upk2(sub2(x[1], pk2(w0.y, w1.y)));
-            bh[hn][0][half] = transpose8(h2_bits(h0));
-            bh[hn][1][half] = transpose8(h2_bits(h1));
-            bl[hn][0][half] = transpose8(h2_bits(__floats2half2_rn(d0.x, d1.x)));
-            bl[hn][1][half] = transpose8(h2_bits(__floats2half2_rn(d0.y, d1.y)));
+            const uint32_t l0 = h2_bits(__floats2half2_rn(d0.x, d1.x)), l1 = h2_bits(__floats2half2_rn(d0.y, d1.y));
+            if (kTwice) {  // columns 0 .. 3: the hi parts, columns 4 .. 7, of the same heads: the lo parts
+                bh[hn][0][half] = transpose8(c < 2 ? h2_bits(h0) : l0);
+                bh[hn][1][half] = transpose8(c < 2 ? h2_bits(h1) : l1);
+            } else {
+                bh[hn][0][half] = transpose8(h2_bits(h0));
+                bh[hn][1][half] = transpose8(h2_bits(h1));
+                bl[hn][0][half] = transpose8(l0);
+                bl[hn][1][half] = transpose8(l1);
+            }
         }
     // ---- O^T += V^T (step P)^T
     {
@@ -441,7 +452,7 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
                 for (int hn = 0; hn < HN; ++hn) {
                     float(&o)[4] = st.o[hn][2 * j + k];
                     mma_add(o, a, bh[hn][j >> 1][0], bh[hn][j >> 1][1]);
-                    mma_add(o, a, bl[hn][j >> 1][0], bl[hn][j >> 1][1]);
+                    if (!kTwice) mma_add(o, a, bl[hn][j >> 1][0], bl[hn][j >> 1][1]);
                 }
             }
     }
@@ -490,7 +501,7 @@ __device__ __forceinline__ void put_row(const Attn4Args &A, size_t row, float4 a
     if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-template <typename T, int NQ, int HN>
+template <typename T, int NQ, int HN, bool kTwice>
 __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     k_attn4(const __grid_constant__ Attn4Args A) {
     constexpr int kWarps = Shape<HN>::kWarps, kThreads = Shape<HN>::kThreads;
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     UnitAt unit = unit_at(0, (int)(S.start0 - f0));
     auto queries_of = [&](const UnitAt &x) {
         const int u = u0 + x.i;
-        return query_part<T>(static_cast<const T *>(A.Q) + ((size_t)x.b * A.hq + (size_t)(u - x.b * A.hkv) * g) * kHeadDim, g);
+        return query_part<T, kTwice>(static_cast<const T *>(A.Q) + ((size_t)x.b * A.hq + (size_t)(u - x.b * A.hkv) * g) * kHeadDim, g);
     };
     q4::Vec8<T> qpart = queries_of(unit);  // in flight during the lookups
 
@@ -661,7 +672,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
                     __syncwarp();
                     issue(n + kSlots - 1);
-                    attend_page4<NQ, HN>(q, ring + (n % kSlots) * q4::kRecord,
+                    attend_page4<NQ, HN, kTwice>(q, ring + (n % kSlots) * q4::kRecord,
                                          (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
                 }
             }
@@ -734,7 +745,11 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                 const float4 ml = S.ml[w][hh];
                 if (ml.y == 0.f) continue;  // no page
                 const float wt = ml.y == ml.y ? exp2_fast(ml.x - M) : ml.y;  // a sum that is not a number spreads
-                const float4 x = *reinterpret_cast<const float4 *>(&S.o[w][hh][4 * lane]);
+                float4 x = *reinterpret_cast<const float4 *>(&S.o[w][hh][4 * lane]);
+                if (kTwice) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&S.o[w][hh + 4][4 * lane]);
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
                 const float off = lane < 16 ? ml.z : ml.w;
                 L = fmaf(ml.y, wt, L);
                 acc.x = fmaf(x.x + off, wt, acc.x), acc.y = fmaf(x.y + off, wt, acc.y);
@@ -880,9 +895,9 @@ static_assert(2 * kMaxRuns + kHeadDim <= 8 * kRow, "the joining weights and sums
 static_assert(2 * (sizeof(Smem<2, 1>) + 1024) <= 227 * 1024 && sizeof(Smem<2, 2>) <= 227 * 1024 - 1024,
               "two CTAs an SM, one with more than 8 heads a group");
 
-template <typename T, int NQ, int HN>
+template <typename T, int NQ, int HN, bool kTwice>
 cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
-    auto kern = k_attn4<T, NQ, HN>;
+    auto kern = k_attn4<T, NQ, HN, kTwice>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<NQ, HN>));
     if (e != cudaSuccess) return e;
     // every CTA resident at once (no CTA waits for another, but equal runs should start together)
@@ -918,8 +933,12 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
     const Attn4Ws w = ws_layout(p, sms, ws);
     A.ticket = w.ticket, A.part_ml = w.part_ml, A.part_o = w.part_o;
     if (p.dtype == ICE_BF16)
-        return A.g <= 8 ? launch_t<__nv_bfloat16, 1, 1>(A, sms, s) : launch_t<__nv_bfloat16, 1, 2>(A, sms, s);
-    return A.g <= 8 ? launch_t<float, 2, 1>(A, sms, s) : launch_t<float, 2, 2>(A, sms, s);
+        return A.g <= 4   ? launch_t<__nv_bfloat16, 1, 1, true>(A, sms, s)
+               : A.g <= 8 ? launch_t<__nv_bfloat16, 1, 1, false>(A, sms, s)
+                          : launch_t<__nv_bfloat16, 1, 2, false>(A, sms, s);
+    return A.g <= 4   ? launch_t<float, 2, 1, true>(A, sms, s)
+           : A.g <= 8 ? launch_t<float, 2, 1, false>(A, sms, s)
+                      : launch_t<float, 2, 2, false>(A, sms, s);
 }
 
 }  // namespace ice
