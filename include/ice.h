@@ -511,7 +511,7 @@ ice_status ice_decode_plan(const ice_params *p, int32_t budget_tokens, int32_t m
  */
 typedef struct ice_rows {
     void *data;
-    int64_t batch, token, head; /* strides in elements, >= 0 */
+    int64_t batch, token, head; /* strides in elements, >= 0; below d only in inputs */
 } ice_rows;
 
 /*

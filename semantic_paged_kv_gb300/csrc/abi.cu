@@ -683,12 +683,23 @@ static ice_status check_rows(const ice_params *p, const ice_rows *r, const char 
     return ICE_OK;
 }
 
+// A view that is written: its rows must not lie on one another.
+static ice_status check_rows_out(const ice_params *p, int32_t n_new, int32_t heads, const ice_rows *r,
+                                 const char *what) {
+    ice_status st = check_rows(p, r, what);
+    if (st) return st;
+    const int64_t d = p->head_dim;
+    if ((r->batch < d && p->batch > 1) || (r->token < d && n_new > 1) || (r->head < d && heads > 1))
+        return fail(ICE_ERR_INVALID_ARG, "%s: a stride below d puts rows that are written on one another", what);
+    return ICE_OK;
+}
+
 // Input and output views go together (both or neither).
-static ice_status check_rows_pair(const ice_params *p, const ice_rows *in, const ice_rows *out, const char *what,
-                                  const char *what_out) {
+static ice_status check_rows_pair(const ice_params *p, int32_t n_new, int32_t heads, const ice_rows *in,
+                                  const ice_rows *out, const char *what, const char *what_out) {
     if (!in && !out) return ICE_OK;
     ice_status st = check_rows(p, in, what);
-    return st ? st : check_rows(p, out, what_out);
+    return st ? st : check_rows_out(p, n_new, heads, out, what_out);
 }
 
 static ice_status check_rope(const ice_rope *r) {
@@ -744,8 +755,9 @@ ice_status ice_qkv_rope(const ice_params *p, int32_t n_new, const ice_rows *q, c
     ice_status st = check_params(p);
     if (st) return st;
     if ((st = check_new(p, n_new))) return st;
-    if ((st = check_rows_pair(p, q, q_out, "q", "q_out")) || (st = check_rows_pair(p, k, k_out, "k", "k_out")) ||
-        (st = check_rows_pair(p, v, v_out, "v", "v_out")) || (st = check_rope(rope)))
+    if ((st = check_rows_pair(p, n_new, p->n_q_heads, q, q_out, "q", "q_out")) ||
+        (st = check_rows_pair(p, n_new, p->n_kv_heads, k, k_out, "k", "k_out")) ||
+        (st = check_rows_pair(p, n_new, p->n_kv_heads, v, v_out, "v", "v_out")) || (st = check_rope(rope)))
         return st;
     if (n_new == 0) return ICE_OK;
     return cuda_status(launch_qkv_rope(*p, n_new, q, k, v, positions, start, counts, rope, q_out, k_out, v_out,
@@ -760,7 +772,7 @@ ice_status ice_cache4_append(const ice_params *p, int32_t n_new, const ice_rows 
     ice_status st = check_params(p);
     if (st) return st;
     if ((st = check_new(p, n_new))) return st;
-    if ((st = check_rows_pair(p, q, q_out, "q", "q_out")) || (st = check_rows(p, k, "k")) ||
+    if ((st = check_rows_pair(p, n_new, p->n_q_heads, q, q_out, "q", "q_out")) || (st = check_rows(p, k, "k")) ||
         (st = check_rows(p, v, "v")) || (st = check_rope(rope)) || (st = check_cache4(cache)))
         return st;
     if (!start) return fail(ICE_ERR_INVALID_ARG, "start is NULL");
@@ -776,7 +788,8 @@ ice_status ice_cache4_read(const ice_params *p, int32_t n_new, const ice_cache4 
     ice_status st = check_params(p);
     if (st) return st;
     if ((st = check_new(p, n_new))) return st;
-    if ((st = check_cache4(cache)) || (st = check_rows(p, k_out, "k_out")) || (st = check_rows(p, v_out, "v_out")))
+    if ((st = check_cache4(cache)) || (st = check_rows_out(p, n_new, p->n_kv_heads, k_out, "k_out")) ||
+        (st = check_rows_out(p, n_new, p->n_kv_heads, v_out, "v_out")))
         return st;
     if (!start) return fail(ICE_ERR_INVALID_ARG, "start is NULL");
     if (n_new == 0) return ICE_OK;

@@ -797,6 +797,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
 #pragma unroll
                     for (int i = 0; i < kAhead; ++i) y[i] = row_of(k0 + i * split);
                     M = -FLT_MAX, L = 0.f;
+                    __syncwarp();  // the weights of the head before have been read
                     for (int k = lane; k < runs; k += 32) {
                         const float2 x = __ldcg(ml + 2 * k * g + (k ? 0 : skip) + hh);
                         M = fmaxf(M, x.x);

@@ -109,6 +109,8 @@ CASES = [
     ("rope: misaligned data", lambda: _qkv(ko=_rows(data=A + 8)), INV, "k_out must be"),
     ("rope: stride of 8 bytes", lambda: _qkv(q=_rows(token=132)), INV, "q: strides"),
     ("rope: negative stride", lambda: _qkv(q=_rows(head=-128)), INV, "q: strides"),
+    ("rope: output rows on one another", lambda: _qkv(ko=_rows(head=0)), INV, "k_out: a stride below d"),
+    ("read: output rows on one another", lambda: _read(vo=_rows(token=64)), INV, "v_out: a stride below d"),
     ("rope: rotary_dim too large", lambda: _qkv(rope=_rope(rotary_dim=144)), UNS, "rotary_dim"),
     ("rope: rotary_dim 0", lambda: _qkv(rope=_rope(rotary_dim=0)), UNS, "rotary_dim"),
     ("rope: interleaved 2", lambda: _qkv(rope=_rope(interleaved=2)), INV, "interleaved"),
@@ -162,6 +164,7 @@ def test_refusal(call, status, message):
 
 
 def test_nothing_to_do_is_ok():
+    assert _qkv(n=0, q=_rows(token=0), qo=_rows(token=0)) == ice.ICE_OK  # no second token to lie on the first
     assert _qkv(n=0) == ice.ICE_OK and _append(n=0) == ice.ICE_OK and _read(n=0) == ice.ICE_OK
     assert _qkv(q=None, qo=None, k=None, ko=None, v=None, vo=None) == ice.ICE_OK
 
