@@ -852,18 +852,6 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     }
 }
 
-// SMs of the current device (asked of the driver once a device).
-int device_sms() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    n = n > 0 ? n : 1;
-    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 int max_ctas(int sms) { return 2 * sms < kMaxRuns ? 2 * sms : kMaxRuns; }
 
 // The partial results lie before the tickets, at sizes that no shape changes:
@@ -910,6 +898,18 @@ cudaError_t launch_t(const Attn4Args &A, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+// SMs of the current device (asked of the driver once a device).
+int device_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    n = n > 0 ? n : 1;
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 size_t attn4_workspace(const ice_params &p) { return ws_layout(p, device_sms(), nullptr).bytes; }
 

@@ -206,6 +206,7 @@ cudaError_t launch_cache4_read(const ice_params &p, int n_new, const ice_cache4 
 cudaError_t launch_pool4_pack(const ice_params &p, const ice_index &idx, int first_token, void *records, int32_t *err,
                               cudaStream_t s);
 cudaError_t launch_pool4_unpack(const ice_params &p, const ice_index &idx, const void *records, cudaStream_t s);
+int device_sms();  // of the current device
 size_t attn4_workspace(const ice_params &p);
 // records NULL: no selected pages; cache NULL: no token-ordered pages.
 cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records, const int32_t *page_len,

@@ -15,10 +15,15 @@
 // both elements of a pair are in one lane and nothing is exchanged but the
 // norm's sum.  k_qkv_rope: 8 lanes take four heads of one token, whose cos and
 // sin stay in registers; all loads are issued before the arithmetic.
-// k_cache4_append: its first CTAs take the queries that way; then one warp per
+// k_cache4_append: CTAs of the queries work that way; in the others a warp per
 // block of 16 cache slots and KV head quantises up to 16 rows, four at a time,
 // into a record in shared memory, and writes the record (all 16 slots new) or
-// only the new tokens' bytes of it.
+// only the new tokens' bytes of it; with few blocks a warp takes four slots.  The quantising CTAs are bound by their
+// instructions, those of the queries by HBM, so both kinds run side by side:
+// the former lie evenly among the first three quarters of the grid, and what
+// is left at the end is short.  Appending 4 x 4099 tokens of 32/8 heads: 48.8
+// us (5.9 TB/s); spread over the whole grid 52.9, queries first 54.8, K and V
+// first 53.2.
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
@@ -280,17 +285,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : (kNorm ? 5 : 6)
 
 template <typename T, int kLayout, bool kNorm>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : (kNorm ? 5 : 6)) k_cache4_append(
-    const __grid_constant__ RopeArgs A, unsigned q_items, int q_blocks, unsigned n_items, int blocks,
-    unsigned char *__restrict__ records, const int32_t *__restrict__ table, int n_pages, int max_pages) {
+    const __grid_constant__ RopeArgs A, unsigned q_items, unsigned spread, unsigned kv_blocks, unsigned n_items, int blocks,
+    bool split, unsigned char *__restrict__ records, const int32_t *__restrict__ table, int n_pages, int max_pages) {
     __shared__ __align__(16) unsigned char s_rec[kThreads / 32][q4::kRecord];
     dep_wait();
-    if ((int)blockIdx.x < q_blocks) {  // the queries
-        dense_chunk<T, kLayout, kNorm, kQ>(A, blockIdx.x * kGroups + threadIdx.x / 8, q_items);
+    const unsigned kv = spread ? min(__umulhi(blockIdx.x, spread), kv_blocks) : blockIdx.x;  // K and V CTAs before this one
+    if (spread && min(__umulhi(blockIdx.x + 1, spread), kv_blocks) == kv) {  // the queries
+        dense_chunk<T, kLayout, kNorm, kQ>(A, (blockIdx.x - kv) * kGroups + threadIdx.x / 8, q_items);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 3, l = lane & 7;
-    const unsigned item = (blockIdx.x - q_blocks) * (kThreads / 32) + warp;
+    unsigned item = kv * (kThreads / 32) + warp;
     if (item >= n_items) return;
+    const int part = split ? (int)(item & 3u) : 0;  // four of the block's slots, when it is split
+    if (split) item >>= 2;
     const int h = (int)(item % A.hkv);
     const int x = (int)(item / A.hkv % blocks);
     const int b = (int)(item / A.hkv / blocks);
@@ -298,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : (kNorm ? 5 : 6)
     const int cnt = count_of(A, b);
     const long long blk = (s0 >> 4) + x;  // block of 16 cache slots (floor also for a negative start)
     const long long t0 = blk * kPage;
-    const long long ta = t0 > s0 ? t0 : s0, tb = t0 + kPage < s0 + cnt ? t0 + kPage : s0 + cnt;
+    const long long p0 = t0 + 4 * part, p1 = split ? p0 + 4 : t0 + kPage;
+    const long long ta = p0 > s0 ? p0 : s0, tb = p1 < s0 + cnt ? p1 : s0 + cnt;
     if (ta >= tb) return;
     int pg = -1;
     if (blk >= 0 && blk < max_pages) pg = table[(size_t)b * max_pages + blk];
@@ -469,15 +478,25 @@ cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows 
                                  const ice_cache4 &cache, int32_t *err, cudaStream_t s) {
     RopeArgs A = rope_args(p, n_new, q, k, v, positions, start, counts, rope, q_out, nullptr, nullptr, err);
     const unsigned q_items = (unsigned)(q ? (long long)p.batch * n_new * ceil_div(p.n_q_heads, kHeads) : 0);
-    const int q_blocks = ceil_div(q_items, kGroups);
+    const unsigned q_blocks = (unsigned)ceil_div(q_items, kGroups);
     const int blocks = cache4_blocks(n_new);
-    const unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
-    const dim3 grid((unsigned)(q_blocks + ceil_div(items, kThreads / 32)));
+    unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
+    // Few blocks leave most of an SM's warps empty while each works on its 16 rows: a warp then takes four of them.  In
+    // bf16 1 x 128 tokens of 8 heads take 3.4 us so, 6.3 with whole blocks; 4 x 1200 (16 blocks an SM) 14.6 and 15.3, 8 x
+    // 1200 31 and 28.  fp32: 1 x 128 4.3 and 9.5, 2 x 1200 (8 an SM) 21.3 and 21.4, 4 x 1200 41 and 37.
+    const bool split = n_new > 4 && (long long)items <= (p.dtype == ICE_BF16 ? 16 : 8) * device_sms();
+    if (split) items *= 4;
+    const unsigned kv_blocks = (unsigned)ceil_div(items, kThreads / 32), n = q_blocks + kv_blocks;
+    // min(floor(i spread / 2^32), kv_blocks) CTAs of K and V come before CTA i: none before CTA 0, one more after at
+    // most every CTA (spread < 2^32), all of them before CTA `over` <= n
+    const unsigned over = max(kv_blocks + 1, n / 4 * 3);
+    const unsigned spread = q_blocks ? (unsigned)(((unsigned long long)kv_blocks << 32) / over + 1) : 0u;
+    const dim3 grid(n);
     unsigned char *r = static_cast<unsigned char *>(cache.records);
     auto kern = pick(p, A, k_cache4_append<__nv_bfloat16, kHalves, false>, k_cache4_append<__nv_bfloat16, kHalves, true>,
                      k_cache4_append<__nv_bfloat16, kAny, true>, k_cache4_append<float, kAny, true>);
-    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, q_items, q_blocks, items, blocks, r, cache.table,
-                            cache.n_pages, cache.max_pages);
+    return launch_dependent(kern, grid, dim3(kThreads), 0, s, A, q_items, spread, kv_blocks, items, blocks, split, r,
+                            cache.table, cache.n_pages, cache.max_pages);
 }
 
 }  // namespace ice

@@ -208,6 +208,30 @@ def test_append_and_read(B, T, hq, hkv, dtype, rd, inter, norm, starts):
             assert torch.equal(o[b, :, :n], y[b, :, a:a + n].float().to(DT[dtype])) and bool((o[b, :, n:] == 7).all())
 
 
+@pytest.mark.parametrize("dtype,norm", [("bf16", False), ("bf16", True), ("fp32", False)])
+def test_append_many_blocks(dtype, norm):
+    """A call of many blocks (a warp each) writes the bytes that calls of few tokens (a warp per four slots) write, and
+    the same queries."""
+    B, T, hq, hkv, part = 6, 1291, 8, 8, 101  # 6 * 8 * 82 = 3936 blocks: more than 16 an SM
+    p = _params(B, hq, hkv, dtype)
+    _, q, k, v = _qkv(B, T, hq, hkv, dtype, 61)
+    w = (1 + 0.3 * torch.randn(D, generator=_gen(3), device="cuda")).to(DT[dtype])
+    rope = ice.Rope(_table(128, 1400)[1], q_norm=w if norm else None, k_norm=w if norm else None)
+    start = torch.tensor([0, 15, 1, 16, 7, 90], dtype=torch.int32, device="cuda")
+    counts = torch.tensor([T, T - 300, 0, 5, T, T - 1], dtype=torch.int32, device="cuda")
+    recs, bt = _cache(B, (90 + T) // S + 2, hkv, 62)
+    recs2, err, r = recs.clone(), _err(), ice.rows
+    qo, qo2 = (torch.full((B, T, hq, D), 7.0, dtype=DT[dtype], device="cuda") for _ in range(2))
+    ice.ice_cache4_append(p, T, r(q), r(k), r(v), None, start, counts, rope, r(qo), ice.Cache4(recs, bt), err)
+    for a in range(0, T, part):
+        n = min(part, T - a)
+        x = [t[:, a:a + n] for t in (q, k, v, qo2)]
+        ice.ice_cache4_append(p, n, *map(r, x[:3]), None, start + a, (counts - a).clamp(0, n), rope, r(x[3]),
+                              ice.Cache4(recs2, bt), err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    assert torch.equal(recs, recs2) and torch.equal(qo, qo2)
+
+
 def test_append_refuses_on_the_device():
     """Cache positions, pages and rotation positions outside their ranges: those tokens are left out."""
     B, T, hq, hkv = 3, 20, 4, 2
