@@ -5,9 +5,16 @@
 // papernotes.org "IceCache: Memory-Efficient KV-cache Management for
 // Long-Sequence LLMs", 关键设计 1, over the unit's pages only.
 //
-// Bound by HBM (a page of 16 tokens of one KV head is one 2304-byte record,
-// read once), and next to that by instruction issue: at the measured copy rate
-// an SM gets a page every ~100 clocks.
+// A page of 16 tokens of one KV head is one 2304-byte record, read once; at the
+// measured copy rate an SM could get one every ~98 clocks.  Long caches are
+// bound by that and by instruction issue in about equal parts: the same loop
+// over pages without their copies takes 111 clocks a page and SM (250 instructions
+// on four schedulers, 62 clocks, and 24 products that block one for 8 clocks
+// each, 48), the copies alone take 305 us where the whole takes 369 us (16 sequences x 100k tokens, 64/8 heads: 1.84 GB
+// at 5.0 TB/s, 74% of the copy rate; 4 heads a group 347 us).  Short ones are
+// bound by a chain of latencies (1 sequence x 16k tokens, 32/8 heads: 13.4 us):
+// counts of the units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the
+// run's other pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
 //
 // Work: the pages of all units, one after another, are cut into equal runs,
 // one per CTA, whatever the units' lengths; a unit counts kOver pages more
@@ -15,9 +22,8 @@
 // do not gather in few CTAs.  A unit that a run cuts leaves partial results in
 // the workspace, joined by its last CTA in run order (so the bits do not
 // depend on timing).  Inside a CTA place f of the run goes to warp f % 8; a
-// warp looks up its pages 32 at a time, one a lane, well
-// before their copies start, so that its loop over pages does little else than
-// attend.
+// warp looks up its pages 32 at a time, one a lane, well before their copies
+// start, so that its loop over pages does little else than attend.
 //
 // Per page and warp, with tokens as the rows (M = 16) and the g <= 8 query
 // heads as the columns (N = 8) of m16n8k16 products, so that a group of 8
@@ -35,14 +41,14 @@
 //     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
 //     by a power of two that follows the largest step; the 8 x 8 transposes of
 //     P by movmatrix.  A product blocks the scheduler for 8 clocks (24 of them
-//     are 43% of the measured 111 clocks a page and SM with g = 8 and no copy),
-//     so with g <= 4 the columns 4 .. 7 hold heads 0 .. 3 again and take the lo
-//     parts: one product a tile instead of two.  The codes go in centred and as normal numbers, (code -
-//     7.5) 2^-10: a mean over many values cancels down to the noise of its
-//     sums, and the tensor core aligns subnormal operands by their nominal
-//     exponent, which costs six of its bits (relative error of O: 1e-5 with
-//     plain codes, 1.2e-6 with centred subnormals, 4e-7 so).  sum mid P joins
-//     at the end of the unit.
+//     are 43% of the 111 clocks above), so with g <= 4 the columns 4 .. 7 hold
+//     heads 0 .. 3 again and take the lo parts: one product a tile instead of
+//     two.  The codes go in centred and as normal numbers, (code - 7.5) 2^-10:
+//     a mean over many values cancels down to the noise of its sums, and the
+//     tensor core aligns subnormal operands by their nominal exponent, which
+//     costs six of its bits (relative error of O: 1e-5 with plain codes, 1.2e-6
+//     with centred subnormals, 4e-7 so).  sum mid P joins at the end of the
+//     unit.
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -58,14 +64,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSlots = 2;          // pages of a warp's ring: one attended, one on its way
+constexpr int kSlots = 2;          // pages of a warp's ring: one attended, one on its way (three: 364 us at 100k tokens
+                                   // instead of 369, but 1% more for short sequences, whose CTAs start later)
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
-constexpr int kOver = 24;          // places that a unit takes beside its pages
+// Places that a unit takes beside its pages: 61 ragged sequences of 1 to 4097 tokens (488 units) take 31 us with 8,
+// 24.1 with 16, 23.7 with 24 and 24.5 with 32.
+constexpr int kOver = 24;
 constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
-constexpr int kMinRun = 8;    // places of a run, at least: one page per warp
+constexpr int kMinRun = 8;         // places of a run, at least: one page per warp (two are slower: fewer CTAs at work)
 
 struct Attn4Args {
     const void *Q;
@@ -82,6 +91,9 @@ struct Attn4Args {
     int32_t *ticket, *err;
 };
 
+// Two CTAs of 8 warps an SM, 128 registers a thread: 16 warps hide a page's latencies behind one another.  12 warps of
+// 168 registers take 374 us where these take 369, 20 of 96 (which spill) 404.  More than 8 heads a group need two
+// accumulator tiles: one CTA of 8 warps.
 template <int HN> struct Shape {
     static constexpr int kHeads = 8 * HN;
     static constexpr int kCtas = HN == 1 ? 2 : 1;    // per SM
@@ -178,7 +190,9 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent of a positive finite float (-127 for subnormals).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
-constexpr int kFlush = 32;  // pages after which a warp's sums leave the tensor core's accumulators (they truncate)
+// Pages after which a warp's sums leave the tensor core's accumulators, whose sums truncate: the relative error of O at
+// 100k tokens is 8e-7 so, 8e-6 without; the time is the same.
+constexpr int kFlush = 32;
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
@@ -287,7 +301,8 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int gr = 0; gr < 2; ++gr) q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-kCodeScale<NQ>);
+            for (int gr = 0; gr < 2; ++gr)
+                q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-kCodeScale<NQ>);
     }
 }
 
@@ -475,6 +490,8 @@ __device__ __forceinline__ int places_of(int n) { return n > 0 ? n + kOver : 0; 
 
 // One record (address behind the length bits) into shared memory, by the
 // lanes of a warp in 16-byte pieces, as one group; nothing for place entry 0.
+// (One bulk copy per page with an mbarrier costs 52 instructions a page more
+// in waits and phases: 379 us instead of 369.)
 __device__ __forceinline__ void copy_record(uint32_t dst, unsigned long long entry) {
     const int lane = threadIdx.x & 31;
     if (entry != 0) {
@@ -579,7 +596,8 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     UnitAt unit = unit_at(0, (int)(S.start0 - f0));
     auto queries_of = [&](const UnitAt &x) {
         const int u = u0 + x.i;
-        return query_part<T, kTwice>(static_cast<const T *>(A.Q) + ((size_t)x.b * A.hq + (size_t)(u - x.b * A.hkv) * g) * kHeadDim, g);
+        const size_t row = (size_t)x.b * A.hq + (size_t)(u - x.b * A.hkv) * g;
+        return query_part<T, kTwice>(static_cast<const T *>(A.Q) + row * kHeadDim, g);
     };
     q4::Vec8<T> qpart = queries_of(unit);  // in flight during the lookups
 
@@ -588,8 +606,9 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     unsigned long long *pages = S.page[warp];
     if (lane == 0) S.look[warp] = unit;
     const uint32_t ring = su32(S.ring[warp][0]);
-    auto issue = [&](int n) {  // the copy of place n: one group a place, also where there is no page
-        copy_record(ring + (n % kSlots) * q4::kRecord, pages[n & (2 * kBatch - 1)]);
+    auto slot_of = [&](int n) { return ring + (n % kSlots) * q4::kRecord; };
+    auto issue = [&](int n, uint32_t to) {  // the copy of place n: one group a place, also where there is no page
+        copy_record(to, pages[n & (2 * kBatch - 1)]);
     };
     int looked = 0, issued = 0;  // places looked up, and those whose copy was started
     auto look_further = [&]() {
@@ -630,7 +649,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         if (looked == 0) {  // the first copies start while the lengths are on their way
             *entry = reinterpret_cast<unsigned long long>(src);
             __syncwarp();
-            for (; issued < kSlots - 1; ++issued) issue(issued);
+            for (; issued < kSlots - 1; ++issued) issue(issued, slot_of(issued));
             __syncwarp();
         }
         *entry = reinterpret_cast<unsigned long long>(src) | (unsigned long long)min(max(len, 0), kPage) << kLenShift;
@@ -659,21 +678,23 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         if (any)
             for (; issued < n + kSlots - 1; ++issued) {  // (after places without a page)
                 if (issued >= looked) look_further();
-                issue(issued);
+                issue(issued, slot_of(issued));
             }
         prepare_queries<T, NQ, HN>(qpart, A.scale, S.q, q);
+        uint32_t freed = slot_of(n + kSlots - 1), slot = slot_of(n);  // of places n - 1 and n
         for (bool flushed = false; n < n_end; flushed = true) {
             const int until = min(n_end, n + kFlush);
             while (n < until) {
                 while (looked - n <= kBatch / 2) look_further();
                 const int stop = min(until, looked - (kSlots - 1));
                 for (; n < stop; ++n) {
-                    // place n has arrived (n + 1 and n + 2 may be on their way), and every lane is done with n - 1
+                    // place n has arrived, and every lane is done with n - 1
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
                     __syncwarp();
-                    issue(n + kSlots - 1);
-                    attend_page4<NQ, HN, kTwice>(q, ring + (n % kSlots) * q4::kRecord,
-                                         (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
+                    issue(n + kSlots - 1, freed);
+                    attend_page4<NQ, HN, kTwice>(q, slot, (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
+                    freed = slot;
+                    slot = slot == slot_of(kSlots - 1) ? ring : slot + q4::kRecord;
                 }
             }
             issued = n + kSlots - 1;
@@ -786,7 +807,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                 float4 acc;
                 for (int hh = warp / split; hh < g; hh += split == 1 ? kWarps : g) {
                     // the first rows are on their way while the weights are found
-                    constexpr int kAhead = 8;
+                    constexpr int kAhead = 10;
                     const int k0 = warp % split;
                     const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
                     auto row_of = [&](int k) {
@@ -816,17 +837,15 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                     __syncwarp();
                     acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int k = k0; k < runs; k += kAhead * split) {
-                        float4 z[kAhead];
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i) z[i] = y[i];
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i) y[i] = row_of(k + (kAhead + i) * split);
 #pragma unroll
                         for (int i = 0; i < kAhead; ++i) {
                             const float w = k + i * split < runs ? wt[k + i * split].x : 0.f;
-                            acc.x = fmaf(z[i].x, w, acc.x), acc.y = fmaf(z[i].y, w, acc.y);
-                            acc.z = fmaf(z[i].z, w, acc.z), acc.w = fmaf(z[i].w, w, acc.w);
+                            acc.x = fmaf(y[i].x, w, acc.x), acc.y = fmaf(y[i].y, w, acc.y);
+                            acc.z = fmaf(y[i].z, w, acc.z), acc.w = fmaf(y[i].w, w, acc.w);
                         }
+                        if (k + kAhead * split < runs)
+#pragma unroll
+                            for (int i = 0; i < kAhead; ++i) y[i] = row_of(k + (kAhead + i) * split);
                     }
                     if (split == 1)
                         put_row(A, row0 + hh, acc, M, L);

@@ -2,28 +2,40 @@
 // the position rotation in one pass (ice_qkv_rope), and the same with K and V
 // appended to a paged cache in 4 bits (ice_cache4_append).
 //
-//   norm      y = (x r) w, r = 1 / sqrt(mean(x^2) + eps); the sum of squares
-//             is an error-free double-float sum, so r is the correctly
-//             rounded value;
+//   norm      y = (x r) w, r = 1 / sqrt(mean(x^2) + eps).  Keys take the sum
+//             of squares as an error-free double-float sum (a 4-bit code may
+//             hang on its last bit), queries as a plain fp32 sum;
 //   rotation  (a, b) <- (a cos - b sin, b cos + a sin), each product rounded
 //             once (no contraction).  Keys of an fp32 cache take the products
 //             with their rounding errors: their codes hang on the last bit.
 //
-// Both are bound by HBM for prompts (each row read and written once) and by
-// latency for single tokens.  8 lanes hold a row as two 8-element vectors: for
-// pairs (i, i + rotary_dim / 2) vectors l and l + rotary_dim / 16, so that
-// both elements of a pair are in one lane and nothing is exchanged but the
-// norm's sum.  k_qkv_rope: 8 lanes take four heads of one token, whose cos and
-// sin stay in registers; all loads are issued before the arithmetic.
+// Prompts are bound by HBM, each row read and written once: 1 x 36k tokens of
+// 32/8 heads 137 us, 6.75 TB/s, the copy rate.  With norms the sums share the
+// bound: 1 x 20k tokens of 64/8 heads 140 us, 5.9 TB/s (150 us with error-free
+// sums for the queries too).  Single tokens are bound by latency: 3.2 us for 16
+// sequences.
+//
+// 8 lanes hold a row as two 8-element vectors: for pairs (i, i + rotary_dim /
+// 2) vectors l and l + rotary_dim / 16, so that both elements of a pair are in
+// one lane and nothing is exchanged but the norm's sum.  k_qkv_rope: 8 lanes
+// take four heads of one token, whose cos and sin stay in registers; all loads
+// are issued before the arithmetic.
+//
 // k_cache4_append: CTAs of the queries work that way; in the others a warp per
 // block of 16 cache slots and KV head quantises up to 16 rows, four at a time,
 // into a record in shared memory, and writes the record (all 16 slots new) or
-// only the new tokens' bytes of it; with few blocks a warp takes four slots.  The quantising CTAs are bound by their
-// instructions, those of the queries by HBM, so both kinds run side by side:
-// the former lie evenly among the first three quarters of the grid, and what
-// is left at the end is short.  Appending 4 x 4099 tokens of 32/8 heads: 48.8
-// us (5.9 TB/s); spread over the whole grid 52.9, queries first 54.8, K and V
-// first 53.2.
+// only the new tokens' bytes of it; with few blocks a warp takes four slots.
+// The quantising CTAs are bound by their instructions (alone: 23 us, 3.0 TB/s),
+// those of the queries by HBM, so both kinds run side by side: the former lie
+// evenly among the first three quarters of the grid, and what is left at the
+// end is short.  Appending 4 x 4099 tokens of 32/8 heads: 48.8 us (5.9 TB/s);
+// spread over the whole grid 52.9, queries first 54.8, K and V first 53.2.
+//
+// The launch bounds trade registers for warps: at least 6 CTAs (24 warps) an SM
+// in bf16 (the 36k prompt 159 us with 4, the same with 8; the append 56 us with
+// 4, 52 with 8), in fp32 3 for the rotation (4 the same, 5 155 us instead of 146
+// for 20k tokens) and 4 for the append (20k tokens 143 us; with 3 157, without
+// a bound 192).
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
@@ -268,9 +280,10 @@ __device__ __forceinline__ void dense_chunk(const RopeArgs &A, unsigned item, un
     }
 }
 
-// CTAs [0, q_blocks) take the queries, the next k_blocks the keys, the rest the values.
+// CTAs [0, q_blocks) take the queries, the next k_blocks the keys, the rest the
+// values.
 template <typename T, int kLayout, bool kNorm>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : (kNorm ? 5 : 6)) k_qkv_rope(
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 6) k_qkv_rope(
     const __grid_constant__ RopeArgs A, unsigned q_items, unsigned kv_items, int q_blocks, int k_blocks) {
     dep_wait();
     const int block = blockIdx.x;
@@ -284,12 +297,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : (kNorm ? 5 : 6)
 }
 
 template <typename T, int kLayout, bool kNorm>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : (kNorm ? 5 : 6)) k_cache4_append(
-    const __grid_constant__ RopeArgs A, unsigned q_items, unsigned spread, unsigned kv_blocks, unsigned n_items, int blocks,
-    bool split, unsigned char *__restrict__ records, const int32_t *__restrict__ table, int n_pages, int max_pages) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 6) k_cache4_append(
+    const __grid_constant__ RopeArgs A, unsigned q_items, unsigned spread, unsigned kv_blocks, unsigned n_items,
+    int blocks, bool split, unsigned char *__restrict__ records, const int32_t *__restrict__ table, int n_pages,
+    int max_pages) {
     __shared__ __align__(16) unsigned char s_rec[kThreads / 32][q4::kRecord];
     dep_wait();
-    const unsigned kv = spread ? min(__umulhi(blockIdx.x, spread), kv_blocks) : blockIdx.x;  // K and V CTAs before this one
+    // K and V CTAs before this one
+    const unsigned kv = spread ? min(__umulhi(blockIdx.x, spread), kv_blocks) : blockIdx.x;
     if (spread && min(__umulhi(blockIdx.x + 1, spread), kv_blocks) == kv) {  // the queries
         dense_chunk<T, kLayout, kNorm, kQ>(A, (blockIdx.x - kv) * kGroups + threadIdx.x / 8, q_items);
         return;

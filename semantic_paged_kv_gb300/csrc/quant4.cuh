@@ -34,7 +34,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ float bf16_rn(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // Extremes of values as (min, -max), both taken by min: one exchange serves
 // two values.  bf16 values stay packed, (min, -max) in one word.
@@ -204,11 +208,31 @@ __device__ __forceinline__ uint32_t codes_ordinary(const float (&x)[8], float mi
 // clamping, step's reciprocal is normal, and mid keeps its distance (above).
 __device__ __forceinline__ bool ordinary(float step, float mid, float lo, float hi) {
     constexpr float kBig = 12582912.f;
-    float inv;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
-    const float n = fmaf(mid, inv, kBig) - kBig, off = fmaf(-n, step, mid);
+    const float n = fmaf(mid, rcp_fast(step), kBig) - kBig, off = fmaf(-n, step, mid);
     return (step >= 7.9e-31f) & (hi - mid < 8.f * step) & (mid - lo <= 8.f * step) & (fabsf(mid) < 4096.f * step) &
            (fabsf(off) >= 0.001953125f * step);
+}
+
+// The same for fp32 values: t = (x - mid) / step + 7.5 within 2^-19 (x - mid
+// and the sum rounded once, 2^-21 each at |x - mid| <= 8 step; a reciprocal
+// within an ulp, 2^-20), so its nearest integer is the code unless t lies
+// nearer than that to a border.  `far` becomes the largest distance of a t from
+// its integer: codes with one above kSure are to be found the exact way (some
+// 2^-15 of all values).
+constexpr float kSure = 0.5f - 1.52587890625e-5f;  // 0.5 - 2^-16
+__device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float mid, float inv, float &far) {
+    constexpr float kBig = 12582912.f;  // 1.5 * 2^23
+    const pair_t mid2 = pk2(mid, mid), inv2 = pk2(inv, inv), off2 = pk2(7.5f, 7.5f), big2 = pk2(kBig, kBig);
+    uint32_t w = 0u - 0x4B400000u * 0x11111111u;  // the bits of 1.5 * 2^23 in every nibble
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const pair_t t = fma2(sub2(pk2(x[2 * i], x[2 * i + 1]), mid2), inv2, off2), u = add2(t, big2);
+        const float2 d = upk2(sub2(t, sub2(u, big2))), b = upk2(u);
+        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+        w += __float_as_uint(b.x) * (1u << (8 * i));
+        w += __float_as_uint(b.y) * (16u << (8 * i));
+    }
+    return w;
 }
 
 // Codes of any group: also steps below 2^-100 (the reciprocal leaves fp32's
@@ -258,23 +282,27 @@ __device__ __forceinline__ void quantise_row(const Vec8<T> &a, const Vec8<T> &b,
     a.get(x);
     b.get(y);
     if (sizeof(T) == 2 && __all_sync(0xffffffffu, ordinary(sm.x, sm.y, lo, hi) | !live)) {
-        float ia, ib;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ia) : "f"(ga.x));
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ib) : "f"(gb.x));
-        ca = codes_ordinary(x, ga.y, ia);
-        cb = codes_ordinary(y, gb.y, ib);
-    } else {
-        ca = codes_any<T>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], ga.x, ga.y);
-        cb = codes_any<T>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], gb.x, gb.y);
+        ca = codes_ordinary(x, ga.y, rcp_fast(ga.x));
+        cb = codes_ordinary(y, gb.y, rcp_fast(gb.x));
+        return;
     }
+    if (sizeof(T) == 4) {
+        float far = 0.f;
+        ca = codes_near(x, ga.y, rcp_fast(ga.x), far);
+        cb = codes_near(y, gb.y, rcp_fast(gb.x), far);
+        const bool fits = (sm.x >= 7.9e-31f) & (hi - sm.y <= 8.f * sm.x) & (sm.y - lo <= 8.f * sm.x);
+        if (__all_sync(0xffffffffu, (fits & (far < kSure)) | !live)) return;
+    }
+    ca = codes_any<T>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], ga.x, ga.y);
+    cb = codes_any<T>(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], gb.x, gb.y);
 }
 
-// The values that a vector's codes stand for: mid + step (code - 7.5), one
-// rounding.  A code at bit 7 of 2^16 adds its value.
-__device__ __forceinline__ void values_of(uint32_t w, float2 sm, float (&x)[8]) {
+// The values that the first n codes of a word stand for: mid + step (code -
+// 7.5), one rounding.  A code at bit 7 of 2^16 adds its value.
+template <int n> __device__ __forceinline__ void values_of(uint32_t w, float2 sm, float (&x)[n]) {
     const pair_t step = pk2(sm.x, sm.x), mid = pk2(sm.y, sm.y), off = pk2(65543.5f, 65543.5f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < n / 2; ++i) {
         const uint32_t a = i == 0 ? w << 7 : w >> (i == 0 ? 0 : 8 * i - 7), b = i == 0 ? w << 3 : w >> (i == 0 ? 0 : 8 * i - 3);
         const pair_t c = sub2(pk2(__uint_as_float((a & 0x780u) | 0x47800000u),
                                   __uint_as_float((b & 0x780u) | 0x47800000u)), off);

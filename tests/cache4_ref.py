@@ -16,8 +16,14 @@ def groups(x):
     bad = ~torch.isfinite((g.amax(-1).float() - g.amin(-1).float())) | torch.isnan(g).any(-1)
     step = torch.where(bad, torch.zeros_like(step), step)
     mid = torch.where(bad, torch.full_like(mid, math.nan), mid)
-    q = (g - mid.double()[..., None]) / torch.where(step > 0, step, torch.ones_like(step)).double()[..., None] + 7.5
-    c = torch.round(torch.nan_to_num(q)).clamp(0, 15)
+    st, mi = torch.where(step > 0, step, torch.ones_like(step)).double()[..., None], mid.double()[..., None]
+    # x - mid with its rounding error (Knuth 1969): a tiny x beside a large mid is not lost; m * step is exact
+    d = g - mi
+    e = (g - (d - (d - g))) - (mi + (d - g))
+    m = torch.round(torch.nan_to_num(d / st))
+    rem = (d - m * st) + e
+    even = m + 7 + (m.long() + 7) % 2  # the even one of m + 7 and m + 8
+    c = torch.where(rem > 0, m + 8, torch.where(rem < 0, m + 7, even)).clamp(0, 15)
     c = torch.where((step > 0)[..., None], c, torch.zeros_like(c))
     return torch.stack((step, mid), -1), c.flatten(-2).long()
 

@@ -642,6 +642,32 @@ def test_codes_on_borders():
         assert ice.ice_check(err) == ice.ICE_OK and torch.equal(recs[0], ref.encode(k, v))
 
 
+def test_fp32_codes_next_to_borders():
+    """fp32 values on the borders between two codes and up to some units in the last place beside them."""
+    n, g = 3000, _gen(131)
+    x = torch.randn((n, S, 2, D // 2), generator=g, device="cuda")
+    x *= torch.exp2(torch.randint(-40, 40, (n, S, 2, 1), generator=g, device="cuda").float())
+    x += torch.randint(-2, 3, (n, S, 2, 1), generator=g, device="cuda") * x.abs().amax(-1, keepdim=True)
+    meta, _ = ref.groups(x.reshape(n, S, D))
+    step, mid = (meta.view(n, S, 2, 2)[..., i:i + 1].double() for i in range(2))
+    lo, hi = x.amin(-1, keepdim=True), x.amax(-1, keepdim=True)
+    at = torch.randint(-7, 8, x.shape, generator=g, device="cuda")
+    near = (mid + at * step).float()
+    ulps = torch.randint(-9, 10, x.shape, generator=g, device="cuda")
+    near = (near.double() + ulps * torch.where(near == 0, 1e-30, near.abs().double() * 2.0 ** -24)).float()
+    near = torch.minimum(torch.maximum(near, lo), hi)
+    keep = (x == lo) | (x == hi) | (torch.arange(n, device="cuda") % 3 == 0)[:, None, None, None]
+    k = torch.where(keep, x, near).reshape(n, S, D)
+    assert torch.equal(ref.groups(k)[0], meta)  # the extremes are as they were
+    v = k.flip(0).contiguous()
+    lens = torch.full((1, n), S, dtype=torch.int32, device="cuda")
+    cnt = torch.full((1,), n, dtype=torch.int32, device="cuda")
+    recs, err = torch.empty((1, n, R), dtype=torch.uint8, device="cuda"), _err()
+    ice.ice_pool4_pack(_params(1, 1, 1, "fp32", page_cap=n), _ix(n_pages=cnt, page_len=lens, pool_k=k, pool_v=v), 0,
+                       recs, err)
+    assert ice.ice_check(err) == ice.ICE_OK and torch.equal(recs[0], ref.encode(k, v))
+
+
 def test_long_context_of_shared_pages():
     """100k tokens a sequence (the warps' sums are flushed on the way), sequences sharing the pages of a small cache."""
     B, hq, hkv, n = 2, 64, 8, 100003
