@@ -74,7 +74,7 @@ constexpr int kOver = 24;
 constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
-constexpr int kMinRun = 8;         // places of a run, at least: one page per warp (two are slower: fewer CTAs at work)
+constexpr int kMinRun = 8;         // places of a run, at least: one page per warp (16 are slower: fewer CTAs at work)
 
 struct Attn4Args {
     const void *Q;
@@ -191,7 +191,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
 // Pages after which a warp's sums leave the tensor core's accumulators, whose sums truncate: the relative error of O at
-// 100k tokens is 8e-7 so, 8e-6 without; the time is the same.
+// 100k tokens is 8e-7 so, 8e-6 without.
 constexpr int kFlush = 32;
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
