@@ -115,6 +115,8 @@ ice_status ice_host_pool_create(size_t pool_bytes, size_t staging_bytes, int32_t
         release(hp);
         return ICE_ERR_OOM;
     }
+    // pinned memory may come with what an earlier owner left there: slots that no page fills go to the device as zeros
+    if (staging_bytes) memset(hp->staging, 0, staging_bytes);
     if (fault_armed("hostpool") || cudaHostGetDevicePointer(&hp->k_dev, hp->k_host, 0) != cudaSuccess ||
         cudaHostGetDevicePointer(&hp->v_dev, hp->v_host, 0) != cudaSuccess ||
         cudaEventCreateWithFlags(&hp->copied, cudaEventDisableTiming) != cudaSuccess) {

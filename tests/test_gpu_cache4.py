@@ -773,6 +773,28 @@ def test_host_pool_in_4_bits():
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+def test_host_pool_staging_starts_at_zero():
+    """Slots that no page has filled are zero, also in memory that another pool has used before."""
+    cfg = ice.Config(batch=1, n_q_heads=8, n_kv_heads=2, n_tokens=600)
+    U, n = cfg.units, 64
+    assert cfg.page_cap >= n
+    sel = torch.arange(n, dtype=torch.int32).expand(U, n).contiguous()
+    lens = torch.full((U, cfg.page_cap), S, dtype=torch.int32)
+    for count in (n, 1, 0):
+        hp = ice.HostPool(cfg, n, n_threads=2)
+        try:
+            dst = torch.full((hp.staging_bytes,), FILL, dtype=torch.uint8, device="cuda")
+            for which in "kv":
+                hp.host_array(which)[:] = 0x3F80
+            cnt = torch.full((U,), count, dtype=torch.int32)
+            ice.ice_host_pool_gather_h2d(hp, cfg.params(), sel, cnt, lens, n, dst)
+            torch.cuda.synchronize()
+        finally:
+            hp.close()
+        kv = dst[:2 * U * n * S * D * 2].view(2, U, n, -1)
+        assert int(kv[:, :, count:].count_nonzero()) == 0 and bool(kv[:, :, :count].any(-1).all())
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 3.0])
 def test_attention_scales_and_values_that_are_not_numbers(scale):
     p = _params(1, 8, 1, "bf16")
