@@ -74,6 +74,11 @@ constexpr int kOver = 24;
 constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
+// A unit of more than kJoinRows rows of partial results (runs times heads) is joined in two levels, groups of kGroup
+// runs by their last CTAs and then the groups: one CTA reads 10 rows a warp and latency, a further ticket costs about 2
+// us.  One sequence of 16k tokens of 16/1 heads takes 16.3 us so and 24.2 in one level, of 100k tokens 20.1 and 36.6
+// (4/1 heads 15.5 and 24.2); the 38 runs of 4 heads of 16k tokens of 32/8 heads 15.8 in two levels and 13.4 in one.
+constexpr int kGroup = 16, kJoinRows = 256;
 constexpr int kMinRun = 8;         // places of a run, at least: one page per warp (16 are slower: fewer CTAs at work)
 
 struct Attn4Args {
@@ -88,7 +93,7 @@ struct Attn4Args {
     float scale;
     float *O, *lse;
     float *part_o, *part_ml;
-    int32_t *ticket, *err;
+    int32_t *ticket, *group_ticket, *err;
 };
 
 // Two CTAs of 8 warps an SM, 128 registers a thread: 16 warps hide a page's latencies behind one another.  12 warps of
@@ -518,6 +523,112 @@ __device__ __forceinline__ void put_row(const Attn4Args &A, size_t row, float4 a
     if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+// Whether this CTA is the last of n to come here (all of its threads call; what the others wrote can then be read).
+__device__ __forceinline__ bool last_of(int32_t *ticket, int n, int *last) {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();  // (the whole CTA's stores: they come before the barrier)
+        *last = atomicAdd(ticket, 1) == n - 1;
+    }
+    __syncthreads();
+    if (!*last) return false;
+    __threadfence();
+    return true;
+}
+
+// Sums of n parts (rows of [.., 128] and (maximum, sum) pairs): the first one's rows at `first`, the others' at k *
+// stride.  put(head, acc, M, L) is called by one warp a head, a lane's 4 elements each.
+template <int kWarps, typename Put>
+__device__ __forceinline__ void join_parts(float *scratch, const float *po, const float2 *ml, int first, int stride,
+                                           int n, int g, Put put) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a head's parts go to as many warps as there are for it, whose sums meet in shared memory
+    const int split = g >= kWarps ? 1 : kWarps / g;
+    float2 *wt = reinterpret_cast<float2 *>(scratch) + warp * kMaxRuns;  // of this warp's head
+    float *sums = scratch + 2 * kWarps * kMaxRuns;
+    float M, L;
+    float4 acc;
+    for (int hh = warp / split; hh < g; hh += split == 1 ? kWarps : g) {
+        // the first rows are on their way while the weights are found
+        constexpr int kAhead = 10;
+        const int k0 = warp % split;
+        const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
+        auto row_of = [&](int k) {
+            return k < n ? __ldcg(row + (size_t)(k * stride + (k ? 0 : first)) * (kHeadDim / 4))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 y[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) y[i] = row_of(k0 + i * split);
+        M = -FLT_MAX, L = 0.f;
+        __syncwarp();  // the weights of the head before have been read
+        for (int k = lane; k < n; k += 32) {
+            const float2 x = __ldcg(ml + k * stride + (k ? 0 : first) + hh);
+            M = fmaxf(M, x.x);
+            wt[k] = x;
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        for (int k = lane; k < n; k += 32) {
+            const float2 x = wt[k];
+            const float w = x.y == 0.f ? 0.f : (x.y == x.y ? exp2_fast(x.x - M) : x.y);
+            L = fmaf(x.y, w, L);
+            wt[k].x = w;
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        __syncwarp();
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = k0; k < n; k += kAhead * split) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float w = k + i * split < n ? wt[k + i * split].x : 0.f;
+                acc.x = fmaf(y[i].x, w, acc.x), acc.y = fmaf(y[i].y, w, acc.y);
+                acc.z = fmaf(y[i].z, w, acc.z), acc.w = fmaf(y[i].w, w, acc.w);
+            }
+            if (k + kAhead * split < n)
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) y[i] = row_of(k + (kAhead + i) * split);
+        }
+        if (split == 1)
+            put(hh, acc, M, L);
+        else
+            *reinterpret_cast<float4 *>(sums + warp * kHeadDim + 4 * lane) = acc;
+    }
+    if (split > 1) {  // (at most one head a warp: g <= kWarps / split)
+        __syncthreads();
+        if (warp % split == 0 && warp / split < g) {
+            for (int w = 1; w < split; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(sums + (warp + w) * kHeadDim + 4 * lane);
+                acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
+            }
+            put(warp / split, acc, M, L);
+        }
+    }
+}
+
+// A unit of many runs (the first one's part at 2 ca, or behind it with `inside`): the last CTA of each group of kGroup
+// runs joins the group's parts in the place of its first one.  True in those CTAs.  (Not inlined: the loop over pages
+// keeps its registers.)
+template <int kWarps>
+__device__ __noinline__ bool join_group(float *part_o, float *part_ml, int32_t *group_ticket, float *scratch, int *last,
+                                        int g, int ca, int runs, bool inside) {
+    const int group = ((int)blockIdx.x - ca) / kGroup, from = ca + group * kGroup;
+    const bool second = inside && group == 0;
+    int32_t *ticket = group_ticket + 2 * from + (second ? 1 : 0);
+    const int n = min(kGroup, runs - group * kGroup), first = second ? g : 0;
+    if (!last_of(ticket, n, last)) return false;
+    float *po = part_o + (size_t)from * 2 * g * kHeadDim;
+    float2 *ml = reinterpret_cast<float2 *>(part_ml) + (size_t)from * 2 * g;
+    join_parts<kWarps>(scratch, po, ml, first, 2 * g, n, g, [&](int hh, float4 acc, float M, float L) {
+        const int lane = threadIdx.x & 31;
+        *reinterpret_cast<float4 *>(po + (size_t)(first + hh) * kHeadDim + 4 * lane) = acc;
+        if (lane == 0) ml[first + hh] = make_float2(M, L);
+    });
+    if (threadIdx.x == 0) *ticket = 0;
+    return true;
+}
+
 template <typename T, int NQ, int HN, bool kTwice>
 __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
     k_attn4(const __grid_constant__ Attn4Args A) {
@@ -787,81 +898,19 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
             // the unit's runs: CTAs ca .. cb; a run's part is its second one when the unit starts inside the run
             const long long us = f0 + unit.first;
             const int ca = (int)(us / share), cb = (int)((us + unit.n - 1) / share);
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();  // (the whole CTA's stores: they come before the barrier)
-                S.last = atomicAdd(A.ticket + u, 1) == cb - ca;
+            const bool inside = us > (long long)ca * share;
+            int runs = cb - ca + 1, stride = 2 * g;
+            bool go = true;
+            if (runs > kGroup && runs * g > kJoinRows) {
+                go = join_group<kWarps>(A.part_o, A.part_ml, A.group_ticket, &S.o[0][0][0], &S.last, g, ca, runs,
+                                        inside);
+                runs = (runs + kGroup - 1) / kGroup, stride *= kGroup;
             }
-            __syncthreads();
-            if (S.last) {
-                __threadfence();
-                // a head's runs go to as many warps as there are for it, whose sums meet in shared memory
-                const int runs = cb - ca + 1, split = g >= kWarps ? 1 : kWarps / g;
-                float2 *wt = reinterpret_cast<float2 *>(&S.o[0][0][0]) + warp * kMaxRuns;  // of this warp's head
-                float *sums = reinterpret_cast<float *>(&S.o[0][0][0]) + 2 * kWarps * kMaxRuns;
-                const float2 *ml = reinterpret_cast<const float2 *>(A.part_ml) + (size_t)ca * 2 * g;
-                const float *po = A.part_o + (size_t)ca * 2 * g * kHeadDim;
-                // (the first run's part is its second one when the unit starts inside it)
-                const int skip = us > (long long)ca * share ? g : 0;
-                float M, L;
-                float4 acc;
-                for (int hh = warp / split; hh < g; hh += split == 1 ? kWarps : g) {
-                    // the first rows are on their way while the weights are found
-                    constexpr int kAhead = 10;
-                    const int k0 = warp % split;
-                    const float4 *row = reinterpret_cast<const float4 *>(po + (size_t)hh * kHeadDim) + lane;
-                    auto row_of = [&](int k) {
-                        return k < runs ? __ldcg(row + (size_t)(2 * k * g + (k ? 0 : skip)) * (kHeadDim / 4))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-                    };
-                    float4 y[kAhead];
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) y[i] = row_of(k0 + i * split);
-                    M = -FLT_MAX, L = 0.f;
-                    __syncwarp();  // the weights of the head before have been read
-                    for (int k = lane; k < runs; k += 32) {
-                        const float2 x = __ldcg(ml + 2 * k * g + (k ? 0 : skip) + hh);
-                        M = fmaxf(M, x.x);
-                        wt[k] = x;
-                    }
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                    for (int k = lane; k < runs; k += 32) {
-                        const float2 x = wt[k];
-                        const float w = x.y == 0.f ? 0.f : (x.y == x.y ? exp2_fast(x.x - M) : x.y);
-                        L = fmaf(x.y, w, L);
-                        wt[k].x = w;
-                    }
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-                    __syncwarp();
-                    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int k = k0; k < runs; k += kAhead * split) {
-#pragma unroll
-                        for (int i = 0; i < kAhead; ++i) {
-                            const float w = k + i * split < runs ? wt[k + i * split].x : 0.f;
-                            acc.x = fmaf(y[i].x, w, acc.x), acc.y = fmaf(y[i].y, w, acc.y);
-                            acc.z = fmaf(y[i].z, w, acc.z), acc.w = fmaf(y[i].w, w, acc.w);
-                        }
-                        if (k + kAhead * split < runs)
-#pragma unroll
-                            for (int i = 0; i < kAhead; ++i) y[i] = row_of(k + (kAhead + i) * split);
-                    }
-                    if (split == 1)
-                        put_row(A, row0 + hh, acc, M, L);
-                    else
-                        *reinterpret_cast<float4 *>(sums + warp * kHeadDim + 4 * lane) = acc;
-                }
-                if (split > 1) {  // (at most one head a warp: g <= kWarps / split)
-                    __syncthreads();
-                    if (warp % split == 0 && warp / split < g) {
-                        for (int w = 1; w < split; ++w) {
-                            const float4 y = *reinterpret_cast<const float4 *>(sums + (warp + w) * kHeadDim + 4 * lane);
-                            acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
-                        }
-                        put_row(A, row0 + warp / split, acc, M, L);
-                    }
-                }
+            if (go && last_of(A.ticket + u, runs, &S.last)) {
+                join_parts<kWarps>(&S.o[0][0][0], A.part_o + (size_t)ca * 2 * g * kHeadDim,
+                                   reinterpret_cast<const float2 *>(A.part_ml) + (size_t)ca * 2 * g, inside ? g : 0,
+                                   stride, runs, g,
+                                   [&](int hh, float4 acc, float M, float L) { put_row(A, row0 + hh, acc, M, L); });
                 if (tid == 0) A.ticket[u] = 0;
             }
         }
@@ -879,7 +928,7 @@ int max_ctas(int sms) { return 2 * sms < kMaxRuns ? 2 * sms : kMaxRuns; }
 struct Attn4Ws {
     float *part_ml;   // [2 runs, g, 2]
     float *part_o;    // [2 runs, g, 128]
-    int32_t *ticket;  // [units] zero between calls
+    int32_t *group_ticket, *ticket;  // [2 runs], [units]: zero between calls
     size_t bytes;
 };
 Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
@@ -894,6 +943,7 @@ Attn4Ws ws_layout(const ice_params &p, int sms, void *base) {
     const size_t parts = 2 * (size_t)max_ctas(sms) * 16;  // (g <= 16)
     w.part_ml = reinterpret_cast<float *>(take(sizeof(float) * parts * 2));
     w.part_o = reinterpret_cast<float *>(take(sizeof(float) * parts * kHeadDim));
+    w.group_ticket = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * 2 * max_ctas(sms)));
     w.ticket = reinterpret_cast<int32_t *>(take(sizeof(int32_t) * units_of(p)));
     w.bytes = off;
     return w;
@@ -951,7 +1001,7 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
     A.O = O, A.lse = lse, A.err = err;
     const int sms = device_sms();
     const Attn4Ws w = ws_layout(p, sms, ws);
-    A.ticket = w.ticket, A.part_ml = w.part_ml, A.part_o = w.part_o;
+    A.ticket = w.ticket, A.group_ticket = w.group_ticket, A.part_ml = w.part_ml, A.part_o = w.part_o;
     if (p.dtype == ICE_BF16)
         return A.g <= 4   ? launch_t<__nv_bfloat16, 1, 1, true>(A, sms, s)
                : A.g <= 8 ? launch_t<__nv_bfloat16, 1, 1, false>(A, sms, s)

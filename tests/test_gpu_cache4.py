@@ -795,6 +795,46 @@ def test_host_pool_staging_starts_at_zero():
         assert int(kv[:, :, count:].count_nonzero()) == 0 and bool(kv[:, :, :count].any(-1).all())
 
 
+MANY_RUNS = [  # hq, hkv, dtype, lens: units whose partial results are joined in groups first
+    (16, 1, "bf16", [16001]), (4, 1, "fp32", [40000]), (24, 2, "bf16", [9000, 1, 21000]), (8, 1, "bf16", [30000, 13, 9999]),
+    (11, 1, "fp32", [700, 12000]),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,dtype,lens", MANY_RUNS)
+def test_attention_of_many_runs(hq, hkv, dtype, lens):
+    B, scale = len(lens), 0.088
+    p = _params(B, hq, hkv, dtype)
+    blocks = -(-max(lens) // S)
+    recs = _random_records(700, hkv, 141)
+    bt = torch.randint(0, 700, (B, blocks), generator=_gen(142), device="cuda").int()
+    Q = torch.randn((B, hq, D), generator=_gen(143), device="cuda").to(DT[dtype])
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache = ice.Cache4(recs, bt)
+    got = []
+    for _ in range(4):  # the tickets of every call are those of the next one
+        ice.ice_cache4_attn_decode(p, Q, cache, ln, scale, O, lse, ws, err)
+        got.append((O.clone(), lse.clone()))
+    assert ice.ice_check(err) == ice.ICE_OK
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+    K, V = _rows_of(recs, bt, 0)
+    _check_attn(O, lse, Q, lambda b, h: (K[b, h, :lens[b]], V[b, h, :lens[b]]), B, hkv, scale)
+    # one after the other with a call of another shape in the same workspace
+    p2, Q2 = _params(1, 32, 8, "bf16"), torch.randn((1, 32, D), generator=_gen(144), device="cuda").bfloat16()
+    recs2, bt2 = _random_records(300, 8, 145), torch.arange(300, dtype=torch.int32, device="cuda").view(1, 300)
+    ln2 = torch.tensor([4700], dtype=torch.int32, device="cuda")
+    ws = ice.workspace(max(ice.ice_attn4_workspace_bytes(x) for x in (p, p2)))
+    O2, lse2, ws2, _ = _attn_buffers(1, 32, p2)
+    ice.ice_cache4_attn_decode(p2, Q2, ice.Cache4(recs2, bt2), ln2, scale, O2, lse2, ws2, err)
+    for _ in range(3):
+        x, y = torch.empty_like(O), torch.empty_like(O2)
+        ice.ice_cache4_attn_decode(p, Q, cache, ln, scale, x, None, ws, err)
+        ice.ice_cache4_attn_decode(p2, Q2, ice.Cache4(recs2, bt2), ln2, scale, y, None, ws, err)
+        assert torch.equal(x, got[0][0]) and torch.equal(y, O2)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 3.0])
 def test_attention_scales_and_values_that_are_not_numbers(scale):
     p = _params(1, 8, 1, "bf16")
