@@ -10,8 +10,8 @@
 // bound by that and by instruction issue in about equal parts: the same loop
 // over pages without their copies takes 111 clocks a page and SM (250 instructions
 // on four schedulers, 62 clocks, and 24 products that block one for 8 clocks
-// each, 48), the copies alone take 305 us where the whole takes 369 us (16 sequences x 100k tokens, 64/8 heads: 1.84 GB
-// at 5.0 TB/s, 74% of the copy rate; 4 heads a group 347 us).  Short ones are
+// each, 48), the copies alone take 305 us where the whole takes 372 us (16 sequences x 100k tokens, 64/8 heads: 1.84 GB
+// at 5.0 TB/s, 73% of the copy rate; 4 heads a group 347 us, 16 heads 568).  Short ones are
 // bound by a chain of latencies (1 sequence x 16k tokens, 32/8 heads: 13.4 us):
 // counts of the units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the
 // run's other pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
@@ -97,8 +97,8 @@ struct Attn4Args {
 };
 
 // Two CTAs of 8 warps an SM, 128 registers a thread: 16 warps hide a page's latencies behind one another.  12 warps of
-// 168 registers take 374 us where these take 369, 20 of 96 (which spill) 404.  More than 8 heads a group need two
-// accumulator tiles: one CTA of 8 warps.
+// 168 registers take 374 us where these took 369, 20 of 96 (which spill) 404.  More than 8 heads a group need two
+// accumulator tiles: one CTA of 8 warps (8 sequences x 100k tokens of 16 heads a group 292 us; 10 warps 341, 12 293).
 template <int HN> struct Shape {
     static constexpr int kHeads = 8 * HN;
     static constexpr int kCtas = HN == 1 ? 2 : 1;    // per SM
