@@ -143,7 +143,8 @@ def exported_symbols() -> list[str]:
             "ice_decode_plan",
             "ice_insert_workspace_bytes", "ice_insert_tokens", "ice_rope_table", "ice_qkv_rope",
             "ice_cache4_append", "ice_cache4_read", "ice_pool4_bytes", "ice_pool4_pack", "ice_pool4_unpack",
-            "ice_attn4_workspace_bytes", "ice_cache4_attn_decode", "ice_sparse_attn_decode4", "ice_host_pool_create", "ice_host_pool_destroy",
+            "ice_attn4_workspace_bytes", "ice_cache4_attn_decode", "ice_sparse_attn_decode4",
+            "ice_host_pool_create", "ice_host_pool_destroy",
             "ice_host_pool_pointers", "ice_host_pool_staging_bytes", "ice_host_pool_gather_h2d"]
 
 
@@ -552,12 +553,14 @@ def ice_pool4_bytes(params: IceParams) -> int:
 
 
 def ice_pool4_pack(params, index, first_token: int, records, err, stream=None):
-    _check(load().ice_pool4_pack(params, index.struct if isinstance(index, Index) else index, first_token, _ptr(records), _ptr(err),
-                                 _stream(stream)))
+    """index: an Index, or an IceIndex with the arrays that ice.h names."""
+    x = index.struct if isinstance(index, Index) else index
+    _check(load().ice_pool4_pack(params, x, first_token, _ptr(records), _ptr(err), _stream(stream)))
 
 
 def ice_pool4_unpack(params, index, records, err, stream=None):
-    _check(load().ice_pool4_unpack(params, index.struct if isinstance(index, Index) else index, _ptr(records), _ptr(err), _stream(stream)))
+    x = index.struct if isinstance(index, Index) else index
+    _check(load().ice_pool4_unpack(params, x, _ptr(records), _ptr(err), _stream(stream)))
 
 
 def ice_attn4_workspace_bytes(params: IceParams) -> int:

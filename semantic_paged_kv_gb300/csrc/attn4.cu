@@ -8,13 +8,14 @@
 // A page of 16 tokens of one KV head is one 2304-byte record, read once; at the
 // measured copy rate an SM could get one every ~98 clocks.  Long caches are
 // bound by that and by instruction issue in about equal parts: the same loop
-// over pages without their copies takes 111 clocks a page and SM (250 instructions
-// on four schedulers, 62 clocks, and 24 products that block one for 8 clocks
-// each, 48), the copies alone take 305 us where the whole takes 372 us (16 sequences x 100k tokens, 64/8 heads: 1.84 GB
-// at 5.0 TB/s, 73% of the copy rate; 4 heads a group 347 us, 16 heads 568).  Short ones are
-// bound by a chain of latencies (1 sequence x 16k tokens, 32/8 heads: 13.4 us):
-// counts of the units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the
-// run's other pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
+// over pages without their copies takes 111 clocks a page and SM (250
+// instructions on four schedulers, 62 clocks, and 24 products that block one for
+// 8 clocks each, 48), the copies alone take 305 us where the whole takes 372 us
+// (16 sequences x 100k tokens, 64/8 heads: 1.84 GB at 5.0 TB/s, 73% of the copy
+// rate; 4 heads a group 347 us, 16 heads 568).  Short ones are bound by a chain
+// of latencies (1 sequence x 16k tokens, 32/8 heads: 13.4 us): counts of the
+// units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the run's other
+// pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
 //
 // Work: the pages of all units, one after another, are cut into equal runs,
 // one per CTA, whatever the units' lengths; a unit counts kOver pages more

@@ -497,8 +497,8 @@ cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows 
     const int blocks = cache4_blocks(n_new);
     unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
     // Few blocks leave most of an SM's warps empty while each works on its 16 rows: a warp then takes four of them.  In
-    // bf16 1 x 128 tokens of 8 heads take 3.4 us so, 6.3 with whole blocks; 4 x 1200 (16 blocks an SM) 14.6 and 15.3, 8 x
-    // 1200 31 and 28.  fp32: 1 x 128 4.3 and 9.5, 2 x 1200 (8 an SM) 21.3 and 21.4, 4 x 1200 41 and 37.
+    // bf16 1 x 128 tokens of 8 heads take 3.4 us so, 6.3 with whole blocks; 4 x 1200 (16 blocks an SM) 14.6 and 15.3,
+    // 8 x 1200 31 and 28.  fp32: 1 x 128 4.3 and 9.5, 2 x 1200 (8 an SM) 21.3 and 21.4, 4 x 1200 41 and 37.
     const bool split = n_new > 4 && (long long)items <= (p.dtype == ICE_BF16 ? 16 : 8) * device_sms();
     if (split) items *= 4;
     const unsigned kv_blocks = (unsigned)ceil_div(items, kThreads / 32), n = q_blocks + kv_blocks;
