@@ -34,8 +34,8 @@
 // The launch bounds trade registers for warps: at least 6 CTAs (24 warps) an SM
 // in bf16 (the 36k prompt 159 us with 4, the same with 8; the append 56 us with
 // 4, 52 with 8), in fp32 3 for the rotation (4 the same, 5 155 us instead of 146
-// for 20k tokens) and 4 for the append (20k tokens 143 us; with 3 157, without
-// a bound 192).
+// for 20k tokens) and 4 for the append (20k tokens 129 us; with 3 139, without
+// a bound 167).
 #include "common.cuh"
 #include "internal.h"
 #include "quant4.cuh"
@@ -497,9 +497,9 @@ cudaError_t launch_cache4_append(const ice_params &p, int n_new, const ice_rows 
     const int blocks = cache4_blocks(n_new);
     unsigned items = (unsigned)((long long)p.batch * blocks * p.n_kv_heads);
     // Few blocks leave most of an SM's warps empty while each works on its 16 rows: a warp then takes four of them.  In
-    // bf16 1 x 128 tokens of 8 heads take 3.4 us so, 6.3 with whole blocks; 4 x 1200 (16 blocks an SM) 14.6 and 15.3,
-    // 8 x 1200 31 and 28.  fp32: 1 x 128 4.3 and 9.5, 2 x 1200 (8 an SM) 21.3 and 21.4, 4 x 1200 41 and 37.
-    const bool split = n_new > 4 && (long long)items <= (p.dtype == ICE_BF16 ? 16 : 8) * device_sms();
+    // bf16 1 x 128 tokens of 8 heads take 3.4 us so, 6.2 with whole blocks; 2 x 1200 8.7 and 12.6, 4 x 1200 (16 blocks
+    // an SM) 14.7 and 15.0, 8 x 1200 31 and 28.  fp32: 1 x 128 4.0 and 7.7, 4 x 1200 27.6 and 27.1, 8 x 1200 54 and 48.
+    const bool split = n_new > 4 && (long long)items <= 16 * device_sms();
     if (split) items *= 4;
     const unsigned kv_blocks = (unsigned)ceil_div(items, kThreads / 32), n = q_blocks + kv_blocks;
     // min(floor(i spread / 2^32), kv_blocks) CTAs of K and V come before CTA i: none before CTA 0, one more after at
