@@ -10,10 +10,10 @@
 // bound by that and by instruction issue in about equal parts: the same loop
 // over pages without their copies takes 111 clocks a page and SM (250
 // instructions on four schedulers, 62 clocks, and 24 products that block one for
-// 8 clocks each, 48), the copies alone take 305 us where the whole takes 372 us
-// (16 sequences x 100k tokens, 64/8 heads: 1.84 GB at 5.0 TB/s, 73% of the copy
-// rate; 4 heads a group 347 us, 16 heads 568).  Short ones are bound by a chain
-// of latencies (1 sequence x 16k tokens, 32/8 heads: 13.4 us): counts of the
+// 8 clocks each, 48), the copies alone take 305 us where the whole takes 359 us
+// (16 sequences x 100k tokens, 64/8 heads: 1.84 GB at 5.1 TB/s, 76% of the copy
+// rate; 4 heads a group 331 us, 16 heads 584).  Short ones are bound by a chain
+// of latencies (1 sequence x 16k tokens, 32/8 heads: 13.5 us): counts of the
 // units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the run's other
 // pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
 //
@@ -65,13 +65,15 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSlots = 2;          // pages of a warp's ring: one attended, one on its way (three: 364 us at 100k tokens
-                                   // instead of 369, but 1% more for short sequences, whose CTAs start later)
+// Pages of a warp's ring: one attended, two on their way (16 sequences x 100k tokens 359 us; with two slots 371, short
+// sequences 1% less).
+constexpr int kSlots = 3;
 constexpr int kBatch = 32;         // places looked up at a time
 constexpr int kLenShift = 58;      // device addresses are below 2^57
 // Places that a unit takes beside its pages: 61 ragged sequences of 1 to 4097 tokens (488 units) take 31 us with 8,
-// 24.1 with 16, 23.7 with 24 and 24.5 with 32.
-constexpr int kOver = 24;
+// 23.5 with 24, 22.1 with 28, 22.8 with 34 and 23.9 with 44; 32 ragged sequences of up to 2000 tokens 15.5 with 28 and
+// 11.7 with 34; 128 units of 64 to 128 pages 18.9, 18.4, 18.2 and 17.9.
+constexpr int kOver = 34;
 constexpr int kUnits = 512;        // units whose page counts a CTA keeps at hand
 constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflict-free 16-byte stores)
 constexpr int kMaxRuns = 384;      // CTAs, at most
@@ -134,6 +136,7 @@ template <int NQ, int HN> struct Smem {
     long long sum[kWarps];
     long long start0;  // places before unit u0
     int u0, last;
+    UnitAt unit;
 };
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -780,9 +783,8 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         while (unit.n == 0 || unit.end() <= 0) unit = unit_at(unit.i + 1, unit.end()), first = false;
         if (unit.first >= run) break;
         if (!first) qpart = queries_of(unit);
+        if (tid == 0) S.unit = unit;  // (kept there while the pages take the registers)
         const int pa = max(unit.first, 0), pb = min(unit.end(), run);
-        const int u = u0 + unit.i, b = unit.b;
-        const size_t row0 = (size_t)b * A.hq + (size_t)(u - b * A.hkv) * g;
         st.init();
         int n = pa > warp ? (pa - warp + kWarps - 1) / kWarps : 0;
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
@@ -866,6 +868,9 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         }
         __syncthreads();
         // ---- joined: 32 threads a head, 4 elements each
+        unit = S.unit;
+        const int u = u0 + unit.i, b = unit.b;
+        const size_t row0 = (size_t)b * A.hq + (size_t)(u - b * A.hkv) * g;
         const bool whole = unit.first >= 0 && unit.end() <= run;
         const size_t part = ((size_t)blockIdx.x * 2 + (unit.first > 0 ? 1 : 0)) * g;
         for (int hh = warp; hh < g; hh += kWarps) {
