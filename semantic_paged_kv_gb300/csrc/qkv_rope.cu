@@ -168,11 +168,14 @@ __device__ __forceinline__ void norm_row(float (&a)[8], float (&b)[8], const flo
     for (int i = 0; i < 8; ++i) {
         const pair_t f = i < 4 ? pk2(a[2 * (i & 3)], a[2 * (i & 3) + 1]) : pk2(b[2 * (i & 3)], b[2 * (i & 3) + 1]);
         if (kExact) {
-            const pair_t t = mul2(f, f);
+            // bf16 squares are exact; those of fp32 values are rounded once, as scalars (a packed product that a packed
+            // sum takes comes out fused, and its rounding error, added here, would count twice)
+            const float2 x = upk2(f);
+            const pair_t t = sizeof(T) == 2 ? mul2(f, f) : pk2(__fmul_rn(x.x, x.x), __fmul_rn(x.y, x.y));
             pair_t er;
             two_sum2(sum2, t, sum2, er);
             lo2 = add2(lo2, er);
-            if (sizeof(T) == 4) lo2 = add2(lo2, fma2(f, f, sub2(pk2(0.f, 0.f), t)));  // bf16 squares are exact
+            if (sizeof(T) == 4) lo2 = add2(lo2, fma2(f, f, sub2(pk2(0.f, 0.f), t)));
         } else {
             sum2 = fma2(f, f, sum2);
         }

@@ -1,0 +1,75 @@
+"""The operators of the 4-bit pages where their number ranges end, where heads and tokens of one call differ in size,
+and over more units than a CTA keeps at hand, against the 64-bit restatement in cache4_ref.py."""
+import pytest
+import torch
+
+import cache4_ref as ref
+import semantic_paged_kv_gb300 as ice
+from test_gpu_cache4 import D, DT, _cache, _err, _gen, _params, _qkv, _rows_of, _table
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------ append: the norm --
+def _normed(x, w, eps):
+    """Norm of keys as ice.h states it, an fp32 rounding at each step, the sum of squares rounded once."""
+    ms = x.double().square().sum(-1, keepdim=True).float() / D
+    r = (1 / (ms + torch.tensor(eps, dtype=torch.float32, device="cuda")).double().sqrt()).float()
+    return (x.float() * r) * w.float()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norm_of_keys_to_the_last_bit(dtype):
+    """Keys after the norm alone: the error-free sum of squares leaves no rounding but its own."""
+    B, T, hkv = 1, 3000, 2
+    x = torch.randn((B, T, hkv, D), generator=_gen(211), device="cuda")
+    x *= torch.exp2(torch.randint(-3, 4, x.shape, generator=_gen(212), device="cuda").float())
+    k = x.to(DT[dtype])
+    w = (1 + 0.3 * torch.randn(D, generator=_gen(213), device="cuda")).to(DT[dtype])
+    out, err = torch.empty_like(k), _err()
+    ice.ice_qkv_rope(_params(B, hkv, hkv, dtype), T, None, ice.rows(k), None, None, None, None,
+                     ice.Rope(None, k_norm=w, eps=1e-6), None, ice.rows(out), None, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    assert torch.equal(out, _normed(k, w, 1e-6).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype,rd,inter,norm", [("bf16", 128, False, True), ("bf16", 64, True, True),
+                                                 ("bf16", 128, False, False), ("fp32", 128, False, True),
+                                                 ("fp32", 96, True, True), ("fp32", 128, False, False)])
+def test_append_at_positions_unlike_the_slots(dtype, rd, inter, norm):
+    """The tail behind an index: cache slots from 0, rotation positions behind the prompt, any order; norms in fp32
+    too.  The records against the restatement."""
+    B, T, hq, hkv = 3, 45, 4, 2
+    p = _params(B, hq, hkv, dtype)
+    _, q, k, v = _qkv(B, T, hq, hkv, dtype, 221, 3.0)
+    table = _table(rd, 120000)[1]
+    pos = torch.randint(0, 120000, (B, T), generator=_gen(222), device="cuda").int()
+    w = (1 + 0.3 * torch.randn(D, generator=_gen(223), device="cuda")).to(DT[dtype])
+    rope = ice.Rope(table, interleaved=inter, q_norm=w if norm else None, k_norm=w if norm else None)
+    start = torch.tensor([0, 3, 16], dtype=torch.int32, device="cuda")
+    blocks = 5
+    recs, bt = _cache(B, blocks, hkv, 224)
+    qo, err, r = torch.empty((B, T, hq, D), dtype=DT[dtype], device="cuda"), _err(), ice.rows
+    ice.ice_cache4_append(p, T, r(q), r(k), r(v), pos, start, None, rope, r(qo), ice.Cache4(recs, bt), err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    y = _normed(k, w, 1e-6) if norm else k.float()
+    cs = table[pos.long()]
+    if dtype == "fp32":  # products and their sum before one rounding
+        y = ref.rotate(y, cs, inter).float()
+    else:  # each product and their sum rounded to fp32, then to bf16
+        c, s = cs[..., None, :, 0], cs[..., None, :, 1]
+        z = y.clone()
+        a, b = (slice(0, rd, 2), slice(1, rd, 2)) if inter else (slice(0, rd // 2), slice(rd // 2, rd))
+        z[..., a] = y[..., a] * c - y[..., b] * s
+        z[..., b] = y[..., b] * c + y[..., a] * s
+        y = z.to(DT[dtype])
+    K, V = _rows_of(recs, bt, 0)
+    for b in range(B):
+        a = int(start[b])
+        assert torch.equal(K[b, :, a:a + T], ref.held(y[b]).transpose(0, 1))
+        assert torch.equal(V[b, :, a:a + T], ref.held(v[b]).transpose(0, 1))
+    # the queries at those positions, relative to 64 bits: norm and rotation round at most 8 times in fp32
+    want = ref.rotate(ref.norm(q, w, 1e-6) if norm else q.double(), cs, inter)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    tol = half * want.abs() + 8 * 2.0 ** -24 * 2 * want.abs().amax(-1, keepdim=True)
+    assert bool(((qo.double() - want).abs() <= tol).all())
