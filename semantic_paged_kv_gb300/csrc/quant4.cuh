@@ -139,7 +139,9 @@ template <> struct Vec8<float> {
 // rounding error.  The quotient by 15 is corrected by its remainder, which
 // rounds it correctly (Markstein 1990: a quotient within an ulp and a correctly
 // rounded reciprocal); differences below 1e-30, whose remainder could
-// underflow, are divided.
+// underflow, are divided.  The extremes' sum can overflow where mid does not:
+// mid takes their halves, which bf16 values (and fp32 ones of that size) have
+// exactly.
 template <typename T>
 __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     float d, er = 0.f;
@@ -151,7 +153,9 @@ __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     float step = fmaf(fmaf(-15.f, q, d) + er, 1.f / 15.f, q);
     if (d < 1e-30f) step = d / 15.f;
     if (!(d < INFINITY)) return make_float2(0.f, __int_as_float(0x7fc00000));
-    return make_float2(step, (hi + lo) * 0.5f);
+    float mid = fmaf(hi, 0.5f, lo * 0.5f);
+    if (sizeof(T) == 4 && fabsf(hi + lo) < INFINITY) mid = (hi + lo) * 0.5f;
+    return make_float2(step, mid);
 }
 
 // The word of a vector's 8 codes, rint((x - mid) / step + 7.5) with ties to
@@ -236,14 +240,15 @@ __device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float mid, f
 }
 
 // Codes of any group: also steps below 2^-100 (the reciprocal leaves fp32's
-// normal range; both sides scaled) and extremes outside the codes' range by
-// the rounding of step and mid.
+// normal range; both sides scaled up), mid beside fp32's largest value (mid + k
+// step could overflow; scaled down, step stays above 2^-100) and extremes
+// outside the codes' range by the rounding of step and mid.
 template <typename T>
 __device__ __noinline__ uint32_t codes_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
                                             float x7, float step, float mid) {
     if (!(step > 0.f)) return 0u;
     const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
-    const float up = step < 7.9e-31f ? 1.2676506e30f : 1.f;  // 2^100
+    const float up = step < 7.9e-31f ? 1.2676506e30f : (fabsf(mid) > 1e38f ? 0.0009765625f : 1.f);  // 2^100, 2^-10
     step *= up, mid *= up;
     float y[8];
 #pragma unroll

@@ -1,13 +1,65 @@
 """The operators of the 4-bit pages where their number ranges end, where heads and tokens of one call differ in size,
 and over more units than a CTA keeps at hand, against the 64-bit restatement in cache4_ref.py."""
+import math
+
 import pytest
 import torch
 
 import cache4_ref as ref
 import semantic_paged_kv_gb300 as ice
-from test_gpu_cache4 import D, DT, _cache, _err, _gen, _params, _qkv, _rows_of, _table
+from test_gpu_cache4 import D, DT, R, S, _cache, _err, _gen, _ix, _params, _qkv, _rows_of, _table
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------- quantiser --
+def _pack(k, v, dtype):
+    """Records and the values read back of pages k, v [n, 16, 128]."""
+    n = k.shape[0]
+    p = _params(1, 1, 1, dtype, page_cap=n)
+    lens = torch.full((1, n), S, dtype=torch.int32, device="cuda")
+    cnt = torch.full((1,), n, dtype=torch.int32, device="cuda")
+    recs, err = torch.empty((1, n, R), dtype=torch.uint8, device="cuda"), _err()
+    ice.ice_pool4_pack(p, _ix(n_pages=cnt, page_len=lens, pool_k=k, pool_v=v), 0, recs, err)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    ice.ice_pool4_unpack(p, _ix(n_pages=cnt, page_len=lens, pool_k=ko, pool_v=vo), recs, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    return recs[0], ko, vo
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_groups_at_the_top_of_the_range(dtype):
+    """Extremes whose sum overflows fp32 while their difference does not: mid is finite, and so is what the group
+    stands for."""
+    n, g = 64, _gen(201)
+    big = float(torch.finfo(torch.bfloat16).max)
+    x = torch.rand((n, S, D), generator=g, device="cuda") * 1.5e38 + 1.8e38  # 1.8e38 .. 3.3e38
+    x[1] = x[1].sign() * 3e38
+    x[2] = big
+    x[3] = 3.3e38 + torch.rand((S, D), generator=g, device="cuda") * 4e36  # a narrow group beside the largest value
+    x[4, :, ::3] = 1e38
+    x[5, :, 1::2] = 2.0 ** 127
+    x[6] = 1.7e38 + torch.rand((S, D), generator=g, device="cuda") * 1e37  # sums on either side of the overflow
+    x[:, 8:] *= -1
+    k = x.to(DT[dtype]).clamp(-big, big)
+    if dtype == "fp32":  # mid rounds up, so that mid + 7 step lies beyond fp32's largest value
+        k[7] = torch.linspace(3.31244e38, torch.finfo(torch.float32).max, D, device="cuda")[torch.randperm(D, generator=g,
+                                                                                                        device="cuda")]
+        k[7, :, 0], k[7, :, 1], k[7, :, 64], k[7, :, 65] = k[7].amax(), k[7].amin(), k[7].amax(), k[7].amin()
+    v = k.flip(1).contiguous()
+    recs, ko, vo = _pack(k, v, dtype)
+    assert torch.equal(recs, ref.encode(k, v))
+    for o, y in ((ko, k), (vo, v)):
+        assert torch.equal(o, ref.held(y).float().to(DT[dtype]))
+    assert bool(ko[1].isfinite().all()) and bool((ko[1].float().abs() > 2.9e38).all()) and torch.equal(ko[2], k[2])
+
+
+def test_lowest_fp32_value():
+    """fp32 values beyond the largest bf16 number: mid rounds to infinity, as bf16((max + min) / 2) does."""
+    k = torch.full((1, S, D), torch.finfo(torch.float32).min, device="cuda")
+    v = -k
+    recs, ko, vo = _pack(k, v, "fp32")
+    assert torch.equal(recs, ref.encode(k, v)) and bool((ko == -math.inf).all()) and bool((vo == math.inf).all())
 
 
 # ------------------------------------------------------ append: the norm --
