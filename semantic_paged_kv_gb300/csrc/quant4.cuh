@@ -163,27 +163,25 @@ __device__ __forceinline__ float2 step_mid(float lo, float hi) {
 // mid) / step (from an approximate reciprocal; which of two neighbours it is
 // does not matter), the code is k + 8 where the remainder x - mid - k step is
 // positive, k + 7 where it is negative, and the even one of the two where it
-// is zero.  The remainder's sign is exact (bf16: as far as x - mid is): k step is (4 bits times 8), and a
-// fused multiply-add rounds a nonzero difference to one of the same sign.  fp32
-// values take mid + k step as an unevaluated sum.
-template <typename T>
+// is zero.  The remainder's sign is exact: k step is (4 bits times 8), and mid
+// + k step goes in as an unevaluated sum (x - mid alone would lose a tiny x).
 __device__ __forceinline__ uint32_t codes_in(const float (&x)[8], float step, float mid, float inv) {
     constexpr float kBig = 12582912.f;  // 1.5 * 2^23: integers end up in the low bits
+    const pair_t mid2 = pk2(mid, mid), inv2 = pk2(inv, inv), step2 = pk2(step, step), big2 = pk2(kBig, kBig);
     uint32_t w = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float d = x[e] - mid, t = fmaf(d, inv, kBig), k = t - kBig;
-        float rem;
-        if (sizeof(T) == 2) {
-            rem = fmaf(-k, step, d);
-        } else {
-            float s, er;
-            two_sum(mid, k * step, s, er);
-            rem = (x[e] - s) - er;
-        }
+    auto code = [&](int e, float t, float rem) {
         const int b = __float_as_int(t);
         const bool below = __float_as_int(rem) < (b & 1);  // negative, or zero and k odd
         w |= (uint32_t)min(max(b - 0x4B400000 + 8 - (below ? 1 : 0), 0), 15) << (4 * e);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const pair_t x2 = pk2(x[2 * i], x[2 * i + 1]), t = fma2(sub2(x2, mid2), inv2, big2);
+        pair_t s, er;
+        two_sum2(mid2, mul2(sub2(t, big2), step2), s, er);  // (exact products: it does not matter if they are fused)
+        const float2 b = upk2(t), rem = upk2(sub2(sub2(x2, s), er));
+        code(2 * i, b.x, rem.x);
+        code(2 * i + 1, b.y, rem.y);
     }
     return w;
 }
@@ -242,18 +240,25 @@ __device__ __forceinline__ uint32_t codes_near(const float (&x)[8], float mid, f
 // Codes of any group: also steps below 2^-100 (the reciprocal leaves fp32's
 // normal range; both sides scaled up), mid beside fp32's largest value (mid + k
 // step could overflow; scaled down, step stays above 2^-100) and extremes
-// outside the codes' range by the rounding of step and mid.
+// outside the codes' range by the rounding of step and mid: far outside for
+// fp32 values only (mid is within half a last place of bf16 values, whose
+// extremes differ by one at least).
 template <typename T>
 __device__ __noinline__ uint32_t codes_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
                                             float x7, float step, float mid) {
     if (!(step > 0.f)) return 0u;
-    const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+    float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
     const float up = step < 7.9e-31f ? 1.2676506e30f : (fabsf(mid) > 1e38f ? 0.0009765625f : 1.f);  // 2^100, 2^-10
-    step *= up, mid *= up;
-    float y[8];
+    if (up != 1.f) {
+        step *= up, mid *= up;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(x[e] * up, mid - 9.f * step), mid + 9.f * step);
-    return codes_in<T>(y, step, mid, 1.f / step);
+        for (int e = 0; e < 8; ++e) x[e] *= up;
+    }
+    if (sizeof(T) == 4) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], mid - 9.f * step), mid + 9.f * step);
+    }
+    return codes_in(x, step, mid, 1.f / step);
 }
 
 // (step, mid) as stored: one word a group.

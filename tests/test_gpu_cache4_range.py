@@ -62,6 +62,25 @@ def test_lowest_fp32_value():
     assert torch.equal(recs, ref.encode(k, v)) and bool((ko == -math.inf).all()) and bool((vo == math.inf).all())
 
 
+def test_codes_of_tiny_values_beside_large_ones():
+    """x - mid does not fit fp32: the code of a tiny value hangs on its sign where mid lies on a border."""
+    n, g = 2000, _gen(202)
+    x = torch.randint(-13, 18, (n, S, D), generator=g, device="cuda").float()
+    x[..., 0::64], x[..., 1::64] = 17, -13  # step 2, mid 2: 0 lies half a step from two codes
+    tiny = torch.exp2(torch.randint(-80, -15, (n, S, D), generator=g, device="cuda").float())
+    tiny *= torch.randint(-1, 2, (n, S, D), generator=g, device="cuda")
+    at = torch.arange(D, device="cuda") % 4 == 2
+    x = torch.where(at, tiny, x)
+    x[0, 0, 2] = 3e-8
+    x[n // 2:] *= torch.exp2(torch.randint(-60, 60, (n - n // 2, S, 1), generator=g, device="cuda").float())
+    k = x.bfloat16()
+    v = k.flip(-1).contiguous()
+    recs, _, _ = _pack(k, v, "bf16")
+    meta, codes = ref.groups(k)
+    assert meta[0, 0, 0].tolist() == [2.0, 2.0] and int(codes[0, 0, 2]) == 7
+    assert torch.equal(recs, ref.encode(k, v))
+
+
 # ------------------------------------------------------ append: the norm --
 def _normed(x, w, eps):
     """Norm of keys as ice.h states it, an fp32 rounding at each step, the sum of squares rounded once."""
