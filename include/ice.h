@@ -674,7 +674,9 @@ ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes);
  * token gives O = 0 and lse = -inf.  The pages are split evenly over the GPU,
  * whatever the lengths; every run of a call gives the same bits.
  * A page outside [0, n_pages) sets ICE_ERR_CAPACITY in err_dev and its tokens
- * are left out.
+ * are left out.  A head whose query is not finite (bf16: or has |scale q| of
+ * 2^117 and more) gives NaN in O and lse of a sequence that has tokens; the
+ * other heads do not depend on it.
  */
 ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_cache4 *cache, const int32_t *lens,
                                   float scale, float *O, float *lse, void *ws, size_t ws_bytes, int32_t *err_dev,

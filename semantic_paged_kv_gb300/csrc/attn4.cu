@@ -120,8 +120,8 @@ struct UnitAt {
 // What the CTA's threads share to prepare the queries of a unit.
 template <int NQ, int HN> struct QueryScratch {
     uint2 f[NQ][HN][8][32];  // fragments by lane
-    float sum[8 * HN][2];
-    float big[Shape<HN>::kWarps];
+    float2 sum[8 * HN];
+    float factor[8 * HN];
 };
 
 template <int NQ, int HN> struct Smem {
@@ -234,12 +234,13 @@ template <int HN> struct State {
     }
 };
 
-// The group's queries as B fragments (columns = heads), in fp16 after a common
-// power of two, and what the scores need of them.
+// The group's queries as B fragments (columns = heads), in fp16 after a power
+// of two of each head (a head beside one that is far larger, or not finite,
+// keeps its bits), and what the scores need of them.
 template <int NQ, int HN> struct Queries {
     uint32_t f;           // shared address of this lane's fragments (QueryScratch::f)
     float sum[HN][2][2];  // sum q over a group, in the products' scale, for this lane's columns (heads 2 c, 2 c + 1)
-    float factor;         // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
+    pair_t factor[HN];    // > 0: scale log2(e) over the powers of two of q and of the codes (its sign goes to q)
 };
 
 // Codes of K as operands: c 2^-24 (kLow; kHigh times 16, and its queries over 16), or with fp32 queries centred() ones,
@@ -262,27 +263,29 @@ __device__ __forceinline__ q4::Vec8<T> query_part(const T *Qg, int g) {
 template <typename T, int NQ, int HN>
 __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float scale, QueryScratch<NQ, HN> &X,
                                                 Queries<NQ, HN> &q) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, c = lane & 3;
     const float sl = scale * 1.4426950408889634f;
     float x[8];
     part.get(x);
     float big = 0.f, s = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e])), s += x[e];
+    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]));
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    const int e2 = min(max(14 - exponent_of(big), -113), 126);  // the largest element lands in [2^14, 2^15)
+    const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(x[e], up, s);
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     const int head = tid >> 4, vec = tid & 15;
-    if (head < 8 * HN && (tid & 7) == 0) X.sum[head][vec >> 3] = s;
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-    if (lane == 0) X.big[warp] = big;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < Shape<HN>::kWarps; ++w) big = fmaxf(big, X.big[w]);
-    const int e2 = min(max(14 - exponent_of(big), -100), 126);  // the largest query lands in [2^14, 2^15)
-    const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
-    q.factor = sl == 0.f ? 1.f : fabsf(sl) * pow2(kCodeScale<NQ>) * pow2(-e2);
     if (head < 8 * HN) {
+        if ((vec & 7) == 0) (vec ? X.sum[head].y : X.sum[head].x) = s * pow2(-kCodeScale<NQ>);
+        if (vec == 0) {
+            // a head that is not finite, or whose factor would not be (bf16: |scale q| from 2^117 on), is not a number
+            const float f = sl == 0.f ? 1.f : fabsf(sl) * pow2(kCodeScale<NQ>) * pow2(-e2);
+            X.factor[head] = big < INFINITY && f < INFINITY ? f : __int_as_float(0x7fc00000);
+        }
         // element 8 vec + e is code e of word vec: half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
         uint32_t f[NQ][4];
 #pragma unroll
@@ -308,10 +311,11 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
 #pragma unroll
     for (int hn = 0; hn < HN; ++hn) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int gr = 0; gr < 2; ++gr)
-                q.sum[hn][gr][e] = X.sum[8 * hn + 2 * c + e][gr] * up * pow2(-kCodeScale<NQ>);
+        for (int e = 0; e < 2; ++e) {
+            const float2 sum = X.sum[8 * hn + 2 * c + e];
+            q.sum[hn][0][e] = sum.x, q.sum[hn][1][e] = sum.y;
+        }
+        q.factor[hn] = pk2(X.factor[8 * hn + 2 * c], X.factor[8 * hn + 2 * c + 1]);
     }
 }
 
@@ -385,17 +389,17 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
-            const float2 old = upk2(st.minus_m[hn]);
+            const float2 old = upk2(st.minus_m[hn]), factor = upk2(q.factor[hn]);
             float now[2], al[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float mx = fmaxf(s[hn][e], s[hn][2 + e]);
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float was = e ? old.y : old.x;
-                now[e] = fminf(was, -mx * q.factor);
+                const float was = e ? old.y : old.x, fe = e ? factor.y : factor.x;
+                now[e] = fminf(was, -mx * fe);
                 al[e] = exp2_fast(now[e] - was);
-                st.limit[hn][e] = (kLazy - now[e]) / q.factor;
+                st.limit[hn][e] = (kLazy - now[e]) / fe;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     st.o[hn][t][e] *= al[e];
@@ -436,7 +440,7 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const float2 y = upk2(fma2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), pk2(q.factor, q.factor), st.minus_m[hn]));
+            const float2 y = upk2(fma2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), q.factor[hn], st.minus_m[hn]));
             const float p[2] = {exp2_fast(y.x), exp2_fast(y.y)};
             st.l[hn] = add2(st.l[hn], pk2(p[0], p[1]));
             pair_t x[2];

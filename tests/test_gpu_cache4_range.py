@@ -7,7 +7,7 @@ import torch
 
 import cache4_ref as ref
 import semantic_paged_kv_gb300 as ice
-from test_gpu_cache4 import D, DT, R, S, _cache, _err, _gen, _ix, _params, _qkv, _rows_of, _table
+from test_gpu_cache4 import D, DT, R, S, _attn_buffers, _cache, _err, _gen, _ix, _params, _qkv, _rows_of, _table
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,86 @@ def test_append_at_positions_unlike_the_slots(dtype, rd, inter, norm):
     half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     tol = half * want.abs() + 8 * 2.0 ** -24 * 2 * want.abs().amax(-1, keepdim=True)
     assert bool(((qo.double() - want).abs() <= tol).all())
+
+
+# -------------------------------------------------------------- attention --
+def _one_unit(k, v, Q, dtype, scale=0.088, lens=None):
+    """Attention of one KV head over pages k, v [n, 16, 128] (held in 4 bits): O, lse, and the values attended to."""
+    n, hq = k.shape[0], Q.shape[0]
+    p = _params(1, hq, 1, dtype)
+    recs = ref.encode(k, v).view(n, 1, R)
+    bt = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+    O, lse, ws, err = _attn_buffers(1, hq, p)
+    ln = torch.tensor([lens or n * S], dtype=torch.int32, device="cuda")
+    ice.ice_cache4_attn_decode(p, Q[None].contiguous(), ice.Cache4(recs, bt), ln, scale, O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    K, V = (x.reshape(-1, D)[:int(ln)] for x in ref.decode(recs[:, 0]))
+    return O[0].double(), lse[0].double(), K, V
+
+
+def _rms_check(O, q, K, V, scale, what=""):
+    o, _ = ref.attention(q, K, V, scale)
+    tol = ref.attention_rms_tolerance(q, K, V, scale)
+    for h in range(q.shape[0]):
+        e = float((O[h] - o[h]).norm())
+        assert e <= float(tol[h]), (what, h, e / float(o[h].norm()), float(tol[h] / o[h].norm()))
+
+
+HEADS = [("bf16", 4), ("bf16", 8), ("bf16", 16), ("fp32", 3), ("fp32", 8), ("fp32", 12)]
+
+
+def _one_hot_check(O, lse, q, K, V, scale):
+    """A head whose largest score takes all the weight (its lead is more than the scores' errors)."""
+    o, l = ref.attention(q[None], K, V, scale)
+    s = (q @ K.T * scale).sort(descending=True).values
+    e = 16 * 2.0 ** -23 * 3 * scale * float(q.abs() @ K.abs().amax(0))
+    assert float(s[0] - s[1]) > 2 * e + 60
+    assert float((O - o[0]).abs().max()) <= (2.0 ** -20 + 2.0 ** -21) * float(V.abs().max())  # the weights' 22 bits
+    assert abs(float(lse - l[0])) <= e
+
+
+@pytest.mark.parametrize("dtype,hq", HEADS)
+def test_heads_of_one_group_do_not_disturb_each_other(dtype, hq):
+    """A head whose query is not finite, is large or tiny leaves the other heads of its group as they are."""
+    n = 40
+    k, v = (torch.randn((n, S, D), generator=_gen(s), device="cuda").bfloat16() for s in (231, 232))
+    plain = torch.randn((hq, D), generator=_gen(233), device="cuda").to(DT[dtype])
+    _, wlse, K, V = _one_unit(k, v, plain, dtype)
+    for what in (math.inf, -math.inf, math.nan, 2.0 ** 24, 2.0 ** -60, 2.0 ** -110):
+        Q = plain.clone()
+        finite = math.isfinite(what)
+        if finite:
+            Q[1] = (Q[1].double() * what).to(DT[dtype])
+        else:
+            Q[1, 77] = what
+        O, lse, _, _ = _one_unit(k, v, Q, dtype)
+        other = [h for h in range(hq) if h != 1]
+        # (not to the last bit: the group's running maxima move together)
+        _rms_check(O[other], Q[other].double(), K, V, 0.088, what)
+        assert float((lse[other] - wlse[other]).abs().max()) <= 2.0 ** -18, what
+        if not finite:
+            assert bool(O[1].isnan().all()) and bool(lse[1].isnan())
+        elif what < 1:  # scores of 2^-50: the mean
+            o, l = ref.attention(Q[1:2].double(), K, V, 0.088)
+            to, tl = ref.attention_tolerance(Q[1:2].double(), K, V, 0.088)
+            assert float((O[1] - o[0]).abs().max()) <= to and abs(float(lse[1] - l[0])) <= tl
+        else:
+            _one_hot_check(O[1], lse[1], Q[1].double(), K, V, 0.088)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_largest_queries(dtype):
+    """Queries up to the type's largest value, over keys small enough that no score overflows."""
+    n, hq = 20, 4
+    k, v = (torch.randn((n, S, D), generator=_gen(s), device="cuda") for s in (241, 242))
+    k = (k * 2.0 ** (-115 if dtype == "bf16" else -125)).bfloat16()  # (fp32: steps are subnormal)
+    Q = torch.randn((hq, D), generator=_gen(243), device="cuda")
+    Q = (Q / Q.abs().max() * float(torch.finfo(torch.bfloat16).max)).to(DT[dtype])
+    if dtype == "bf16":  # |scale q| stays below 2^116
+        Q = (Q.double() * 2.0 ** -10).bfloat16()
+    Q[2] = (Q[2].double() * 2.0 ** -100).to(DT[dtype])
+    O, lse, K, V = _one_unit(k, v.bfloat16(), Q, dtype)
+    for h in range(hq):
+        o, l = ref.attention(Q[h:h + 1].double(), K, V, 0.088)
+        to, tl = ref.attention_tolerance(Q[h:h + 1].double(), K, V, 0.088)
+        assert float((O[h] - o[0]).abs().max()) <= to and abs(float(lse[h] - l[0])) <= tl, h
