@@ -199,6 +199,12 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) <
 // Exponent of a positive finite float (-127 for subnormals).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
+// The running maxima in powers of two, from minus the scores (-FLT_MAX: no score yet).
+__device__ __forceinline__ float2 max_of(unsigned long long minus, unsigned long long factor) {
+    const float2 m = upk2(mul2(minus, factor));
+    return make_float2(fmaxf(-m.x, -FLT_MAX), fmaxf(-m.y, -FLT_MAX));
+}
+
 // Pages after which a warp's sums leave the tensor core's accumulators, whose sums truncate: the relative error of O at
 // 100k tokens is 8e-7 so, 8e-6 without.
 constexpr int kFlush = 32;
@@ -214,8 +220,8 @@ using q4::pair_t;
 // 32 j + 4 r + 2 k + i / 2.
 template <int HN> struct State {
     float o[HN][8][4];
-    pair_t minus_m[HN];          // minus the running maximum (in powers of two), heads 2 c and 2 c + 1
-    float limit[HN][2];          // score (before Queries::factor) above which the maximum moves
+    pair_t minus_m[HN];          // minus the running maximum score (before Queries::factor), heads 2 c and 2 c + 1
+    float limit[HN][2];          // score above which the maximum moves
     pair_t l[HN];                // sum of P over this lane's tokens
     pair_t off[HN][2];           // sum of P mid, groups 0 and 1, this lane's tokens
     pair_t vscale;               // of each group: power of two on step P
@@ -397,9 +403,9 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
                 const float was = e ? old.y : old.x, fe = e ? factor.y : factor.x;
-                now[e] = fminf(was, -mx * fe);
-                al[e] = exp2_fast(now[e] - was);
-                st.limit[hn][e] = (kLazy - now[e]) / fe;
+                now[e] = fminf(was, -mx);
+                al[e] = exp2_fast((now[e] - was) * fe);
+                st.limit[hn][e] = kLazy / fe - now[e];
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     st.o[hn][t][e] *= al[e];
@@ -440,7 +446,8 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const float2 y = upk2(fma2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), q.factor[hn], st.minus_m[hn]));
+            // (differences of scores first: those of large scores are exact, their products with the factor are not)
+            const float2 y = upk2(mul2(add2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), st.minus_m[hn]), q.factor[hn]));
             const float p[2] = {exp2_fast(y.x), exp2_fast(y.y)};
             st.l[hn] = add2(st.l[hn], pk2(p[0], p[1]));
             pair_t x[2];
@@ -822,11 +829,11 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
             const float back[2] = {1024.f / vs.x, 1024.f / vs.y};  // codes went in times 2^-10 (both factors normal)
 #pragma unroll
             for (int hn = 0; hn < HN; ++hn) {
-                const float2 m2 = upk2(st.minus_m[hn]);
+                const float2 m2 = max_of(st.minus_m[hn], q.factor[hn]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int head = 8 * hn + 2 * c + e;
-                    const float m = -(e ? m2.y : m2.x);
+                    const float m = e ? m2.y : m2.x;
                     const float before = flushed ? exp2_fast(S.ml[warp][head].x - m) : 0.f;
                     __syncwarp();
                     if (r == 0) S.ml[warp][head].x = m;
@@ -850,7 +857,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         // ---- and its softmax sums
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
-            const float2 m2 = upk2(st.minus_m[hn]);
+            const float2 m2 = max_of(st.minus_m[hn], q.factor[hn]);
             pair_t l2 = st.l[hn], off2[2] = {st.off[hn][0], st.off[hn][1]};
             auto other = [](pair_t x, int by) {
                 const float2 y = upk2(x);
@@ -866,8 +873,8 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
             }
             if (r == 0) {
                 const float2 l = upk2(l2), x = upk2(off2[0]), y = upk2(off2[1]);
-                S.ml[warp][8 * hn + 2 * c] = make_float4(-m2.x, l.x, x.x, x.y);
-                S.ml[warp][8 * hn + 2 * c + 1] = make_float4(-m2.y, l.y, y.x, y.y);
+                S.ml[warp][8 * hn + 2 * c] = make_float4(m2.x, l.x, x.x, x.y);
+                S.ml[warp][8 * hn + 2 * c + 1] = make_float4(m2.y, l.y, y.x, y.y);
             }
         }
         __syncthreads();

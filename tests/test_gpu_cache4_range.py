@@ -211,6 +211,25 @@ def test_heads_of_one_group_do_not_disturb_each_other(dtype, hq):
             _one_hot_check(O[1], lse[1], Q[1].double(), K, V, 0.088)
 
 
+@pytest.mark.parametrize("dtype,hq", HEADS)
+def test_scores_beyond_2_to_31(dtype, hq):
+    """Scores whose last place is far more than the range of exp: the largest takes it all."""
+    n = 40
+    k, v = (torch.randn((n, S, D), generator=_gen(s), device="cuda").bfloat16() for s in (231, 232))
+    plain = torch.randn((hq, D), generator=_gen(233), device="cuda").to(DT[dtype])
+    for size in (2.0 ** 34, 2.0 ** 60, 2.0 ** 100):
+        for heads in (range(hq), (1,)):
+            Q = plain.clone()
+            for h in heads:
+                Q[h] = (Q[h].double() * size).to(DT[dtype])
+            O, lse, K, V = _one_unit(k, v, Q, dtype)
+            for h in heads:
+                _one_hot_check(O[h], lse[h], Q[h].double(), K, V, 0.088)
+            other = [h for h in range(hq) if h not in heads]
+            if other:
+                _rms_check(O[other], Q[other].double(), K, V, 0.088, size)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_largest_queries(dtype):
     """Queries up to the type's largest value, over keys small enough that no score overflows."""
