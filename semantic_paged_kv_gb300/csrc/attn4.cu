@@ -196,6 +196,8 @@ __device__ __forceinline__ uint32_t centred(uint32_t x, bool high) {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// The inverse of a power of two 2^e, -126 <= e <= 126.
+__device__ __forceinline__ float inverse_of(float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); }
 // Exponent of a positive finite float (-127 for subnormals).
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 255u) - 127; }
 
@@ -824,9 +826,10 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
             }
             issued = n + kSlots - 1;
             __syncwarp();
-            // ---- the warp's sums of V to shared memory, in the scale of the running maximum
+            // ---- the warp's sums of V to shared memory, in the scale of the running maximum (and times 2^-10, as the codes
+            // went in: with that factor too a power of two for the largest steps would overflow)
             const float2 vs = upk2(st.vscale);
-            const float back[2] = {1024.f / vs.x, 1024.f / vs.y};  // codes went in times 2^-10 (both factors normal)
+            const float back[2] = {inverse_of(vs.x), inverse_of(vs.y)};
 #pragma unroll
             for (int hn = 0; hn < HN; ++hn) {
                 const float2 m2 = max_of(st.minus_m[hn], q.factor[hn]);
@@ -901,8 +904,8 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                 }
                 const float off = lane < 16 ? ml.z : ml.w;
                 L = fmaf(ml.y, wt, L);
-                acc.x = fmaf(x.x + off, wt, acc.x), acc.y = fmaf(x.y + off, wt, acc.y);
-                acc.z = fmaf(x.z + off, wt, acc.z), acc.w = fmaf(x.w + off, wt, acc.w);
+                acc.x = fmaf(fmaf(x.x, 1024.f, off), wt, acc.x), acc.y = fmaf(fmaf(x.y, 1024.f, off), wt, acc.y);
+                acc.z = fmaf(fmaf(x.z, 1024.f, off), wt, acc.z), acc.w = fmaf(fmaf(x.w, 1024.f, off), wt, acc.w);
             }
             if (whole) {
                 put_row(A, row0 + hh, acc, M, L);

@@ -246,3 +246,15 @@ def test_largest_queries(dtype):
         o, l = ref.attention(Q[h:h + 1].double(), K, V, 0.088)
         to, tl = ref.attention_tolerance(Q[h:h + 1].double(), K, V, 0.088)
         assert float((O[h] - o[0]).abs().max()) <= to and abs(float(lse[h] - l[0])) <= tl, h
+
+
+@pytest.mark.parametrize("size", [1e38, 2.0 ** -100])
+def test_largest_and_smallest_values(size):
+    """Steps of 2^123 (three tokens: their sum stays below fp32's largest number) and of 2^-103."""
+    for tokens in (1, 2, 3):
+        k = torch.randn((1, S, D), generator=_gen(281), device="cuda")
+        v = (torch.rand((1, S, D), generator=_gen(282), device="cuda") * 2 - 1) * size
+        v[..., 0::64], v[..., 1::64] = size, -size
+        Q = torch.randn((8, D), generator=_gen(283), device="cuda").bfloat16()
+        O, lse, K, V = _one_unit(k.bfloat16(), v.bfloat16(), Q, "bf16", lens=tokens)
+        _rms_check(O, Q.double(), K, V, 0.088)
