@@ -40,8 +40,8 @@
 //     end of the unit.
 //   O^T += V^T (step P)^T: V codes as operands the same way (the record pairs
 //     two tokens in a word); step P in fp16 hi + lo parts (22 bits), scaled
-//     by a power of two that follows the largest step; the 8 x 8 transposes of
-//     P by movmatrix.  A product blocks the scheduler for 8 clocks (24 of them
+//     by a power of two of each head that follows the steps and their weights;
+//     the 8 x 8 transposes of P by movmatrix.  A product blocks the scheduler for 8 clocks (24 of them
 //     are 43% of the 111 clocks above), so with g <= 4 the columns 4 .. 7 hold
 //     heads 0 .. 3 again and take the lo parts: one product a tile instead of
 //     two.  The codes go in centred and as normal numbers, (code - 7.5) 2^-10:
@@ -130,6 +130,8 @@ template <int NQ, int HN> struct Smem {
     float o[kWarps][Shape<HN>::kHeads][kRow];  // reused for the joining weights
     QueryScratch<NQ, HN> q;
     float4 ml[kWarps][Shape<HN>::kHeads];  // maximum, sum, and each group's sum P mid
+    float4 scale[kWarps][HN][4];  // a warp's powers of two on step P, both groups of heads 2 c and 2 c + 1
+    float4 most[kWarps][HN][4];  // and the largest step P that they were found for
     int2 units[kUnits];  // (selected pages, cache tokens) of the units from unit `base` on
     unsigned long long page[kWarps][2 * kBatch];  // pages looked up: address | length << kLenShift; 0: no page
     UnitAt look[kWarps];  // a warp's place in its lookups
@@ -211,6 +213,7 @@ __device__ __forceinline__ float2 max_of(unsigned long long minus, unsigned long
 // 100k tokens is 8e-7 so, 8e-6 without.
 constexpr int kFlush = 32;
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
+constexpr int kTopScale = 119;  // powers of two on step P, at most
 // Codes as fp16 operands: c 2^-24 at bit 0 of a half, c 2^-20 at bit 4.
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
@@ -223,21 +226,18 @@ using q4::pair_t;
 template <int HN> struct State {
     float o[HN][8][4];
     pair_t minus_m[HN];          // minus the running maximum score (before Queries::factor), heads 2 c and 2 c + 1
-    float limit[HN][2];          // score above which the maximum moves
     pair_t l[HN];                // sum of P over this lane's tokens
     pair_t off[HN][2];           // sum of P mid, groups 0 and 1, this lane's tokens
-    pair_t vscale;               // of each group: power of two on step P
-    float vlimit[2];             // and the step that it holds up to
+    uint32_t scales;             // shared address of the powers of two on step P (Smem::scale) of this lane's heads
+    float vlimit[2];             // of each group: the step that they hold up to
     __device__ __forceinline__ void init() {
 #pragma unroll
         for (int hn = 0; hn < HN; ++hn) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) o[hn][t][0] = o[hn][t][1] = o[hn][t][2] = o[hn][t][3] = 0.f;
             minus_m[hn] = pk2(FLT_MAX, FLT_MAX);
-            limit[hn][0] = limit[hn][1] = -INFINITY;
             l[hn] = off[hn][0] = off[hn][1] = pk2(0.f, 0.f);
         }
-        vscale = pk2(pow2(120), pow2(120));
         vlimit[0] = vlimit[1] = 0.f;
     }
 };
@@ -329,7 +329,8 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
 
 // Folds one page (record at shared address `rec`, its first `len` slots; whatever the others hold).
 template <int NQ, int HN, bool kTwice>
-__device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t rec, int len, State<HN> &st) {
+__device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t rec, int len, State<HN> &st,
+                                             Smem<NQ, HN> &S) {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     // ---- S^T = K Q^T, an accumulator per group
     float s[HN][4];
@@ -389,75 +390,149 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
     }
     const float2 v00 = q4::unpack_meta(n0.x), v01 = q4::unpack_meta(n0.y);  // (step, mid): token r, groups 0, 1
     const float2 v10 = q4::unpack_meta(n1.x), v11 = q4::unpack_meta(n1.y);  // token r + 8
-    // ---- the running maxima and the scale of step P, only when one has to move
+    // ---- scores from the running maxima, in powers of two (differences first: those of large scores are exact, their
+    // products with the factor are not)
+    pair_t y[HN][2];
+    auto from_max = [&]() {
+#pragma unroll
+        for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                y[hn][half] = mul2(add2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), st.minus_m[hn]), q.factor[hn]);
+    };
+    from_max();
+    // ---- the running maxima and the scales of step P, only when one has to move
     bool move = exceeds(v00.x, v10.x, v01.x, v11.x, st.vlimit[0], st.vlimit[1]);
 #pragma unroll
-    for (int hn = 0; hn < HN; ++hn)
-        move |= exceeds(s[hn][0], s[hn][2], s[hn][1], s[hn][3], st.limit[hn][0], st.limit[hn][1]);
+    for (int hn = 0; hn < HN; ++hn) {
+        const float2 a = upk2(y[hn][0]), b = upk2(y[hn][1]);
+        move |= exceeds(a.x, a.y, b.x, b.y, kLazy, kLazy);
+    }
     if (__any_sync(0xffffffffu, move)) {
+        // the page's largest scores, its largest and smallest steps (not negative: ordered as their bits are)
+        float mx[HN][2];
 #pragma unroll
-        for (int hn = 0; hn < HN; ++hn) {
-            const float2 old = upk2(st.minus_m[hn]), factor = upk2(q.factor[hn]);
-            float now[2], al[2];
+        for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(s[hn][e], s[hn][2 + e]);
+            for (int e = 0; e < 2; ++e) mx[hn][e] = fmaxf(s[hn][e], s[hn][2 + e]);
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float was = e ? old.y : old.x, fe = e ? factor.y : factor.x;
-                now[e] = fminf(was, -mx);
-                al[e] = exp2_fast((now[e] - was) * fe);
-                st.limit[hn][e] = kLazy / fe - now[e];
+        for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    st.o[hn][t][e] *= al[e];
-                    st.o[hn][t][2 + e] *= al[e];
+            for (int hn = 0; hn < HN; ++hn)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    mx[hn][e] = fmaxf(mx[hn][e], __shfl_xor_sync(0xffffffffu, mx[hn][e], off));
+        const bool live0 = r < len, live1 = r + 8 < len;
+        auto largest = [](float x, float y) {
+            return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(x, y))));
+        };
+        auto smallest = [&](float x, float y) {
+            return __uint_as_float(__reduce_min_sync(0xffffffffu, min(__float_as_uint(live0 ? x : INFINITY),
+                                                                      __float_as_uint(live1 ? y : INFINITY))));
+        };
+        const float top[2] = {largest(v00.x, v10.x), largest(v01.x, v11.x)};
+        const float low[2] = {smallest(v00.x, v10.x), smallest(v01.x, v11.x)};
+        float4(*scale)[4] = S.scale[threadIdx.x >> 5], (*most)[4] = S.most[threadIdx.x >> 5];
+        // The powers of two on step P: those that the page's steps ask for (steps up to [2^5, 2^6) now, up to 2^7 before a
+        // power moves again: with P <= 2^8 below fp16's 2^16), but more where they would put the largest step P that was
+        // seen at such a move below 2^2 (a value row of little weight may be far larger than those that matter).
+        auto power_for = [](float step) { return min(5 - exponent_of(step), kTopScale); };  // >= -122
+        auto holds_to = [](int e) { return pow2(min(7 - e, 127)); };
+        if (st.vlimit[0] == 0.f && low[0] >= 0.125f * top[0] && low[1] >= 0.125f * top[1]) {
+            // the first page, of steps that differ little: every head gives one of them a weight of 1 (one sequence of
+            // 16k tokens 13.2 us so, 13.8 by the way below)
+            const int e0 = power_for(top[0]), e1 = power_for(top[1]);
+            const float to0 = pow2(e0), to1 = pow2(e1);
+#pragma unroll
+            for (int hn = 0; hn < HN; ++hn) {
+                const float2 was = upk2(st.minus_m[hn]);
+                st.minus_m[hn] = pk2(fminf(was.x, -mx[hn][0]), fminf(was.y, -mx[hn][1]));
+                if (r == 0) {
+                    scale[hn][c] = make_float4(to0, to1, to0, to1);
+                    most[hn][c] = make_float4(low[0], low[1], low[0], low[1]);
                 }
-                st.off[hn][e] = mul2(st.off[hn][e], pk2(al[e], al[e]));
             }
-            st.minus_m[hn] = pk2(now[0], now[1]);
-            st.l[hn] = mul2(st.l[hn], pk2(al[0], al[1]));
-        }
-        float2 vs = upk2(st.vscale);
+            st.vlimit[0] = holds_to(e0), st.vlimit[1] = holds_to(e1);
+            from_max();
+        } else {
+            float al[HN][2];  // factors on the sums
 #pragma unroll
-        for (int gr = 0; gr < 2; ++gr) {
-            float mx = gr ? fmaxf(v01.x, v11.x) : fmaxf(v00.x, v10.x);
+            for (int hn = 0; hn < HN; ++hn) {
+                const float2 was = upk2(st.minus_m[hn]), factor = upk2(q.factor[hn]);
+                const float now[2] = {fminf(was.x, -mx[hn][0]), fminf(was.y, -mx[hn][1])};
+                al[hn][0] = exp2_fast((now[0] - was.x) * factor.x), al[hn][1] = exp2_fast((now[1] - was.y) * factor.y);
+                st.minus_m[hn] = pk2(now[0], now[1]);
+                st.l[hn] = mul2(st.l[hn], pk2(al[hn][0], al[hn][1]));
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            if (mx > st.vlimit[gr]) {
-                // steps up to [2^5, 2^6) now, up to 2^7 before the scale moves again: with P <= 2^8 below fp16's 2^16
-                const int e = min(5 - exponent_of(mx), 119);  // >= -122
-                const float to = pow2(e), down = to / (gr ? vs.y : vs.x);
-                (gr ? vs.y : vs.x) = to;
-                st.vlimit[gr] = pow2(min(7 - e, 127));
+                for (int e = 0; e < 2; ++e) st.off[hn][e] = mul2(st.off[hn][e], pk2(al[hn][e], al[hn][e]));
+            }
+            from_max();
+            uint32_t ps[HN][2];  // exponents of the page's largest step P, both groups
+#pragma unroll
+            for (int hn = 0; hn < HN; ++hn) {
+                const float2 y0 = upk2(y[hn][0]), y1 = upk2(y[hn][1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float p0 = exp2_fast(e ? y0.y : y0.x), p1 = exp2_fast(e ? y1.y : y1.x);
+                    ps[hn][e] = __float_as_uint(fmaxf(p0 * v00.x, p1 * v10.x)) >> 23 |
+                                (__float_as_uint(fmaxf(p0 * v01.x, p1 * v11.x)) >> 23) << 16;
+                }
+            }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
                 for (int hn = 0; hn < HN; ++hn)
 #pragma unroll
-                    for (int t = 4 * gr; t < 4 * gr + 4; ++t)
+                    for (int e = 0; e < 2; ++e)
+                        ps[hn][e] = __vmaxu2(ps[hn][e], __shfl_xor_sync(0xffffffffu, ps[hn][e], off));
+            int high[2] = {-126, -126};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st.o[hn][t][i] *= down;
+            for (int hn = 0; hn < HN; ++hn) {
+                float4 v4 = scale[hn][c], m4 = most[hn][c];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int gr = 0; gr < 2; ++gr) {
+                        float &vs = e ? (gr ? v4.w : v4.z) : (gr ? v4.y : v4.x);
+                        float &m = e ? (gr ? m4.w : m4.z) : (gr ? m4.y : m4.x);
+                        m = fmaxf(m * al[hn][e], __uint_as_float((gr ? ps[hn][e] >> 16 : ps[hn][e] & 0xFFFFu) << 23));
+                        const int had = exponent_of(vs);
+                        int to = top[gr] > holds_to(had) ? power_for(top[gr]) : had;
+                        if (m > 0.f) to = min(max(to, 2 - exponent_of(m)), kTopScale);
+                        high[gr] = max(high[gr], to);
+                        vs = pow2(to);
+                        // (sums that have lost all weight go: their power may rise without end)
+                        const float f = al[hn][e] == 0.f ? 0.f : al[hn][e] * pow2(min(max(to - had, -126), 127));
+#pragma unroll
+                        for (int t = 4 * gr; t < 4 * gr + 4; ++t) st.o[hn][t][e] *= f, st.o[hn][t][2 + e] *= f;
+                    }
+                __syncwarp();
+                if (r == 0) scale[hn][c] = v4, most[hn][c] = m4;
             }
+            st.vlimit[0] = holds_to(high[0]), st.vlimit[1] = holds_to(high[1]);
         }
-        st.vscale = pk2(vs.x, vs.y);
+        __syncwarp();
     }
     // ---- P, and step P of both groups in hi + lo parts, transposed to B fragments
     uint32_t bh[HN][2][2], bl[HN][2][2];  // [group][token half]
-    const pair_t f[2] = {mul2(pk2(v00.x, v01.x), st.vscale), mul2(pk2(v10.x, v11.x), st.vscale)};
+    const pair_t f[2] = {pk2(v00.x, v01.x), pk2(v10.x, v11.x)};
     const pair_t b[2] = {pk2(v00.y, v01.y), pk2(v10.y, v11.y)};
 #pragma unroll
-    for (int hn = 0; hn < HN; ++hn)
+    for (int hn = 0; hn < HN; ++hn) {
+        const uint4 v4 = lds128(st.scales + hn * 64);
+        const pair_t vscale[2] = {pk2(__uint_as_float(v4.x), __uint_as_float(v4.y)),
+                                  pk2(__uint_as_float(v4.z), __uint_as_float(v4.w))};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            // (differences of scores first: those of large scores are exact, their products with the factor are not)
-            const float2 y = upk2(mul2(add2(pk2(s[hn][2 * half], s[hn][2 * half + 1]), st.minus_m[hn]), q.factor[hn]));
-            const float p[2] = {exp2_fast(y.x), exp2_fast(y.y)};
+            const float2 z = upk2(y[hn][half]);
+            const float p[2] = {exp2_fast(z.x), exp2_fast(z.y)};
             st.l[hn] = add2(st.l[hn], pk2(p[0], p[1]));
             pair_t x[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const pair_t pp = pk2(p[e], p[e]);
                 st.off[hn][e] = fma2(pp, b[half], st.off[hn][e]);
-                x[e] = mul2(pp, f[half]);
+                x[e] = mul2(mul2(pp, f[half]), vscale[e]);
             }
             const float2 x0 = upk2(x[0]), x1 = upk2(x[1]);
             const __half2 h0 = __floats2half2_rn(x0.x, x1.x), h1 = __floats2half2_rn(x0.y, x1.y);
@@ -474,6 +549,7 @@ __device__ __forceinline__ void attend_page4(const Queries<NQ, HN> &q, uint32_t 
                 bl[hn][1][half] = transpose8(l1);
             }
         }
+    }
     // ---- O^T += V^T (step P)^T
     {
         const uint4 x0 = lds128(rec + q4::kV + c * 128 + r * 16), x1 = lds128(rec + q4::kV + 512 + c * 128 + r * 16);
@@ -799,6 +875,12 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
         if (tid == 0) S.unit = unit;  // (kept there while the pages take the registers)
         const int pa = max(unit.first, 0), pb = min(unit.end(), run);
         st.init();
+        st.scales = su32(&S.scale[warp][0][c]);
+        if (lane < 4 * HN) {
+            S.most[warp][lane >> 2][lane & 3] = make_float4(0.f, 0.f, 0.f, 0.f);
+            S.scale[warp][lane >> 2][lane & 3] =
+                make_float4(pow2(kTopScale), pow2(kTopScale), pow2(kTopScale), pow2(kTopScale));
+        }
         int n = pa > warp ? (pa - warp + kWarps - 1) / kWarps : 0;
         const int n_end = pb > warp ? (pb - warp + kWarps - 1) / kWarps : 0;
         const bool any = n < n_end;
@@ -819,7 +901,7 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
                     __syncwarp();
                     issue(n + kSlots - 1, freed);
-                    attend_page4<NQ, HN, kTwice>(q, slot, (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st);
+                    attend_page4<NQ, HN, kTwice>(q, slot, (int)(pages[n & (2 * kBatch - 1)] >> kLenShift), st, S);
                     freed = slot;
                     slot = slot == slot_of(kSlots - 1) ? ring : slot + q4::kRecord;
                 }
@@ -828,8 +910,6 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
             __syncwarp();
             // ---- the warp's sums of V to shared memory, in the scale of the running maximum (and times 2^-10, as the codes
             // went in: with that factor too a power of two for the largest steps would overflow)
-            const float2 vs = upk2(st.vscale);
-            const float back[2] = {inverse_of(vs.x), inverse_of(vs.y)};
 #pragma unroll
             for (int hn = 0; hn < HN; ++hn) {
                 const float2 m2 = max_of(st.minus_m[hn], q.factor[hn]);
@@ -837,13 +917,14 @@ __global__ void __launch_bounds__(Shape<HN>::kThreads, Shape<HN>::kCtas)
                 for (int e = 0; e < 2; ++e) {
                     const int head = 8 * hn + 2 * c + e;
                     const float m = e ? m2.y : m2.x;
+                    const float2 vs = *(reinterpret_cast<const float2 *>(&S.scale[warp][hn][c]) + e);
                     const float before = flushed ? exp2_fast(S.ml[warp][head].x - m) : 0.f;
                     __syncwarp();
                     if (r == 0) S.ml[warp][head].x = m;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float(&o0)[4] = st.o[hn][2 * j], (&o1)[4] = st.o[hn][2 * j + 1];
-                        const float f = back[j >> 1];
+                        const float f = inverse_of(j < 2 ? vs.x : vs.y);
                         float4 *at = reinterpret_cast<float4 *>(&S.o[warp][head][32 * j + 4 * r]);
                         float4 x = make_float4(o0[e] * f, o0[2 + e] * f, o1[e] * f, o1[2 + e] * f);
                         if (flushed) {

@@ -119,15 +119,18 @@ def attention_rms_tolerance(q, k, v, scale):
     """Bounds on the norm of O - O64 of each head, for roundings that are independent of one another (four times what
     they leave; the norm covers 128 elements).  A score is made of products in units of a code, q (k - lo) with lo the
     group's lowest value, and of lo sum q, in at most 16 sums one after another, each off by up to 2^-24 of a partial sum
-    of random signs (its root mean square: A); the queries' 22 bits add 2^-23 of a product.  A weight is off by that
-    and by its own 2^-21 (exponential, 22 bits beside the step).  Sums of fp32 values leave 2^-20 of O."""
+    of random signs (its root mean square: A); the queries' 22 bits add 2^-23 of a product.  With O = sum w v / sum w the
+    derivative of O by a score is w (v - O): a score that is off by e moves O by w e |v - O|.  A weight's own 2^-21
+    (exponential, 22 bits beside the step) moves it by up to w 2^-21 (|v| + |O|).  Sums of fp32 values leave 2^-20 of O."""
     if k.shape[0] == 0:
         return torch.zeros(q.shape[0], dtype=q.dtype, device=q.device)
     kg, qg = k.unflatten(-1, (2, G)), q.unflatten(-1, (2, G))
     lo = kg.amin(-1)
     spread = (kg - lo[..., None]).flatten(-2)
     A = (q.square() @ spread.square().T).sqrt() + (qg.sum(-1)[:, None] * lo[None]).abs().sum(-1)
-    e = scale * (4 * 2.0 ** -24 * A + 2.0 ** -23 * (q.square() @ k.square().T).sqrt()) + 2.0 ** -21
+    e = scale * (4 * 2.0 ** -24 * A + 2.0 ** -23 * (q.square() @ k.square().T).sqrt())
     w = torch.softmax(q @ k.T * scale, -1)
-    size = v.norm(dim=-1)
-    return 4 * (w * e * size).square().sum(-1).sqrt() + 2.0 ** -20 * (w @ v).norm(dim=-1)
+    o = w @ v
+    size = v.norm(dim=-1) + o.norm(dim=-1, keepdim=True)
+    away = (v.square().sum(-1) - 2 * (o @ v.T) + o.square().sum(-1, keepdim=True)).clamp(min=0).sqrt()
+    return 4 * (w * (e * away + 2.0 ** -21 * size)).square().sum(-1).sqrt() + 2.0 ** -20 * o.norm(dim=-1)

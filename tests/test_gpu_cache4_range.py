@@ -248,6 +248,55 @@ def test_largest_queries(dtype):
         assert float((O[h] - o[0]).abs().max()) <= to and abs(float(lse[h] - l[0])) <= tl, h
 
 
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 14, 2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("at", [0, 3000, 4095])
+@pytest.mark.parametrize("dtype,hq", [("bf16", 4), ("bf16", 8), ("bf16", 16), ("fp32", 8)])
+def test_value_rows_of_no_weight(dtype, hq, at, ratio):
+    """A value row that is far larger than the others, in a token without weight: the other rows keep their bits."""
+    n, g = 256, _gen(251)
+    base = torch.randn(D, generator=g, device="cuda")
+    Q = (base + 0.5 * torch.randn((hq, D), generator=g, device="cuda")).to(DT[dtype])
+    k = torch.randn((n * S, D), generator=g, device="cuda")
+    v = 1 + torch.randn((n * S, D), generator=g, device="cuda")
+    # scores of about -0.088 * 128 * 16 = -180: a weight of e^-180 = 2^-260 beside 2^60
+    k[at], v[at] = -16 * base, v[at] * ratio
+    O, lse, K, V = _one_unit(k.view(n, S, D).bfloat16(), v.view(n, S, D).bfloat16(), Q, dtype)
+    _rms_check(O, Q.double(), K, V, 0.088)
+
+
+@pytest.mark.parametrize("dtype,hq", [("bf16", 4), ("bf16", 8), ("bf16", 16), ("fp32", 8)])
+def test_value_rows_that_only_some_heads_see(dtype, hq):
+    """One token of huge values that half of the heads give all their weight, the others none."""
+    n, g = 64, _gen(261)
+    base = torch.randn(D, generator=g, device="cuda")
+    sign = torch.where(torch.arange(hq, device="cuda") % 2 == 0, 1.0, -1.0)[:, None]
+    Q = (sign * base + 0.3 * torch.randn((hq, D), generator=g, device="cuda")).to(DT[dtype])
+    k = torch.randn((n * S, D), generator=g, device="cuda")
+    v = 1 + torch.randn((n * S, D), generator=g, device="cuda")
+    for at in (0, 500, 1023):
+        k2, v2 = k.clone(), v.clone()
+        k2[at], v2[at] = 16 * base, v[at] * 2.0 ** 20
+        O, lse, K, V = _one_unit(k2.view(n, S, D).bfloat16(), v2.view(n, S, D).bfloat16(), Q, dtype)
+        _rms_check(O, Q.double(), K, V, 0.088, at)
+
+
+def test_small_values_of_large_weight():
+    """A first token of small values and most of the weight beside ordinary ones, steps that rise page after page, and
+    a late token that takes the weight from all before it."""
+    n, g, hq = 300, _gen(271), 8
+    Q = torch.randn((hq, D), generator=g, device="cuda").bfloat16()
+    k = torch.randn((n * S, D), generator=g, device="cuda")
+    v = 1 + torch.randn((n * S, D), generator=g, device="cuda")
+    k[0], v[0] = Q.float().mean(0) * 12, v[0] * 2.0 ** -12
+    rising = v * torch.exp2(torch.arange(n * S, device="cuda") / 200.0)[:, None]
+    falling = v * torch.exp2(-torch.arange(n * S, device="cuda") / 200.0)[:, None]
+    late = k.clone()
+    late[n * S - 5] = Q.float().mean(0) * 40
+    for kk, vv in ((k, v), (k, rising), (k, falling), (late, v), (late, falling), (late, rising)):
+        O, lse, K, V = _one_unit(kk.view(n, S, D).bfloat16(), vv.view(n, S, D).bfloat16(), Q, "bf16")
+        _rms_check(O, Q.double(), K, V, 0.088)
+
+
 @pytest.mark.parametrize("size", [1e38, 2.0 ** -100])
 def test_largest_and_smallest_values(size):
     """Steps of 2^123 (three tokens: their sum stays below fp32's largest number) and of 2^-103."""
