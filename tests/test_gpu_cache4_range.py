@@ -7,7 +7,8 @@ import torch
 
 import cache4_ref as ref
 import semantic_paged_kv_gb300 as ice
-from test_gpu_cache4 import D, DT, R, S, _attn_buffers, _cache, _err, _gen, _ix, _params, _qkv, _rows_of, _table
+from test_gpu_cache4 import (D, DT, R, S, _attn_buffers, _cache, _err, _gen, _ix, _params, _poison, _qkv,
+                             _random_records, _rows_of, _table)
 
 pytestmark = pytest.mark.gpu
 
@@ -144,6 +145,27 @@ def test_append_at_positions_unlike_the_slots(dtype, rd, inter, norm):
     half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
     tol = half * want.abs() + 8 * 2.0 ** -24 * 2 * want.abs().amax(-1, keepdim=True)
     assert bool(((qo.double() - want).abs() <= tol).all())
+
+
+def test_pack_of_many_inserted_tokens():
+    """Only the tokens from first_token on, hundreds of them a unit: the records of a whole pack."""
+    B, hq, hkv, N, first = 2, 6, 3, 900, 123
+    cfg = ice.Config(batch=B, n_q_heads=hq, n_kv_heads=hkv, n_tokens=N, seed=5)
+    p = cfg.params()
+    K, V = (torch.randn((B, hkv, N, D), generator=_gen(s), device="cuda").bfloat16() for s in (1, 2))
+    idx, err = ice.Index(cfg), _err()
+    ice.ice_build_index(p, K, V, idx, ice.workspace(ice.ice_build_workspace_bytes(p)), err)
+    whole = torch.zeros(ice.ice_pool4_bytes(p), dtype=torch.uint8, device="cuda").view(cfg.units, cfg.page_cap, R)
+    part = torch.zeros_like(whole)
+    ice.ice_pool4_pack(p, idx, 0, whole, err)
+    ice.ice_pool4_pack(p, idx, first, part, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    wk, wv = (x.view(cfg.units, cfg.page_cap, S, D) for x in ref.decode(whole.view(-1, R)))
+    pk, pv = (x.view(cfg.units, cfg.page_cap, S, D) for x in ref.decode(part.view(-1, R)))
+    tok = idx.page_tokens
+    new = (tok >= first)[..., None]
+    for a, b in ((wk, pk), (wv, pv)):
+        assert torch.equal(torch.where(new, a, torch.zeros_like(a)), b)
 
 
 # -------------------------------------------------------------- attention --
@@ -307,3 +329,132 @@ def test_largest_and_smallest_values(size):
         Q = torch.randn((8, D), generator=_gen(283), device="cuda").bfloat16()
         O, lse, K, V = _one_unit(k.bfloat16(), v.bfloat16(), Q, "bf16", lens=tokens)
         _rms_check(O, Q.double(), K, V, 0.088)
+
+
+ACCURACY = [  # hq, hkv, dtype, lens
+    (4, 1, "bf16", [1, 16, 17, 300]), (32, 8, "bf16", [2049, 5]), (64, 8, "bf16", [4097]), (16, 1, "bf16", [4000, 100]),
+    (4, 1, "fp32", [1, 33, 500]), (8, 1, "fp32", [1754]), (12, 1, "fp32", [900, 2]), (64, 8, "bf16", [100003]),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,dtype,lens", ACCURACY)
+def test_accuracy(hq, hkv, dtype, lens):
+    """The error's norm against what independent roundings leave."""
+    B, g = len(lens), hq // hkv
+    p = _params(B, hq, hkv, dtype)
+    blocks = -(-max(lens) // S)
+    recs = _random_records(700, hkv, 291)
+    bt = torch.randint(0, 700, (B, blocks), generator=_gen(292), device="cuda").int()
+    Q = torch.randn((B, hq, D), generator=_gen(293), device="cuda").to(DT[dtype])
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), torch.tensor(lens, dtype=torch.int32, device="cuda"), 0.088,
+                               O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    for b in range(B):
+        for h in range(hkv):
+            K, V = (x.reshape(-1, D)[:lens[b]] for x in ref.decode(recs[bt[b].long(), h]))
+            hs = slice(h * g, (h + 1) * g)
+            _rms_check(O[b, hs].double(), Q[b, hs].double(), K, V, 0.088, (b, h))
+
+
+# ------------------------------------------------------------- many units --
+def _check_units(O, lse, Q, kv_of, B, hkv, scale, only):
+    g = Q.shape[1] // hkv
+    for b in range(B):
+        for h in range(hkv):
+            hs = slice(h * g, (h + 1) * g)
+            if not only(b):
+                continue
+            k, v = kv_of(b, h)
+            q = Q[b, hs].double()
+            o, l = ref.attention(q, k, v, scale)
+            to, tl = ref.attention_tolerance(q, k, v, scale)
+            assert float((O[b, hs].double() - o).abs().max()) <= to, (b, h)
+            assert float((lse[b, hs].double() - l).abs().max()) <= tl, (b, h)
+
+
+def test_more_units_than_a_cta_keeps_at_hand():
+    """1280 units of ragged lengths, empty ones among them."""
+    B, hq, hkv = 40, 32, 32
+    g = torch.Generator().manual_seed(301)
+    lens = torch.randint(0, 90, (B,), generator=g).tolist()
+    lens[0], lens[7], lens[8], lens[B - 1] = 0, 0, 0, 0
+    lens[20] = 1500
+    p = _params(B, hq, hkv, "bf16")
+    blocks = -(-max(lens) // S)
+    _, bt = _cache(B, blocks, 1, 302)
+    recs = _random_records(B * blocks + 2, hkv, 303)
+    Q = torch.randn((B, hq, D), generator=_gen(304), device="cuda").bfloat16()
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), ln, 0.088, O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    empty = ln == 0
+    assert bool((O[empty] == 0).all()) and bool((lse[empty] == -math.inf).all())
+
+    def kv_of(b, h):
+        k, v = ref.decode(recs[bt[b, :-(-lens[b] // S)].long(), h])
+        return k.reshape(-1, D)[:lens[b]], v.reshape(-1, D)[:lens[b]]
+
+    _check_units(O, lse, Q, kv_of, B, hkv, 0.088, lambda b: lens[b] > 0)
+
+
+def test_runs_that_pass_many_empty_units():
+    """Long sequences with hundreds of empty ones between them: a CTA's run walks past the units it keeps at hand."""
+    B, hq, hkv = 3000, 2, 1
+    at = {0: 80000, 1: 33, 700: 5, 1300: 16, 1900: 160003, 2500: 1, 2501: 20, 2999: 100000}  # runs of about 70 pages
+    p = _params(B, hq, hkv, "bf16")
+    blocks = -(-max(at.values()) // S)
+    recs = _random_records(900, hkv, 311)
+    bt = torch.randint(0, 900, (B, blocks), generator=_gen(312), device="cuda").int()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for b, n in at.items():
+        lens[b] = n
+    Q = torch.randn((B, hq, D), generator=_gen(313), device="cuda").bfloat16()
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    for _ in range(2):
+        O.fill_(7.0)
+        ice.ice_cache4_attn_decode(p, Q, ice.Cache4(recs, bt), lens, 0.088, O, lse, ws, err)
+        assert ice.ice_check(err) == ice.ICE_OK
+        empty = lens == 0
+        assert bool((O[empty] == 0).all()) and bool((lse[empty] == -math.inf).all())
+
+        def kv_of(b, h):
+            k, v = ref.decode(recs[bt[b].long(), h])
+            return k.reshape(-1, D)[:at[b]], v.reshape(-1, D)[:at[b]]
+
+        _check_units(O, lse, Q, kv_of, B, hkv, 0.088, lambda b: b in at)
+
+
+def test_selected_pages_of_many_units():
+    """600 units of selected pages (none for some) and a tail that some sequences lack."""
+    B, hq, hkv, P, most = 75, 16, 8, 12, 9
+    U = B * hkv
+    p = _params(B, hq, hkv, "bf16", page_cap=P)
+    recs = _random_records(U, P, 321)
+    lens = torch.randint(0, S + 1, (U, P), generator=_gen(322), device="cuda").int()
+    count = torch.randint(0, most + 1, (U,), generator=_gen(323), device="cuda").int()
+    sel = torch.rand((U, P), generator=_gen(324), device="cuda").argsort(1)[:, :most].int().contiguous()
+    tail = torch.randint(0, 40, (B,), generator=torch.Generator().manual_seed(325)).tolist()
+    tail[0] = tail[30] = 0
+    count[:hkv] = 0  # sequence 0: nothing at all
+    _, bt = _cache(B, 3, 1, 326)
+    trec = _poison(_random_records(B * 3 + 2, hkv, 327), bt, tail, hkv)
+    Q = torch.randn((B, hq, D), generator=_gen(328), device="cuda").bfloat16()
+    O, lse, ws, err = _attn_buffers(B, hq, p)
+    ice.ice_sparse_attn_decode4(p, Q, recs, lens, sel, count, ice.Cache4(trec, bt),
+                                torch.tensor(tail, dtype=torch.int32, device="cuda"), 0.088, O, lse, ws, err)
+    assert ice.ice_check(err) == ice.ICE_OK
+    assert bool((O[0] == 0).all()) and bool((lse[0] == -math.inf).all())
+    tk, tv = _rows_of(trec, bt, 0)
+    slot = torch.arange(S, device="cuda")
+
+    def kv_of(b, h):
+        u = b * hkv + h
+        pg = sel[u, :int(count[u])].long()
+        ok = slot < lens[u, pg][:, None]
+        k, v = (x[ok] for x in ref.decode(recs[u, pg]))
+        return torch.cat((k, tk[b, h, :tail[b]])), torch.cat((v, tv[b, h, :tail[b]]))
+
+    _check_units(O, lse, Q, kv_of, B, hkv, 0.088,
+                 lambda b: b > 0 and (tail[b] > 0 or int(count[b * hkv:b * hkv + hkv].min()) > 0))
