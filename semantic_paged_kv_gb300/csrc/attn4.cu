@@ -303,7 +303,8 @@ __device__ __forceinline__ void prepare_queries(const q4::Vec8<T> &part, float s
         if (vec == 0) {
             // a head that is not finite, or whose factor would not be (bf16: |scale q| from 2^117 on), is not a number
             const float f = sl == 0.f ? 1.f : fabsf(sl) * pow2(kCodeScale<NQ>) * pow2(-e2);
-            X.factor[head] = big < INFINITY && f < INFINITY ? f : __int_as_float(0x7fc00000);
+            // (and never zero: slots without a token have a score of -inf)
+            X.factor[head] = big < INFINITY && f < INFINITY ? fmaxf(f, FLT_MIN) : __int_as_float(0x7fc00000);
         }
         // element 8 vec + e is code e of word vec: half e / 4, nibble e % 4; the nibbles at bit 4 weigh 16 times more
         uint32_t f[NQ][4];

@@ -270,6 +270,19 @@ def test_largest_queries(dtype):
         assert float((O[h] - o[0]).abs().max()) <= to and abs(float(lse[h] - l[0])) <= tl, h
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens", [5, 100])
+def test_smallest_queries_and_scales(dtype, tokens):
+    """Scores far below fp32's smallest number: the mean of the values, also where a page has slots without a token."""
+    n = -(-tokens // S)
+    k, v = (torch.randn((n, S, D), generator=_gen(s), device="cuda").bfloat16() for s in (241, 242))
+    for size, scale in ((2.0 ** -120, 1e-30), (2.0 ** -126, 1.0), (0.0, 0.088), (1.0, 1e-38), (2.0 ** -120, -1e-30)):
+        Q = (torch.randn((6, D), generator=_gen(243), device="cuda") * size).to(DT[dtype])
+        O, lse, K, V = _one_unit(k, v, Q, dtype, scale, tokens)
+        _rms_check(O, Q.double(), K, V, scale, size)
+        assert float((lse - math.log(tokens)).abs().max()) <= 2.0 ** -20
+
+
 @pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 14, 2.0 ** 30, 2.0 ** 60])
 @pytest.mark.parametrize("at", [0, 3000, 4095])
 @pytest.mark.parametrize("dtype,hq", [("bf16", 4), ("bf16", 8), ("bf16", 16), ("fp32", 8)])
