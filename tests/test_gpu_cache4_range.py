@@ -332,6 +332,23 @@ def test_small_values_of_large_weight():
         _rms_check(O, Q.double(), K, V, 0.088)
 
 
+@pytest.mark.parametrize("dtype,hq", [("bf16", 4), ("bf16", 8), ("bf16", 16), ("fp32", 8)])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -20, 2.0 ** -7])
+def test_first_token_of_all_the_weight_and_small_values(dtype, hq, size):
+    """What a head attends to where it attends to nothing: the other tokens' values are far larger, their weights small."""
+    n, g = 256, _gen(276)
+    base = torch.randn(D, generator=g, device="cuda")
+    Q = (base + 0.3 * torch.randn((hq, D), generator=g, device="cuda")).to(DT[dtype])
+    k = torch.randn((n * S, D), generator=g, device="cuda")
+    v = 1 + torch.randn((n * S, D), generator=g, device="cuda")
+    k[0], v[0] = 2 * base, v[0] * size  # a score of about 22
+    O, lse, K, V = _one_unit(k.view(n, S, D).bfloat16(), v.view(n, S, D).bfloat16(), Q, dtype)
+    _rms_check(O, Q.double(), K, V, 0.088)
+    k[n * S // 2], v[n * S // 2] = 2 * base, v[0]  # and once more, late
+    O, lse, K, V = _one_unit(k.view(n, S, D).bfloat16(), v.view(n, S, D).bfloat16(), Q, dtype)
+    _rms_check(O, Q.double(), K, V, 0.088)
+
+
 @pytest.mark.parametrize("size", [1e38, 2.0 ** -100])
 def test_largest_and_smallest_values(size):
     """Steps of 2^123 (three tokens: their sum stays below fp32's largest number) and of 2^-103."""
