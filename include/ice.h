@@ -364,6 +364,8 @@ ice_status ice_decode_workspace_bytes(const ice_params *p, int32_t budget_tokens
  * (-s, page id); sel_pages[u, 0..sel_count[u]) is the ascending union of the
  * g lists, sel_pages [U, max_sel] int32 (rest -1), sel_count [U] int32.
  * max_sel must be >= min(g * k, page_cap).
+ * The pool is not read: idx->pool_k and pool_v may be NULL here (pages kept in
+ * 4 bits, or on the host).
  */
 /*
  * With n_levels = 3 the selection descends ([A] 关键设计 2: the query finds
@@ -507,7 +509,8 @@ ice_status ice_decode_plan(const ice_params *p, int32_t budget_tokens, int32_t m
  * contiguous.  data is 16-byte aligned and the strides are multiples of 16
  * bytes, so one projection's output holds q, k and v side by side, and an
  * output view may put heads before tokens (K, V [B, Hkv, N, d] of
- * ice_build_index: batch = Hkv N d, token = d, head = N d).
+ * ice_build_index: batch = Hkv N d, token = d, head = N d).  Rows that are
+ * written must not lie on one another.
  */
 typedef struct ice_rows {
     void *data;
@@ -572,9 +575,11 @@ ice_status ice_qkv_rope(const ice_params *p, int32_t n_new, const ice_rows *q, c
  * elements of a row are two groups of 64; a group holds
  *   step = bf16((max - min) / 15), mid = bf16((max + min) / 2),
  *   code = clamp(rint((x - mid) / step + 7.5), 0, 15)   (0 when step = 0),
- * and stands for mid + step (code - 7.5).  A group with an infinite or NaN
- * element (or whose max - min overflows fp32) holds mid = NaN and stands for
- * NaN throughout.  Bytes of a record:
+ * and stands for mid + step (code - 7.5).  (The quotient and the mean are
+ * rounded to fp32 on the way; the code is that of the exact quotient, ties to
+ * even.  An fp32 mean beyond bf16's largest value gives an infinite mid.)  A
+ * group with an infinite or NaN element (or whose max - min overflows fp32)
+ * holds mid = NaN and stands for NaN throughout.  Bytes of a record:
  *   [0, 1024)     K codes: 64 bytes a token; a 4-byte word holds 8 codes, the
  *                 first in the lowest bits; the codes of elements 8 w .. 8 w +
  *                 7 are word 4 (w % 4) + w / 4 of the token;
@@ -597,7 +602,8 @@ ice_status ice_pool4_bytes(const ice_params *p, size_t *bytes);
  * n_indexed[u] - 1 of every unit are written, at their page and slot, and
  * nothing else: after ice_insert_tokens, first_token = the token count before
  * it.  (A new page's pad slots are then left as they were; no entry point
- * reads them.)
+ * reads them.)  That is meant for a few tokens a unit; from a few hundred on
+ * the whole pool is packed faster.
  * Reads idx->n_pages, page_len, pool_k and pool_v (device memory or a host
  * pool's device pointers), with first_token > 0 n_indexed, token_page,
  * token_slot, pool_k and pool_v; the other arrays of idx may be NULL.  The
@@ -640,9 +646,10 @@ typedef struct ice_cache4 {
  * before them and slots behind them stay as they were.  Tokens of one call
  * must fall into different slots (two sequences that share a page they both
  * append to do not).
- * ICE_ERR_CAPACITY in err_dev, and that token left out, when its cache
- * position is outside [0, 16 max_pages), its page outside [0, n_pages) or its
- * rotation position outside [0, n_positions).
+ * ICE_ERR_CAPACITY in err_dev, and that token left out of the cache, when its
+ * cache position is outside [0, 16 max_pages), its page outside [0, n_pages) or
+ * its rotation position outside [0, n_positions); its rows of q_out are written
+ * unless the rotation position is the reason.
  */
 ice_status ice_cache4_append(const ice_params *p, int32_t n_new, const ice_rows *q, const ice_rows *k,
                              const ice_rows *v, const int32_t *positions, const int32_t *start, const int32_t *counts,
@@ -677,6 +684,11 @@ ice_status ice_attn4_workspace_bytes(const ice_params *p, size_t *bytes);
  * are left out.  A head whose query is not finite (bf16: or has |scale q| of
  * 2^117 and more) gives NaN in O and lse of a sequence that has tokens; the
  * other heads do not depend on it.
+ * Arithmetic: products of fp16 parts, fp32 sums.  bf16 queries go in as they
+ * are (elements below 2^-27 of a head's largest lose bits), fp32 queries with
+ * 22 bits; weights times steps with 22 bits, not less than 2^-24 of the largest
+ * that a warp has met.  Sums of weight times value are divided at the end: the
+ * largest |v| times the number of tokens has to stay below 2^119.
  */
 ice_status ice_cache4_attn_decode(const ice_params *p, const void *Q, const ice_cache4 *cache, const int32_t *lens,
                                   float scale, float *O, float *lse, void *ws, size_t ws_bytes, int32_t *err_dev,

@@ -8,11 +8,13 @@
 // A page of 16 tokens of one KV head is one 2304-byte record, read once; at the
 // measured copy rate an SM could get one every ~98 clocks.  Long caches are
 // bound by that and by instruction issue in about equal parts: the same loop
-// over pages without their copies takes 111 clocks a page and SM (250
+// over pages without their copies takes about 110 clocks a page and SM (250
 // instructions on four schedulers, 62 clocks, and 24 products that block one for
-// 8 clocks each, 48), the copies alone take 305 us where the whole takes 359 us
-// (16 sequences x 100k tokens, 64/8 heads: 1.84 GB at 5.1 TB/s, 76% of the copy
-// rate; 4 heads a group 331 us, 16 heads 584).  Short ones are bound by a chain
+// 8 clocks each, 48), the copies alone take 305 us where the whole takes 357 us
+// (16 sequences x 100k tokens, 64/8 heads: 1.84 GB at 5.2 TB/s, 76% of the copy
+// rate; 4 heads a group 334 us).  The products' share grows with 9 to 16 heads a
+// group (48 a page; 580 us with 16) and with fp32 queries (32 a page, and K's
+// codes centred: 420 us, with 4 heads a group 390).  Short ones are bound by a chain
 // of latencies (1 sequence x 16k tokens, 32/8 heads: 13.5 us): counts of the
 // units 1.5 us, page numbers 1.0, queries 0.8, first page 1.6, the run's other
 // pages 2.5, the warps' join 1.3, the ticket 1.0, the runs' join 2.5.
@@ -35,6 +37,10 @@
 //     pair turns codes into operands, nothing is converted; the queries carry
 //     the factor 16 between the two.  Each group of 64 has its accumulator:
 //     S = sum_groups step (q . c) + (mid - 7.5 step) sum q.
+//     (bf16 queries: subnormal operands, whose sums lose some bits, see below;
+//     O's relative error is 3.5e-7 where fp32 products leave 3e-7, lse's 7e-8
+//     and 3e-8: fewer instructions were worth that.  fp32 queries go in as two
+//     fp16 parts, 22 bits, and the codes centred: 2.5e-7.)
 //   softmax: the running maximum only moves when a score passes it by 2^8 (one
 //     vote per page instead of reductions); sums stay in their lanes until the
 //     end of the unit.
@@ -65,7 +71,7 @@ namespace {
 
 using namespace tc;
 
-// Pages of a warp's ring: one attended, two on their way (16 sequences x 100k tokens 359 us; with two slots 371, short
+// Pages of a warp's ring: one attended, two on their way (16 sequences x 100k tokens 357 us; with two slots 371, short
 // sequences 1% less).
 constexpr int kSlots = 3;
 constexpr int kBatch = 32;         // places looked up at a time
@@ -79,7 +85,7 @@ constexpr int kRow = kHeadDim + 4;  // padded row of the warps' outputs (conflic
 constexpr int kMaxRuns = 384;      // CTAs, at most
 // A unit of more than kJoinRows rows of partial results (runs times heads) is joined in two levels, groups of kGroup
 // runs by their last CTAs and then the groups: one CTA reads 10 rows a warp and latency, a further ticket costs about 2
-// us.  One sequence of 16k tokens of 16/1 heads takes 16.3 us so and 24.2 in one level, of 100k tokens 20.1 and 36.6
+// us.  One sequence of 16k tokens of 16/1 heads takes 16.1 us so and 24.2 in one level, of 100k tokens 20.2 and 36.6
 // (4/1 heads 15.5 and 24.2); the 38 runs of 4 heads of 16k tokens of 32/8 heads 15.8 in two levels and 13.4 in one.
 constexpr int kGroup = 16, kJoinRows = 256;
 constexpr int kMinRun = 8;         // places of a run, at least: one page per warp (16 are slower: fewer CTAs at work)
@@ -230,7 +236,7 @@ template <int HN> struct State {
     pair_t off[HN][2];           // sum of P mid, groups 0 and 1, this lane's tokens
     uint32_t scales;             // shared address of the powers of two on step P (Smem::scale) of this lane's heads
     pair_t vscale[HN][2];        // and the powers: in registers with more than 8 heads a group (16 x 100k tokens of 16
-                                 // heads 568 us, 608 when loaded every page; 8 heads 359 loaded, 363 in registers)
+                                 // heads 568 us, when loaded every page 608; 8 heads 363 us, when loaded every page 359)
     float vlimit[2];             // of each group: the step that they hold up to
     __device__ __forceinline__ void init() {
 #pragma unroll

@@ -9,10 +9,10 @@
 // four rows at a time; the record is put together (or taken apart) in shared
 // memory, because its V part interleaves two tokens, and moved in 16-byte
 // vectors (the finished record by one bulk store).  32 units x 12487 pages (4.2
-// GB): pack 692 us, 6.06 TB/s, next to HBM bound by issue (1680 instructions a
-// page, the schedulers 77% busy); unpack 601 us, 6.98 TB/s (the copy rate is
-// 6.78).  8 units x 2017 pages (170 MB): 34 and 30 us.  fp32, 8 units x 6001
-// pages (0.9 GB): 123 and 137 us.  Rows of 4 x 4099 tokens of 8 heads leave a
+// GB): pack 708 us, 5.92 TB/s, next to HBM bound by issue (1720 instructions a
+// page, the schedulers 76% busy); unpack 602 us, 6.96 TB/s (the copy rate is
+// 6.78).  8 units x 2017 pages (170 MB): 34 and 28 us.  fp32, 8 units x 6001
+// pages (0.9 GB): 121 and 135 us.  Rows of 4 x 4099 tokens of 8 heads leave a
 // cache in 11.3 us, 6.2 TB/s.
 #include "common.cuh"
 #include "internal.h"
@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_pool4_pack(const T *__restrict_
     }
 }
 
-// Tokens first .. n_indexed - 1 of every unit, one row of 8 lanes each.
+// Tokens first .. n_indexed - 1 of every unit, one row of 8 lanes each, a CTA a
+// unit: up to 16 tokens of 8 units take 3.5 us, 128 take 11, 1024 72 (a whole
+// pack of 8 x 16k tokens 29).
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_pool4_tokens(
     const T *__restrict__ pool_k, const T *__restrict__ pool_v, const int32_t *__restrict__ n_indexed,

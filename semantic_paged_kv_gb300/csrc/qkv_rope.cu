@@ -28,8 +28,13 @@
 // The quantising CTAs are bound by their instructions (alone: 23 us, 3.0 TB/s),
 // those of the queries by HBM, so both kinds run side by side: the former lie
 // evenly among the first three quarters of the grid, and what is left at the
-// end is short.  Appending 4 x 4099 tokens of 32/8 heads: 48.8 us (5.9 TB/s);
+// end is short.  Appending 4 x 4099 tokens of 32/8 heads: 49.5 us (5.8 TB/s);
 // spread over the whole grid 52.9, queries first 54.8, K and V first 53.2.
+//
+// Other forms, 1 x 16k tokens of 64/8 heads (floors 100 and 106 us): rotation in
+// halves 100 us, with norms 117, pairs (2 i, 2 i + 1) 112, 64 of 128 elements
+// 113, the former with norms 124; append with its read 112, 135, 129, 133 and
+// 148 (the kernels with norms or other rotations spill 76 to 324 bytes).
 //
 // The launch bounds trade registers for warps: at least 6 CTAs (24 warps) an SM
 // in bf16 (the 36k prompt 159 us with 4, the same with 8; the append 56 us with
