@@ -179,7 +179,7 @@ __device__ __forceinline__ uint32_t codes_in(const float (&x)[8], float step, fl
         const pair_t x2 = pk2(x[2 * i], x[2 * i + 1]), t = fma2(sub2(x2, mid2), inv2, big2);
         pair_t s, er;
         two_sum2(mid2, mul2(sub2(t, big2), step2), s, er);  // (exact products: it does not matter if they are fused)
-        const float2 b = upk2(t), rem = upk2(sub2(sub2(x2, s), er));
+        const float2 b = upk2(t), rem = upk2(add2(sub2(sub2(x2, s), er), 0ull));  // (+ 0: no zero with a sign)
         code(2 * i, b.x, rem.x);
         code(2 * i + 1, b.y, rem.y);
     }

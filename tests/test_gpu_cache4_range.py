@@ -82,6 +82,22 @@ def test_codes_of_tiny_values_beside_large_ones():
     assert torch.equal(recs, ref.encode(k, v))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_codes_of_negative_zeros(dtype):
+    """-0.0 halfway between two codes has the code of 0.0 (values pruned to zero keep their signs)."""
+    n, g = 500, _gen(203)
+    x = (torch.randn((n, S, D), generator=g, device="cuda") * 4).round() / 4
+    x[..., 0::64], x[..., 1::64] = 3, -3  # mid 0
+    x = torch.where(torch.rand((n, S, D), generator=g, device="cuda") < 0.3, torch.zeros_like(x), x)
+    x[..., 0::64], x[..., 1::64] = 3, -3
+    minus = torch.where(x == 0, -torch.zeros_like(x), x)
+    assert bool(torch.signbit(minus[x == 0]).all())
+    plus = _pack(x.to(DT[dtype]), x.flip(0).contiguous().to(DT[dtype]), dtype)[0]
+    recs = _pack(minus.to(DT[dtype]), minus.flip(0).contiguous().to(DT[dtype]), dtype)[0]
+    assert torch.equal(recs, plus)
+    assert torch.equal(recs, ref.encode(x.to(DT[dtype]), x.flip(0).to(DT[dtype])))
+
+
 # ------------------------------------------------------ append: the norm --
 def _normed(x, w, eps):
     """Norm of keys as ice.h states it, an fp32 rounding at each step, the sum of squares rounded once."""
