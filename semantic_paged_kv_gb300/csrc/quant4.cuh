@@ -139,9 +139,12 @@ template <> struct Vec8<float> {
 // rounding error.  The quotient by 15 is corrected by its remainder, which
 // rounds it correctly (Markstein 1990: a quotient within an ulp and a correctly
 // rounded reciprocal); differences below 1e-30, whose remainder could
-// underflow, are divided.  The extremes' sum can overflow where mid does not:
+// underflow, are divided (fp32's in 64 bits, which hold them).  The extremes' sum can overflow where mid does not:
 // mid takes their halves, which bf16 values (and fp32 ones of that size) have
 // exactly.
+static __device__ __noinline__ float tiny_step(float lo, float hi) {
+    return (float)(((double)hi - (double)lo) / 15.0);
+}
 template <typename T>
 __device__ __forceinline__ float2 step_mid(float lo, float hi) {
     float d, er = 0.f;
@@ -151,7 +154,7 @@ __device__ __forceinline__ float2 step_mid(float lo, float hi) {
         two_sum(hi, -lo, d, er);
     const float q = d * (1.f / 15.f);
     float step = fmaf(fmaf(-15.f, q, d) + er, 1.f / 15.f, q);
-    if (d < 1e-30f) step = d / 15.f;
+    if (d < 1e-30f) step = sizeof(T) == 2 || d == 0.f ? d / 15.f : tiny_step(lo, hi);
     if (!(d < INFINITY)) return make_float2(0.f, __int_as_float(0x7fc00000));
     float mid = fmaf(hi, 0.5f, lo * 0.5f);
     if (sizeof(T) == 4 && fabsf(hi + lo) < INFINITY) mid = (hi + lo) * 0.5f;

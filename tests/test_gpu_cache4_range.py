@@ -82,6 +82,25 @@ def test_codes_of_tiny_values_beside_large_ones():
     assert torch.equal(recs, ref.encode(k, v))
 
 
+def test_steps_of_tiny_fp32_groups():
+    """Extremes below 1e-30 whose difference is rounded in fp32: the step is that of the difference itself (pairs whose
+    rounded difference leads to the other neighbour in bf16, and random ones)."""
+    pairs = [(-2.33786149e-31, 1.69214669e-31), (-6.59842301e-33, 6.44674383e-33), (-8.90160388e-37, 1.06593559e-36),
+             (-3.16460062e-36, 3.38143391e-36), (-6.64765244e-34, 4.04464372e-34), (-3.024296e-32, 3.16877219e-32),
+             (-2.35131282e-36, 1.27435275e-36), (-2.08655305e-36, 1.38482852e-36), (-2.33794003e-34, 1.76688602e-34),
+             (-5.57138979e-35, 3.36824447e-35), (-1.77763456e-34, 1.4173592e-34), (-2.41923673e-31, 2.15966195e-31)]
+    n, g = 200, _gen(204)
+    x = torch.rand((n, S, D), generator=g, device="cuda") * 2 - 1
+    x *= torch.exp2(torch.randint(-149, -95, (n, S, 1), generator=g, device="cuda").float())
+    for i, (lo, hi) in enumerate(pairs):
+        x[i, :, :] = torch.rand((S, D), generator=g, device="cuda") * lo
+        x[i, :, 5::64], x[i, :, 40::64] = lo, hi
+    x = torch.where(x == 0, torch.zeros_like(x), x)
+    k, v = x.contiguous(), x.flip(0).contiguous()
+    recs, _, _ = _pack(k, v, "fp32")
+    assert torch.equal(recs, ref.encode(k, v))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_codes_of_negative_zeros(dtype):
     """-0.0 halfway between two codes has the code of 0.0 (values pruned to zero keep their signs)."""
