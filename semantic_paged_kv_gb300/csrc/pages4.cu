@@ -9,7 +9,7 @@
 // four rows at a time; the record is put together (or taken apart) in shared
 // memory, because its V part interleaves two tokens, and moved in 16-byte
 // vectors (the finished record by one bulk store).  32 units x 12487 pages (4.2
-// GB): pack 708 us, 5.92 TB/s, next to HBM bound by issue (1720 instructions a
+// GB): pack 710 us, 5.91 TB/s, next to HBM bound by issue (1720 instructions a
 // page, the schedulers 76% busy); unpack 602 us, 6.96 TB/s (the copy rate is
 // 6.78).  8 units x 2017 pages (170 MB): 34 and 28 us.  fp32, 8 units x 6001
 // pages (0.9 GB): 121 and 135 us.  Rows of 4 x 4099 tokens of 8 heads leave a

@@ -28,7 +28,7 @@
 // The quantising CTAs are bound by their instructions (alone: 23 us, 3.0 TB/s),
 // those of the queries by HBM, so both kinds run side by side: the former lie
 // evenly among the first three quarters of the grid, and what is left at the
-// end is short.  Appending 4 x 4099 tokens of 32/8 heads: 49.5 us (5.8 TB/s);
+// end is short.  Appending 4 x 4099 tokens of 32/8 heads: 49.9 us (5.8 TB/s);
 // spread over the whole grid 52.9, queries first 54.8, K and V first 53.2.
 //
 // Other forms, 1 x 16k tokens of 64/8 heads (floors 100 and 106 us): rotation in
