@@ -710,6 +710,124 @@ ice_status ice_sparse_attn_decode4(const ice_params *p, const void *Q, const voi
                                    const ice_cache4 *cache, const int32_t *lens, float scale, float *O, float *lse,
                                    void *ws, size_t ws_bytes, int32_t *err_dev, void *stream);
 
+/* ------------------------------------------------ trees of drafted tokens -- */
+/*
+ * Speculative decoding over the 4-bit pages: a draft proposes a tree of tokens
+ * for every sequence, the model attends to all of them in one pass
+ * (ice_cache4_attn_tree, or ice_sparse_attn_tree4 over selected pages), the
+ * target's probabilities decide which of them stand (ice_tree_verify), and the
+ * accepted ones' keys and values go into the caches (ice_cache4_commit).
+ *
+ * Nodes t < counts[b] of sequence b: node 0 is the last accepted token, whose
+ * keys and values are not in the cache yet; parents[b, t] < t is the node that
+ * node t follows, -1 where it follows the cache's last token (a parent outside
+ * -1 .. t - 1 sets ICE_ERR_INVALID_ARG in err_dev and counts as -1).  parents
+ * NULL is a chain (node t follows t - 1): the tokens of a prompt's chunk, for
+ * instance.  The rotary position of a node is its depth in the tree behind the
+ * cache's tokens: ice_qkv_rope takes it in `positions`.
+ */
+typedef struct ice_tree {
+    const int32_t *parents; /* device [B, n_nodes] int32, or NULL */
+    const int32_t *counts;  /* device [B] int32 (clamped to 0 .. n_nodes), or NULL: n_nodes */
+    int32_t n_nodes;        /* nodes a sequence can have, >= 0; with parents at most ICE_TREE_NODES in the attention */
+} ice_tree;
+#define ICE_TREE_NODES 256
+
+/* Workspace bytes of the two attention calls below (the same for every shape;
+ * no contents are needed before or kept after a call).  Calls that share one
+ * must not overlap on the GPU. */
+ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes);
+
+/*
+ * Attention of a tree's nodes over a token-ordered 4-bit cache and over one
+ * another:
+ *   O[b, t, h] = sum_j exp(scale q . k_j) v_j / sum_j exp(scale q . k_j)
+ * over the cache's tokens j < lens[b], the ancestors of node t and t itself.
+ * q and O are rows [B, n_nodes, Hq, d], k and v rows [B, n_nodes, Hkv, d], of
+ * dtype (rotated; ice_qkv_rope's outputs); nodes' keys and values go in as they
+ * are, not in 4 bits.  cache may be NULL, with lens NULL: the nodes alone.
+ * Rows behind counts[b] are neither read nor written.
+ *  - lens and pages outside their ranges as in ice_cache4_attn_decode.
+ *  - A node's infinities and NaN reach only the rows that see it.
+ *  - Every run of a call gives the same bits.
+ * Arithmetic: O is rounded once, to dtype.
+ */
+ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
+                                const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,
+                                const ice_rows *O, void *ws, size_t ws_bytes, int32_t *err_dev, void *stream);
+
+/* The same over the selected pages of a 4-bit pool (records, page_len,
+ * sel_pages, sel_count and max_sel as in ice_sparse_attn_decode4; all nodes of
+ * a sequence share a unit's selection), a cache's tokens (NULL: none) and the
+ * tree, in one softmax. */
+ice_status ice_sparse_attn_tree4(const ice_params *p, const ice_tree *tree, const ice_rows *q, const void *records,
+                                 const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count,
+                                 int32_t max_sel, const ice_cache4 *cache, const int32_t *lens, const ice_rows *k,
+                                 const ice_rows *v, float scale, const ice_rows *O, void *ws, size_t ws_bytes,
+                                 int32_t *err_dev, void *stream);
+
+/* Probabilities [B, n_nodes, vocab] of dtype: row (b, t) starts b * batch + t *
+ * node elements behind data, its elements contiguous (data aligned to one
+ * element). */
+typedef struct ice_probs {
+    const void *data;
+    int64_t batch, node; /* strides in elements, >= 0 */
+} ice_probs;
+#define ICE_VERIFY_NODES 1024
+
+/*
+ * Which drafted tokens the target model accepts.  tokens [B, n_nodes] int32 are
+ * the nodes' tokens (node 0's is not read), target row t the target model's
+ * probabilities of the token behind node t, draft row t the draft's.  The walk
+ * starts at node 0; at node i, with p and q the rows of i, the children c of i
+ * are tried in order, x = tokens[c]:
+ *   draft given      beta = 0 and mass = 1 at first; c is accepted if
+ *                    uniform[c] q(x) mass < p(x) - beta q(x); if not, beta += mass
+ *                    and mass = sum max(p - beta q, 0), whose shares are what is
+ *                    left to draw from (a refusal where mass = 0 changes nothing);
+ *   draft NULL       every drafted token is certain: accepted if uniform[c] mass <
+ *                    p(x), mass = 1 at first; if not, mass falls by p(x), to 0 at
+ *                    least, and x is left out (p(x) = 0) from then on;
+ *   uniform NULL     greedy: accepted if x is the first of p's largest elements.
+ * The walk goes on at an accepted child.  Where no child is left, next_token is
+ * drawn: the first y whose running sum of weights (max(p - beta q, 0), or p
+ * without what was left out) passes uniform[0] times their sum; of p itself if
+ * that sum is 0; greedy: the first of p's largest elements.  uniform [B,
+ * n_nodes] float are random numbers in [0, 1), one a node.  So each drafted
+ * token drawn from its parent's row of draft gives tokens distributed as the
+ * target's.  Chains (parents NULL) are verified the same way.
+ * path [B, n_nodes] int32: the accepted nodes, node 0 first, -1 behind them;
+ * n_path [B] int32: how many (0 and next_token -1 where counts[b] = 0).
+ *  - A token outside [0, vocab) sets ICE_ERR_CAPACITY in err_dev and its node is
+ *    not accepted; nodes that follow none (a second root) are not reached.
+ *  - NaN and negative probabilities count as 0 (greedy: NaN is never the
+ *    largest).  A row of no probability at all gives next_token -1 and
+ *    ICE_ERR_INVALID_ARG in err_dev.
+ * Decisions are taken in 64 bits and sums in pairs of 32 (48 bits), in one order:
+ * every run of a call gives the same answer.
+ */
+ice_status ice_tree_verify(int32_t batch, int32_t vocab, int32_t dtype, const ice_tree *tree, const ice_probs *target,
+                           const ice_probs *draft, const int32_t *tokens, const float *uniform, int32_t *path,
+                           int32_t *n_path, int32_t *next_token, int32_t *err_dev, void *stream);
+
+/*
+ * The accepted nodes' keys and values into the 4-bit caches of n_layers layers:
+ * token start[b] + i of layer l's cache becomes row (b, path[b, i]) of layer l's
+ * k and v in 4 bits, i < n_path[b] (path [B, n_nodes] and n_path [B] as
+ * ice_tree_verify writes them).  k and v are layer 0's rows [B, n_nodes, Hkv, d]
+ * (rotated), layer l's k_layer and v_layer elements behind them; layer l's
+ * records start l * records_layer bytes behind cache->records, n_pages of them
+ * a layer, all layers under cache->table.  Only those tokens' bytes are
+ * written; start is not changed.  Tokens of one call must fall into different
+ * slots, and records of layers must not lie on one another.
+ * ICE_ERR_CAPACITY in err_dev, and that row left out, where path is outside 0
+ * .. n_nodes - 1 or the token outside the cache.
+ */
+ice_status ice_cache4_commit(const ice_params *p, int32_t n_layers, int32_t n_nodes, const ice_rows *k,
+                             const ice_rows *v, int64_t k_layer, int64_t v_layer, const int32_t *path,
+                             const int32_t *n_path, const int32_t *start, const ice_cache4 *cache,
+                             int64_t records_layer, int32_t *err_dev, void *stream);
+
 /* ----------------------------------------------------- host page pool --- */
 /*
  * Step a12: the page pool in pinned host memory, with the selected pages of

@@ -68,6 +68,14 @@ class IceCache4(ctypes.Structure):
                 ("max_pages", ctypes.c_int32)]
 
 
+class IceTree(ctypes.Structure):
+    _fields_ = [("parents", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("n_nodes", ctypes.c_int32)]
+
+
+class IceProbs(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("node", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -83,6 +91,7 @@ def load() -> ctypes.CDLL:
     P, i32, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     pp, pi = ctypes.POINTER(IceParams), ctypes.POINTER(IceIndex)
     pr, po, pc = ctypes.POINTER(IceRows), ctypes.POINTER(IceRope), ctypes.POINTER(IceCache4)
+    pt, pb, i64 = ctypes.POINTER(IceTree), ctypes.POINTER(IceProbs), ctypes.c_int64
     sigs = {
         "ice_status_string": ([i32], ctypes.c_char_p),
         "ice_last_error": ([], ctypes.c_char_p),
@@ -119,6 +128,11 @@ def load() -> ctypes.CDLL:
         "ice_attn4_workspace_bytes": ([pp, ctypes.POINTER(sz)], i32),
         "ice_cache4_attn_decode": ([pp, P, pc, P, f32, P, P, P, sz, P, P], i32),
         "ice_sparse_attn_decode4": ([pp, P, P, P, P, P, i32, pc, P, f32, P, P, P, sz, P, P], i32),
+        "ice_tree_workspace_bytes": ([pp, ctypes.POINTER(sz)], i32),
+        "ice_cache4_attn_tree": ([pp, pt, pr, pc, P, pr, pr, f32, pr, P, sz, P, P], i32),
+        "ice_sparse_attn_tree4": ([pp, pt, pr, P, P, P, P, i32, pc, P, pr, pr, f32, pr, P, sz, P, P], i32),
+        "ice_tree_verify": ([i32, i32, i32, pt, pb, pb, P, P, P, P, P, P, P], i32),
+        "ice_cache4_commit": ([pp, i32, i32, pr, pr, i64, i64, P, P, P, pc, i64, P, P], i32),
         "ice_host_pool_create": ([sz, sz, i32, ctypes.POINTER(P)], i32),
         "ice_host_pool_destroy": ([P], i32),
         "ice_host_pool_pointers": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P)], i32),
@@ -144,7 +158,8 @@ def exported_symbols() -> list[str]:
             "ice_insert_workspace_bytes", "ice_insert_tokens", "ice_rope_table", "ice_qkv_rope",
             "ice_cache4_append", "ice_cache4_read", "ice_pool4_bytes", "ice_pool4_pack", "ice_pool4_unpack",
             "ice_attn4_workspace_bytes", "ice_cache4_attn_decode", "ice_sparse_attn_decode4",
-            "ice_host_pool_create", "ice_host_pool_destroy",
+            "ice_tree_workspace_bytes", "ice_cache4_attn_tree", "ice_sparse_attn_tree4", "ice_tree_verify",
+            "ice_cache4_commit", "ice_host_pool_create", "ice_host_pool_destroy",
             "ice_host_pool_pointers", "ice_host_pool_staging_bytes", "ice_host_pool_gather_h2d"]
 
 
@@ -580,6 +595,82 @@ def ice_sparse_attn_decode4(params, Q, records, page_len, sel_pages, sel_count, 
                                           _ptr(sel_pages), _ptr(sel_count), sel_pages.shape[-1], cache,
                                           _ptr(lens), float(scale), _ptr(O), _ptr(lse), _ptr(ws), _nbytes(ws),
                                           _ptr(err), _stream(stream)))
+
+
+# --------------------------------------------- trees of drafted tokens ----
+ICE_TREE_NODES, ICE_VERIFY_NODES = 256, 1024
+
+
+class Tree(IceTree):
+    """ice_tree: parents [B, n_nodes] int32 (None: a chain) and counts [B] int32 (None: n_nodes everywhere)."""
+
+    def __init__(self, parents=None, counts=None, n_nodes: int | None = None):
+        if n_nodes is None:
+            if parents is None:
+                raise IceError(ICE_ERR_INVALID_ARG, "a chain needs n_nodes")
+            n_nodes = parents.shape[-1]
+        if parents is not None and (parents.dtype != torch.int32 or parents.dim() != 2 or
+                                    parents.shape[1] != n_nodes or not parents.is_contiguous()):
+            raise IceError(ICE_ERR_INVALID_ARG, "parents are contiguous int32 [B, n_nodes]")
+        if counts is not None and (counts.dtype != torch.int32 or counts.dim() != 1 or not counts.is_contiguous()):
+            raise IceError(ICE_ERR_INVALID_ARG, "counts are contiguous int32 [B]")
+        super().__init__(_ptr(parents), _ptr(counts), n_nodes)
+        self.keep = (parents, counts)
+
+
+def probs(t: torch.Tensor) -> IceProbs:
+    """Probabilities [B, n_nodes, vocab] (bf16 or fp32, elements of a row contiguous, any other strides) as ice_probs."""
+    if t.dim() != 3 or t.dtype not in (torch.bfloat16, torch.float32) or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise IceError(ICE_ERR_INVALID_ARG, f"probabilities are bf16 or fp32 [B, n_nodes, vocab] with contiguous rows: "
+                                            f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    r = IceProbs(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+    r.keep = t
+    return r
+
+
+def ice_tree_workspace_bytes(params: IceParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ice_tree_workspace_bytes(params, ctypes.byref(n)))
+    return n.value
+
+
+def ice_cache4_attn_tree(params, tree, q, cache, lens, k, v, scale, O, ws, err, stream=None):
+    """q, k, v and O are ``rows(...)`` views, tree a Tree, cache a Cache4 (or None, with lens None)."""
+    _check(load().ice_cache4_attn_tree(params, tree, q, cache, _ptr(lens), k, v, float(scale), O, _ptr(ws),
+                                       _nbytes(ws), _ptr(err), _stream(stream)))
+
+
+def ice_sparse_attn_tree4(params, tree, q, records, page_len, sel_pages, sel_count, cache, lens, k, v, scale, O, ws,
+                          err, stream=None):
+    _check(load().ice_sparse_attn_tree4(params, tree, q, _ptr(records), _ptr(page_len), _ptr(sel_pages),
+                                        _ptr(sel_count), sel_pages.shape[-1], cache, _ptr(lens), k, v, float(scale),
+                                        O, _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)))
+
+
+def ice_tree_verify(tree, target, draft, tokens, uniform, path, n_path, next_token, err, stream=None):
+    """target and draft (or None) are ``probs(...)`` views, tokens and path [B, n_nodes] int32, uniform [B, n_nodes]
+    fp32 (or None: greedy), n_path and next_token [B] int32."""
+    B, n, vocab = target.keep.shape
+    dt = target.keep.dtype
+    if draft is not None and (draft.keep.dtype != dt or tuple(draft.keep.shape) != (B, n, vocab)):
+        raise IceError(ICE_ERR_INVALID_ARG, "draft and target have one type and shape")
+    if n != tree.n_nodes:
+        raise IceError(ICE_ERR_INVALID_ARG, f"target has {n} rows a sequence, the tree {tree.n_nodes} nodes")
+    for x, t, shape in ((tokens, torch.int32, (B, n)), (path, torch.int32, (B, n)), (uniform, torch.float32, (B, n)),
+                        (n_path, torch.int32, (B,)), (next_token, torch.int32, (B,))):
+        if x is not None and (x.dtype != t or tuple(x.shape) != shape or not x.is_contiguous()):
+            raise IceError(ICE_ERR_INVALID_ARG, f"expected contiguous {t} {shape}, got {x.dtype} {tuple(x.shape)}")
+    _check(load().ice_tree_verify(B, vocab, ICE_BF16 if dt == torch.bfloat16 else ICE_FP32, tree, target, draft,
+                                  _ptr(tokens), _ptr(uniform), _ptr(path), _ptr(n_path), _ptr(next_token), _ptr(err),
+                                  _stream(stream)))
+
+
+def ice_cache4_commit(params, n_layers, n_nodes, k, v, path, n_path, start, cache, err, *, k_layer=0, v_layer=0,
+                      records_layer=0, stream=None):
+    """k and v are layer 0's ``rows(...)`` views, k_layer and v_layer the elements and records_layer the bytes from a
+    layer to the next (not read with one layer)."""
+    _check(load().ice_cache4_commit(params, n_layers, n_nodes, k, v, k_layer, v_layer, _ptr(path), _ptr(n_path),
+                                    _ptr(start), cache, records_layer, _ptr(err), _stream(stream)))
 
 
 # ----------------------------------------------------- buffer helpers -----

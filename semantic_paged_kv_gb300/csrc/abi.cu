@@ -899,4 +899,129 @@ ice_status ice_sparse_attn_decode4(const ice_params *p, const void *Q, const voi
                        "ice_sparse_attn_decode4");
 }
 
+// ------------------------------------------------- trees of drafted tokens --
+static ice_status check_tree(const ice_tree *t) {
+    if (!t) return fail(ICE_ERR_INVALID_ARG, "tree is NULL");
+    if (t->n_nodes < 0) return fail(ICE_ERR_INVALID_ARG, "n_nodes must be >= 0");
+    return ICE_OK;
+}
+
+ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (!bytes) return fail(ICE_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = tree_workspace();
+    return ICE_OK;
+}
+
+// What both attention calls check (cache NULL: no cached tokens).
+static ice_status tree_attn_common(const ice_params *p, const ice_tree *tree, const ice_rows *q,
+                                   const ice_cache4 *cache, const int32_t *lens, const ice_rows *k, const ice_rows *v,
+                                   float scale, const ice_rows *O, void *ws, size_t ws_bytes) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if ((st = check_tree(tree)) || (st = check_new(p, tree->n_nodes))) return st;
+    if (tree->parents && tree->n_nodes > ICE_TREE_NODES)
+        return fail(ICE_ERR_UNSUPPORTED, "a tree with parents has at most %d nodes here", ICE_TREE_NODES);
+    if ((st = check_rows(p, q, "q")) || (st = check_rows(p, k, "k")) || (st = check_rows(p, v, "v")) ||
+        (st = check_rows_out(p, tree->n_nodes, p->n_q_heads, O, "O")))
+        return st;
+    if (cache) {
+        if ((st = check_cache4(cache))) return st;
+        if (!lens) return fail(ICE_ERR_INVALID_ARG, "a cache needs lens");
+    } else if (lens) {
+        return fail(ICE_ERR_INVALID_ARG, "lens without a cache");
+    }
+    if (!std::isfinite(scale)) return fail(ICE_ERR_INVALID_ARG, "scale must be finite");
+    return check_ws(ws, ws_bytes, tree_workspace());
+}
+
+ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
+                                const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,
+                                const ice_rows *O, void *ws, size_t ws_bytes, int32_t *err_dev, void *stream) {
+    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes);
+    if (st) return st;
+    if (cache && (long long)units_of(*p) * cache->max_pages > (1ll << 38))
+        return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * max_pages > 2^38)");
+    if (tree->n_nodes == 0) return ICE_OK;
+    return cuda_status(launch_tree(*p, *tree, *q, nullptr, nullptr, nullptr, nullptr, 0, cache, lens, *k, *v, scale,
+                                   *O, ws, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_cache4_attn_tree");
+}
+
+ice_status ice_sparse_attn_tree4(const ice_params *p, const ice_tree *tree, const ice_rows *q, const void *records,
+                                 const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count,
+                                 int32_t max_sel, const ice_cache4 *cache, const int32_t *lens, const ice_rows *k,
+                                 const ice_rows *v, float scale, const ice_rows *O, void *ws, size_t ws_bytes,
+                                 int32_t *err_dev, void *stream) {
+    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes);
+    if (st) return st;
+    if (!records || !aligned16(records))
+        return fail(ICE_ERR_INVALID_ARG, "records must be a 16-byte aligned device pointer");
+    if (!page_len || !sel_pages || !sel_count)
+        return fail(ICE_ERR_INVALID_ARG, "page_len, sel_pages and sel_count must be non-NULL");
+    if (max_sel < 1) return fail(ICE_ERR_INVALID_ARG, "max_sel must be >= 1");
+    if (max_sel > (1 << 27) - 1) return fail(ICE_ERR_UNSUPPORTED, "max_sel must be below 2^27");
+    if ((long long)units_of(*p) * (max_sel + (cache ? (long long)cache->max_pages : 0)) > (1ll << 38))
+        return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * pages > 2^38)");
+    if (tree->n_nodes == 0) return ICE_OK;
+    return cuda_status(launch_tree(*p, *tree, *q, records, page_len, sel_pages, sel_count, max_sel, cache, lens, *k,
+                                   *v, scale, *O, ws, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_sparse_attn_tree4");
+}
+
+static ice_status check_probs(const ice_probs *x, int32_t dtype, const char *what) {
+    if (!x->data || ((uintptr_t)x->data & (dtype == ICE_BF16 ? 1u : 3u)))
+        return fail(ICE_ERR_INVALID_ARG, "%s must be a device pointer aligned to its elements", what);
+    if (x->batch < 0 || x->node < 0) return fail(ICE_ERR_INVALID_ARG, "%s: strides must not be negative", what);
+    return ICE_OK;
+}
+
+ice_status ice_tree_verify(int32_t batch, int32_t vocab, int32_t dtype, const ice_tree *tree, const ice_probs *target,
+                           const ice_probs *draft, const int32_t *tokens, const float *uniform, int32_t *path,
+                           int32_t *n_path, int32_t *next_token, int32_t *err_dev, void *stream) {
+    if (batch < 1 || vocab < 1) return fail(ICE_ERR_INVALID_ARG, "batch and vocab must be >= 1");
+    if (batch >= 1 << 24 || vocab > 1 << 28)
+        return fail(ICE_ERR_UNSUPPORTED, "batch must be below 2^24 and vocab at most 2^28");
+    if (dtype != ICE_BF16 && dtype != ICE_FP32) return fail(ICE_ERR_INVALID_ARG, "dtype must be ICE_BF16 or ICE_FP32");
+    ice_status st = check_tree(tree);
+    if (st) return st;
+    if (tree->n_nodes < 1) return fail(ICE_ERR_INVALID_ARG, "n_nodes must be >= 1");
+    if (tree->n_nodes > ICE_VERIFY_NODES)
+        return fail(ICE_ERR_UNSUPPORTED, "at most %d nodes are supported", ICE_VERIFY_NODES);
+    if (!target) return fail(ICE_ERR_INVALID_ARG, "target is NULL");
+    if ((st = check_probs(target, dtype, "target")) || (draft && (st = check_probs(draft, dtype, "draft")))) return st;
+    if (!tokens || !path || !n_path || !next_token)
+        return fail(ICE_ERR_INVALID_ARG, "tokens, path, n_path and next_token must be non-NULL");
+    return cuda_status(launch_tree_verify(batch, vocab, dtype, *tree, *target, draft, tokens, uniform, path, n_path,
+                                          next_token, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_tree_verify");
+}
+
+ice_status ice_cache4_commit(const ice_params *p, int32_t n_layers, int32_t n_nodes, const ice_rows *k,
+                             const ice_rows *v, int64_t k_layer, int64_t v_layer, const int32_t *path,
+                             const int32_t *n_path, const int32_t *start, const ice_cache4 *cache,
+                             int64_t records_layer, int32_t *err_dev, void *stream) {
+    ice_status st = check_params(p);
+    if (st) return st;
+    if (n_layers < 0) return fail(ICE_ERR_INVALID_ARG, "n_layers must be >= 0");
+    if ((long long)n_layers * p->batch > (1ll << 30))
+        return fail(ICE_ERR_UNSUPPORTED, "too many layers in one call (n_layers * batch > 2^30)");
+    if ((st = check_new(p, n_nodes)) || (st = check_rows(p, k, "k")) || (st = check_rows(p, v, "v")) ||
+        (st = check_cache4(cache)))
+        return st;
+    const int64_t vec = p->dtype == ICE_BF16 ? 8 : 4;
+    if (k_layer < 0 || v_layer < 0 || k_layer % vec || v_layer % vec)
+        return fail(ICE_ERR_INVALID_ARG, "k_layer and v_layer must be multiples of 16 bytes and not negative");
+    if (records_layer < 0 || records_layer % 16)
+        return fail(ICE_ERR_INVALID_ARG, "records_layer must be a multiple of 16 bytes and not negative");
+    if (n_layers > 1 && records_layer < (int64_t)cache->n_pages * p->n_kv_heads * ICE_RECORD4_BYTES)
+        return fail(ICE_ERR_INVALID_ARG, "records_layer puts the records of two layers on one another");
+    if (!path || !n_path || !start) return fail(ICE_ERR_INVALID_ARG, "path, n_path and start must be non-NULL");
+    if (n_nodes == 0 || n_layers == 0) return ICE_OK;
+    return cuda_status(launch_cache4_commit(*p, n_layers, n_nodes, *k, *v, k_layer, v_layer, path, n_path, start,
+                                            *cache, records_layer, err_dev, static_cast<cudaStream_t>(stream)),
+                       "ice_cache4_commit");
+}
+
 }  // extern "C"

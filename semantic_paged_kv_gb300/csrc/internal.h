@@ -214,6 +214,21 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
                          const int32_t *lens, float scale, float *O, float *lse, void *ws, int32_t *err,
                          cudaStream_t s);
 
+// ------------------------------------------------ trees of drafted tokens --
+size_t tree_workspace();
+// records NULL: no selected pages; cache NULL: no token-ordered pages.
+cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,
+                        const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count, int max_sel,
+                        const ice_cache4 *cache, const int32_t *lens, const ice_rows &k, const ice_rows &v, float scale,
+                        const ice_rows &o, void *ws, int32_t *err, cudaStream_t s);
+cudaError_t launch_tree_verify(int batch, int vocab, int dtype, const ice_tree &t, const ice_probs &target,
+                               const ice_probs *draft, const int32_t *tokens, const float *uniform, int32_t *path,
+                               int32_t *n_path, int32_t *next, int32_t *err, cudaStream_t s);
+cudaError_t launch_cache4_commit(const ice_params &p, int n_layers, int n_nodes, const ice_rows &k, const ice_rows &v,
+                                 long long k_layer, long long v_layer, const int32_t *path, const int32_t *n_path,
+                                 const int32_t *start, const ice_cache4 &cache, long long records_layer, int32_t *err,
+                                 cudaStream_t s);
+
 // Allocation-free attention: scratch in the library's static device array.
 size_t attention_noalloc_bytes(const ice_params &p, int max_sel);
 cudaError_t launch_attention_noalloc(const ice_params &p, const void *Q, const void *kbuf, const void *vbuf,

@@ -1,0 +1,240 @@
+// Attention of drafted tokens over 4-bit pages: what its kernels share -- the
+// cut of the work into runs, the ancestors of nodes, and partial results.
+//
+// A unit (sequence, KV head) with n nodes has n g query rows (row r: node r / g,
+// head r % g of the group), cut into blocks of R rows.  A segment is one block
+// and all that it attends to: tiles of 8 pages (128 slots; selected pages, then
+// the cache's), then tiles of 128 nodes up to the block's last one.  The tiles
+// of all segments, one after another, are cut into equal runs, one per CTA,
+// whatever the lengths; a segment counts kTreeOver tiles more than it has (what
+// starting and ending one costs).  A segment that runs cut leaves partial
+// results in the workspace, joined in run order by a second kernel.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "quant4.cuh"
+
+namespace ice {
+namespace tree {
+
+constexpr int kTile = 128;                  // slots or nodes of a tile
+constexpr int kTilePages = kTile / kPage;
+constexpr int kMaxNodes = ICE_TREE_NODES;   // of a tree with parents
+constexpr int kWords = kMaxNodes / 32;
+constexpr int kPartRows = 256;              // rows of a partial result, at most
+constexpr int kTreeOver = 2;
+constexpr int kMinRun = 2;                  // tiles of a run, at least
+
+// The segment that starts in a CTA and goes on in the next ones (runs 0: none).
+struct Part {
+    int32_t unit, block, runs, inside;
+};
+
+struct Args {
+    ice_rows q, k, v, o;
+    const int32_t *parents, *counts;
+    int n_nodes;
+    const unsigned char *pool;  // selected pages (NULL: none)
+    const int32_t *page_len, *sel_pages, *sel_count;
+    int page_cap, max_sel;
+    const unsigned char *cache;  // token-ordered pages (NULL: none)
+    const int32_t *table, *lens;
+    int n_pages, max_pages;
+    int g, hq, hkv, units;
+    float scale;
+    float *part_o;    // [2 CTAs, kPartRows, 128]
+    float2 *part_ml;  // [2 CTAs, kPartRows]: maximum (powers of two), sum
+    Part *parts;      // [CTAs]
+    int32_t *err;
+};
+
+__device__ __forceinline__ int nodes_of(const Args &A, int b) {
+    return A.counts ? min(max(A.counts[b], 0), A.n_nodes) : A.n_nodes;
+}
+// (selected pages, cache tokens) of a unit.
+__device__ __forceinline__ int2 counts_of(const Args &A, int u) {
+    int2 n = make_int2(0, 0);
+    if (A.pool) n.x = min(max(A.sel_count[u], 0), A.max_sel);
+    if (A.cache) {
+        const int t = A.lens[u / A.hkv], most = A.max_pages * kPage;  // < 2^31
+        if (t < 0 || t > most) set_err(A.err, ICE_ERR_CAPACITY);
+        n.y = min(max(t, 0), most);
+    }
+    return n;
+}
+__device__ __forceinline__ int pages_of(int2 n) { return n.x + (n.y + kPage - 1) / kPage; }
+// (pages < 2^28: no overflow)
+__device__ __forceinline__ int page_tiles(int2 n) { return (pages_of(n) + kTilePages - 1) / kTilePages; }
+
+// Unit u, block blk: its tiles start at place `first` of the run (a negative
+// one before it), n of them, the first n_page of pages.
+struct Segment {
+    int u, blk, blocks, nodes;
+    int2 cnt;
+    int n_page, n;
+    long long first;
+    __device__ __forceinline__ long long end() const { return first + n; }
+};
+
+template <int R> __device__ __forceinline__ int node_tiles(int nodes, int g, int blk) {
+    const long long last = ((long long)(blk + 1) * R - 1) / g;
+    return (int)(last < nodes ? last : nodes - 1) / kTile + 1;
+}
+template <int R> __device__ __forceinline__ int blocks_of(int nodes, int g) {
+    return (int)(((long long)nodes * g + R - 1) / R);
+}
+template <int R> __device__ __forceinline__ long long places_of(int2 cnt, int nodes, int g) {
+    const int blocks = blocks_of<R>(nodes, g);
+    long long n = (long long)blocks * (page_tiles(cnt) + kTreeOver);
+    for (int i = 0; i < blocks; ++i) n += node_tiles<R>(nodes, g, i);
+    return n;
+}
+template <int R> __device__ __forceinline__ void load_unit(const Args &A, int u, Segment &s) {
+    s.u = u;
+    s.blk = 0;
+    s.nodes = nodes_of(A, u / A.hkv);
+    s.cnt = counts_of(A, u);
+    s.blocks = blocks_of<R>(s.nodes, A.g);
+    s.n_page = page_tiles(s.cnt);
+}
+template <int R> __device__ __forceinline__ void size_segment(const Args &A, long long place, Segment &s) {
+    s.n = s.n_page + node_tiles<R>(s.nodes, A.g, s.blk);
+    s.first = place + kTreeOver;
+}
+// The segment after s.
+template <int R> __device__ __forceinline__ void next_segment(const Args &A, Segment &s) {
+    const long long place = s.end();
+    if (++s.blk >= s.blocks) {
+        int u = s.u;
+        do load_unit<R>(A, ++u, s);
+        while (s.blocks == 0 && u + 1 < A.units);
+    }
+    size_segment<R>(A, place, s);
+}
+
+struct PlanScratch {
+    long long sum[32];
+    Segment seg;
+};
+struct Run {
+    long long f0, share;
+    int n;  // places (0: none)
+};
+// This CTA's run and its first segment (all threads call; S is read by all after it returns).
+template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Args &A, PlanScratch &S) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (A.units + kThreads - 1) / kThreads;
+    const int ua = min(tid * per, A.units), ub = min(ua + per, A.units);
+    long long mine = 0;
+    for (int u = ua; u < ub; ++u) mine += places_of<R>(counts_of(A, u), nodes_of(A, u / A.hkv), A.g);
+    long long before = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += y;
+    }
+    if (lane == 31) S.sum[warp] = before;
+    __syncthreads();
+    long long total = 0;
+    before -= mine;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += S.sum[w];
+        total += S.sum[w];
+    }
+    Run r;
+    r.share = (total + gridDim.x - 1) / gridDim.x;
+    if (r.share < kMinRun + kTreeOver) r.share = kMinRun + kTreeOver;
+    r.f0 = r.share * blockIdx.x;
+    r.n = (int)max(min(r.share, total - r.f0), 0ll);
+    if (r.n > 0 && r.f0 >= before && r.f0 < before + mine) {
+        long long at = before;
+        for (int u = ua; u < ub; ++u) {
+            Segment s;
+            load_unit<R>(A, u, s);
+            for (; s.blk < s.blocks; ++s.blk) {
+                size_segment<R>(A, at - r.f0, s);
+                if (s.end() > 0) break;
+                at = s.end() + r.f0;
+            }
+            if (s.blk < s.blocks) {
+                S.seg = s;
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    return r;
+}
+// A segment whose first tile is in this CTA's run and whose last one is not: its runs.  (One at most starts in a CTA.)
+__device__ __forceinline__ Part part_of(const Segment &s, const Run &r) {
+    const long long us = r.f0 + s.first;
+    const long long ca = us / r.share, cb = (us + s.n - 1) / r.share;
+    return Part{s.u, s.blk, (int)(cb - ca + 1), us > ca * r.share ? 1 : 0};
+}
+
+// Ancestors of the nodes of a tree, themselves among them, by pointer jumping.
+struct Ancestors {
+    uint32_t mask[2][kMaxNodes][kWords];
+    int16_t up[2][kMaxNodes];
+};
+// The buffer of X.mask that holds them (threads 0 .. n_threads - 1 call, with a barrier among them as `sync`).
+template <typename Sync>
+__device__ __forceinline__ int find_ancestors(const int32_t *parents, int nodes, Ancestors &X, int32_t *err, int tid,
+                                              int n_threads, Sync sync) {
+    for (int t = tid; t < nodes; t += n_threads) {
+        int a = parents[t];
+        if (a >= t || a < -1) {
+            set_err(err, ICE_ERR_INVALID_ARG);
+            a = -1;
+        }
+        X.up[0][t] = (int16_t)a;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) X.mask[0][t][w] = w == t >> 5 ? 1u << (t & 31) : 0u;
+    }
+    int cur = 0;
+    for (int reach = 1; reach < nodes; reach <<= 1, cur ^= 1) {
+        sync();
+        for (int t = tid; t < nodes; t += n_threads) {
+            const int a = X.up[cur][t];
+            X.up[cur ^ 1][t] = a >= 0 ? X.up[cur][a] : (int16_t)-1;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+                X.mask[cur ^ 1][t][w] = X.mask[cur][t][w] | (a >= 0 ? X.mask[cur][a][w] : 0u);
+        }
+    }
+    sync();
+    return cur;
+}
+
+// Record and used slots of page x of a unit (nullptr: none).
+__device__ __forceinline__ const unsigned char *page_at(const Args &A, int u, int2 cnt, int x, int &len) {
+    len = 0;
+    if (x < cnt.x) {
+        const int id = A.sel_pages[(size_t)u * A.max_sel + x];
+        if (id >= 0 && id < A.page_cap) {
+            const size_t at = (size_t)u * A.page_cap + id;
+            len = min(max(A.page_len[at], 0), kPage);
+            return A.pool + at * q4::kRecord;
+        }
+        set_err(A.err, ICE_ERR_CAPACITY);
+        return nullptr;
+    }
+    x -= cnt.x;
+    const int rest = cnt.y - x * kPage, b = u / A.hkv;
+    if (rest <= 0) return nullptr;
+    const int id = A.table[(size_t)b * A.max_pages + x];
+    if (id >= 0 && id < A.n_pages) {
+        len = min(rest, kPage);
+        return A.cache + ((size_t)id * A.hkv + (u - b * A.hkv)) * q4::kRecord;
+    }
+    set_err(A.err, ICE_ERR_CAPACITY);
+    return nullptr;
+}
+
+}  // namespace tree
+
+// fp32 rows: the kernel on the CUDA cores.
+cudaError_t launch_tree_fp32(const tree::Args &A, int grid, cudaStream_t s);
+
+}  // namespace ice

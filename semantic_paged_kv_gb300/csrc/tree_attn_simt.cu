@@ -1,0 +1,339 @@
+// Attention of drafted tokens over 4-bit pages on the CUDA cores:
+// ice_cache4_attn_tree and ice_sparse_attn_tree4 for fp32 rows.
+//   O[t] = sum_j exp(scale q_t . k_j) v_j / sum_j exp(scale q_t . k_j),
+// j over the unit's pages, the ancestors of node t and t itself.
+//
+// 64 rows and 128 tokens a tile, keys and values unpacked to fp32 in shared
+// memory, 8 x 4 scores (then 8 x 4 outputs) a thread.  A warp owns 8 rows: their
+// maxima and sums stay in it.  A tile's product with V is summed apart and then
+// added, which keeps the rounding of long sums down.
+#include <float.h>
+
+#include "tree.cuh"
+
+namespace ice {
+namespace {
+
+using namespace tree;
+
+constexpr int kRows = 64, kThreads = 256;
+constexpr int kKRow = kHeadDim + 4;  // padded (conflict-free 16-byte loads of 32 rows)
+
+struct Smem {
+    float k[kTile][kKRow];
+    float v[kTile][kHeadDim];
+    float q[kRows][kHeadDim];
+    float p[kRows][kTile];
+    Ancestors anc;
+    int len[kTilePages];
+    PlanScratch plan;
+};
+
+template <typename T> __device__ __forceinline__ const T *row_ptr(const ice_rows &r, int b, int t, int h) {
+    return static_cast<const T *>(r.data) + (long long)b * r.batch + (long long)t * r.token + (long long)h * r.head;
+}
+
+// One page's rows in fp32, by a warp: lane (token, group).  Slots behind `len` are zero.
+__device__ __forceinline__ void unpack_page(const unsigned char *rec, int len, int slot0, Smem &S) {
+    const int lane = threadIdx.x & 31, t = lane >> 1, grp = lane & 1;
+    const bool live = rec && t < len;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        float2 sm = make_float2(0.f, 0.f);
+        if (live)
+            sm = q4::unpack_meta(*reinterpret_cast<const uint32_t *>(rec + (kv ? q4::kVMeta : q4::kKMeta) + t * 8 +
+                                                                      grp * 4));
+        float *dst = (kv ? S.v[slot0 + t] : S.k[slot0 + t]) + grp * 64;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int w = grp * 8 + i;
+            float x[8];
+            q4::values_of<8>(live ? (kv ? q4::get_v(rec, t, w) : q4::get_k(rec, t, w)) : 0u, sm, x);
+            reinterpret_cast<float4 *>(dst)[2 * i] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4 *>(dst)[2 * i + 1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant__ Args A) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    Smem &S = *reinterpret_cast<Smem *>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = A.g;
+    dep_wait();
+    const Run run = plan_run<kRows, kThreads>(A, S.plan);
+    Part part{0, 0, 0, 0};
+    const float sl = A.scale * 1.4426950408889634f;
+    int anc_b = -1, anc = 0;
+    if (run.n > 0) {
+        Segment seg = S.plan.seg;
+        for (;; next_segment<kRows>(A, seg)) {
+            const int i0 = (int)max(-seg.first, 0ll), i1 = (int)min((long long)seg.n, run.n - seg.first);
+            if (seg.first >= run.n) break;
+            if (i0 >= i1) continue;  // (its tiles lie in the runs before)
+            const int b = seg.u / A.hkv, h = seg.u - b * A.hkv;
+            const int row0 = seg.blk * kRows, rows = min(kRows, seg.nodes * g - row0);
+            __syncthreads();  // the segment before has been read
+            for (int i = tid; i < kRows * kHeadDim / 8; i += kThreads) {
+                const int r = i / (kHeadDim / 8), c = i % (kHeadDim / 8) * 8;
+                float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (r < rows) {
+                    const int t = (row0 + r) / g, hh = (row0 + r) % g;
+                    load8<T>(row_ptr<T>(A.q, b, t, h * g + hh) + c, x);
+                }
+                *reinterpret_cast<float4 *>(&S.q[r][c]) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4 *>(&S.q[r][c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+            if (A.parents && i1 > seg.n_page && anc_b != b) {
+                anc = find_ancestors(A.parents + (size_t)b * A.n_nodes, seg.nodes, S.anc, A.err, tid, kThreads,
+                                     [] { __syncthreads(); });
+                anc_b = b;
+            }
+            float o[8][4], m[8], l[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                m[i] = -FLT_MAX, l[i] = 0.f;
+                o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            }
+            for (int tile = i0; tile < i1; ++tile) {
+                const bool nodes = tile >= seg.n_page;
+                const int j0 = (tile - seg.n_page) * kTile;  // first node of the tile
+                if (!nodes) {
+                    const int x = tile * kTilePages + warp;
+                    int len = 0;
+                    const unsigned char *rec = x < pages_of(seg.cnt) ? page_at(A, seg.u, seg.cnt, x, len) : nullptr;
+                    unpack_page(rec, len, warp * kPage, S);
+                    if (lane == 0) S.len[warp] = len;
+                } else {
+                    for (int i = tid; i < kTile * kHeadDim / 8; i += kThreads) {
+                        const int r = i / (kHeadDim / 8), c = i % (kHeadDim / 8) * 8;
+                        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                        if (j0 + r < seg.nodes) {
+                            load8<T>(row_ptr<T>(A.k, b, j0 + r, h) + c, x);
+                            load8<T>(row_ptr<T>(A.v, b, j0 + r, h) + c, y);
+                        }
+                        *reinterpret_cast<float4 *>(&S.k[r][c]) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4 *>(&S.k[r][c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+                        *reinterpret_cast<float4 *>(&S.v[r][c]) = make_float4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<float4 *>(&S.v[r][c + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+                    }
+                }
+                __syncthreads();
+                // ---- scores: rows 8 warp + i, slots lane + 32 j
+                float s[8][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 2
+                for (int d = 0; d < kHeadDim; d += 4) {
+                    float4 kk[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const float4 *>(&S.k[lane + 32 * j][d]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 qq = *reinterpret_cast<const float4 *>(&S.q[8 * warp + i][d]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            s[i][j] = fmaf(qq.x, kk[j].x, s[i][j]);
+                            s[i][j] = fmaf(qq.y, kk[j].y, s[i][j]);
+                            s[i][j] = fmaf(qq.z, kk[j].z, s[i][j]);
+                            s[i][j] = fmaf(qq.w, kk[j].w, s[i][j]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int node = (row0 + 8 * warp + i) / g;
+                    float mx = m[i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int slot = lane + 32 * j;
+                        bool sees;
+                        if (!nodes)
+                            sees = (slot & (kPage - 1)) < S.len[slot / kPage];
+                        else if (j0 + slot >= seg.nodes || node >= seg.nodes)
+                            sees = false;
+                        else
+                            sees = A.parents ? S.anc.mask[anc][node][(j0 + slot) >> 5] >> (slot & 31) & 1u
+                                             : j0 + slot <= node;
+                        s[i][j] = sees ? s[i][j] * sl : -INFINITY;
+                        mx = fmaxf(mx, s[i][j]);
+                    }
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float f = exp2f(m[i] - mx);
+                    m[i] = mx;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float p = s[i][j] == -INFINITY ? 0.f : exp2f(s[i][j] - mx);
+                        sum += p;
+                        S.p[8 * warp + i][lane + 32 * j] = p;
+                    }
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    l[i] = fmaf(l[i], f, sum);
+                    o[i][0] *= f, o[i][1] *= f, o[i][2] *= f, o[i][3] *= f;
+                }
+                __syncwarp();
+                // ---- outputs: rows 8 warp + i, elements 4 lane ..
+                float a[8][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i][0] = a[i][1] = a[i][2] = a[i][3] = 0.f;
+#pragma unroll 2
+                for (int j = 0; j < kTile; j += 4) {
+                    float4 vv[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) vv[e] = *reinterpret_cast<const float4 *>(&S.v[j + e][4 * lane]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 pp = *reinterpret_cast<const float4 *>(&S.p[8 * warp + i][j]);
+                        const float w[4] = {pp.x, pp.y, pp.z, pp.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // (a node's infinities and NaN reach only the rows that see it)
+                            if (nodes && w[e] == 0.f) continue;
+                            a[i][0] = fmaf(w[e], vv[e].x, a[i][0]);
+                            a[i][1] = fmaf(w[e], vv[e].y, a[i][1]);
+                            a[i][2] = fmaf(w[e], vv[e].z, a[i][2]);
+                            a[i][3] = fmaf(w[e], vv[e].w, a[i][3]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i][0] += a[i][0], o[i][1] += a[i][1], o[i][2] += a[i][2], o[i][3] += a[i][3];
+                __syncthreads();
+            }
+            const bool whole = seg.first >= 0 && seg.end() <= run.n;
+            if (!whole && seg.first >= 0) part = part_of(seg, run);
+            const size_t slot = (size_t)blockIdx.x * 2 + (seg.first > 0 ? 1 : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 8 * warp + i;
+                if (r >= rows) break;
+                if (whole) {
+                    const float inv = 1.f / l[i];
+                    const int t = (row0 + r) / g, hh = (row0 + r) % g;
+                    T *out = const_cast<T *>(row_ptr<T>(A.o, b, t, h * g + hh)) + 4 * lane;
+                    if (sizeof(T) == 4)
+                        *reinterpret_cast<float4 *>(out) =
+                            make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+                    else {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(o[i][0] * inv, o[i][1] * inv),
+                                             y = __floats2bfloat162_rn(o[i][2] * inv, o[i][3] * inv);
+                        *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
+                                                                     *reinterpret_cast<const uint32_t *>(&y));
+                    }
+                } else {
+                    *reinterpret_cast<float4 *>(A.part_o + (slot * kPartRows + r) * kHeadDim + 4 * lane) =
+                        make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    if (lane == 0) A.part_ml[slot * kPartRows + r] = make_float2(m[i], l[i]);
+                }
+            }
+            if (seg.end() >= run.n) break;
+        }
+    }
+    if (tid == 0) A.parts[blockIdx.x] = part;
+}
+
+// The rows of the segments that runs cut, a warp each: CTA (c, y) takes rows 8 y .. of the one that starts in run c.
+template <typename T, int kBlock>
+__global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ Args A) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+    dep_wait();
+    const Part p = A.parts[c];
+    if (p.runs == 0) return;
+    const int b = p.unit / A.hkv, h = p.unit - b * A.hkv, nodes = nodes_of(A, b);
+    const int row0 = p.block * kBlock, r = blockIdx.y * 8 + warp;
+    if (r >= min(kBlock, nodes * A.g - row0)) return;
+    auto slot_of = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? p.inside : 0)) * kPartRows + r; };
+    float M = -FLT_MAX;
+    for (int k = lane; k < p.runs; k += 32) M = fmaxf(M, A.part_ml[slot_of(k)].x);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < p.runs; ++k) {
+        const float2 ml = A.part_ml[slot_of(k)];
+        const float4 x = *reinterpret_cast<const float4 *>(A.part_o + slot_of(k) * kHeadDim + 4 * lane);
+        const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+        L = fmaf(ml.y, w, L);
+        if (ml.y != 0.f) {
+            acc.x = fmaf(x.x, w, acc.x), acc.y = fmaf(x.y, w, acc.y);
+            acc.z = fmaf(x.z, w, acc.z), acc.w = fmaf(x.w, w, acc.w);
+        }
+    }
+    const float inv = 1.f / L;
+    T *out = const_cast<T *>(row_ptr<T>(A.o, b, (row0 + r) / A.g, h * A.g + (row0 + r) % A.g)) + 4 * lane;
+    if (sizeof(T) == 4)
+        *reinterpret_cast<float4 *>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
+                             y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
+}
+
+struct Ws {
+    float *part_o;
+    float2 *part_ml;
+    Part *parts;
+    size_t bytes;
+};
+Ws ws_layout(int ctas, void *base) {
+    Ws w{};
+    char *b = static_cast<char *>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *r = b ? b + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return r;
+    };
+    w.part_o = reinterpret_cast<float *>(take(sizeof(float) * 2 * ctas * kPartRows * kHeadDim));
+    w.part_ml = reinterpret_cast<float2 *>(take(sizeof(float2) * 2 * ctas * kPartRows));
+    w.parts = reinterpret_cast<Part *>(take(sizeof(Part) * ctas));
+    w.bytes = off;
+    return w;
+}
+
+template <typename T> cudaError_t launch_simt(const Args &A, int grid, cudaStream_t s) {
+    auto kern = k_tree_simt<T>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem), s, A);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k_tree_join<T, kRows>, dim3(grid, kRows / 8), dim3(256), 0, s, A);
+}
+static_assert(sizeof(Smem) <= 227 * 1024, "one CTA an SM");
+
+}  // namespace
+
+size_t tree_workspace() { return ws_layout(device_sms(), nullptr).bytes; }
+
+cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,
+                        const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count, int max_sel,
+                        const ice_cache4 *cache, const int32_t *lens, const ice_rows &k, const ice_rows &v, float scale,
+                        const ice_rows &o, void *ws, int32_t *err, cudaStream_t s) {
+    Args A{};
+    A.q = q, A.k = k, A.v = v, A.o = o;
+    A.parents = t.parents, A.counts = t.counts, A.n_nodes = t.n_nodes;
+    A.pool = static_cast<const unsigned char *>(records);
+    A.page_len = page_len, A.sel_pages = sel_pages, A.sel_count = sel_count;
+    A.page_cap = p.page_cap, A.max_sel = max_sel;
+    if (cache) {
+        A.cache = static_cast<const unsigned char *>(cache->records);
+        A.table = cache->table, A.n_pages = cache->n_pages, A.max_pages = cache->max_pages;
+        A.lens = lens;
+    }
+    A.g = p.n_q_heads / p.n_kv_heads, A.hq = p.n_q_heads, A.hkv = p.n_kv_heads, A.units = units_of(p);
+    A.scale = scale;
+    A.err = err;
+    const int sms = device_sms();
+    const Ws w = ws_layout(sms, ws);
+    A.part_o = w.part_o, A.part_ml = w.part_ml, A.parts = w.parts;
+    return p.dtype == ICE_BF16 ? launch_simt<__nv_bfloat16>(A, sms, s) : launch_simt<float>(A, sms, s);
+}
+
+}  // namespace ice
