@@ -923,6 +923,8 @@ static ice_status tree_attn_common(const ice_params *p, const ice_tree *tree, co
     if ((st = check_tree(tree)) || (st = check_new(p, tree->n_nodes))) return st;
     if (tree->parents && tree->n_nodes > ICE_TREE_NODES)
         return fail(ICE_ERR_UNSUPPORTED, "a tree with parents has at most %d nodes here", ICE_TREE_NODES);
+    if ((long long)tree->n_nodes * (p->n_q_heads / p->n_kv_heads) > 1 << 30)
+        return fail(ICE_ERR_UNSUPPORTED, "too many rows a KV head (n_nodes * heads of a group > 2^30)");
     if ((st = check_rows(p, q, "q")) || (st = check_rows(p, k, "k")) || (st = check_rows(p, v, "v")) ||
         (st = check_rows_out(p, tree->n_nodes, p->n_q_heads, O, "O")))
         return st;

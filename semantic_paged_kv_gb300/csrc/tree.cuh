@@ -43,8 +43,8 @@ struct Args {
     int n_pages, max_pages;
     int g, hq, hkv, units;
     float scale;
-    float *part_o;    // [2 CTAs, kPartRows, 128]
-    float2 *part_ml;  // [2 CTAs, kPartRows]: maximum (powers of two), sum
+    float4 *part_o;   // [2 CTAs, 32, kPartRows]: elements 4 i .. of a row's result over the run's tokens
+    float2 *part_ml;  // [2 CTAs, kPartRows]: its maximum (powers of two) and sum
     Part *parts;      // [CTAs]
     int32_t *err;
 };
@@ -232,9 +232,30 @@ __device__ __forceinline__ const unsigned char *page_at(const Args &A, int u, in
     return nullptr;
 }
 
+// Place of elements 4 i .. of row r of a partial result.
+__device__ __forceinline__ size_t part_at(size_t slot, int i, int r) {
+    return (slot * (kHeadDim / 4) + i) * kPartRows + r;
+}
+
+template <typename T> __device__ __forceinline__ const T *row_ptr(const ice_rows &r, int b, int t, int h) {
+    return static_cast<const T *>(r.data) + (long long)b * r.batch + (long long)t * r.token + (long long)h * r.head;
+}
+template <typename T> __device__ __forceinline__ T *row_out(const ice_rows &r, int b, int t, int h) {
+    return static_cast<T *>(r.data) + (long long)b * r.batch + (long long)t * r.token + (long long)h * r.head;
+}
+// Four elements of a row, rounded to its type.
+__device__ __forceinline__ void put4(float *out, float4 x) { *reinterpret_cast<float4 *>(out) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *out, float4 x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(out) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
 }  // namespace tree
 
-// fp32 rows: the kernel on the CUDA cores.
-cudaError_t launch_tree_fp32(const tree::Args &A, int grid, cudaStream_t s);
+// The attention kernels: their runs' results, the cut segments' in parts (joined by launch_tree).
+constexpr int kTreeRowsSimt = 64, kTreeRowsTc = 256;  // rows of a block
+cudaError_t launch_tree_simt(const tree::Args &A, int grid, cudaStream_t s);
+cudaError_t launch_tree_tc(const tree::Args &A, int grid, cudaStream_t s);
 
 }  // namespace ice

@@ -16,7 +16,7 @@ namespace {
 
 using namespace tree;
 
-constexpr int kRows = 64, kThreads = 256;
+constexpr int kRows = kTreeRowsSimt, kThreads = 256;
 constexpr int kKRow = kHeadDim + 4;  // padded (conflict-free 16-byte loads of 32 rows)
 
 struct Smem {
@@ -28,10 +28,6 @@ struct Smem {
     int len[kTilePages];
     PlanScratch plan;
 };
-
-template <typename T> __device__ __forceinline__ const T *row_ptr(const ice_rows &r, int b, int t, int h) {
-    return static_cast<const T *>(r.data) + (long long)b * r.batch + (long long)t * r.token + (long long)h * r.head;
-}
 
 // One page's rows in fp32, by a warp: lane (token, group).  Slots behind `len` are zero.
 __device__ __forceinline__ void unpack_page(const unsigned char *rec, int len, int slot0, Smem &S) {
@@ -211,22 +207,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
             for (int i = 0; i < 8; ++i) {
                 const int r = 8 * warp + i;
                 if (r >= rows) break;
+                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                const float4 x = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
                 if (whole) {
-                    const float inv = 1.f / l[i];
-                    const int t = (row0 + r) / g, hh = (row0 + r) % g;
-                    T *out = const_cast<T *>(row_ptr<T>(A.o, b, t, h * g + hh)) + 4 * lane;
-                    if (sizeof(T) == 4)
-                        *reinterpret_cast<float4 *>(out) =
-                            make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
-                    else {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(o[i][0] * inv, o[i][1] * inv),
-                                             y = __floats2bfloat162_rn(o[i][2] * inv, o[i][3] * inv);
-                        *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
-                                                                     *reinterpret_cast<const uint32_t *>(&y));
-                    }
+                    put4(row_out<T>(A.o, b, (row0 + r) / g, h * g + (row0 + r) % g) + 4 * lane, x);
                 } else {
-                    *reinterpret_cast<float4 *>(A.part_o + (slot * kPartRows + r) * kHeadDim + 4 * lane) =
-                        make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                    A.part_o[part_at(slot, lane, r)] = x;
                     if (lane == 0) A.part_ml[slot * kPartRows + r] = make_float2(m[i], l[i]);
                 }
             }
@@ -236,104 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     if (tid == 0) A.parts[blockIdx.x] = part;
 }
 
-// The rows of the segments that runs cut, a warp each: CTA (c, y) takes rows 8 y .. of the one that starts in run c.
-template <typename T, int kBlock>
-__global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ Args A) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-    dep_wait();
-    const Part p = A.parts[c];
-    if (p.runs == 0) return;
-    const int b = p.unit / A.hkv, h = p.unit - b * A.hkv, nodes = nodes_of(A, b);
-    const int row0 = p.block * kBlock, r = blockIdx.y * 8 + warp;
-    if (r >= min(kBlock, nodes * A.g - row0)) return;
-    auto slot_of = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? p.inside : 0)) * kPartRows + r; };
-    float M = -FLT_MAX;
-    for (int k = lane; k < p.runs; k += 32) M = fmaxf(M, A.part_ml[slot_of(k)].x);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < p.runs; ++k) {
-        const float2 ml = A.part_ml[slot_of(k)];
-        const float4 x = *reinterpret_cast<const float4 *>(A.part_o + slot_of(k) * kHeadDim + 4 * lane);
-        const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-        L = fmaf(ml.y, w, L);
-        if (ml.y != 0.f) {
-            acc.x = fmaf(x.x, w, acc.x), acc.y = fmaf(x.y, w, acc.y);
-            acc.z = fmaf(x.z, w, acc.z), acc.w = fmaf(x.w, w, acc.w);
-        }
-    }
-    const float inv = 1.f / L;
-    T *out = const_cast<T *>(row_ptr<T>(A.o, b, (row0 + r) / A.g, h * A.g + (row0 + r) % A.g)) + 4 * lane;
-    if (sizeof(T) == 4)
-        *reinterpret_cast<float4 *>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv),
-                             y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
-    }
-}
-
-struct Ws {
-    float *part_o;
-    float2 *part_ml;
-    Part *parts;
-    size_t bytes;
-};
-Ws ws_layout(int ctas, void *base) {
-    Ws w{};
-    char *b = static_cast<char *>(base);
-    size_t off = 0;
-    auto take = [&](size_t bytes) {
-        char *r = b ? b + off : nullptr;
-        off += (bytes + 255) & ~(size_t)255;
-        return r;
-    };
-    w.part_o = reinterpret_cast<float *>(take(sizeof(float) * 2 * ctas * kPartRows * kHeadDim));
-    w.part_ml = reinterpret_cast<float2 *>(take(sizeof(float2) * 2 * ctas * kPartRows));
-    w.parts = reinterpret_cast<Part *>(take(sizeof(Part) * ctas));
-    w.bytes = off;
-    return w;
-}
-
-template <typename T> cudaError_t launch_simt(const Args &A, int grid, cudaStream_t s) {
-    auto kern = k_tree_simt<T>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem), s, A);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(k_tree_join<T, kRows>, dim3(grid, kRows / 8), dim3(256), 0, s, A);
-}
 static_assert(sizeof(Smem) <= 227 * 1024, "one CTA an SM");
 
 }  // namespace
 
-size_t tree_workspace() { return ws_layout(device_sms(), nullptr).bytes; }
-
-cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,
-                        const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count, int max_sel,
-                        const ice_cache4 *cache, const int32_t *lens, const ice_rows &k, const ice_rows &v, float scale,
-                        const ice_rows &o, void *ws, int32_t *err, cudaStream_t s) {
-    Args A{};
-    A.q = q, A.k = k, A.v = v, A.o = o;
-    A.parents = t.parents, A.counts = t.counts, A.n_nodes = t.n_nodes;
-    A.pool = static_cast<const unsigned char *>(records);
-    A.page_len = page_len, A.sel_pages = sel_pages, A.sel_count = sel_count;
-    A.page_cap = p.page_cap, A.max_sel = max_sel;
-    if (cache) {
-        A.cache = static_cast<const unsigned char *>(cache->records);
-        A.table = cache->table, A.n_pages = cache->n_pages, A.max_pages = cache->max_pages;
-        A.lens = lens;
-    }
-    A.g = p.n_q_heads / p.n_kv_heads, A.hq = p.n_q_heads, A.hkv = p.n_kv_heads, A.units = units_of(p);
-    A.scale = scale;
-    A.err = err;
-    const int sms = device_sms();
-    const Ws w = ws_layout(sms, ws);
-    A.part_o = w.part_o, A.part_ml = w.part_ml, A.parts = w.parts;
-    return p.dtype == ICE_BF16 ? launch_simt<__nv_bfloat16>(A, sms, s) : launch_simt<float>(A, sms, s);
+cudaError_t launch_tree_simt(const Args &A, int grid, cudaStream_t s) {
+    auto kern = k_tree_simt<float>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(grid), dim3(kThreads), sizeof(Smem), s, A);
 }
 
 }  // namespace ice
