@@ -22,7 +22,7 @@ constexpr int kTile = 128;                  // slots or nodes of a tile
 constexpr int kTilePages = kTile / kPage;
 constexpr int kMaxNodes = ICE_TREE_NODES;   // of a tree with parents
 constexpr int kWords = kMaxNodes / 32;
-constexpr int kPartRows = 256;              // rows of a partial result, at most
+constexpr int kPartRows = 128;              // rows of a partial result, at most
 constexpr int kTreeOver = 2;
 constexpr int kMinRun = 2;                  // tiles of a run, at least
 
@@ -78,11 +78,11 @@ struct Segment {
 };
 
 template <int R> __device__ __forceinline__ int node_tiles(int nodes, int g, int blk) {
-    const long long last = ((long long)(blk + 1) * R - 1) / g;
-    return (int)(last < nodes ? last : nodes - 1) / kTile + 1;
+    const int last = ((blk + 1) * R - 1) / g;  // (n_nodes g <= 2^30)
+    return min(last, nodes - 1) / kTile + 1;
 }
 template <int R> __device__ __forceinline__ int blocks_of(int nodes, int g) {
-    return (int)(((long long)nodes * g + R - 1) / R);
+    return (nodes * g + R - 1) / R;
 }
 template <int R> __device__ __forceinline__ long long places_of(int2 cnt, int nodes, int g) {
     const int blocks = blocks_of<R>(nodes, g);
@@ -143,7 +143,7 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
         total += S.sum[w];
     }
     Run r;
-    r.share = (total + gridDim.x - 1) / gridDim.x;
+    r.share = total < (1ll << 30) ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     if (r.share < kMinRun + kTreeOver) r.share = kMinRun + kTreeOver;
     r.f0 = r.share * blockIdx.x;
     r.n = (int)max(min(r.share, total - r.f0), 0ll);
@@ -166,11 +166,14 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
     __syncthreads();
     return r;
 }
-// A segment whose first tile is in this CTA's run and whose last one is not: its runs.  (One at most starts in a CTA.)
+// A segment whose first tile is in this CTA's run (a full one) and whose last one is not: its runs.  (One at most starts in
+// a CTA.)
 __device__ __forceinline__ Part part_of(const Segment &s, const Run &r) {
-    const long long us = r.f0 + s.first;
-    const long long ca = us / r.share, cb = (us + s.n - 1) / r.share;
-    return Part{s.u, s.blk, (int)(cb - ca + 1), us > ca * r.share ? 1 : 0};
+    const long long beyond = s.end() - r.n;
+    const int more = beyond < (1ll << 30) && r.share < (1ll << 30)
+                         ? (int)(((unsigned)beyond + (unsigned)r.share - 1) / (unsigned)r.share)
+                         : (int)((beyond + r.share - 1) / r.share);
+    return Part{s.u, s.blk, 1 + more, s.first > 0 ? 1 : 0};
 }
 
 // Ancestors of the nodes of a tree, themselves among them, by pointer jumping.
@@ -207,29 +210,28 @@ __device__ __forceinline__ int find_ancestors(const int32_t *parents, int nodes,
     return cur;
 }
 
-// Record and used slots of page x of a unit (nullptr: none).
-__device__ __forceinline__ const unsigned char *page_at(const Args &A, int u, int2 cnt, int x, int &len) {
+// Record and used slots of a unit's page x, whose number is id (nullptr: there is no such page).
+__device__ __forceinline__ const unsigned char *page_of_id(const Args &A, int u, int2 cnt, int x, int id, int &len) {
     len = 0;
     if (x < cnt.x) {
-        const int id = A.sel_pages[(size_t)u * A.max_sel + x];
         if (id >= 0 && id < A.page_cap) {
             const size_t at = (size_t)u * A.page_cap + id;
             len = min(max(A.page_len[at], 0), kPage);
             return A.pool + at * q4::kRecord;
         }
-        set_err(A.err, ICE_ERR_CAPACITY);
-        return nullptr;
-    }
-    x -= cnt.x;
-    const int rest = cnt.y - x * kPage, b = u / A.hkv;
-    if (rest <= 0) return nullptr;
-    const int id = A.table[(size_t)b * A.max_pages + x];
-    if (id >= 0 && id < A.n_pages) {
-        len = min(rest, kPage);
+    } else if (id >= 0 && id < A.n_pages) {
+        const int b = u / A.hkv;
+        len = min(cnt.y - (x - cnt.x) * kPage, kPage);
         return A.cache + ((size_t)id * A.hkv + (u - b * A.hkv)) * q4::kRecord;
     }
     set_err(A.err, ICE_ERR_CAPACITY);
     return nullptr;
+}
+// (x < pages_of(cnt))
+__device__ __forceinline__ const unsigned char *page_at(const Args &A, int u, int2 cnt, int x, int &len) {
+    const int id = x < cnt.x ? A.sel_pages[(size_t)u * A.max_sel + x]
+                             : A.table[(size_t)(u / A.hkv) * A.max_pages + (x - cnt.x)];
+    return page_of_id(A, u, cnt, x, id, len);
 }
 
 // Place of elements 4 i .. of row r of a partial result.
@@ -254,7 +256,7 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *out, float4 x) {
 }  // namespace tree
 
 // The attention kernels: their runs' results, the cut segments' in parts (joined by launch_tree).
-constexpr int kTreeRowsSimt = 64, kTreeRowsTc = 256;  // rows of a block
+constexpr int kTreeRowsSimt = 64, kTreeRowsTc = 128;  // rows of a block
 cudaError_t launch_tree_simt(const tree::Args &A, int grid, cudaStream_t s);
 cudaError_t launch_tree_tc(const tree::Args &A, int grid, cudaStream_t s);
 
