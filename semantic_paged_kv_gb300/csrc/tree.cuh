@@ -178,36 +178,39 @@ __device__ __forceinline__ Part part_of(const Segment &s, const Run &r) {
 
 // Ancestors of the nodes of a tree, themselves among them, by pointer jumping.
 struct Ancestors {
-    uint32_t mask[2][kMaxNodes][kWords];
-    int16_t up[2][kMaxNodes];
+    uint32_t mask[kMaxNodes][kWords];
+    int16_t up[kMaxNodes];
 };
-// The buffer of X.mask that holds them (threads 0 .. n_threads - 1 call, with a barrier among them as `sync`).
+// By kMaxNodes threads, thread t node t, with a barrier among them as `sync`.
 template <typename Sync>
-__device__ __forceinline__ int find_ancestors(const int32_t *parents, int nodes, Ancestors &X, int32_t *err, int tid,
-                                              int n_threads, Sync sync) {
-    for (int t = tid; t < nodes; t += n_threads) {
-        int a = parents[t];
-        if (a >= t || a < -1) {
+__device__ __forceinline__ void find_ancestors(const int32_t *parents, int nodes, Ancestors &X, int32_t *err, int t,
+                                               Sync sync) {
+    uint32_t mine[kWords];
+    int up = -1;
+    if (t < nodes) {
+        up = parents[t];
+        if (up >= t || up < -1) {
             set_err(err, ICE_ERR_INVALID_ARG);
-            a = -1;
+            up = -1;
         }
-        X.up[0][t] = (int16_t)a;
-#pragma unroll
-        for (int w = 0; w < kWords; ++w) X.mask[0][t][w] = w == t >> 5 ? 1u << (t & 31) : 0u;
     }
-    int cur = 0;
-    for (int reach = 1; reach < nodes; reach <<= 1, cur ^= 1) {
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) mine[w] = w == t >> 5 ? 1u << (t & 31) : 0u;
+    for (int reach = 1;; reach <<= 1) {
+        if (t < nodes) {
+            X.up[t] = (int16_t)up;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) X.mask[t][w] = mine[w];
+        }
         sync();
-        for (int t = tid; t < nodes; t += n_threads) {
-            const int a = X.up[cur][t];
-            X.up[cur ^ 1][t] = a >= 0 ? X.up[cur][a] : (int16_t)-1;
+        if (reach >= nodes) return;
+        if (up >= 0) {
 #pragma unroll
-            for (int w = 0; w < kWords; ++w)
-                X.mask[cur ^ 1][t][w] = X.mask[cur][t][w] | (a >= 0 ? X.mask[cur][a][w] : 0u);
+            for (int w = 0; w < kWords; ++w) mine[w] |= X.mask[up][w];
+            up = X.up[up];
         }
+        sync();
     }
-    sync();
-    return cur;
 }
 
 // Record and used slots of a unit's page x, whose number is id (nullptr: there is no such page).

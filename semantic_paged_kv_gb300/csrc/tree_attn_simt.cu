@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     const Run run = plan_run<kRows, kThreads>(A, S.plan);
     Part part{0, 0, 0, 0};
     const float sl = A.scale * 1.4426950408889634f;
-    int anc_b = -1, anc = 0;
+    int anc_b = -1;
     if (run.n > 0) {
         Segment seg = S.plan.seg;
         for (;; next_segment<kRows>(A, seg)) {
@@ -81,8 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                 *reinterpret_cast<float4 *>(&S.q[r][c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
             }
             if (A.parents && i1 > seg.n_page && anc_b != b) {
-                anc = find_ancestors(A.parents + (size_t)b * A.n_nodes, seg.nodes, S.anc, A.err, tid, kThreads,
-                                     [] { __syncthreads(); });
+                find_ancestors(A.parents + (size_t)b * A.n_nodes, seg.nodes, S.anc, A.err, tid, [] { __syncthreads(); });
                 anc_b = b;
             }
             float o[8][4], m[8], l[8];
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                         else if (j0 + slot >= seg.nodes || node >= seg.nodes)
                             sees = false;
                         else
-                            sees = A.parents ? S.anc.mask[anc][node][(j0 + slot) >> 5] >> (slot & 31) & 1u
+                            sees = A.parents ? S.anc.mask[node][(j0 + slot) >> 5] >> (slot & 31) & 1u
                                              : j0 + slot <= node;
                         s[i][j] = sees ? s[i][j] * sl : -INFINITY;
                         mx = fmaxf(mx, s[i][j]);
@@ -222,6 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     if (tid == 0) A.parts[blockIdx.x] = part;
 }
 
+static_assert(kThreads == kMaxNodes, "a thread a node");
 static_assert(sizeof(Smem) <= 227 * 1024, "one CTA an SM");
 
 }  // namespace

@@ -7,8 +7,8 @@
 // T g query rows meet every key, so that the work is a matrix product (tcgen05)
 // and the 4-bit pages are unpacked once for up to 128 rows.
 //
-// Roles in a CTA (20 warps, one CTA an SM):
-//   10 warps unpack tiles of 128 tokens to fp16 in shared memory, page by page in
+// Roles in a CTA (24 warps, one CTA an SM):
+//   14 warps unpack tiles of 128 tokens to fp16 in shared memory, page by page in
 //     turn (K rows by token, V transposed: tokens are the contraction of the
 //     second product), the next page on its way in their registers; three tiles
 //     of K and of V;
@@ -40,7 +40,7 @@ using namespace tree;
 using namespace tc;
 
 constexpr int kRows = kTreeRowsTc;
-constexpr int kSoftWarps = 8, kLoadWarps = 10, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kSoftWarps = 8, kLoadWarps = 14, kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 2);
 constexpr int kStages = 3;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
@@ -48,9 +48,11 @@ constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColP = 448;
 // A tile's Info is overwritten with K of the tile kInfos behind it, which waits for the scores of kStages tiles before
 // that, which wait for the weights of two before those.
 constexpr int kInfos = 8;
+static_assert(32 * kSoftWarps == kMaxNodes, "a softmax thread a node");
 static_assert(kInfos >= kStages + 2, "an Info outlives its softmax");
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 constexpr float kTop = 6.f;   // powers of two that P has above exp2(score - maximum)
+constexpr float kMost = 16384.f;  // of the sum of a thread's weights of a tile (2^(kTop + kLazy)); above, the maximum moves
 // kind::f16 instruction descriptor: D fp32, A and B fp16, both K-major, M = N = 128.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
@@ -63,7 +65,7 @@ struct Info {
 };
 // A load warp's (step, mid) of 16 tokens in fp16.
 struct MetaScratch {
-    uint32_t k[16][2];     // (2^10 step, mid) of both groups
+    uint32_t k[16][4];     // 2^10 step and mid, each twice, of both groups
     uint16_t v[2][2][16];  // [group][2^10 step, mid][token]
 };
 
@@ -94,6 +96,19 @@ __device__ __forceinline__ Smem &shared() {
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void pair_sync() {
     asm volatile("bar.sync %0, 64;" ::"r"(2 + (int)((threadIdx.x >> 5) & 3)) : "memory");
+}
+// The same, and whether x holds in all 64 threads.
+__device__ __forceinline__ bool pair_all(bool x) {
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.s32 p, %1, 0;\n\t"
+        "barrier.red.and.pred q, %2, 64, p;\n\t"
+        "selp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((int)x), "r"(2 + (int)((threadIdx.x >> 5) & 3))
+        : "memory");
+    return all != 0;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -199,14 +214,6 @@ __device__ __forceinline__ uint32_t high_pair(uint32_t w, uint32_t step, uint32_
     return hfma2(hfma2(w & 0x00F000F0u, 0x64006400u, 0x9F809F80u), step, mid);
 }
 
-// A page of a tile on its way.
-struct Raw {
-    uint4 k[2];      // K: tokens 8 j + k_token(), words lane % 4 + 4 x
-    uint2 v[4];      // V: pieces p and p + 8 of four token pairs (below)
-    uint2 meta;      // (step, mid) of K (lanes 0 .. 15) or V (16 .. 31) of token lane % 16
-    int live;        // used slots
-};
-
 struct Loader {
     const Args &A;
     Smem &S;
@@ -232,31 +239,44 @@ struct Loader {
         base = -1;
         look_ahead(s, 0);
     }
-    // The page of this warp's slot n on its way.
-    __device__ __forceinline__ void load(const Segment &s, int n, Raw &R) {
+    // a page on its way (nothing of it waits)
+    const unsigned char *rec;
+    int live;        // used slots
+    uint2 meta;      // (step, mid) of K (lanes 0 .. 15) or V (16 .. 31) of token lane % 16
+    uint4 k[2];      // K: tokens 8 j + k_token(), words lane % 4 + 4 x
+    uint2 v[4];      // V: pieces p and p + 8 of four token pairs (below)
+
+    // The page of this warp's slot n; where there is none, some record (its codes meet steps of zero).
+    __device__ __forceinline__ void find(const Segment &s, int n) {
         if (base != (n & ~31)) {  // 32 further pages, whose numbers have been on their way since the last time
             base = n & ~31;
             const int x = place(base), id = ahead;
             page = nullptr, page_len = 0;
             if (x < pages_of(s.cnt)) page = page_of_id(A, s.u, s.cnt, x, id, page_len);
+            if (!page) page = A.cache ? A.cache : A.pool;
             look_ahead(s, base + 32);
         }
-        const unsigned char *p = reinterpret_cast<const unsigned char *>(
+        rec = reinterpret_cast<const unsigned char *>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(page), n & 31));
-        R.live = __shfl_sync(0xffffffffu, page_len, n & 31);
-        R.meta = make_uint2(0u, 0u);
-        R.k[0] = R.k[1] = make_uint4(0u, 0u, 0u, 0u);
+        live = __shfl_sync(0xffffffffu, page_len, n & 31);
+        // the one after it into L2 (unless its number is still on its way): its loads then take half the time
+        const unsigned char *after = reinterpret_cast<const unsigned char *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(page), (n + 1) & 31));
+        if (((n + 1) & 31) && lane < q4::kRecord / 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(after + 128 * lane));
+    }
+    __device__ __forceinline__ void load_k() {
+        meta = make_uint2(0u, 0u);
+        if ((lane & 15) < live)
+            meta = *reinterpret_cast<const uint2 *>(rec + (lane < 16 ? q4::kKMeta : q4::kVMeta) + (lane & 15) * 8);
+        const uint4 *x = reinterpret_cast<const uint4 *>(rec) + 4 * k_token() + (lane & 3);
+        k[0] = ld_stream16(x);
+        k[1] = ld_stream16(x + 32);
+    }
+    __device__ __forceinline__ void load_v() {
+        const uint2 *x = reinterpret_cast<const uint2 *>(rec + q4::kV) + v_half() * 64 + (v_piece() & 7) * 2 + (lane >> 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) R.v[i] = make_uint2(0u, 0u);
-        if (!p) return;
-        if ((lane & 15) < R.live)
-            R.meta = *reinterpret_cast<const uint2 *>(p + (lane < 16 ? q4::kKMeta : q4::kVMeta) + (lane & 15) * 8);
-        const uint4 *k = reinterpret_cast<const uint4 *>(p) + 4 * k_token() + (lane & 3);
-        R.k[0] = ld_stream16(k);
-        R.k[1] = ld_stream16(k + 32);
-        const uint2 *v = reinterpret_cast<const uint2 *>(p + q4::kV) + v_half() * 64 + (v_piece() & 7) * 2 + (lane >> 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) R.v[i] = __ldg(v + 16 * i);
+        for (int i = 0; i < 4; ++i) v[i] = __ldg(x + 16 * i);
     }
     // A lane's V: pieces p and p + 8 (of one group) for 8 tokens, half of the page.  Of any 8 lanes that store together, the
     // piece's lowest bit, the half and which two of a piece's four elements come first differ, so that they reach all banks.
@@ -264,15 +284,16 @@ struct Loader {
     __device__ __forceinline__ int v_piece() const { return (lane & 1) | ((lane >> 1) & 6) | (lane & 16); }
 
     // (step, mid): powers of two, operands, and what the softmax has to know.
-    __device__ __forceinline__ void put_meta(const Raw &R, int slot, Info &info) {
+    __device__ __forceinline__ void put_meta(int slot, Info &info) {
         MetaScratch &M = S.meta[warp];
         const int t = lane & 15;
-        const float2 a = q4::unpack_meta(R.meta.x), c = q4::unpack_meta(R.meta.y);
+        const float2 a = q4::unpack_meta(meta.x), c = q4::unpack_meta(meta.y);
         const int e = exponent_for(fmaxf(fabsf(a.y) + 7.5f * a.x, fabsf(c.y) + 7.5f * c.x));
         const float f = pow2(-e), f10 = 1024.f * f;
         const uint32_t x = half2_of(a.x * f10, a.y * f), y = half2_of(c.x * f10, c.y * f);
         if (lane < 16) {
-            *reinterpret_cast<uint2 *>(M.k[t]) = make_uint2(x, y);
+            *reinterpret_cast<uint4 *>(M.k[t]) = make_uint4(__byte_perm(x, x, 0x1010), __byte_perm(x, x, 0x3232),
+                                                            __byte_perm(y, y, 0x1010), __byte_perm(y, y, 0x3232));
             info.kf[16 * slot + t] = pow2(e);
         } else {
             M.v[0][0][t] = (uint16_t)x, M.v[0][1][t] = (uint16_t)(x >> 16);
@@ -280,28 +301,28 @@ struct Loader {
             info.vf[16 * slot + t] = (float)e;
         }
         const bool odd = __any_sync(0xffffffffu, e != 0);
-        if (lane == 0) info.mask[slot] = (uint16_t)((1u << R.live) - 1u), info.odd[slot] = odd;
+        if (lane == 0) info.mask[slot] = (uint16_t)((1u << live) - 1u), info.odd[slot] = odd;
         __syncwarp();
     }
     // K lanes: tokens four apart are neighbours, so that any 8 lanes that store together reach all banks.
     __device__ __forceinline__ int k_token() const { return (lane >> 3) | (lane & 4); }
-    __device__ __forceinline__ void put_k(const Raw &R, int slot, uint32_t dst) {
+    __device__ __forceinline__ void put_k(int slot, uint32_t dst) {
         const int i = lane & 3;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int t = 8 * j + k_token();
-            const uint2 m = *reinterpret_cast<const uint2 *>(S.meta[warp].k[t]);
+            const uint4 m = *reinterpret_cast<const uint4 *>(S.meta[warp].k[t]);
             const uint32_t row = dst + (16 * slot + t) * 128, a0 = row + ((i ^ (t & 7)) << 4), a1 = a0 ^ 64u;
             // word x: elements 8 (i + 4 x) .., in group x / 2
-            put8(a0, R.k[j].x, m.x), put8(a1, R.k[j].y, m.x);
-            put8(a0 + kHalfBytes, R.k[j].z, m.y), put8(a1 + kHalfBytes, R.k[j].w, m.y);
+            put8(a0, k[j].x, m.x, m.y), put8(a1, k[j].y, m.x, m.y);
+            put8(a0 + kHalfBytes, k[j].z, m.z, m.w), put8(a1 + kHalfBytes, k[j].w, m.z, m.w);
         }
     }
-    __device__ __forceinline__ static void put8(uint32_t at, uint32_t w, uint32_t m) {
-        const uint32_t st = __byte_perm(m, m, 0x1010), md = __byte_perm(m, m, 0x3232), u = w >> 8;
+    __device__ __forceinline__ static void put8(uint32_t at, uint32_t w, uint32_t st, uint32_t md) {
+        const uint32_t u = w >> 8;
         sts128(at, low_pair(w, st, md), high_pair(w, st, md), low_pair(u, st, md), high_pair(u, st, md));
     }
-    __device__ __forceinline__ void put_v(const Raw &R, int slot, uint32_t dst) {
+    __device__ __forceinline__ void put_v(int slot, uint32_t dst) {
         const uint16_t(&vm)[2][16] = S.meta[warp].v[lane >> 4];
         const uint4 st = *reinterpret_cast<const uint4 *>(&vm[0][8 * v_half()]);
         const uint4 md = *reinterpret_cast<const uint4 *>(&vm[1][8 * v_half()]);
@@ -312,8 +333,8 @@ struct Loader {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // elements e and e + 1 of the piece
                 const int e = 2 * (x ^ flip), by = 4 * e;
-                const uint32_t w0 = (y ? R.v[0].y : R.v[0].x) >> by, w1 = (y ? R.v[1].y : R.v[1].x) >> by;
-                const uint32_t w2 = (y ? R.v[2].y : R.v[2].x) >> by, w3 = (y ? R.v[3].y : R.v[3].x) >> by;
+                const uint32_t w0 = (y ? v[0].y : v[0].x) >> by, w1 = (y ? v[1].y : v[1].x) >> by;
+                const uint32_t w2 = (y ? v[2].y : v[2].x) >> by, w3 = (y ? v[3].y : v[3].x) >> by;
                 const uint32_t at = base + y * 32 * 128 + e * 128;
                 sts128(at + ((c ^ e) << 4), low_pair(w0, st.x, md.x), low_pair(w1, st.y, md.y),
                        low_pair(w2, st.z, md.z), low_pair(w3, st.w, md.w));
@@ -412,20 +433,28 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[stage_of(tile_at())]);
         };
-        Raw R;
         L.start(seg, P.i0);
-        if (x < pages) L.load(seg, 0, R);
-        for (int n = 1; x < pages; ++n, x += kLoadWarps) {
-            Raw next = R;
-            if (x + kLoadWarps < pages) L.load(seg, n, next);  // (on its way while this one is unpacked)
+        if (x < pages) {
+            L.find(seg, 0);
+            L.load_k();
+            L.load_v();
+        }
+        for (int n = 1; x < pages; ++n) {
+            const int slot = slot_at(), next = x + kLoadWarps;
+            const uint32_t at = tile_at();
             if (!begin(S.k_empty)) return;
-            L.put_meta(R, slot_at(), S.info[tile_at() & (kInfos - 1)]);
-            L.put_k(R, slot_at(), su32(S.k[stage_of(tile_at())]));
+            L.put_meta(slot, S.info[at & (kInfos - 1)]);
+            L.put_k(slot, su32(S.k[stage_of(at)]));
             end(S.k_full);
+            if (next < pages) {  // (the next page's loads as soon as their registers are free)
+                L.find(seg, n);
+                L.load_k();
+            }
             if (!begin(S.v_empty)) return;
-            L.put_v(R, slot_at(), su32(S.v[stage_of(tile_at())]));
+            L.put_v(slot, su32(S.v[stage_of(at)]));
             end(S.v_full);
-            R = next;
+            if (next < pages) L.load_v();
+            x = next;
         }
         for (; x < slots; x += kLoadWarps) {
             Info &info = S.info[tile_at() & (kInfos - 1)];
@@ -515,12 +544,12 @@ __device__ __forceinline__ bool raise(float &m, float top, bool first, float &f)
 }
 
 // Row's bits of the 64 nodes from j0 on.
-__device__ __forceinline__ uint2 node_mask(const Smem &S, bool tree, int anc, int node, int j0) {
+__device__ __forceinline__ uint2 node_mask(const Smem &S, bool tree, int node, int j0) {
     uint32_t mask[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         if (tree) {
-            mask[c] = S.anc.mask[anc][node][(j0 >> 5) + c];
+            mask[c] = S.anc.mask[node][(j0 >> 5) + c];
         } else {
             const int n = node - (j0 + 32 * c) + 1;
             mask[c] = n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u);
@@ -532,31 +561,29 @@ __device__ __forceinline__ uint2 node_mask(const Smem &S, bool tree, int anc, in
 // The weights of this thread's 64 scores and their sum.  Columns are loaded ahead while others are worked on.
 struct Scores {
     uint32_t s_at, p_at, mask[2];
-    template <bool kMask> __device__ __forceinline__ void seen(int c, float (&x)[16]) const {
-        if (!kMask) return;
+    __device__ __forceinline__ void seen(int c, float (&x)[16]) const {
+        const uint32_t w = (c < 2 ? mask[0] : mask[1]) >> (16 * (c & 1));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = mask[c >> 1] >> (16 * (c & 1) + i) & 1u ? x[i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) x[i] = w >> i & 1u ? x[i] : -INFINITY;
     }
-    template <bool kMask> __device__ __forceinline__ float largest() const {
-        float s[2][16], top[2] = {-INFINITY, -INFINITY};
-        tmem_ld16f(s_at, s[0]);
-#pragma unroll
+    __device__ __forceinline__ float largest() const {
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
+            float x[16];
+            tmem_ld16f(s_at + 16 * c, x);
             tmem_wait_ld();
-            tmem_ld16f(s_at + 16 * ((c + 1) & 3), s[(c + 1) & 1]);
-            float(&x)[16] = s[c & 1];
-            seen<kMask>(c, x);
+            seen(c, x);
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 top[0] = max3(top[0], x[i], x[i + 1]), top[1] = max3(top[1], x[i + 2], x[i + 3]);
         }
-        tmem_wait_ld();
         return fmaxf(top[0], top[1]);
     }
-    // exp2(score r + off)
-    template <bool kMask> __device__ __forceinline__ float weights(float r, float off, float l) const {
+    // exp2(score r + off), and their sum
+    template <bool kMask> __device__ __forceinline__ float weights(float r, float off, uint32_t (&w)[2][16]) const {
         const unsigned long long r2 = pk2(r, r), off2 = pk2(off, off);
-        unsigned long long sum[2] = {pk2(l, 0.f), pk2(0.f, 0.f)};
+        unsigned long long sum[2] = {0ull, 0ull};
         float s[2][16];
         tmem_ld16f(s_at, s[0]);
 #pragma unroll
@@ -564,19 +591,21 @@ struct Scores {
             tmem_wait_ld();
             if (c < 3) tmem_ld16f(s_at + 16 * (c + 1), s[(c + 1) & 1]);
             float(&x)[16] = s[c & 1];
-            seen<kMask>(c, x);
-            uint32_t w[8];
+            if (kMask) seen(c, x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float2 y = upk2(fma2(pk2(x[2 * i], x[2 * i + 1]), r2, off2));
                 const float a = exp2_fast(y.x), b = exp2_fast(y.y);
                 sum[i & 1] = add2(sum[i & 1], pk2(a, b));
-                w[i] = half2_of(a, b);
+                w[c >> 1][8 * (c & 1) + i] = half2_of(a, b);
             }
-            tmem_st8(p_at + 8 * c, w);
         }
         const float2 t = upk2(add2(sum[0], sum[1]));
         return t.x + t.y;
+    }
+    __device__ __forceinline__ void store(const uint32_t (&w)[2][16]) const {
+        tmem_st16(p_at, w[0]);
+        tmem_st16(p_at + 16, w[1]);
     }
     // The same where keys or values carry powers of two of their own, or the two maxima have parted.
     __device__ __forceinline__ float2 largest_any(const float *kf, const float *vf, float r) const {
@@ -620,7 +649,7 @@ struct Scores {
 
 // A segment's tiles (the CTA's tiles from tile0 on, the first n_page of pages), by the 256 softmax threads: thread (row,
 // half).
-__device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, int n_page, int node, int anc, float factor) {
+__device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, int n_page, int node, float factor, int rows) {
     Smem &S = shared();
     const int warp = threadIdx.x >> 5, row = threadIdx.x & 127, hf = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -632,34 +661,57 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
         wait_for(S, S.s_ready[at & 1], at >> 1 & 1);
         __syncwarp();
         fence_after();
+        if ((row & ~31) >= rows) {  // no row of this warp (and its partner): its rows of P and O mean nothing
+            fence_before();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&S.p_ready[at & 1]);
+            continue;
+        }
         const Info &info = S.info[at & (kInfos - 1)];
         const uint2 mask = i < n_page ? *reinterpret_cast<const uint2 *>(&info.mask[4 * hf])
-                                      : node_mask(S, S.args.parents != nullptr, anc, node, (i - n_page) * kTile + 64 * hf);
+                                      : node_mask(S, S.args.parents != nullptr, node, (i - n_page) * kTile + 64 * hf);
         const uint4 odd = *reinterpret_cast<const uint4 *>(info.odd);
         const Scores X{tmem + lanes + kColS + 128 * (at & 1) + 64 * hf, tmem + lanes + kColP + 32 * hf, {mask.x, mask.y}};
         const bool full = __all_sync(0xffffffffu, (mask.x & mask.y) == 0xffffffffu);
         const bool apart = __any_sync(0xffffffffu, (odd.x | odd.y | odd.z | odd.w) != 0u || !(R.m == R.mo));
-        // the row's maximum: that of its two threads
-        float2 top = apart  ? X.largest_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r)
-                     : full ? make_float2(X.largest<false>() * R.r, 0.f)
-                            : make_float2(X.largest<true>() * R.r, 0.f);
-        S.half[at & 1][hf][row] = top;
-        pair_sync();
-        const float2 other = S.half[at & 1][hf ^ 1][row];
-        top.x = fmaxf(top.x, other.x);
-        top.y = apart ? fmaxf(top.y, other.y) : top.x;
-        float f, fo;
-        const bool up = raise(R.m, top.x, i == 0, f), up_o = raise(R.mo, top.y, i == 0, fo);
-        if (up) R.l *= f;
-        if (i > 0) {  // P's place has been read, and O is that of the tile before
-            wait_for(S, S.v_empty[stage_of(at - 1)], round_of(at - 1));
+        // P's place has been read, and O is that of the tile before
+        auto o_done = [&] {
+            if (i > 0) wait_for(S, S.v_empty[stage_of(at - 1)], round_of(at - 1));
             __syncwarp();
             fence_after();
+        };
+        // Against the maximum as it is first: weights that would be too large for fp16 show in their sum.
+        bool done = false;
+        if (i > 0 && !apart) {
+            uint32_t w[2][16];
+            const float l = full ? X.weights<false>(R.r, kTop - R.m, w) : X.weights<true>(R.r, kTop - R.m, w);
+            done = pair_all(l <= kMost);
+            if (done) {
+                R.l += l;
+                o_done();
+                X.store(w);
+            }
         }
-        if (up_o) scale_o(o_at, fo);
-        R.l = apart  ? X.weights_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r, kTop - R.m, kTop - R.mo, R.l)
-              : full ? X.weights<false>(R.r, kTop - R.m, R.l)
-                     : X.weights<true>(R.r, kTop - R.m, R.l);
+        if (!done) {
+            // the row's maximum: that of its two threads
+            float2 top = apart ? X.largest_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r) : make_float2(X.largest() * R.r, 0.f);
+            S.half[at & 1][hf][row] = top;
+            pair_sync();
+            const float2 other = S.half[at & 1][hf ^ 1][row];
+            top.x = fmaxf(top.x, other.x);
+            top.y = apart ? fmaxf(top.y, other.y) : top.x;
+            float f, fo;
+            if (raise(R.m, top.x, i == 0, f)) R.l *= f;
+            const bool up_o = raise(R.mo, top.y, i == 0, fo);
+            o_done();
+            if (up_o) scale_o(o_at, fo);
+            if (apart) {
+                R.l = X.weights_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r, kTop - R.m, kTop - R.mo, R.l);
+            } else {
+                uint32_t w[2][16];
+                R.l += X.weights<true>(R.r, kTop - R.m, w);
+                X.store(w);
+            }
+        }
         tmem_wait_st();
         fence_before();
         __syncwarp();
@@ -718,7 +770,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     Part part{0, 0, 0, 0};
     uint32_t tile0 = 0;
-    int anc_b = -1, anc = 0;
+    int anc_b = -1;
     Segment seg = S.plan.seg;
     for (;; next_segment<kRows>(A, seg)) {
         if (seg.first >= run.n) break;
@@ -733,11 +785,11 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         if (lane == 0) mbar_arrive(&S.q_full);
         if (A.parents && P.i0 + P.n > seg.n_page && anc_b != P.b) {
             soft_sync();  // (the last ones have been read)
-            anc = find_ancestors(A.parents + (size_t)P.b * A.n_nodes, seg.nodes, S.anc, A.err, threadIdx.x,
-                                 32 * kSoftWarps, [] { soft_sync(); });
+            find_ancestors(A.parents + (size_t)P.b * A.n_nodes, seg.nodes, S.anc, A.err, threadIdx.x,
+                           [] { soft_sync(); });
             anc_b = P.b;
         }
-        Row R = soften_tiles(tmem, tile0, P.n, seg.n_page - P.i0, node, anc, factor);
+        Row R = soften_tiles(tmem, tile0, P.n, seg.n_page - P.i0, node, factor, P.rows);
         tile0 += P.n;
         // ---- the row's result, O / l
         const int free = tile0 & 1;  // (the last tile's side may still be read; the one before it not)
@@ -765,7 +817,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
             if (S.bad) {  // infinities and NaN of the nodes that this row sees
 #pragma unroll 1
                 for (int j = nodes0; j < nodes1; ++j) {
-                    const bool sees = A.parents ? S.anc.mask[anc][node][j >> 5] >> (j & 31) & 1u : j <= node;
+                    const bool sees = A.parents ? S.anc.mask[node][j >> 5] >> (j & 31) & 1u : j <= node;
                     if (!sees) continue;
                     const __nv_bfloat16 *v = row_ptr<__nv_bfloat16>(A.v, P.b, j, P.h) + 64 * hf + 16 * c;
 #pragma unroll
