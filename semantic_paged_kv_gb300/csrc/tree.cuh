@@ -23,8 +23,10 @@ constexpr int kTilePages = kTile / kPage;
 constexpr int kMaxNodes = ICE_TREE_NODES;   // of a tree with parents
 constexpr int kWords = kMaxNodes / 32;
 constexpr int kPartRows = 128;              // rows of a partial result, at most
-constexpr int kTreeOver = 2;
-constexpr int kMinRun = 2;                  // tiles of a run, at least
+// Tiles that a segment takes beside its own (queries, ancestors, results), by the rows of a block.  128 rows: 9 ragged
+// sequences of 32 heads take 103 us with 1, 92 with 2, 80 with 4 and 74 with 6, one tree at 16k 38.5, 37.3, 33.5 and 34.
+template <int R> constexpr int kTreeOver = R == 128 ? 5 : 1;
+constexpr int kMinRun = 1;  // places of a run, at least (the tiny fp32 layout takes 48 us with 2, 29 with 1)
 
 // The segment that starts in a CTA and goes on in the next ones (runs 0: none).
 struct Part {
@@ -86,7 +88,7 @@ template <int R> __device__ __forceinline__ int blocks_of(int nodes, int g) {
 }
 template <int R> __device__ __forceinline__ long long places_of(int2 cnt, int nodes, int g) {
     const int blocks = blocks_of<R>(nodes, g);
-    long long n = (long long)blocks * (page_tiles(cnt) + kTreeOver);
+    long long n = (long long)blocks * (page_tiles(cnt) + kTreeOver<R>);
     for (int i = 0; i < blocks; ++i) n += node_tiles<R>(nodes, g, i);
     return n;
 }
@@ -100,7 +102,7 @@ template <int R> __device__ __forceinline__ void load_unit(const Args &A, int u,
 }
 template <int R> __device__ __forceinline__ void size_segment(const Args &A, long long place, Segment &s) {
     s.n = s.n_page + node_tiles<R>(s.nodes, A.g, s.blk);
-    s.first = place + kTreeOver;
+    s.first = place + kTreeOver<R>;
 }
 // The segment after s.
 template <int R> __device__ __forceinline__ void next_segment(const Args &A, Segment &s) {
@@ -144,7 +146,7 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
     }
     Run r;
     r.share = total < (1ll << 30) ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-    if (r.share < kMinRun + kTreeOver) r.share = kMinRun + kTreeOver;
+    if (r.share < kMinRun) r.share = kMinRun;
     r.f0 = r.share * blockIdx.x;
     r.n = (int)max(min(r.share, total - r.f0), 0ll);
     if (r.n > 0 && r.f0 >= before && r.f0 < before + mine) {

@@ -24,29 +24,29 @@ __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ Args 
     const int row0 = p.block * kBlock, r = blockIdx.y % kGroups * 32 + lane, i = blockIdx.y / kGroups * 8 + warp;
     if (r >= min((long long)kBlock, (long long)nodes * A.g - row0)) return;
     auto slot_of = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? p.inside : 0)); };
-    // (loads of eight runs at a time are in flight)
-    float M = -FLT_MAX;
-    for (int k0 = 0; k0 < p.runs; k0 += 8) {
-        float m[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m[k] = k0 + k < p.runs ? A.part_ml[slot_of(k0 + k) * kPartRows + r].x : -FLT_MAX;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) M = fmaxf(M, m[k]);
-    }
-    float L = 0.f;
+    // eight runs at a time, against the running maximum
+    float M = -FLT_MAX, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < p.runs; k0 += 8) {
         float2 ml[8];
         float4 x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 8; ++k) {
+            ml[k] = make_float2(-FLT_MAX, 0.f);
             if (k0 + k < p.runs) {
                 ml[k] = A.part_ml[slot_of(k0 + k) * kPartRows + r];
                 x[k] = A.part_o[part_at(slot_of(k0 + k), i, r)];
             }
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+        const float f = exp2f(M - top);
+        M = top;
+        L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            if (k0 + k >= p.runs || ml[k].y == 0.f) continue;
+            if (ml[k].y == 0.f) continue;
             const float w = ml[k].y * exp2f(ml[k].x - M);
             L += w;
             if (w != 0.f) {

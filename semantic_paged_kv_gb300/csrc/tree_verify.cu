@@ -25,7 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8, kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCluster = 8, kThreads = 256, kWarps = kThreads / 32, kPieces = kCluster * kWarps;
 constexpr int kMaxNodes = ICE_VERIFY_NODES;
 
 struct VerifyArgs {
@@ -64,10 +64,33 @@ __device__ __forceinline__ Two rest_of(float p, float q, float bh, float bl) {
     return r.hi > 0.f ? r : Two{0.f, 0.f};
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
+// Sums of two rows of weights at once, in packed pairs of fp32 operations (common.cuh).
+struct Sums {
+    unsigned long long hi, lo;
+    __device__ __forceinline__ void add(unsigned long long s, unsigned long long e) {
+        unsigned long long t, r;
+        two_sum2(hi, s, t, r);
+        hi = t;
+        lo = add2(lo, add2(r, e));
+    }
+    __device__ __forceinline__ Two total() const {
+        const float2 h = upk2(hi), l = upk2(lo);
+        Two a, b;
+        a.hi = h.x + l.x, a.lo = l.x - (a.hi - h.x);
+        b.hi = h.y + l.y, b.lo = l.y - (b.hi - h.y);
+        return ice::add(a, b);
+    }
+};
+// max(p - beta q, 0) of two elements, as s + e.
+__device__ __forceinline__ void rests_of(float2 p, float2 q, float bh, float bl, unsigned long long &s,
+                                         unsigned long long &e) {
+    const unsigned long long q2 = pk2(q.x, q.y), b2 = pk2(bh, bh), less = mul2(pk2(-bh, -bh), q2);
+    two_sum2(pk2(p.x, p.y), less, s, e);
+    e = sub2(e, fma2(pk2(bl, bl), q2, fma2(b2, q2, less)));
+    float2 x = upk2(s), y = upk2(e);
+    if (!(x.x + y.x > 0.f)) x.x = y.x = 0.f;
+    if (!(x.y + y.y > 0.f)) x.y = y.y = 0.f;
+    s = pk2(x.x, x.y), e = pk2(y.x, y.y);
 }
 
 // What the CTAs do next: nothing more, sum the weights of a node, find its likeliest token.
@@ -81,23 +104,24 @@ struct Command {
 struct Smem {
     int32_t parent[kMaxNodes], token[kMaxNodes];
     float px[kMaxNodes], qx[kMaxNodes], u[kMaxNodes];  // p and q of a node's token at its parent
+    uint8_t at_once[kMaxNodes];                        // whether it is accepted as its parent's first child
     int32_t out[kMaxNodes];                            // tokens left out at this node (no draft probabilities)
     int n_out, n_path;
     Command cmd;
-    Two part[kWarps];  // sums of the warps' pieces
-    float part_best[kWarps];
-    int part_at[kWarps];
-    // of this CTA, in two passes in turn (read by the whole cluster)
-    Two total[2];
-    float best[2];
-    int best_at[2];
+    // of this CTA's warps' pieces, in two passes in turn (read by the whole cluster): sums; the largest element
+    Two part[2][kWarps];
+    float best[2][kWarps];
+    int best_at[2][kWarps];
+    // the draw: a piece, the sum before it and the sum to pass
+    int piece, first, last;
+    double start, want, warp_sum[kWarps];
 };
 
 __device__ __forceinline__ void join_best(float &best, int &at, float y, int k) {
     if (k >= 0 && (at < 0 || better(y, k, best, at))) best = y, at = k;
 }
 
-template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 2)
     k_tree_verify(const __grid_constant__ VerifyArgs A) {
     __shared__ Smem S;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -134,28 +158,79 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
                 if (draft) qx = Elem<T>::load(draft + up * A.d_node + x);
             }
         }
-        S.parent[t] = up, S.token[t] = x, S.px[t] = px, S.qx[t] = qx;
-        S.u[t] = greedy ? 0.f : A.uniform[(size_t)b * n_nodes + t];
+        const float u = greedy ? 0.f : A.uniform[(size_t)b * n_nodes + t];
+        S.parent[t] = up, S.token[t] = x, S.px[t] = px, S.qx[t] = qx, S.u[t] = u;
+        S.at_once[t] = draft ? (double)u * (double)qx < (double)px : u < px;  // (48 bits: exact)
     }
     if (tid == 0) S.n_out = 0;
     __syncthreads();
 
-    // A warp's piece of a row: per elements from i0 on.
-    const int per = (A.vocab + kCluster * kWarps - 1) / (kCluster * kWarps);
-    auto piece = [&](int w) { return min((rank * kWarps + w) * per, A.vocab); };
-    auto weight = [&](const Command &c, int i) {
-        const float x = Elem<T>::load(target + c.node * A.t_node + i);
-        if (draft && !c.plain) return rest_of(x, Elem<T>::load(draft + c.node * A.d_node + i), c.bh, c.bl);
-        Two r{x > 0.f ? x : 0.f, 0.f};
+    // The rows of a node: `head` elements before p's first whole 16-byte vector, the whole vectors, the rest.  q's row is
+    // read in vectors too where it starts at the same place of one.
+    constexpr int kVec = 16 / (int)sizeof(T);
+    struct Rows {
+        const T *p, *q;
+        int head, vecs, per;  // vectors: all, of a warp's piece
+        bool same;
+    };
+    auto rows_of = [&](int node) {
+        Rows r;
+        r.p = target + node * A.t_node, r.q = draft ? draft + node * A.d_node : nullptr;
+        const int at = (int)(reinterpret_cast<uintptr_t>(r.p) / sizeof(T) % kVec);
+        r.head = min((kVec - at) % kVec, A.vocab);
+        r.vecs = (A.vocab - r.head) / kVec;
+        r.same = r.q && (int)(reinterpret_cast<uintptr_t>(r.q) / sizeof(T) % kVec) == at;
+        r.per = (r.vecs + kPieces - 1) / kPieces;
+        return r;
+    };
+    // First element of piece g (warp g % kWarps of CTA g / kWarps): the head goes to the first, the rest to the last.
+    auto piece = [&](const Rows &r, int g) {
+        return g == 0 ? 0 : (g == kPieces ? A.vocab : r.head + min(g * r.per, r.vecs) * kVec);
+    };
+    auto weight_of = [&](const Command &c, int i, float p, float q) {
+        if (draft && !c.plain) return rest_of(p, q, c.bh, c.bl);
+        Two r{p > 0.f ? p : 0.f, 0.f};
         if (!c.plain)
             for (int j = 0; j < S.n_out; ++j)
                 if (S.out[j] == i) r.hi = 0.f;
         return r;
     };
+    auto weight = [&](const Command &c, const Rows &r, int i) {
+        return weight_of(c, i, Elem<T>::load(r.p + i), draft && !c.plain ? Elem<T>::load(r.q + i) : 0.f);
+    };
+    // Calls use(v, raw p, raw q) for the vectors of this lane in piece g, several of them on their way at a time.
+    constexpr int kAhead = 4;
+    auto for_vectors = [&](const Rows &r, bool with_q, int g, auto use) {
+        const int v1 = min((g + 1) * r.per, r.vecs);
+        for (int v = g * r.per + lane; v < v1; v += 32 * kAhead) {
+            uint4 p[kAhead], q[kAhead];
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h) {
+                const int i = r.head + min(v + 32 * h, v1 - 1) * kVec;
+                p[h] = __ldg(reinterpret_cast<const uint4 *>(r.p + i));
+                if (with_q && r.same) {
+                    q[h] = __ldg(reinterpret_cast<const uint4 *>(r.q + i));
+                } else if (with_q) {
+                    union {
+                        T x[kVec];
+                        uint4 v;
+                    } y;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) y.x[e] = r.q[i + e];
+                    q[h] = y.v;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < kAhead; ++h)
+                if (v + 32 * h < v1) use(r.head + (v + 32 * h) * kVec, p[h], q[h]);
+        }
+    };
 
     // ---- the walk, by warp 0 of every CTA: children up to `tried` have been tried
     int node = 0, tried = 0, n_path = 1, likeliest = -1, pass = 0;
     double beta = 0., mass = 1., sum = 0.;
+    bool fresh = true;           // no child of `node` has been refused
+    Two two[2] = {};             // sums of pieces 2 lane and 2 lane + 1
     bool summed = false, searched = false;  // `sum` and the parts are those of the next command's weights
     Command cmd{kDone, 0, 0.f, 0.f, 0};
     if (tid == 0 && rank == 0) path[0] = 0;
@@ -182,14 +257,18 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
                 if (greedy) {
                     take = x == likeliest;
                 } else if (draft) {
-                    const double px = S.px[c], qx = S.qx[c];
-                    take = (double)S.u[c] * qx * mass < px - beta * qx;
+                    if (fresh) {
+                        take = S.at_once[c];
+                    } else {
+                        const double px = S.px[c], qx = S.qx[c];
+                        take = (double)S.u[c] * qx * mass < px - beta * qx;
+                    }
                     if (!take && mass > 0.) beta += mass, cmd.op = kSum;
                 } else {
                     bool gone = false;
                     for (int i = lane; i < S.n_out; i += 32) gone |= S.out[i] == x;
                     const float px = __any_sync(0xffffffffu, gone) ? 0.f : S.px[c];
-                    take = (double)S.u[c] * mass < (double)px;
+                    take = fresh ? S.at_once[c] : (double)S.u[c] * mass < (double)px;
                     if (!take && px > 0.f) {
                         mass = fmax(mass - (double)px, 0.);
                         summed = false;
@@ -198,7 +277,9 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
                         __syncwarp();
                     }
                 }
+                fresh = false;
                 if (take) {
+                    fresh = true;
                     if (rank == 0 && lane == 0) path[n_path] = c;
                     ++n_path;
                     node = tried = c, beta = 0., mass = 1., summed = false;
@@ -215,60 +296,78 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
         __syncthreads();
         cmd = S.cmd;
         if (cmd.op == kDone) break;
-        const int i0 = piece(warp), i1 = piece(warp + 1);
+        const Rows r = rows_of(cmd.node);
+        const int g = rank * kWarps + warp;
+        const bool with_q = draft && !cmd.plain;
+        // (elements outside the whole vectors: one a lane, behind the others)
+        const int edge = g == 0 && lane < r.head ? lane
+                         : g == kPieces - 1 && r.head + r.vecs * kVec + lane < A.vocab && lane < kVec
+                             ? r.head + r.vecs * kVec + lane
+                             : -1;
         if (cmd.op == kSum) {
-            Two s[4];
+            Sums s[2] = {{0ull, 0ull}, {0ull, 0ull}};
+            for_vectors(r, with_q, g, [&](int i, const uint4 &pv, const uint4 &qv) {
+                float p[kVec], q[kVec];
+                Elem<T>::unpack(pv, p);
+                if (with_q) Elem<T>::unpack(qv, q);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] = Two{0.f, 0.f};
-            for (int i = i0 + lane; i < i1; i += 128)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (i + 32 * k < i1) s[k] = add(s[k], weight(cmd, i + 32 * k));
-            Two t = add(add(s[0], s[1]), add(s[2], s[3]));
+                for (int e = 0; e < kVec; e += 2) {
+                    unsigned long long w, d = 0ull;
+                    if (with_q)
+                        rests_of(make_float2(p[e], p[e + 1]), make_float2(q[e], q[e + 1]), cmd.bh, cmd.bl, w, d);
+                    else
+                        w = pk2(weight_of(cmd, i + e, p[e], 0.f).hi, weight_of(cmd, i + e + 1, p[e + 1], 0.f).hi);
+                    s[e >> 1 & 1].add(w, d);
+                }
+            });
+            Two t = add(s[0].total(), s[1].total());
+            if (edge >= 0) t = add(t, weight(cmd, r, edge));
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1)
                 t = add(t, Two{__shfl_xor_sync(0xffffffffu, t.hi, off), __shfl_xor_sync(0xffffffffu, t.lo, off)});
-            if (lane == 0) S.part[warp] = t;
-            __syncthreads();
-            if (tid == 0) {
-                for (int w = 1; w < kWarps; ++w) t = add(t, S.part[w]);
-                S.total[pass & 1] = t;
-            }
+            if (lane == 0) S.part[pass & 1][warp] = t;
         } else {
-            const T *p = target + cmd.node * A.t_node;
             float best = -INFINITY;
             int at = -1;
-            for (int i = i0 + lane; i < i1; i += 32) {
-                const float x = Elem<T>::load(p + i);
-                if (x == x) join_best(best, at, x, i);
+            for_vectors(r, false, g, [&](int i, const uint4 &pv, const uint4 &) {
+                float p[kVec];
+                Elem<T>::unpack(pv, p);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (p[e] == p[e]) join_best(best, at, p[e], i + e);
+            });
+            if (edge >= 0) {
+                const float x = Elem<T>::load(r.p + edge);
+                if (x == x) join_best(best, at, x, edge);
             }
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) {
                 const float y = __shfl_xor_sync(0xffffffffu, best, off);
                 join_best(best, at, y, __shfl_xor_sync(0xffffffffu, at, off));
             }
-            if (lane == 0) S.part_best[warp] = best, S.part_at[warp] = at;
-            __syncthreads();
-            if (tid == 0) {
-                for (int w = 1; w < kWarps; ++w) join_best(best, at, S.part_best[w], S.part_at[w]);
-                S.best[pass & 1] = best, S.best_at[pass & 1] = at;
-            }
+            if (lane == 0) S.best[pass & 1][warp] = best, S.best_at[pass & 1][warp] = at;
         }
         cluster.sync();
-        if (warp == 0) {
-            const Smem *o = cluster.map_shared_rank(&S, lane & (kCluster - 1));
+        if (warp == 0) {  // pieces 2 lane and 2 lane + 1
+            static_assert(kPieces == 64 && kWarps % 2 == 0, "two pieces a lane");
+            const Smem *o = cluster.map_shared_rank(&S, 2 * lane / kWarps);
+            const int w = 2 * lane % kWarps;
             if (cmd.op == kSum) {
-                const Two t = o->total[pass & 1];
-                sum = 0.;
-                for (int r = 0; r < kCluster; ++r)
-                    sum += value(Two{__shfl_sync(0xffffffffu, t.hi, r), __shfl_sync(0xffffffffu, t.lo, r)});
+                two[0] = o->part[pass & 1][w], two[1] = o->part[pass & 1][w + 1];
+                Two t = add(two[0], two[1]);
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1)
+                    t = add(t, Two{__shfl_xor_sync(0xffffffffu, t.hi, off), __shfl_xor_sync(0xffffffffu, t.lo, off)});
+                // (the lanes' orders of addition differ: the first one's)
+                sum = value(Two{__shfl_sync(0xffffffffu, t.hi, 0), __shfl_sync(0xffffffffu, t.lo, 0)});
                 summed = true;
                 if (draft && !cmd.plain) mass = sum;
             } else {
-                float best = o->best[pass & 1];
-                int at = o->best_at[pass & 1];
+                float best = o->best[pass & 1][w];
+                int at = o->best_at[pass & 1][w];
+                join_best(best, at, o->best[pass & 1][w + 1], o->best_at[pass & 1][w + 1]);
 #pragma unroll
-                for (int off = 4; off >= 1; off >>= 1) {
+                for (int off = 16; off >= 1; off >>= 1) {
                     const float y = __shfl_xor_sync(0xffffffffu, best, off);
                     join_best(best, at, y, __shfl_xor_sync(0xffffffffu, at, off));
                 }
@@ -278,58 +377,70 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
         }
         ++pass;
     }
-    // ---- the draw: the CTA, the warp's piece, the lane's stretch and the element where the running sum passes u sum
-    // (behind roundings, or with u = 1: the last element of any weight)
-    if (warp == 0 && !greedy) {
-        if (!(sum > 0.)) {
-            if (rank == 0 && lane == 0) {
-                A.next[b] = -1;
-                set_err(A.err, ICE_ERR_INVALID_ARG);
-            }
-        } else {
-            const double want = (double)S.u[0] * sum;
-            double start = 0.;
-            bool passed = false;
-            // the first of n values (lane's w; lanes in order) whose running sum from `start` on is beyond `want`; `start`
-            // becomes the sum before it (passed: there was one)
-            auto find = [&](double w) {
-                double s = w;
+    cluster.barrier_arrive();  // (the others' sums have been read; they may leave while this CTA draws)
+    // ---- the draw: the piece, the thread's stretch of it and the element where the running sum passes u sum (behind
+    // roundings, or with u = 1: the last element of any weight)
+    if (warp == 0) {
+        int chosen = -1;
+        if (!greedy && sum > 0.) {
+            const double want = (double)S.u[0] * sum, a = value(two[0]), w = a + value(two[1]);
+            double s = w;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, s, off);
-                    if (lane >= off) s += y;
-                }
-                const unsigned some = __ballot_sync(0xffffffffu, w > 0.);
-                const unsigned hit = __ballot_sync(0xffffffffu, w > 0. && start + s > want);
-                const int k = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-                start += __shfl_sync(0xffffffffu, s - w, k);
-                passed = hit != 0u;
-                return k;
-            };
-            const Two t = cluster.map_shared_rank(&S, lane & (kCluster - 1))->total[(pass - 1) & 1];
-            if (find(lane < kCluster ? value(t) : 0.) == rank) {
-                const int w = find(lane < kWarps ? value(S.part[lane]) : 0.);
-                const int i0 = piece(w), i1 = piece(w + 1), stretch = (i1 - i0 + 31) / 32;
-                Two s{0.f, 0.f};
-                for (int i = i0 + lane * stretch; i < min(i0 + (lane + 1) * stretch, i1); ++i) s = add(s, weight(cmd, i));
-                const int j0 = i0 + find(value(s)) * stretch, j1 = min(j0 + stretch, i1);
-                int x = -1;
-                for (int j = j0; j < j1; j += 32) {
-                    const double v = j + lane < j1 ? value(weight(cmd, j + lane)) : 0.;
-                    if (!__any_sync(0xffffffffu, v > 0.)) continue;
-                    const double from = start;
-                    const int k = find(v);
-                    x = j + k;
-                    if (passed) break;
-                    start = from + warp_sum(v);
-                }
-                if (lane == 0) A.next[b] = x;
+            for (int off = 1; off < 32; off <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, s, off);
+                if (lane >= off) s += y;
             }
+            const unsigned some = __ballot_sync(0xffffffffu, w > 0.), hit = __ballot_sync(0xffffffffu, w > 0. && s > want);
+            const int k = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+            const double from = s - w;
+            const bool second = !(a > 0. && from + a > want) && value(two[1]) > 0.;
+            chosen = __shfl_sync(0xffffffffu, 2 * lane + (second ? 1 : 0), k);
+            const double start = __shfl_sync(0xffffffffu, second ? from + a : from, k);
+            if (lane == 0) S.start = start, S.want = want;
+        } else if (!greedy && rank == 0 && lane == 0) {
+            A.next[b] = -1;
+            set_err(A.err, ICE_ERR_INVALID_ARG);
+        }
+        if (lane == 0) S.piece = chosen, S.first = kThreads, S.last = -1, S.n_path = n_path;
+    }
+    __syncthreads();
+    if (S.piece >= 0 && S.piece / kWarps == rank) {
+        const Rows r = rows_of(cmd.node);
+        const int i0 = piece(r, S.piece), i1 = piece(r, S.piece + 1), stretch = (i1 - i0 + kThreads - 1) / kThreads;
+        const int j0 = min(i0 + tid * stretch, i1), j1 = min(j0 + stretch, i1);
+        Two t{0.f, 0.f};
+#pragma unroll 8
+        for (int j = j0; j < j1; ++j) t = add(t, weight(cmd, r, j));
+        const double w = value(t);
+        double s = w;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, off);
+            if (lane >= off) s += y;
+        }
+        if (lane == 31) S.warp_sum[warp] = s;
+        __syncthreads();
+        double from = S.start;
+        for (int k = 0; k < warp; ++k) from += S.warp_sum[k];
+        from += s - w;
+        const unsigned some = __ballot_sync(0xffffffffu, w > 0.);
+        const unsigned hit = __ballot_sync(0xffffffffu, w > 0. && from + w > S.want);
+        if (lane == 0 && hit) atomicMin(&S.first, 32 * warp + __ffs(hit) - 1);
+        if (lane == 0 && some) atomicMax(&S.last, 32 * warp + 31 - __clz(some));
+        __syncthreads();
+        if (tid == (S.first < kThreads ? S.first : S.last)) {
+            int x = -1;
+            for (int j = j0; j < j1; ++j) {
+                const double y = value(weight(cmd, r, j));
+                if (!(y > 0.)) continue;
+                x = j;
+                from += y;
+                if (from > S.want) break;
+            }
+            A.next[b] = x;
         }
     }
     // behind the path: -1
-    if (tid == 0) S.n_path = n_path;
-    __syncthreads();
     if (rank == 0) {
         n_path = S.n_path;
         for (int t = n_path + tid; t < n_nodes; t += kThreads) path[t] = -1;
@@ -341,7 +452,7 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
             }
         }
     }
-    cluster.sync();  // the others may still read this CTA's sums
+    cluster.barrier_wait();  // (the others may still read this CTA's sums)
 }
 
 }  // namespace
