@@ -748,9 +748,18 @@ ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes);
  * are, not in 4 bits.  cache may be NULL, with lens NULL: the nodes alone.
  * Rows behind counts[b] are neither read nor written.
  *  - lens and pages outside their ranges as in ice_cache4_attn_decode.
- *  - A node's infinities and NaN reach only the rows that see it.
+ * O may be q itself (same data and strides); it must not overlap k or v.
+ *  - A node's infinities and NaN reach only the rows that see it.  A row whose
+ *    query is not finite gives NaN.
  *  - Every run of a call gives the same bits.
- * Arithmetic: O is rounded once, to dtype.
+ *  - A bounded wait that gives up sets ICE_ERR_TIMEOUT in err_dev and leaves
+ *    NaN in O.
+ * Arithmetic: O is rounded once, to dtype.  bf16: keys, values and weights go in
+ * as fp16 numbers (11 bits; a token whose |mid| + 7.5 step, or a node whose
+ * largest element, lies outside 2^-4 .. 2^8 has a power of two of its own),
+ * weights from 2^-30 of the row's largest on, fp32 sums; queries are exact.  fp32:
+ * fp32 throughout.  The largest |v| times the number of tokens has to stay below
+ * 2^119.
  */
 ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
                                 const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,

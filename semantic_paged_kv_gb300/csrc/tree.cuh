@@ -49,6 +49,7 @@ struct Args {
     float2 *part_ml;  // [2 CTAs, kPartRows]: its maximum (powers of two) and sum
     Part *parts;      // [CTAs]
     int32_t *err;
+    int fault;  // ICE_FAULT's timeout: the kernel's producers deliver nothing
 };
 
 __device__ __forceinline__ int nodes_of(const Args &A, int b) {
@@ -140,7 +141,8 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
     __syncthreads();
     long long total = 0;
     before -= mine;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    const int warps = min(kThreads / 32, (A.units + 31) / 32);  // that have units
+    for (int w = 0; w < warps; ++w) {
         if (w < warp) before += S.sum[w];
         total += S.sum[w];
     }

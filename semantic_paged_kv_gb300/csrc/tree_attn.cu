@@ -109,6 +109,7 @@ cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &
     A.g = p.n_q_heads / p.n_kv_heads, A.hq = p.n_q_heads, A.hkv = p.n_kv_heads, A.units = units_of(p);
     A.scale = scale;
     A.err = err;
+    A.fault = fault_armed("timeout");
     const int grid = device_sms();  // one CTA an SM
     const Ws w = ws_layout(grid, ws);
     A.part_o = w.part_o, A.part_ml = w.part_ml, A.parts = w.parts;

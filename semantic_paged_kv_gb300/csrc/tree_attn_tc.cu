@@ -195,7 +195,7 @@ __device__ __forceinline__ bool dead(const Smem &S) { return *static_cast<const 
 // A bounded wait; once one has given up, all do.
 __device__ __forceinline__ bool wait_for(Smem &S, unsigned long long &bar, uint32_t parity) {
     if (mbar_test(&bar, parity)) return true;
-    if (!dead(S) && mbar_wait(&bar, parity)) return true;
+    if (!dead(S) && mbar_wait(&bar, parity, S.args.fault ? kFaultWaitNs : kWaitNs)) return true;
     *static_cast<volatile int *>(&S.dead) = 1;
     set_err(S.args.err, ICE_ERR_TIMEOUT);
     return false;
@@ -413,6 +413,7 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
     Smem &S = shared();
     const Args &A = S.args;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps;
+    if (A.fault) return;  // (a test's: nothing arrives)
     Loader L(A, S, w);
     uint32_t tile0 = 0;
     Segment seg = S.plan.seg;
@@ -803,6 +804,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         const bool whole = seg.first >= 0 && seg.end() <= run.n;
         if (!whole && seg.first >= 0) part = part_of(seg, run);
         const size_t slot = (size_t)blockIdx.x * 2 + (seg.first > 0 ? 1 : 0);
+        if (dead(S)) R.l = __int_as_float(0x7fc00000);  // a wait gave up: NaN
         const float inv = R.l == 0.f ? 0.f : 1.f / R.l, f = exp2_fast(0.5f * (R.mo - R.m));
         if (out && !whole && hf == 0) A.part_ml[slot * kPartRows + row] = make_float2(R.m, R.l);
         __nv_bfloat16 *dst = row_out<__nv_bfloat16>(A.o, P.b, node, head) + 64 * hf;

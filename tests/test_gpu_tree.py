@@ -344,6 +344,82 @@ def test_attention_records_behind_4_gb():
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scale", [0.0, -0.09, 3.0])
+def test_attention_scale(scale, dtype):
+    """No weight by the scores, keys that are far away first, and a softmax of one token."""
+    c = Case(2, 11, 8, 2, dtype, True, [300, 17], seed=9)
+    c.scale = scale
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_in_place(dtype):
+    """O over q, in a projection's layout: the same bits."""
+    c = Case(2, 40, 16, 4, dtype, True, [700, 0], counts=[40, 22])
+    want = c.run().clone()
+    before = c.q.clone()
+    c.O = c.q
+    c.run()
+    for b in range(2):
+        n = c.counts[b]
+        assert torch.equal(c.q[b, :n], want[b, :n]) and torch.equal(c.q[b, n:], before[b, n:])
+
+
+def test_attention_long_chain():
+    """A chunk of 3001 tokens behind 40: rows of many blocks, some before and some behind each tile's nodes."""
+    c = Case(1, 3001, 2, 1, "bf16", False, [40])
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
+def test_attention_many_units():
+    """More units than a CTA has threads, most of one or two tiles."""
+    c = Case(40, 2, 32, 32, "bf16", True, [(37 * b) % 90 for b in range(40)])
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
+def test_attention_wait_that_gives_up(monkeypatch):
+    """Pages that never arrive: the waits end, the call says so and leaves NaN, and the next call is right."""
+    c = Case(2, 9, 8, 2, "bf16", True, [3000, 100])
+    monkeypatch.setenv("ICE_FAULT", "timeout")
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_ERR_TIMEOUT
+    for b in range(2):
+        assert bool(torch.isnan(c.O[b, :c.counts[b]]).all()) and bool((c.O[b, c.counts[b]:] == 7).all())
+    monkeypatch.delenv("ICE_FAULT")
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
+def test_attention_workspace_between_shapes_and_graphs():
+    """One workspace for calls of different shapes one after another, eager and captured."""
+    cases = [Case(1, 26, 32, 8, "bf16", True, [5000]), Case(4, 7, 8, 2, "fp32", True, [300, 1, 0, 77]),
+             Case(2, 200, 16, 4, "bf16", False, [100, 2000])]
+    want = [c.run().clone() for c in cases]
+    for c in cases:
+        c.ws = cases[0].ws
+    graphs = []
+    for c in cases:
+        c.O.fill_(7)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run()
+        graphs.append(g)
+    for _ in range(2):
+        for c, g, w in zip(cases, graphs, want):
+            c.O.fill_(7)
+            g.replay()
+            cases[1].run()
+            assert torch.equal(c.O, w) and torch.equal(cases[1].O, want[1])
+
+
 # ----------------------------------------------------------------- verify --
 def _verify(target, draft, tokens, parents, counts, uniform):
     B, T = tokens.shape
