@@ -634,14 +634,22 @@ def ice_tree_workspace_bytes(params: IceParams) -> int:
     return n.value
 
 
+def _check_tree_batch(tree, batch: int) -> None:
+    for name, t in zip(("parents", "counts"), tree.keep):
+        if t is not None and t.shape[0] != batch:
+            raise IceError(ICE_ERR_INVALID_ARG, f"{name} are of {t.shape[0]} sequences, the call of {batch}")
+
+
 def ice_cache4_attn_tree(params, tree, q, cache, lens, k, v, scale, O, ws, err, stream=None):
     """q, k, v and O are ``rows(...)`` views, tree a Tree, cache a Cache4 (or None, with lens None)."""
+    _check_tree_batch(tree, params.batch)
     _check(load().ice_cache4_attn_tree(params, tree, q, cache, _ptr(lens), k, v, float(scale), O, _ptr(ws),
                                        _nbytes(ws), _ptr(err), _stream(stream)))
 
 
 def ice_sparse_attn_tree4(params, tree, q, records, page_len, sel_pages, sel_count, cache, lens, k, v, scale, O, ws,
                           err, stream=None):
+    _check_tree_batch(tree, params.batch)
     _check(load().ice_sparse_attn_tree4(params, tree, q, _ptr(records), _ptr(page_len), _ptr(sel_pages),
                                         _ptr(sel_count), sel_pages.shape[-1], cache, _ptr(lens), k, v, float(scale),
                                         O, _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)))
@@ -656,6 +664,7 @@ def ice_tree_verify(tree, target, draft, tokens, uniform, path, n_path, next_tok
         raise IceError(ICE_ERR_INVALID_ARG, "draft and target have one type and shape")
     if n != tree.n_nodes:
         raise IceError(ICE_ERR_INVALID_ARG, f"target has {n} rows a sequence, the tree {tree.n_nodes} nodes")
+    _check_tree_batch(tree, B)
     for x, t, shape in ((tokens, torch.int32, (B, n)), (path, torch.int32, (B, n)), (uniform, torch.float32, (B, n)),
                         (n_path, torch.int32, (B,)), (next_token, torch.int32, (B,))):
         if x is not None and (x.dtype != t or tuple(x.shape) != shape or not x.is_contiguous()):

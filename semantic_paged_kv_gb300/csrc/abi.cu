@@ -917,7 +917,7 @@ ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes) {
 // What both attention calls check (cache NULL: no cached tokens).
 static ice_status tree_attn_common(const ice_params *p, const ice_tree *tree, const ice_rows *q,
                                    const ice_cache4 *cache, const int32_t *lens, const ice_rows *k, const ice_rows *v,
-                                   float scale, const ice_rows *O, void *ws, size_t ws_bytes) {
+                                   float scale, const ice_rows *O, void *ws, size_t ws_bytes, int32_t max_sel) {
     ice_status st = check_params(p);
     if (st) return st;
     if ((st = check_tree(tree)) || (st = check_new(p, tree->n_nodes))) return st;
@@ -925,6 +925,8 @@ static ice_status tree_attn_common(const ice_params *p, const ice_tree *tree, co
         return fail(ICE_ERR_UNSUPPORTED, "a tree with parents has at most %d nodes here", ICE_TREE_NODES);
     if ((long long)tree->n_nodes * (p->n_q_heads / p->n_kv_heads) > 1 << 30)
         return fail(ICE_ERR_UNSUPPORTED, "too many rows a KV head (n_nodes * heads of a group > 2^30)");
+    if (tree_tiles(*p, tree->n_nodes, (cache ? (double)cache->max_pages : 0.) + max_sel) > 137438953472.)
+        return fail(ICE_ERR_UNSUPPORTED, "too much work in one call (units * blocks of rows * tiles > 2^37)");
     if ((st = check_rows(p, q, "q")) || (st = check_rows(p, k, "k")) || (st = check_rows(p, v, "v")) ||
         (st = check_rows_out(p, tree->n_nodes, p->n_q_heads, O, "O")))
         return st;
@@ -941,7 +943,7 @@ static ice_status tree_attn_common(const ice_params *p, const ice_tree *tree, co
 ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
                                 const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,
                                 const ice_rows *O, void *ws, size_t ws_bytes, int32_t *err_dev, void *stream) {
-    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes);
+    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes, 0);
     if (st) return st;
     if (cache && (long long)units_of(*p) * cache->max_pages > (1ll << 38))
         return fail(ICE_ERR_UNSUPPORTED, "too many pages in one call (units * max_pages > 2^38)");
@@ -956,7 +958,7 @@ ice_status ice_sparse_attn_tree4(const ice_params *p, const ice_tree *tree, cons
                                  int32_t max_sel, const ice_cache4 *cache, const int32_t *lens, const ice_rows *k,
                                  const ice_rows *v, float scale, const ice_rows *O, void *ws, size_t ws_bytes,
                                  int32_t *err_dev, void *stream) {
-    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes);
+    ice_status st = tree_attn_common(p, tree, q, cache, lens, k, v, scale, O, ws, ws_bytes, max_sel);
     if (st) return st;
     if (!records || !aligned16(records))
         return fail(ICE_ERR_INVALID_ARG, "records must be a 16-byte aligned device pointer");

@@ -217,6 +217,8 @@ cudaError_t launch_attn4(const ice_params &p, const void *Q, const void *records
 
 // ------------------------------------------------ trees of drafted tokens --
 size_t tree_workspace();
+// Tiles that a call can have, at most (its runs count them in 32 bits).
+double tree_tiles(const ice_params &p, int n_nodes, double pages);
 // records NULL: no selected pages; cache NULL: no token-ordered pages.
 cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,
                         const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count, int max_sel,

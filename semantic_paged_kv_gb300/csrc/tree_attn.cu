@@ -89,6 +89,11 @@ template <typename T, int kBlock> cudaError_t launch_join(const Args &A, int gri
 
 }  // namespace
 
+double tree_tiles(const ice_params &p, int n_nodes, double pages) {
+    const double rows = (double)n_nodes * (p.n_q_heads / p.n_kv_heads), blocks = rows / kTreeRowsSimt + 1;
+    return units_of(p) * blocks * (pages / kTilePages + n_nodes / kTile + 8);
+}
+
 size_t tree_workspace() { return ws_layout(device_sms(), nullptr).bytes; }
 
 cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,

@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
             for (int i = 0; i < 8; ++i) {
                 const int r = 8 * warp + i;
                 if (r >= rows) break;
-                const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+                const float inv = l[i] != 0.f ? 1.f / l[i] : (whole ? __int_as_float(0x7fc00000) : 0.f);  // (all scores -inf: NaN)
                 const float4 x = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
                 if (whole) {
                     put4(row_out<T>(A.o, b, (row0 + r) / g, h * g + (row0 + r) % g) + 4 * lane, x);

@@ -289,8 +289,8 @@ struct Loader {
         const int t = lane & 15;
         const float2 a = q4::unpack_meta(meta.x), c = q4::unpack_meta(meta.y);
         const int e = exponent_for(fmaxf(fabsf(a.y) + 7.5f * a.x, fabsf(c.y) + 7.5f * c.x));
-        const float f = pow2(-e), f10 = 1024.f * f;
-        const uint32_t x = half2_of(a.x * f10, a.y * f), y = half2_of(c.x * f10, c.y * f);
+        const float f = pow2(-e);  // (up to 2^126: 2^10 goes to the step)
+        const uint32_t x = half2_of(a.x * f * 1024.f, a.y * f), y = half2_of(c.x * f * 1024.f, c.y * f);
         if (lane < 16) {
             *reinterpret_cast<uint4 *>(M.k[t]) = make_uint4(__byte_perm(x, x, 0x1010), __byte_perm(x, x, 0x3232),
                                                             __byte_perm(y, y, 0x1010), __byte_perm(y, y, 0x3232));
@@ -805,7 +805,8 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         if (!whole && seg.first >= 0) part = part_of(seg, run);
         const size_t slot = (size_t)blockIdx.x * 2 + (seg.first > 0 ? 1 : 0);
         if (dead(S)) R.l = __int_as_float(0x7fc00000);  // a wait gave up: NaN
-        const float inv = R.l == 0.f ? 0.f : 1.f / R.l, f = exp2_fast(0.5f * (R.mo - R.m));
+        const float none = whole ? __int_as_float(0x7fc00000) : 0.f;  // (all scores -inf; in a part: nothing seen)
+        const float inv = 1.f / R.l, f = exp2_fast(0.5f * (R.mo - R.m));
         if (out && !whole && hf == 0) A.part_ml[slot * kPartRows + row] = make_float2(R.m, R.l);
         __nv_bfloat16 *dst = row_out<__nv_bfloat16>(A.o, P.b, node, head) + 64 * hf;
         const int nodes0 = max(P.i0 - seg.n_page, 0) * kTile, nodes1 = min((P.i0 + P.n - seg.n_page) * kTile, seg.nodes);
@@ -815,7 +816,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
             tmem_ld16f(tmem + lanes + kColO + 64 * hf + 16 * c, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = R.l == 0.f ? 0.f : x[i] * inv * f * f;
+            for (int i = 0; i < 16; ++i) x[i] = R.l == 0.f ? none : x[i] * inv * f * f;
             if (S.bad) {  // infinities and NaN of the nodes that this row sees
 #pragma unroll 1
                 for (int j = nodes0; j < nodes1; ++j) {
@@ -880,6 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const __grid_constant__
     __syncwarp();
     fence_before();
     __syncthreads();
+    if (dead(S))  // (products that nobody waited for end long before)
+        for (int i = 0; i < 100; ++i) __nanosleep(10000);
     if (tid == 0) A.parts[blockIdx.x] = part;
     if (warp == 0) tmem_dealloc(tmem, 512);
 }

@@ -149,3 +149,26 @@ def test_binding_checks():
         ice.ice_tree_verify(ice.Tree(i32(2, 6)), pr, pr, **ok, err=None, stream=0)
     with pytest.raises(ice.IceError):
         ice.ice_tree_verify(t, pr, ice.probs(torch.zeros(2, 5, 8)), **ok, err=None, stream=0)
+
+
+def test_too_much_work():
+    """More tiles than a run can count; the same nodes behind fewer pages are not refused for it."""
+    tree = lambda: _tree(parents=None, n_nodes=1 << 20)  # noqa: E731
+    assert _attn(tree=tree(), cache=_cache(max_pages=1 << 26)) == UNS
+    assert "too much work" in ice.load().ice_last_error().decode()
+    assert _attn(tree=tree(), cache=_cache(max_pages=1 << 16), ws_bytes=1000) == INV
+    assert _sparse(tree=tree(), max_sel=1 << 26) == UNS
+    assert "too much work" in ice.load().ice_last_error().decode()
+
+
+def test_binding_checks_the_batch_of_a_tree():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    pr = ice.probs(torch.zeros(2, 5, 7))
+    ok = dict(tokens=i32(2, 5), uniform=torch.zeros(2, 5), path=i32(2, 5), n_path=i32(2), next_token=i32(2))
+    for t in (ice.Tree(i32(1, 5)), ice.Tree(i32(2, 5), i32(3)), ice.Tree(None, i32(1), 5)):
+        with pytest.raises(ice.IceError) as e:
+            ice.ice_tree_verify(t, pr, pr, **ok, err=None, stream=0)
+        assert e.value.status == INV
+        with pytest.raises(ice.IceError) as e:
+            ice.ice_cache4_attn_tree(_p(), t, _rows(), None, None, _rows(), _rows(), 0.1, _rows(), None, None, stream=0)
+        assert e.value.status == INV and "sequences" in str(e.value)

@@ -356,6 +356,29 @@ def test_attention_scale(scale, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_smallest_scales(dtype):
+    """Keys and values next to the smallest normal numbers: powers of two of their own up to 2^120."""
+    c = Case(2, 9, 8, 2, dtype, True, [200, 33], k_scale=1e-36, v_scale=1e-36, q_scale=1e30)
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B", [1, 400])
+def test_attention_scores_of_minus_infinity(dtype, B):
+    """A node that sees itself alone, with a score of -inf: NaN there, and nowhere else."""
+    c = Case(B, 3, 4, 2, dtype, True, [0] * B, counts=[3] * B)
+    c.parents_dev.copy_(torch.tensor([[-1, 0, -1]] * B, dtype=torch.int32))
+    c.parents = [[-1, 0, -1]] * B
+    c.k[:, 2, :, 0] = -math.inf
+    c.q[:, 2, :, 0] = 1.0
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    assert bool(torch.isnan(c.O[:, 2]).all()) and bool(torch.isfinite(c.O[:, :2]).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attention_in_place(dtype):
     """O over q, in a projection's layout: the same bits."""
     c = Case(2, 40, 16, 4, dtype, True, [700, 0], counts=[40, 22])
