@@ -26,11 +26,15 @@ constexpr int kPartRows = 128;              // rows of a partial result, at most
 // Tiles that a segment takes beside its own (queries, ancestors, results), by the rows of a block.  128 rows: 9 ragged
 // sequences of 32 heads take 103 us with 1, 92 with 2, 80 with 4 and 74 with 6, one tree at 16k 38.5, 37.3, 33.5 and 34.
 template <int R> constexpr int kTreeOver = R == 128 ? 5 : 1;
+// Places by which the longest segment may pass an equal run, so that each segment stays whole where there is a CTA for each:
+// a cut costs another start and end and the join.
+template <int R> constexpr int kTreeWhole = R == 128 ? 7 : 1;
 constexpr int kMinRun = 1;  // places of a run, at least (the tiny fp32 layout takes 48 us with 2, 29 with 1)
 
 // The segment that starts in a CTA and goes on in the next ones (runs 0: none).
 struct Part {
-    int32_t unit, block, runs, inside;
+    int32_t unit, block, rows;
+    int16_t runs, inside;
 };
 
 struct Args {
@@ -87,11 +91,18 @@ template <int R> __device__ __forceinline__ int node_tiles(int nodes, int g, int
 template <int R> __device__ __forceinline__ int blocks_of(int nodes, int g) {
     return (nodes * g + R - 1) / R;
 }
-template <int R> __device__ __forceinline__ long long places_of(int2 cnt, int nodes, int g) {
-    const int blocks = blocks_of<R>(nodes, g);
-    long long n = (long long)blocks * (page_tiles(cnt) + kTreeOver<R>);
-    for (int i = 0; i < blocks; ++i) n += node_tiles<R>(nodes, g, i);
-    return n;
+// Segments (2^20 at most are counted), their places and those of the longest one.
+struct Load {
+    long long places;
+    int segments, most;
+};
+template <int R> __device__ __forceinline__ void add_unit(int2 cnt, int nodes, int g, Load &l) {
+    const int blocks = blocks_of<R>(nodes, g), each = page_tiles(cnt) + kTreeOver<R>;
+    for (int i = 0; i < blocks; ++i) {
+        const int n = each + node_tiles<R>(nodes, g, i);
+        l.places += n, l.most = max(l.most, n);
+    }
+    l.segments = min(l.segments + blocks, 1 << 20);
 }
 template <int R> __device__ __forceinline__ void load_unit(const Args &A, int u, Segment &s) {
     s.u = u;
@@ -117,8 +128,9 @@ template <int R> __device__ __forceinline__ void next_segment(const Args &A, Seg
 }
 
 struct PlanScratch {
-    long long sum[32];
+    Load sum[32];
     Segment seg;
+    int n;
 };
 struct Run {
     long long f0, share;
@@ -129,55 +141,65 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = (A.units + kThreads - 1) / kThreads;
     const int ua = min(tid * per, A.units), ub = min(ua + per, A.units);
-    long long mine = 0;
-    for (int u = ua; u < ub; ++u) mine += places_of<R>(counts_of(A, u), nodes_of(A, u / A.hkv), A.g);
-    long long before = mine;
+    Load mine{0, 0, 0};
+    for (int u = ua; u < ub; ++u) add_unit<R>(counts_of(A, u), nodes_of(A, u / A.hkv), A.g, mine);
+    long long before = mine.places;
+    int segments = mine.segments;
+    const int most_of_warp = __reduce_max_sync(0xffffffffu, mine.most);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, before, off);
-        if (lane >= off) before += y;
+        const int z = __shfl_up_sync(0xffffffffu, segments, off);
+        if (lane >= off) before += y, segments += z;
     }
-    if (lane == 31) S.sum[warp] = before;
+    if (lane == 31) S.sum[warp] = Load{before, segments, most_of_warp};
     __syncthreads();
-    long long total = 0;
-    before -= mine;
+    Load all{0, 0, 0};
+    before -= mine.places, segments -= mine.segments;
     const int warps = min(kThreads / 32, (A.units + 31) / 32);  // that have units
     for (int w = 0; w < warps; ++w) {
-        if (w < warp) before += S.sum[w];
-        total += S.sum[w];
+        const Load x = S.sum[w];
+        if (w < warp) before += x.places, segments += x.segments;
+        all.places += x.places, all.segments += x.segments, all.most = max(all.most, x.most);
     }
+    const long long total = all.places;
     Run r;
     r.share = total < (1ll << 30) ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     if (r.share < kMinRun) r.share = kMinRun;
+    const bool whole = all.segments <= (int)gridDim.x && all.most <= r.share + kTreeWhole<R>;
     r.f0 = r.share * blockIdx.x;
     r.n = (int)max(min(r.share, total - r.f0), 0ll);
-    if (r.n > 0 && r.f0 >= before && r.f0 < before + mine) {
+    if (whole) r.n = (int)blockIdx.x < all.segments;
+    if (whole ? (int)blockIdx.x >= segments && (int)blockIdx.x < segments + mine.segments
+              : r.n > 0 && r.f0 >= before && r.f0 < before + mine.places) {
         long long at = before;
         for (int u = ua; u < ub; ++u) {
             Segment s;
             load_unit<R>(A, u, s);
-            for (; s.blk < s.blocks; ++s.blk) {
-                size_segment<R>(A, at - r.f0, s);
-                if (s.end() > 0) break;
+            for (; s.blk < s.blocks; ++s.blk, ++segments) {
+                size_segment<R>(A, whole ? 0 : at - r.f0, s);
+                if (whole ? segments == (int)blockIdx.x : s.end() > 0) break;
                 at = s.end() + r.f0;
             }
             if (s.blk < s.blocks) {
                 S.seg = s;
+                S.n = (int)s.end();
                 break;
             }
         }
     }
     __syncthreads();
+    if (whole && r.n) r.n = S.n;
     return r;
 }
 // A segment whose first tile is in this CTA's run (a full one) and whose last one is not: its runs.  (One at most starts in
 // a CTA.)
-__device__ __forceinline__ Part part_of(const Segment &s, const Run &r) {
+template <int R> __device__ __forceinline__ Part part_of(const Segment &s, const Run &r, int g) {
     const long long beyond = s.end() - r.n;
     const int more = beyond < (1ll << 30) && r.share < (1ll << 30)
                          ? (int)(((unsigned)beyond + (unsigned)r.share - 1) / (unsigned)r.share)
                          : (int)((beyond + r.share - 1) / r.share);
-    return Part{s.u, s.blk, 1 + more, s.first > 0 ? 1 : 0};
+    return Part{s.u, s.blk, min(R, s.nodes * g - s.blk * R), (int16_t)(1 + more), (int16_t)(s.first > 0 ? 1 : 0)};
 }
 
 // Ancestors of the nodes of a tree, themselves among them, by pointer jumping.

@@ -4,6 +4,8 @@
 // whole GPU busy, where a last CTA would join them alone).
 #include <float.h>
 
+#include <algorithm>
+
 #include "tree.cuh"
 
 namespace ice {
@@ -11,53 +13,124 @@ namespace {
 
 using namespace tree;
 
-// CTA (c, y) joins rows 32 (y % (kBlock / 32)) .. and elements 32 (y / (kBlock / 32)) .. of the segment that starts in
-// run c: a warp takes 32 rows (neighbours in the parts) and 4 elements.
+// All CTAs find the cut segments in `parts` and take pieces of them in turn: 32 rows (neighbours in the parts) and either 32
+// elements, 4 a warp, or, where a segment has more than kAhead runs, 8 elements, 4 a warp and a quarter of the runs.
+// (One tree at 16k, 8 segments of 19 runs: .. us of the call, 7 with whole columns of runs a warp and CTAs for every place of
+// `parts`.)
+constexpr int kJoinCtas = 4;  // an SM
+constexpr int kMostParts = 256;
+constexpr int kAhead = 5, kSplit = 4;
+struct Cut {
+    Part p;
+    int run, first;  // its first run, the number of its first piece
+};
 template <typename T, int kBlock>
-__global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ Args A) {
+__global__ void __launch_bounds__(256, kJoinCtas) k_tree_join(const __grid_constant__ Args A, int n_parts) {
     constexpr int kGroups = kBlock / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+    __shared__ Cut cuts[kMostParts + 1];
+    __shared__ int2 of_warp[8];  // cuts, pieces
+    __shared__ float4 sum[kSplit][2][32];
+    __shared__ float2 ml_of[kSplit][2][32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto is_split = [](const Part &p) { return p.runs > kAhead; };
     dep_wait();
-    const Part p = A.parts[c];
-    if (p.runs == 0) return;
-    const int b = p.unit / A.hkv, h = p.unit - b * A.hkv, nodes = nodes_of(A, b);
-    const int row0 = p.block * kBlock, r = blockIdx.y % kGroups * 32 + lane, i = blockIdx.y / kGroups * 8 + warp;
-    if (r >= min((long long)kBlock, (long long)nodes * A.g - row0)) return;
-    auto slot_of = [&](int k) { return (size_t)(2 * (c + k) + (k == 0 ? p.inside : 0)); };
-    // eight runs at a time, against the running maximum
-    float M = -FLT_MAX, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < p.runs; k0 += 8) {
-        float2 ml[8];
-        float4 x[8];
+    int pieces, n_cuts;
+    {
+        Part p{};
+        if (tid < n_parts) p = A.parts[tid];
+        const int mine = p.runs == 0 ? 0 : kGroups * (is_split(p) ? kHeadDim / 8 : kHeadDim / 32);
+        const unsigned hit = __ballot_sync(0xffffffffu, mine > 0);
+        int before = mine;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            ml[k] = make_float2(-FLT_MAX, 0.f);
-            if (k0 + k < p.runs) {
-                ml[k] = A.part_ml[slot_of(k0 + k) * kPartRows + r];
-                x[k] = A.part_o[part_at(slot_of(k0 + k), i, r)];
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += y;
+        }
+        if (lane == 31) of_warp[warp] = make_int2(__popc(hit), before);
+        __syncthreads();
+        int at = __popc(hit & ((1u << lane) - 1u));
+        before -= mine, pieces = 0, n_cuts = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const int2 x = of_warp[w];
+            if (w < warp) at += x.x, before += x.y;
+            n_cuts += x.x, pieces += x.y;
+        }
+        if (mine > 0) cuts[at] = Cut{p, tid, before};
+        __syncthreads();
+    }
+    for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        int lo = 0, hi = n_cuts;  // the last cut that starts at or before this piece
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            (cuts[mid].first <= piece ? lo : hi) = mid;
+        }
+        const Cut &c = cuts[lo];
+        const Part &p = c.p;
+        const bool split = is_split(p);
+        const int x = piece - c.first, r = x % kGroups * 32 + lane;
+        const int i = split ? x / kGroups * 2 + (warp & 1) : x / kGroups * 8 + warp;  // 4 elements
+        const int k_first = split ? warp >> 1 : 0, k_step = split ? kSplit : 1, runs = p.runs;
+        const bool live = r < p.rows;
+        float M = -FLT_MAX, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = k_first; live && k0 < runs; k0 += kAhead * k_step) {
+            float2 ml[kAhead];
+            float4 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int k = k0 + j * k_step;
+                ml[j] = make_float2(-FLT_MAX, 0.f);
+                if (k < runs) {
+                    const size_t slot = (size_t)(2 * (c.run + k) + (k == 0 ? p.inside : 0));
+                    ml[j] = A.part_ml[slot * kPartRows + r];
+                    v[j] = A.part_o[part_at(slot, i, r)];
+                }
+            }
+            float top = M;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) top = fmaxf(top, ml[j].x);
+            const float f = exp2f(M - top);
+            M = top;
+            L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (ml[j].y == 0.f) continue;
+                const float w = ml[j].y * exp2f(ml[j].x - M);
+                L += w;
+                if (w != 0.f) {
+                    acc.x = fmaf(v[j].x, w, acc.x), acc.y = fmaf(v[j].y, w, acc.y);
+                    acc.z = fmaf(v[j].z, w, acc.z), acc.w = fmaf(v[j].w, w, acc.w);
+                }
             }
         }
-        float top = M;
+        if (split) {  // (the same for the whole CTA)
+            sum[warp >> 1][warp & 1][lane] = acc, ml_of[warp >> 1][warp & 1][lane] = make_float2(M, L);
+            __syncthreads();
+            if (warp < 2) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
-        const float f = exp2f(M - top);
-        M = top;
-        L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+                for (int k = 1; k < kSplit; ++k) M = fmaxf(M, ml_of[k][warp][lane].x);
+                acc = make_float4(0.f, 0.f, 0.f, 0.f), L = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (ml[k].y == 0.f) continue;
-            const float w = ml[k].y * exp2f(ml[k].x - M);
-            L += w;
-            if (w != 0.f) {
-                acc.x = fmaf(x[k].x, w, acc.x), acc.y = fmaf(x[k].y, w, acc.y);
-                acc.z = fmaf(x[k].z, w, acc.z), acc.w = fmaf(x[k].w, w, acc.w);
+                for (int k = 0; k < kSplit; ++k) {
+                    const float2 ml = ml_of[k][warp][lane];
+                    const float4 v = sum[k][warp][lane];
+                    if (ml.y == 0.f) continue;
+                    const float f = exp2f(ml.x - M);
+                    L = fmaf(ml.y, f, L);
+                    acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+                }
             }
+            __syncthreads();
+        }
+        if (live && (!split || warp < 2)) {
+            const int b = p.unit / A.hkv, h = p.unit - b * A.hkv, row = p.block * kBlock + r;
+            const float inv = 1.f / L;
+            put4(row_out<T>(A.o, b, row / A.g, h * A.g + row % A.g) + 4 * i,
+                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         }
     }
-    const float inv = 1.f / L;
-    put4(row_out<T>(A.o, b, (row0 + r) / A.g, h * A.g + (row0 + r) % A.g) + 4 * i,
-         make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
 struct Ws {
@@ -84,7 +157,7 @@ Ws ws_layout(int ctas, void *base) {
 static_assert(kTreeRowsSimt <= kPartRows && kTreeRowsTc <= kPartRows, "rows of a partial result");
 
 template <typename T, int kBlock> cudaError_t launch_join(const Args &A, int grid, cudaStream_t s) {
-    return launch_dependent(k_tree_join<T, kBlock>, dim3(grid, kBlock / 32 * 4), dim3(256), 0, s, A);
+    return launch_dependent(k_tree_join<T, kBlock>, dim3(kJoinCtas * device_sms()), dim3(256), 0, s, A, grid);
 }
 
 }  // namespace
@@ -94,7 +167,8 @@ double tree_tiles(const ice_params &p, int n_nodes, double pages) {
     return units_of(p) * blocks * (pages / kTilePages + n_nodes / kTile + 8);
 }
 
-size_t tree_workspace() { return ws_layout(device_sms(), nullptr).bytes; }
+static int grid_of() { return std::min(device_sms(), kMostParts); }  // one CTA an SM
+size_t tree_workspace() { return ws_layout(grid_of(), nullptr).bytes; }
 
 cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &q, const void *records,
                         const int32_t *page_len, const int32_t *sel_pages, const int32_t *sel_count, int max_sel,
@@ -115,7 +189,7 @@ cudaError_t launch_tree(const ice_params &p, const ice_tree &t, const ice_rows &
     A.scale = scale;
     A.err = err;
     A.fault = fault_armed("timeout");
-    const int grid = device_sms();  // one CTA an SM
+    const int grid = grid_of();
     const Ws w = ws_layout(grid, ws);
     A.part_o = w.part_o, A.part_ml = w.part_ml, A.parts = w.parts;
     if (p.dtype == ICE_BF16) {

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = A.g;
     dep_wait();
     const Run run = plan_run<kRows, kThreads>(A, S.plan);
-    Part part{0, 0, 0, 0};
+    Part part{};
     const float sl = A.scale * 1.4426950408889634f;
     int anc_b = -1;
     if (run.n > 0) {
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                 __syncthreads();
             }
             const bool whole = seg.first >= 0 && seg.end() <= run.n;
-            if (!whole && seg.first >= 0) part = part_of(seg, run);
+            if (!whole && seg.first >= 0) part = part_of<kRows>(seg, run, g);
             const size_t slot = (size_t)blockIdx.x * 2 + (seg.first > 0 ? 1 : 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

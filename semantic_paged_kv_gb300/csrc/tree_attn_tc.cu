@@ -769,7 +769,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
     const Args &A = S.args;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127, hf = warp >> 2, g = A.g;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    Part part{0, 0, 0, 0};
+    Part part{};
     uint32_t tile0 = 0;
     int anc_b = -1;
     Segment seg = S.plan.seg;
@@ -802,7 +802,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         __syncwarp();
         fence_after();
         const bool whole = seg.first >= 0 && seg.end() <= run.n;
-        if (!whole && seg.first >= 0) part = part_of(seg, run);
+        if (!whole && seg.first >= 0) part = part_of<kRows>(seg, run, g);
         const size_t slot = (size_t)blockIdx.x * 2 + (seg.first > 0 ? 1 : 0);
         if (dead(S)) R.l = __int_as_float(0x7fc00000);  // a wait gave up: NaN
         const float none = whole ? __int_as_float(0x7fc00000) : 0.f;  // (all scores -inf; in a part: nothing seen)
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const __grid_constant__
     __syncthreads();
     fence_after();
     const uint32_t tmem = S.tmem;
-    Part part{0, 0, 0, 0};
+    Part part{};
     if (run.n > 0) {
         if (warp < kSoftWarps)
             part = soften(run, tmem);
