@@ -207,18 +207,13 @@ struct Ancestors {
     uint32_t mask[kMaxNodes][kWords];
     int16_t up[kMaxNodes];
 };
-// By kMaxNodes threads, thread t node t, with a barrier among them as `sync`.
+// By kMaxNodes threads, thread t node t with parent `up`, with a barrier among them as `sync`.
 template <typename Sync>
-__device__ __forceinline__ void find_ancestors(const int32_t *parents, int nodes, Ancestors &X, int32_t *err, int t,
-                                               Sync sync) {
+__device__ __forceinline__ void find_ancestors(int up, int nodes, Ancestors &X, int32_t *err, int t, Sync sync) {
     uint32_t mine[kWords];
-    int up = -1;
-    if (t < nodes) {
-        up = parents[t];
-        if (up >= t || up < -1) {
-            set_err(err, ICE_ERR_INVALID_ARG);
-            up = -1;
-        }
+    if (t < nodes && (up >= t || up < -1)) {
+        set_err(err, ICE_ERR_INVALID_ARG);
+        up = -1;
     }
 #pragma unroll
     for (int w = 0; w < kWords; ++w) mine[w] = w == t >> 5 ? 1u << (t & 31) : 0u;

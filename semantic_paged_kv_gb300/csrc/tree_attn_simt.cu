@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                 *reinterpret_cast<float4 *>(&S.q[r][c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
             }
             if (A.parents && i1 > seg.n_page && anc_b != b) {
-                find_ancestors(A.parents + (size_t)b * A.n_nodes, seg.nodes, S.anc, A.err, tid, [] { __syncthreads(); });
+                find_ancestors(tid < seg.nodes ? A.parents[(size_t)b * A.n_nodes + tid] : -1, seg.nodes, S.anc, A.err, tid,
+                               [] { __syncthreads(); });
                 anc_b = b;
             }
             float o[8][4], m[8], l[8];

@@ -75,6 +75,7 @@ struct Smem {
     Info info[kInfos];
     MetaScratch meta[kLoadWarps];
     Ancestors anc;
+    float factor[kRows];       // of a segment's rows
     float2 half[2][2][kRows];  // what the two threads of a row tell each other, in two tiles in turn
     PlanScratch plan;
     Args args;
@@ -145,6 +146,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+// 16 rows (an eighth of the warps' 128) and 32 columns: lane l has columns 8 k + 2 (l % 4) and the next one of rows l / 4 (r[4
+// k], r[4 k + 1]) and l / 4 + 8.
+__device__ __forceinline__ void tmem_st_fragment(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tensor memory] (+)= A B with A in tensor memory.
@@ -721,46 +732,68 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
     return R;
 }
 
-// This thread's half of its row's query (src null: none) into tensor memory, exact in fp16 after a power of two of the row;
-// the factor of the row's products.
-__device__ __forceinline__ float put_query(Smem &S, const __nv_bfloat16 *src, uint32_t q_at, int row, int hf) {
-    q4::Vec8<__nv_bfloat16> v[8];
+// The queries of a segment into tensor memory, exact in fp16 after a power of two of the row; the factor of this thread's
+// row's products.  Four lanes take a row of 16 (a row of the store's fragment) and read 64 bytes of it together.
+__device__ __forceinline__ float put_queries(Smem &S, const Piece &P, uint32_t q_at) {
+    const Args &A = S.args;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3, row = threadIdx.x & 127;
+    const int first = 32 * (warp & 3) + 16 * (warp >> 2) + (lane >> 2);  // and the one eight behind
+    uint4 v[2][4];  // pieces 4 m + 2 (j % 2) + j / 2 of 8 elements
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        v[c].zero();
-        if (src) v[c].load(src + 64 * hf + 8 * c);
+    for (int i = 0; i < 2; ++i) {
+        const int at = P.row0 + first + 8 * i, node = at / A.g;
+        const uint4 *src = reinterpret_cast<const uint4 *>(row_ptr<__nv_bfloat16>(A.q, P.b, node, P.h * A.g + at - node * A.g));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            v[i][m] = make_uint4(0u, 0u, 0u, 0u);
+            if (first + 8 * i < P.rows) v[i][m] = src[4 * m + 2 * (j & 1) + (j >> 1)];
+        }
     }
-    float big = 0.f;
+    const float sl = A.scale * 1.4426950408889634f;
+    float up[2];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        float x[8];
-        v[c].get(x);
+    for (int i = 0; i < 2; ++i) {
+        uint32_t big2 = 0u;  // magnitudes: bf16 values in the order of their bits
 #pragma unroll
-        for (int e = 0; e < 8; ++e) big = fabsf(x[e]) < INFINITY ? fmaxf(big, fabsf(x[e])) : INFINITY;
+        for (int m = 0; m < 4; ++m) {
+            big2 = __vmaxu2(big2, __vmaxu2(v[i][m].x & 0x7FFF7FFFu, v[i][m].y & 0x7FFF7FFFu));
+            big2 = __vmaxu2(big2, __vmaxu2(v[i][m].z & 0x7FFF7FFFu, v[i][m].w & 0x7FFF7FFFu));
+        }
+        big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 1));
+        big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, 2));
+        const uint32_t big = max(big2 & 0xFFFFu, big2 >> 16);
+        const int e2 = min(max(14 - ((int)(big >> 7) - 127), -113), 126);
+        up[i] = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
+        const float f = sl == 0.f ? 1.f : fabsf(sl) * pow2(-e2);
+        // (never zero: slots that are not seen have a score of -inf)
+        if (j == 0)
+            S.factor[first + 8 * i] = big < 0x7F80u && f < INFINITY ? fmaxf(f, FLT_MIN) : __int_as_float(0x7fc00000);
     }
-    S.half[0][hf][row].x = big;
-    pair_sync();
-    big = fmaxf(big, S.half[0][hf ^ 1][row].x);
-    pair_sync();  // (read before the first tile writes there)
-    const float sl = S.args.scale * 1.4426950408889634f;
-    const int e2 = min(max(14 - ((int)((__float_as_uint(big) >> 23) & 255u) - 127), -113), 126);
-    const float up = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
+    const bool odd = j & 1;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int m = 0; m < 4; m += 2) {
         uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float x[8];
-            v[4 * c + j].get(x);
+        for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[4 * j + e] = half2_of(x[e] * up, x[e + 4] * up);
+            for (int i = 0; i < 2; ++i) {
+                const uint4 y = v[i][m + x];
+                auto lo = [&](uint32_t z) { return __uint_as_float(z << 16) * up[i]; };
+                auto hi = [&](uint32_t z) { return __uint_as_float(z & 0xFFFF0000u) * up[i]; };
+                // elements e and e + 4 side by side (the order of K's); the lane beside has the other half of both pieces
+                const uint32_t a0 = half2_of(lo(y.x), lo(y.z)), a1 = half2_of(hi(y.x), hi(y.z));
+                const uint32_t b0 = half2_of(lo(y.y), lo(y.w)), b1 = half2_of(hi(y.y), hi(y.w));
+                const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? a0 : b0, 1);
+                const uint32_t r1 = __shfl_xor_sync(0xffffffffu, odd ? a1 : b1, 1);
+                w[8 * x + 2 * i] = odd ? r0 : a0, w[8 * x + 2 * i + 1] = odd ? r1 : a1;
+                w[8 * x + 4 + 2 * i] = odd ? b0 : r0, w[8 * x + 4 + 2 * i + 1] = odd ? b1 : r1;
+            }
         }
-        tmem_st16(q_at + 16 * c, w);
+        tmem_st_fragment(q_at + ((uint32_t)(warp >> 2) << 20) + 16 * m, w);
     }
     tmem_wait_st();
-    const float f = sl == 0.f ? 1.f : fabsf(sl) * pow2(-e2);
-    // (never zero: slots that are not seen have a score of -inf)
-    return big < INFINITY && f < INFINITY ? fmaxf(f, FLT_MIN) : __int_as_float(0x7fc00000);
+    pair_sync();
+    return S.factor[row];
 }
 
 // The softmax threads' part; the segment that starts here and goes on in other CTAs.
@@ -779,15 +812,15 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         if (P.n == 0) continue;  // (its tiles lie in the runs before)
         const bool out = row < P.rows;
         const int at_row = P.row0 + min(row, P.rows - 1), node = at_row / g, head = P.h * g + at_row % g;
-        const float factor = put_query(S, out ? row_ptr<__nv_bfloat16>(A.q, P.b, node, head) : nullptr,
-                                       tmem + lanes + kColQ + 32 * hf, row, hf);
+        const bool tree = A.parents && P.i0 + P.n > seg.n_page && anc_b != P.b;
+        const int up = tree && (int)threadIdx.x < seg.nodes ? A.parents[(size_t)P.b * A.n_nodes + threadIdx.x] : -1;
+        const float factor = put_queries(S, P, tmem + lanes + kColQ);
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.q_full);
-        if (A.parents && P.i0 + P.n > seg.n_page && anc_b != P.b) {
+        if (tree) {
             soft_sync();  // (the last ones have been read)
-            find_ancestors(A.parents + (size_t)P.b * A.n_nodes, seg.nodes, S.anc, A.err, threadIdx.x,
-                           [] { soft_sync(); });
+            find_ancestors(up, seg.nodes, S.anc, A.err, threadIdx.x, [] { soft_sync(); });
             anc_b = P.b;
         }
         Row R = soften_tiles(tmem, tile0, P.n, seg.n_page - P.i0, node, factor, P.rows);
