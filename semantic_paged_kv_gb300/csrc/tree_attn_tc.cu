@@ -7,8 +7,8 @@
 // T g query rows meet every key, so that the work is a matrix product (tcgen05)
 // and the 4-bit pages are unpacked once for up to 128 rows.
 //
-// Roles in a CTA (24 warps, one CTA an SM):
-//   14 warps unpack tiles of 128 tokens to fp16 in shared memory, page by page in
+// Roles in a CTA (20 warps, one CTA an SM):
+//   10 warps unpack tiles of 128 tokens to fp16 in shared memory, page by page in
 //     turn (K rows by token, V transposed: tokens are the contraction of the
 //     second product), the next page on its way in their registers; three tiles
 //     of K and of V;
@@ -40,7 +40,7 @@ using namespace tree;
 using namespace tc;
 
 constexpr int kRows = kTreeRowsTc;
-constexpr int kSoftWarps = 8, kLoadWarps = 14, kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kSoftWarps = 8, kLoadWarps = 10, kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 2);
 constexpr int kStages = 3;
 constexpr uint32_t kTileBytes = 128 * 128 * 2, kHalfBytes = kTileBytes / 2;
