@@ -369,9 +369,13 @@ struct Loader {
             for (int off = 1; off < 16; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
             return exponent_for(big);
         };
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             const int token = 16 * slot + 2 * i + (lane >> 4), node = j0 + token;
+            if (j0 + 16 * slot + 2 * i >= s.nodes) {  // (its keys meet no row)
+                if (c == 0) info.kf[token] = 1.f, info.vf[token] = 0.f;
+                continue;
+            }
             q4::Vec8<__nv_bfloat16> kk, vv;
             kk.zero(), vv.zero();
             if (node < s.nodes) {
@@ -397,7 +401,7 @@ struct Loader {
     }
     __device__ __forceinline__ void node_v(uint32_t dst, int slot, const Segment &s, int b, int h, int j0, const Info &info) {
         const int c = lane & 15;
-#pragma unroll 2
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
             const int token = 16 * slot + 4 * i + 2 * (lane >> 4), node = j0 + token;  // and the next one
             float x[8], y[8];
