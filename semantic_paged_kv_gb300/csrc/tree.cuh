@@ -24,10 +24,11 @@ constexpr int kMaxNodes = ICE_TREE_NODES;   // of a tree with parents
 constexpr int kWords = kMaxNodes / 32;
 constexpr int kPartRows = 128;              // rows of a partial result, at most
 // Tiles that a segment takes beside its own (queries, ancestors, results), by the rows of a block.  128 rows: 9 ragged
-// sequences of 32 heads take 103 us with 1, 92 with 2, 80 with 4 and 74 with 6, one tree at 16k 38.5, 37.3, 33.5 and 34.
-template <int R> constexpr int kTreeOver = R == 128 ? 5 : 1;
-// Places by which the longest segment may pass an equal run, so that each segment stays whole where there is a CTA for each:
-// a cut costs another start and end and the join.
+// sequences of 32 heads take 79 us with 3, 73 with 4, 68 with 5, 65 with 6 and 67 with 8, one tree at 16k 29 and then 27.
+template <int R> constexpr int kTreeOver = R == 128 ? 6 : 1;
+// Places by which the longest segment may pass an equal run so that, where there is a CTA for each, all stay whole: a cut costs
+// another start and end, and the join.  128 rows, whole and cut: 26 places against equal runs of 22 40 and 49 us, of 17 40 and
+// 40, of 11 39 and 34; 15 against 13 25 and 34, against 7 27 and 29, against 4 24 and 19; 74 against 63 103 and 86.
 template <int R> constexpr int kTreeWhole = R == 128 ? 7 : 1;
 constexpr int kMinRun = 1;  // places of a run, at least (the tiny fp32 layout takes 48 us with 2, 29 with 1)
 

@@ -15,8 +15,8 @@ using namespace tree;
 
 // All CTAs find the cut segments in `parts` and take pieces of them in turn: 32 rows (neighbours in the parts) and either 32
 // elements, 4 a warp, or, where a segment has more than kAhead runs, 8 elements, 4 a warp and a quarter of the runs.
-// (One tree at 16k, 8 segments of 19 runs: .. us of the call, 7 with whole columns of runs a warp and CTAs for every place of
-// `parts`.)
+// (One tree at 16k, 8 segments of 19 runs: about 4 us of the call; 7 with whole columns of runs a warp and CTAs for every place
+// of `parts`.  What is left is the launch, the list and one or two passes through the memory's latency.)
 constexpr int kJoinCtas = 4;  // an SM
 constexpr int kMostParts = 256;
 constexpr int kAhead = 5, kSplit = 4;
