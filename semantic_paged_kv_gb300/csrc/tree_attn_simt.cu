@@ -7,6 +7,10 @@
 // memory, 8 x 4 scores (then 8 x 4 outputs) a thread.  A warp owns 8 rows: their
 // maxima and sums stay in it.  A tile's product with V is summed apart and then
 // added, which keeps the rounding of long sums down.
+//
+// Bound by issue and latency of one CTA of 8 warps (254 registers): FMA pipe 38%, issue 51% busy.  Measured: 61 nodes of 16/1
+// heads over 100,000 tokens 1.68 ms (30 TFLOP/s), three short sequences of 4/1 heads 27 us.  The same products as packed pairs of
+// fp32 operations took 2.17 ms (the pairs' order costs registers).
 #include <float.h>
 
 #include "tree.cuh"
@@ -207,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
             for (int i = 0; i < 8; ++i) {
                 const int r = 8 * warp + i;
                 if (r >= rows) break;
-                const float inv = l[i] != 0.f ? 1.f / l[i] : (whole ? __int_as_float(0x7fc00000) : 0.f);  // (all scores -inf: NaN)
+                // (all scores -inf: NaN)
+                const float inv = l[i] != 0.f ? 1.f / l[i] : (whole ? __int_as_float(0x7fc00000) : 0.f);
                 const float4 x = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
                 if (whole) {
                     put4(row_out<T>(A.o, b, (row0 + r) / g, h * g + (row0 + r) % g) + 4 * lane, x);

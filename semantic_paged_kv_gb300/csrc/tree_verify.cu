@@ -15,6 +15,11 @@
 // a decision differs from exact arithmetic only where it lies within about
 // 1e-12 of its border.  The order of additions is fixed, so a call always gives
 // the same answer.
+//
+// Bound by latencies: the gather (parents, tokens, probabilities: three loads one after another), then about 2.5 us a refusal
+// (its pass over two rows, a cluster barrier, 64 sums read across it) and the draw.  Measured: a tree of 26 nodes over 128,000
+// fp32 probabilities 14 us, 64 trees of up to 61 nodes in bf16 38 us.  Two CTAs an SM with four vectors a lane ahead; three with
+// two ahead take 14.7 and 35.9 us, four with two ahead 16.4 and 36.9 (spills).
 #include <cooperative_groups.h>
 
 #include "common.cuh"
