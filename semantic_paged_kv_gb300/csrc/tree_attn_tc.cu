@@ -237,7 +237,7 @@ __device__ __forceinline__ uint32_t high_pair(uint32_t w, uint32_t step, uint32_
 struct Loader {
     const Args &A;
     Smem &S;
-    const int lane, warp;  // warp of the load warps; it takes slots warp, warp + 7, .. of a segment's tiles (a tile has 8)
+    const int lane, warp;  // warp of the load warps; it takes slots warp, warp + kLoadWarps, .. of a segment's tiles (a tile has 8)
     // the pages of its slots 32 j .., one a lane; and the page numbers of the next 32
     const unsigned char *page;
     int page_len, ahead, base, x0;
