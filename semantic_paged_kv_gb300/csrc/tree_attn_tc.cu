@@ -92,6 +92,7 @@ struct Smem {
     uint32_t tmem;
     int bad;   // a node's value is not finite
     int dead;  // a wait gave up
+    int seen;  // tiles whose scores are there
 };
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "one CTA an SM");
 
@@ -216,6 +217,21 @@ __device__ __forceinline__ bool dead(const Smem &S) { return *static_cast<const 
 __device__ __forceinline__ bool wait_for(Smem &S, unsigned long long &bar, uint32_t parity) {
     if (mbar_test(&bar, parity)) return true;
     if (!dead(S) && mbar_wait(&bar, parity, S.args.fault ? kFaultWaitNs : kWaitNs)) return true;
+    *static_cast<volatile int *>(&S.dead) = 1;
+    set_err(S.args.err, ICE_ERR_TIMEOUT);
+    return false;
+}
+// Waits until the scores of `tiles` tiles are there.  A wait on a phase's parity cannot tell a phase from the one two before: it
+// is right where the waiting warp is at most a round of the ring ahead.  Warps without a slot in a segment (it has eight a
+// tile) would pass over any number of short segments, so every segment begins with this.
+__device__ __forceinline__ bool wait_seen(Smem &S, int tiles) {
+    const volatile int &seen = S.seen;
+    if (seen >= tiles) return true;
+    const unsigned long long t0 = now_ns();
+    while (!dead(S)) {
+        if (seen >= tiles) return true;
+        if (now_ns() - t0 > kWaitNs) break;
+    }
     *static_cast<volatile int *>(&S.dead) = 1;
     set_err(S.args.err, ICE_ERR_TIMEOUT);
     return false;
@@ -464,6 +480,7 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
             L.load_k();
             L.load_v();
         }
+        if (!wait_seen(S, (int)tile0 - kStages + 1)) return;
         for (int n = 1; x < pages; ++n) {
             const int slot = slot_at(), next = x + kLoadWarps;
             const uint32_t at = tile_at();
@@ -684,6 +701,7 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
     for (int i = 0; i < n; ++i) {
         const uint32_t at = tile0 + i;
         wait_for(S, S.s_ready[at & 1], at >> 1 & 1);
+        if (threadIdx.x == 0) *static_cast<volatile int *>(&S.seen) = (int)at + 1;
         __syncwarp();
         fence_after();
         if ((row & ~31) >= rows) {  // no row of this warp (and its partner): its rows of P and O mean nothing
@@ -904,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const __grid_constant__
         for (int i = 0; i < 2; ++i) mbar_init(&S.s_ready[i], 1), mbar_init(&S.p_ready[i], kSoftWarps);
         mbar_init(&S.q_full, kSoftWarps);
         mbar_init_fence();
-        S.dead = 0, S.bad = 0, S.args = A;
+        S.dead = 0, S.seen = 0, S.bad = 0, S.args = A;
     }
     if (warp == 0) tmem_alloc(&S.tmem, 512);
     dep_wait();

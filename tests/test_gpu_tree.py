@@ -399,6 +399,19 @@ def test_attention_long_chain():
     c.check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,hq,hkv,tree,lens", [
+    (13, 500, 32, 2, False, None), (40, 300, 16, 1, False, None), (30, 40, 32, 8, True, [0] * 20 + [300, 0, 0, 0, 2000] * 2),
+    (24, 200, 16, 2, True, [0, 0, 0, 0, 0, 300] * 4), (60, 9, 16, 4, True, [0] * 40 + [129, 257] * 10)])
+def test_attention_short_segments_before_longer_ones(B, T, hq, hkv, tree, lens, dtype):
+    """Many blocks of one tile, then blocks of several, in one CTA's run: warps that have no part in the short ones wait for
+    them all the same."""
+    c = Case(B, T, hq, hkv, dtype, tree, lens, counts=[T - b % 3 for b in range(B)])
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    c.check()
+
+
 def test_attention_many_units():
     """More units than a CTA has threads, most of one or two tiles."""
     c = Case(40, 2, 32, 32, "bf16", True, [(37 * b) % 90 for b in range(40)])
