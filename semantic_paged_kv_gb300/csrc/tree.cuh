@@ -26,10 +26,11 @@ constexpr int kPartRows = 128;              // rows of a partial result, at most
 // Tiles that a segment takes beside its own (queries, ancestors, results), by the rows of a block.  128 rows: 9 ragged
 // sequences of 32 heads take 79 us with 3, 73 with 4, 68 with 5, 65 with 6 and 67 with 8, one tree at 16k 29 and then 27.
 template <int R> constexpr int kTreeOver = R == 128 ? 6 : 1;
-// Places by which the longest segment may pass an equal run so that, where there is a CTA for each, all stay whole: a cut costs
-// another start and end, and the join.  128 rows, whole and cut: 26 places against equal runs of 22 40 and 49 us, of 17 40 and
-// 40, of 11 39 and 34; 15 against 13 25 and 34, against 7 27 and 29, against 4 24 and 19; 74 against 63 103 and 86.
-template <int R> constexpr int kTreeWhole = R == 128 ? 7 : 1;
+// Places by which the longest segment may pass an equal run so that, where there is a CTA for each and they fill a quarter of the
+// CTAs, all stay whole: a cut costs another start and end, and the join.  128 rows, whole and cut: 26 places against equal runs
+// of 22 40 and 49 us, of 17 40 and 40 (of different lengths 40 and 50), of 11 39 and 34; 15 against 13 25 and 34, against 7 27
+// and 29, against 4 24 and 19; 74 against 63 103 and 86; 8 segments of 10 against 1 21 and 19.
+template <int R> constexpr int kTreeWhole = R == 128 ? 9 : 1;
 constexpr int kMinRun = 1;  // places of a run, at least (the tiny fp32 layout takes 48 us with 2, 29 with 1)
 
 // The segment that starts in a CTA and goes on in the next ones (runs 0: none).
@@ -167,7 +168,7 @@ template <int R, int kThreads> __device__ __forceinline__ Run plan_run(const Arg
     Run r;
     r.share = total < (1ll << 30) ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
     if (r.share < kMinRun) r.share = kMinRun;
-    const bool whole = all.segments <= (int)gridDim.x && all.most <= r.share + kTreeWhole<R>;
+    const bool whole = all.segments <= (int)gridDim.x && 4 * all.segments > (int)gridDim.x && all.most <= r.share + kTreeWhole<R>;
     r.f0 = r.share * blockIdx.x;
     r.n = (int)max(min(r.share, total - r.f0), 0ll);
     if (whole) r.n = (int)blockIdx.x < all.segments;

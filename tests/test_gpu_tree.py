@@ -456,6 +456,21 @@ def test_attention_workspace_between_shapes_and_graphs():
             assert torch.equal(c.O, w) and torch.equal(cases[1].O, want[1])
 
 
+def test_attention_on_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own."""
+    cases = [Case(2, 40, 16, 4, "bf16", True, [3000, 70]), Case(9, 5, 8, 8, "bf16", False, [900] * 9),
+             Case(2, 12, 8, 2, "fp32", True, [500, 40])]
+    want = [c.run().clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(cases, streams):
+            c.run(s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert ice.ice_check(c.err) == ice.ICE_OK and torch.equal(c.O, w)
+
+
 # ----------------------------------------------------------------- verify --
 def _verify(target, draft, tokens, parents, counts, uniform):
     B, T = tokens.shape
