@@ -8,7 +8,8 @@
 // of all segments, one after another, are cut into equal runs, one per CTA,
 // whatever the lengths; a segment counts kTreeOver tiles more than it has (what
 // starting and ending one costs).  A segment that runs cut leaves partial
-// results in the workspace, joined in run order by a second kernel.
+// results in the workspace, joined in a fixed order by a second kernel.  Where every
+// segment has a CTA and none is much longer than such a run, all stay whole.
 #pragma once
 
 #include "common.cuh"
