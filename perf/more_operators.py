@@ -447,7 +447,7 @@ def _plain(st):
 
 # ------------------------------------------------------- the framework's --
 def _plan(st):
-    """What a program keeps beside its buffers: the parameters, the views and the workspace."""
+    """What a program keeps beside its buffers: the parameters, the views, the workspace and buffers that a call fills."""
     import semantic_paged_kv_gb300 as ice
 
     c, pl = st["case"], {}
@@ -464,13 +464,15 @@ def _plan(st):
     if c["op"] == "commit":
         pl["k"], pl["v"] = ice.rows(st["k"][0]), ice.rows(st["v"][0])
         pl["cache"] = ice.Cache4(st["records"][0], st["block_table"])
-        # all layers as one cache, to read them back in one call
+        # all layers as one cache, to read them back in one call: buffers that every call fills
         pages = st["records"].shape[1]
-        first = torch.arange(L, dtype=torch.int32, device="cuda")[:, None, None] * pages
-        table = (st["block_table"] + first).view(L * c["batch"], -1).contiguous()
-        pl["all"] = ice.Cache4(st["records"].view(L * pages, c["hkv"], RECORD), table)
+        pl["first"] = torch.arange(L, dtype=torch.int32, device="cuda")[:, None, None] * pages
+        pl["all_table"] = torch.empty((L, *st["block_table"].shape), dtype=torch.int32, device="cuda")
+        pl["all"] = ice.Cache4(st["records"].view(L * pages, c["hkv"], RECORD), pl["all_table"].flatten(0, 1))
         pl["all_params"] = config(L * c["batch"])
-        pl["all_start"], pl["all_n"] = st["start"].repeat(L), st["n_path"].repeat(L)
+        pl["all_start"], pl["all_n"] = (torch.empty((L, c["batch"]), dtype=torch.int32, device="cuda") for _ in range(2))
+        pl["out"] = torch.empty((2, *st["k"].shape), dtype=st["k"].dtype, device="cuda")
+        st["k_out"], st["v_out"] = pl["out"]
         for f in ("k_out", "v_out"):
             pl[f] = ice.rows(st[f].view(L * c["batch"], c["nodes"], c["hkv"], D))
         return pl
@@ -503,6 +505,10 @@ def _framework(st):
     ice.ice_cache4_commit(pl["params"], c["layers"], c["nodes"], pl["k"], pl["v"], st["path"], st["n_path"],
                           st["start"], pl["cache"], st["err"], k_layer=st["k"].stride(0), v_layer=st["v"].stride(0),
                           records_layer=st["records"].stride(0))
+    torch.add(st["block_table"], pl["first"], out=pl["all_table"])
+    pl["all_start"].copy_(st["start"])
+    pl["all_n"].copy_(st["n_path"])
+    pl["out"].zero_()  # (rows behind the path are not written)
     ice.ice_cache4_read(pl["all_params"], c["nodes"], pl["all"], pl["all_start"], pl["all_n"], pl["k_out"],
                         pl["v_out"], st["err"])
     return {"k": st["k_out"], "v": st["v_out"]}
