@@ -57,8 +57,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
 }
 __device__ __forceinline__ double value(Two a) { return (double)a.hi + (double)a.lo; }
 
-// max(p - beta q, 0) with beta = (bh, bl); NaN counts as 0.
+// What a probability counts as: NaN and negative ones as 0.
+__device__ __forceinline__ float counted(float x) { return fmaxf(x, 0.f); }
+
+// max(p - beta q, 0) with beta = (bh, bl) > 0.  (A p of NaN or below 0 fails the last comparison, and so does an infinite q.)
 __device__ __forceinline__ Two rest_of(float p, float q, float bh, float bl) {
+    q = counted(q);
     const float hi = bh * q, lo = fmaf(bh, q, -hi);
     float s, e;
     two_sum(p, -hi, s, e);
@@ -89,7 +93,7 @@ struct Sums {
 // max(p - beta q, 0) of two elements, as s + e.
 __device__ __forceinline__ void rests_of(float2 p, float2 q, float bh, float bl, unsigned long long &s,
                                          unsigned long long &e) {
-    const unsigned long long q2 = pk2(q.x, q.y), b2 = pk2(bh, bh), less = mul2(pk2(-bh, -bh), q2);
+    const unsigned long long q2 = pk2(counted(q.x), counted(q.y)), b2 = pk2(bh, bh), less = mul2(pk2(-bh, -bh), q2);
     two_sum2(pk2(p.x, p.y), less, s, e);
     e = sub2(e, fma2(pk2(bl, bl), q2, fma2(b2, q2, less)));
     float2 x = upk2(s), y = upk2(e);
@@ -159,8 +163,8 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
                 set_err(A.err, ICE_ERR_CAPACITY);
                 x = -1;
             } else if (!greedy) {
-                px = Elem<T>::load(target + up * A.t_node + x);
-                if (draft) qx = Elem<T>::load(draft + up * A.d_node + x);
+                px = counted(Elem<T>::load(target + up * A.t_node + x));
+                if (draft) qx = counted(Elem<T>::load(draft + up * A.d_node + x));
             }
         }
         const float u = greedy ? 0.f : A.uniform[(size_t)b * n_nodes + t];
@@ -192,8 +196,10 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
     auto piece = [&](const Rows &r, int g) {
         return g == 0 ? 0 : (g == kPieces ? A.vocab : r.head + min(g * r.per, r.vecs) * kVec);
     };
+    // (beta is at least 1 where a child was refused; without one q's row, which may hold anything at a leaf, is not read)
+    auto takes_q = [&](const Command &c) { return draft && !c.plain && c.bh > 0.f; };
     auto weight_of = [&](const Command &c, int i, float p, float q) {
-        if (draft && !c.plain) return rest_of(p, q, c.bh, c.bl);
+        if (takes_q(c)) return rest_of(p, q, c.bh, c.bl);
         Two r{p > 0.f ? p : 0.f, 0.f};
         if (!c.plain)
             for (int j = 0; j < S.n_out; ++j)
@@ -201,7 +207,7 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
         return r;
     };
     auto weight = [&](const Command &c, const Rows &r, int i) {
-        return weight_of(c, i, Elem<T>::load(r.p + i), draft && !c.plain ? Elem<T>::load(r.q + i) : 0.f);
+        return weight_of(c, i, Elem<T>::load(r.p + i), takes_q(c) ? Elem<T>::load(r.q + i) : 0.f);
     };
     // Calls use(v, raw p, raw q) for the vectors of this lane in piece g, several of them on their way at a time.
     constexpr int kAhead = 4;
@@ -303,7 +309,7 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
         if (cmd.op == kDone) break;
         const Rows r = rows_of(cmd.node);
         const int g = rank * kWarps + warp;
-        const bool with_q = draft && !cmd.plain;
+        const bool with_q = takes_q(cmd);
         // (elements outside the whole vectors: one a lane, behind the others)
         const int edge = g == 0 && lane < r.head ? lane
                          : g == kPieces - 1 && r.head + r.vecs * kVec + lane < A.vocab && lane < kVec
