@@ -345,11 +345,11 @@ template <typename T> __global__ void __cluster_dims__(kCluster, 1, 1) __launch_
                 Elem<T>::unpack(pv, p);
 #pragma unroll
                 for (int e = 0; e < kVec; ++e)
-                    if (p[e] == p[e]) join_best(best, at, p[e], i + e);
+                    if (p[e] > 0.f) join_best(best, at, p[e], i + e);  // (counted(p) = 0 is no probability)
             });
             if (edge >= 0) {
                 const float x = Elem<T>::load(r.p + edge);
-                if (x == x) join_best(best, at, x, edge);
+                if (x > 0.f) join_best(best, at, x, edge);
             }
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) {

@@ -123,3 +123,25 @@ def test_rows_that_nobody_drew_from_are_not_read(dtype):
     some[..., 4321] = torch.where(leaf, torch.full_like(some[..., 0], 0.5), some[..., 4321])
     got = _run(target, some, tokens, parents, None, uniform)
     assert got[3] == ice.ICE_OK and all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [1, 50, 5003])
+def test_greedy_rows_without_probability(V, dtype):
+    """Zeros, negative numbers and NaN alone: no child is accepted there, -1 follows, and the call says so."""
+    B, T = 6, 4
+    target, _ = _rows(B, T, V, dtype, 27)
+    parents = torch.tensor([[-1, 0, 1, 2]] * B, dtype=torch.int32, device="cuda")
+    best = target.argmax(-1).int()
+    tokens = torch.cat((best[:, :1], best[:, :-1]), 1).contiguous()  # every drafted token is the likeliest
+    target[1, 0], target[2, 1], target[3, 3], target[4, 2] = 0, -0.25, math.nan, 0
+    target[4, 2, ::2] = math.nan
+    for b, i in ((1, 1), (2, 2), (4, 3)):
+        tokens[b, i] = 0  # the first of the largest, if 0 counted
+    path, n, nxt, err = _run(target, None, tokens, parents, None, None)
+    assert err == ice.ICE_ERR_INVALID_ARG
+    assert n.tolist() == [4, 1, 2, 4, 3, 4] and [nxt[b].item() for b in (1, 2, 3, 4)] == [-1] * 4
+    assert nxt[0] == best[0, 3] and nxt[5] == best[5, 3]
+    keep = torch.tensor([0, 5], device="cuda")
+    _check(target[keep], None, tokens[keep], parents[keep], None, None)
+    _check(target, None, tokens, parents, None, None, ice.ICE_ERR_INVALID_ARG)
