@@ -758,8 +758,9 @@ ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes);
  * as fp16 numbers (11 bits; a token whose |mid| + 7.5 step, or a node whose
  * largest element, lies outside 2^-4 .. 2^8 has a power of two of its own),
  * weights from 2^-30 of the row's largest on, fp32 sums; queries are exact.  fp32:
- * fp32 throughout.  The largest |v| times the number of tokens has to stay below
- * 2^119.
+ * fp32 throughout.  The products q k and their sums have to stay within fp32's
+ * range (keys, queries and scale may lie anywhere in it), and the largest |v|
+ * times the number of tokens below 2^119.
  */
 ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
                                 const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,

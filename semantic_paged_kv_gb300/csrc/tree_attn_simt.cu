@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     dep_wait();
     const Run run = plan_run<kRows, kThreads>(A, S.plan);
     Part part{};
-    const float sl = A.scale * 1.4426950408889634f;
+    const float sl = fminf(fmaxf(A.scale * 1.4426950408889634f, -FLT_MAX), FLT_MAX);
     int anc_b = -1;
     if (run.n > 0) {
         Segment seg = S.plan.seg;

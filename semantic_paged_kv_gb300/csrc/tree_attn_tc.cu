@@ -85,6 +85,7 @@ struct Smem {
     MetaScratch meta[kLoadWarps];
     Ancestors anc;
     float factor[kRows];       // of a segment's rows
+    float2 split[kRows];       // the same as a product (score_of)
     float2 half[2][2][kRows];  // what the two threads of a row tell each other, in two tiles in turn
     PlanScratch plan;
     Args args;
@@ -194,6 +195,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 // 2^e, -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+// Two scores, x times a key's kf and its row's factor.  kf and the factor join first: a large key's power with the product, or
+// a small query's with the scale, leaves fp32's range where the score does not.  Factors in 2^-100 .. 2 are safe as they are;
+// one beyond, which may be no fp32 number itself, goes in two parts (kWide).  (x = 0: 0)
+template <bool kWide> __device__ __forceinline__ float2 scores_of(float x0, float x1, float2 kf, float2 split) {
+    const float2 k = upk2(mul2(pk2(kf.x, kf.y), pk2(split.y, split.y)));
+    if (kWide) return make_float2(x0 * split.x * fminf(k.x, FLT_MAX), x1 * split.x * fminf(k.y, FLT_MAX));
+    return upk2(mul2(pk2(x0, x1), pk2(k.x, k.y)));
+}
+// The factor |sl| 2^-e2 as (1, factor) where that is safe, otherwise with a power of two in 2^-126 .. 2^126 as the second part.
+__device__ __forceinline__ float2 split_of(float sl, int e2) {
+    const float f = fabsf(sl) * pow2(-e2);
+    if (f >= 0x1p-100f && f <= 2.f) return make_float2(1.f, f);
+    const int es = min(max((int)((__float_as_uint(sl) >> 23) & 255u) - 127, -126), 126), e = min(max(es - e2, -126), 126);
+    return make_float2(fabsf(sl) * pow2(-es) * pow2(es - e2 - e), pow2(e));
+}
 // The exponent by whose power a token of largest element `big` is divided (0: none).
 __device__ __forceinline__ int exponent_for(float big) {
     if ((big >= 0.0625f && big <= 256.f) || big == 0.f || !(big < INFINITY)) return 0;
@@ -649,8 +665,9 @@ struct Scores {
         tmem_st16(p_at, w[0]);
         tmem_st16(p_at + 16, w[1]);
     }
-    // The same where keys or values carry powers of two of their own, or the two maxima have parted.
-    __device__ __forceinline__ float2 largest_any(const float *kf, const float *vf, float r) const {
+    // The same where keys or values carry powers of two of their own, or the two maxima have parted.  (Packed pairs: 4 x 50k
+    // tokens that all have powers of their own take 303 us, one score after another 325 to 377 by the order of the factors.)
+    template <bool kWide> __device__ __forceinline__ float2 largest_any(const float *kf, const float *vf, float2 split) const {
         float top = -INFINITY, top_o = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -659,15 +676,20 @@ struct Scores {
             tmem_wait_ld();
             const uint32_t w = (c < 2 ? mask[0] : mask[1]) >> (16 * (c & 1));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float y = w >> i & 1u ? x[i] * kf[16 * c + i] * r : -INFINITY;
-                top = fmaxf(top, y), top_o = fmaxf(top_o, y + vf[16 * c + i]);
+            for (int i = 0; i < 16; i += 2) {
+                float2 y = scores_of<kWide>(x[i], x[i + 1], *reinterpret_cast<const float2 *>(kf + 16 * c + i), split);
+                y.x = w >> i & 1u ? y.x : -INFINITY, y.y = w >> (i + 1) & 1u ? y.y : -INFINITY;
+                const float2 e = *reinterpret_cast<const float2 *>(vf + 16 * c + i);
+                const float2 z = upk2(add2(pk2(y.x, y.y), pk2(e.x, e.y)));
+                top = max3(top, y.x, y.y), top_o = max3(top_o, z.x, z.y);
             }
         }
         return make_float2(top, top_o);
     }
-    __device__ __forceinline__ float weights_any(const float *kf, const float *vf, float r, float off, float off_o,
-                                                 float l) const {
+    template <bool kWide>
+    __device__ __forceinline__ float weights_any(const float *kf, const float *vf, float2 split, float off, float off_o) const {
+        const unsigned long long off2 = pk2(off, off), off_o2 = pk2(off_o, off_o);
+        unsigned long long sum = 0ull;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             float x[16];
@@ -676,16 +698,19 @@ struct Scores {
             tmem_wait_ld();
             const uint32_t w = (c < 2 ? mask[0] : mask[1]) >> (16 * (c & 1));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float y = w >> i & 1u ? x[i] * kf[16 * c + i] * r : -INFINITY;
-                l += exp2_fast(y + off);
-                x[i] = exp2_fast(y + vf[16 * c + i] + off_o);
+            for (int i = 0; i < 16; i += 2) {
+                float2 y = scores_of<kWide>(x[i], x[i + 1], *reinterpret_cast<const float2 *>(kf + 16 * c + i), split);
+                y.x = w >> i & 1u ? y.x : -INFINITY, y.y = w >> (i + 1) & 1u ? y.y : -INFINITY;
+                const float2 e = *reinterpret_cast<const float2 *>(vf + 16 * c + i);
+                const unsigned long long y2 = pk2(y.x, y.y);
+                const float2 a = upk2(add2(y2, off2)), z = upk2(add2(add2(y2, pk2(e.x, e.y)), off_o2));
+                sum = add2(sum, pk2(exp2_fast(a.x), exp2_fast(a.y)));
+                p[i >> 1] = half2_of(exp2_fast(z.x), exp2_fast(z.y));
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[i] = half2_of(x[2 * i], x[2 * i + 1]);
             tmem_st8(p_at + 8 * c, p);
         }
-        return l;
+        const float2 t = upk2(sum);
+        return t.x + t.y;
     }
 };
 
@@ -736,7 +761,12 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
         }
         if (!done) {
             // the row's maximum: that of its two threads
-            float2 top = apart ? X.largest_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r) : make_float2(X.largest() * R.r, 0.f);
+            float2 split = make_float2(1.f, 1.f);
+            if (apart) split = S.split[row];
+            const bool wide = __any_sync(0xffffffffu, split.x != 1.f);
+            const float *kf = &info.kf[64 * hf], *vf = &info.vf[64 * hf];
+            float2 top = !apart ? make_float2(X.largest() * R.r, 0.f)
+                         : wide ? X.largest_any<true>(kf, vf, split) : X.largest_any<false>(kf, vf, split);
             S.half[at & 1][hf][row] = top;
             pair_sync();
             const float2 other = S.half[at & 1][hf ^ 1][row];
@@ -748,7 +778,8 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
             o_done();
             if (up_o) scale_o(o_at, fo);
             if (apart) {
-                R.l = X.weights_any(&info.kf[64 * hf], &info.vf[64 * hf], R.r, kTop - R.m, kTop - R.mo, R.l);
+                R.l += wide ? X.weights_any<true>(kf, vf, split, kTop - R.m, kTop - R.mo)
+                            : X.weights_any<false>(kf, vf, split, kTop - R.m, kTop - R.mo);
             } else {
                 uint32_t w[2][16];
                 R.l += X.weights<true>(R.r, kTop - R.m, w);
@@ -780,7 +811,7 @@ __device__ __forceinline__ float put_queries(Smem &S, const Piece &P, uint32_t q
             if (first + 8 * i < P.rows) v[i][m] = src[4 * m + 2 * (j & 1) + (j >> 1)];
         }
     }
-    const float sl = A.scale * 1.4426950408889634f;
+    const float sl = fminf(fmaxf(A.scale * 1.4426950408889634f, -FLT_MAX), FLT_MAX);
     float up[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -796,9 +827,14 @@ __device__ __forceinline__ float put_queries(Smem &S, const Piece &P, uint32_t q
         const int e2 = min(max(14 - ((int)(big >> 7) - 127), -113), 126);
         up[i] = sl == 0.f ? 0.f : copysignf(pow2(e2), sl);
         const float f = sl == 0.f ? 1.f : fabsf(sl) * pow2(-e2);
-        // (never zero: slots that are not seen have a score of -inf)
-        if (j == 0)
-            S.factor[first + 8 * i] = big < 0x7F80u && f < INFINITY ? fmaxf(f, FLT_MIN) : __int_as_float(0x7fc00000);
+        // (never zero: slots that are not seen have a score of -inf.  It counts where all of a tile's keys have powers of 1:
+        // products are below 2^31 then, and scores with a factor below FLT_MIN as good as 0)
+        if (j == 0) {
+            const float nan = __int_as_float(0x7fc00000);
+            const float2 split = split_of(sl, e2);
+            S.factor[first + 8 * i] = big < 0x7F80u ? fminf(fmaxf(f, FLT_MIN), FLT_MAX) : nan;
+            S.split[first + 8 * i] = make_float2(big < 0x7F80u ? split.x : nan, split.y);
+        }
     }
     const bool odd = j & 1;
 #pragma unroll
