@@ -53,7 +53,7 @@ struct Args {
     int g, hq, hkv, units;
     float scale;
     float4 *part_o;   // [2 CTAs, 32, kPartRows]: elements 4 i .. of a row's result over the run's tokens
-    float2 *part_ml;  // [2 CTAs, kPartRows]: its maximum (powers of two) and sum
+    float2 *part_ml;  // [2 CTAs, kPartRows]: its maximum (powers of two) and sum (times any number, the same for all)
     Part *parts;      // [CTAs]
     int32_t *err;
     int fault;  // ICE_FAULT's timeout: the kernel's producers deliver nothing

@@ -61,6 +61,10 @@ static_assert(32 * kSoftWarps == kMaxNodes, "a softmax thread a node");
 static_assert(kInfos >= kStages + 2, "an Info outlives its softmax");
 constexpr float kLazy = 8.f;  // powers of two that a score may pass the running maximum by
 constexpr float kTop = 6.f;   // powers of two that P has above exp2(score - maximum)
+// On a part's sum: without the power that weights can have, it is at most the number of the part's tokens, and the join's
+// products of sums and values stay as small as the values allow.
+constexpr float kPartSum = 0x1p-14f;
+static_assert(kTop + kLazy == 14.f, "the largest weight");
 constexpr float kMost = 16384.f;  // of the sum of a thread's weights of a tile (2^(kTop + kLazy)); above, the maximum moves
 // kind::f16 instruction descriptor: D fp32, A and B fp16, both K-major, M = N = 128.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
@@ -907,7 +911,7 @@ __device__ __noinline__ Part soften(const Run run, uint32_t tmem) {
         if (dead(S)) R.l = __int_as_float(0x7fc00000);  // a wait gave up: NaN
         const float none = whole ? __int_as_float(0x7fc00000) : 0.f;  // (all scores -inf; in a part: nothing seen)
         const float inv = 1.f / R.l, f = exp2_fast(0.5f * (R.mo - R.m));
-        if (out && !whole && hf == 0) A.part_ml[slot * kPartRows + row] = make_float2(R.m, R.l);
+        if (out && !whole && hf == 0) A.part_ml[slot * kPartRows + row] = make_float2(R.m, R.l * kPartSum);
         __nv_bfloat16 *dst = row_out<__nv_bfloat16>(A.o, P.b, node, head) + 64 * hf;
         const int nodes0 = max(P.i0 - seg.n_page, 0) * kTile, nodes1 = min((P.i0 + P.n - seg.n_page) * kTile, seg.nodes);
 #pragma unroll 1

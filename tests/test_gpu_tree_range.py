@@ -42,3 +42,34 @@ def test_keys_of_very_different_size(dtype):
     c.run()
     assert ice.ice_check(c.err) == ice.ICE_OK
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_largest_values_of_long_sequences(dtype):
+    """The largest |v| times the number of tokens just below 2^119, in segments that runs cut, with scores that rise by 7.9
+    powers of two inside the first run alone: its weights are the largest, and all of them count."""
+    B, hkv, n = 25, 4, 8192
+    c = Case(B, 1, hkv, hkv, dtype, False, [n] * B, counts=[1] * B)
+    x = torch.zeros((2, S, D), device="cuda")
+    x[1, :, 0] = 1.0  # scores of 0 and, below, of 7.9 log 2
+    sign = torch.where(torch.arange(D, device="cuda") % 3 == 0, -1.0, 1.0)
+    v = (2.0 ** 105 * sign).expand(2, S, D).clone()
+    v[..., 64:] = 2.0 ** 105  # (groups of one value are exact in 4 bits; the first one holds two)
+    low, high = ref4.encode(x.bfloat16(), v.bfloat16())
+    c.recs[:] = low
+    for b in range(B):
+        c.recs[c.table[b, 8:168].long()] = high  # tiles 1 .. 20 of the 64
+    c.q.zero_()
+    c.q[..., 0] = 62.0
+    c.k.zero_()
+    c.v.copy_((2.0 ** 105 * sign).expand_as(c.v))
+    c.v[..., 64:] = 2.0 ** 105
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK and bool(torch.isfinite(c.O).all())
+    k0, v0 = c.cached(0, 0)
+    k1, v1 = torch.cat((k0, c.k[0, :, 0].double())), torch.cat((v0, c.v[0, :, 0].double()))
+    keep = torch.ones((1, n + 1), dtype=torch.bool, device="cuda")
+    q = c.q[0, :, 0].double()
+    want, tol = ref.attention(q, k1, v1, keep, c.scale), ref.tolerance(q, k1, v1, keep, c.scale, c.dt)
+    off = (c.O.double() - want).norm(dim=-1)  # (all units have the same inputs)
+    assert bool((off <= tol).all()), float((off / tol).max())
