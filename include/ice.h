@@ -749,8 +749,9 @@ ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes);
  * Rows behind counts[b] are neither read nor written.
  *  - lens and pages outside their ranges as in ice_cache4_attn_decode.
  * O may be q itself (same data and strides); it must not overlap k or v.
- *  - A node's infinities and NaN reach only the rows that see it.  A row whose
- *    query is not finite, or whose scores are all -infinity, gives NaN.
+ *  - A node's infinities and NaN reach only the rows that see it: those of its
+ *    v every such row, whatever the node weighs there.  A row whose query is not
+ *    finite, or whose scores are all -infinity, gives NaN.
  *  - Every run of a call gives the same bits.
  *  - A bounded wait that gives up sets ICE_ERR_TIMEOUT in err_dev and leaves
  *    NaN in O.

@@ -20,6 +20,14 @@ using namespace tree;
 constexpr int kJoinCtas = 4;  // an SM
 constexpr int kMostParts = 256;
 constexpr int kAhead = 5, kSplit = 4;
+// Infinities and NaN of a part go to `odd`: they reach the result whatever the part weighs, as in a segment that is not cut.
+__device__ __forceinline__ void set_apart(float &v, float &odd) {
+    if (!(fabsf(v) < INFINITY)) odd += v, v = 0.f;
+}
+__device__ __forceinline__ void set_apart(float4 &v, float4 &odd) {
+    if (fabsf(v.x) + fabsf(v.y) + (fabsf(v.z) + fabsf(v.w)) < INFINITY) return;
+    set_apart(v.x, odd.x), set_apart(v.y, odd.y), set_apart(v.z, odd.z), set_apart(v.w, odd.w);
+}
 struct Cut {
     Part p;
     int run, first;  // its first run, the number of its first piece
@@ -73,14 +81,14 @@ __global__ void __launch_bounds__(256, kJoinCtas) k_tree_join(const __grid_const
         const int k_first = split ? warp >> 1 : 0, k_step = split ? kSplit : 1, runs = p.runs;
         const bool live = r < p.rows;
         float M = -FLT_MAX, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), odd = acc;
         for (int k0 = k_first; live && k0 < runs; k0 += kAhead * k_step) {
             float2 ml[kAhead];
             float4 v[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const int k = k0 + j * k_step;
-                ml[j] = make_float2(-FLT_MAX, 0.f);
+                ml[j] = make_float2(-FLT_MAX, 0.f), v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < runs) {
                     const size_t slot = (size_t)(2 * (c.run + k) + (k == 0 ? p.inside : 0));
                     ml[j] = A.part_ml[slot * kPartRows + r];
@@ -95,6 +103,7 @@ __global__ void __launch_bounds__(256, kJoinCtas) k_tree_join(const __grid_const
             L *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
+                set_apart(v[j], odd);
                 if (ml[j].y == 0.f) continue;
                 const float w = ml[j].y * exp2f(ml[j].x - M);
                 L += w;
@@ -105,16 +114,18 @@ __global__ void __launch_bounds__(256, kJoinCtas) k_tree_join(const __grid_const
             }
         }
         if (split) {  // (the same for the whole CTA)
+            acc.x += odd.x, acc.y += odd.y, acc.z += odd.z, acc.w += odd.w;
             sum[warp >> 1][warp & 1][lane] = acc, ml_of[warp >> 1][warp & 1][lane] = make_float2(M, L);
             __syncthreads();
             if (warp < 2) {
 #pragma unroll
                 for (int k = 1; k < kSplit; ++k) M = fmaxf(M, ml_of[k][warp][lane].x);
-                acc = make_float4(0.f, 0.f, 0.f, 0.f), L = 0.f;
+                acc = odd = make_float4(0.f, 0.f, 0.f, 0.f), L = 0.f;
 #pragma unroll
                 for (int k = 0; k < kSplit; ++k) {
                     const float2 ml = ml_of[k][warp][lane];
-                    const float4 v = sum[k][warp][lane];
+                    float4 v = sum[k][warp][lane];
+                    set_apart(v, odd);
                     if (ml.y == 0.f) continue;
                     const float f = exp2f(ml.x - M);
                     L = fmaf(ml.y, f, L);
@@ -128,7 +139,8 @@ __global__ void __launch_bounds__(256, kJoinCtas) k_tree_join(const __grid_const
             const int b = p.unit / A.hkv, h = p.unit - b * A.hkv, row = p.block * kBlock + r;
             const float inv = 1.f / L;
             put4(row_out<T>(A.o, b, row / A.g, h * A.g + row % A.g) + 4 * i,
-                 make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                 make_float4(fmaf(acc.x, inv, odd.x), fmaf(acc.y, inv, odd.y), fmaf(acc.z, inv, odd.z),
+                             fmaf(acc.w, inv, odd.w)));
         }
     }
 }

@@ -30,6 +30,7 @@ struct Smem {
     float p[kRows][kTile];
     Ancestors anc;
     int len[kTilePages];
+    int bad;  // a node's value is not finite
     PlanScratch plan;
 };
 
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>(smem_raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = A.g;
+    if (tid == 0) S.bad = 0;
     dep_wait();
     const Run run = plan_run<kRows, kThreads>(A, S.plan);
     Part part{};
@@ -112,6 +114,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                             load8<T>(row_ptr<T>(A.k, b, j0 + r, h) + c, x);
                             load8<T>(row_ptr<T>(A.v, b, j0 + r, h) + c, y);
                         }
+                        // infinities and NaN join the rows that see them at the end
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!(fabsf(y[e]) < INFINITY)) S.bad = 1, y[e] = 0.f;
                         *reinterpret_cast<float4 *>(&S.k[r][c]) = make_float4(x[0], x[1], x[2], x[3]);
                         *reinterpret_cast<float4 *>(&S.k[r][c + 4]) = make_float4(x[4], x[5], x[6], x[7]);
                         *reinterpret_cast<float4 *>(&S.v[r][c]) = make_float4(y[0], y[1], y[2], y[3]);
@@ -190,8 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                         const float w[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            // (a node's infinities and NaN reach only the rows that see it)
-                            if (nodes && w[e] == 0.f) continue;
                             a[i][0] = fmaf(w[e], vv[e].x, a[i][0]);
                             a[i][1] = fmaf(w[e], vv[e].y, a[i][1]);
                             a[i][2] = fmaf(w[e], vv[e].z, a[i][2]);
@@ -213,7 +217,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_simt(const __grid_constant
                 if (r >= rows) break;
                 // (all scores -inf: NaN)
                 const float inv = l[i] != 0.f ? 1.f / l[i] : (whole ? __int_as_float(0x7fc00000) : 0.f);
-                const float4 x = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+                float4 x = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+                if (S.bad) {
+                    const int node = (row0 + r) / g, nodes1 = min((i1 - seg.n_page) * kTile, seg.nodes);
+#pragma unroll 1
+                    for (int j = max(i0 - seg.n_page, 0) * kTile; j < nodes1; ++j) {
+                        if (!(A.parents ? S.anc.mask[node][j >> 5] >> (j & 31) & 1u : j <= node)) continue;
+                        const T *v = row_ptr<T>(A.v, b, j, h) + 4 * lane;
+                        auto add = [](float &to, float y) {
+                            if (!(fabsf(y) < INFINITY)) to += y;
+                        };
+                        add(x.x, Elem<T>::load(v)), add(x.y, Elem<T>::load(v + 1));
+                        add(x.z, Elem<T>::load(v + 2)), add(x.w, Elem<T>::load(v + 3));
+                    }
+                }
                 if (whole) {
                     put4(row_out<T>(A.o, b, (row0 + r) / g, h * g + (row0 + r) % g) + 4 * lane, x);
                 } else {

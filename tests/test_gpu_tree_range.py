@@ -73,3 +73,35 @@ def test_largest_values_of_long_sequences(dtype):
     want, tol = ref.attention(q, k1, v1, keep, c.scale), ref.tolerance(q, k1, v1, keep, c.scale, c.dt)
     off = (c.O.double() - want).norm(dim=-1)  # (all units have the same inputs)
     assert bool((off <= tol).all()), float((off / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,hq,hkv,lens", [(1, 8, 2, [5000]), (1, 8, 2, [20000]), (2, 8, 2, [100, 0]), (60, 8, 2, [40] * 60),
+                                           (3, 32, 8, [900, 0, 300]), (100, 4, 1, [8192] * 100)])
+def test_infinities_of_nodes_that_weigh_nothing(B, hq, hkv, lens, dtype):
+    """Infinities and NaN in V of nodes whose scores lie hundreds of powers of two below the cached tokens': they reach every
+    row that sees them, and no other one, however the batch cuts the work into runs."""
+    T = 20
+    c = Case(B, T, hq, hkv, dtype, True, lens, counts=[T] * B, seed=21)
+    g = hq // hkv
+    c.q.abs_()
+    c.k.abs_().mul_(-60)
+    clean = c.run().clone()
+    inf, nan, two, minus = 3, 5, 7, 9
+    c.v[:, inf, :, 5] = math.inf
+    c.v[:, nan, :, 70] = math.nan
+    c.v[:, two, :, 5] = -math.inf
+    c.v[:, minus, :, 127] = -math.inf
+    got = c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    plain = [d for d in range(D) if d not in (5, 70, 127)]
+    assert torch.equal(got[..., plain], clean[..., plain]) and bool(torch.isfinite(clean).all())
+    for b in range(B):
+        own = ref.sees(c.parents[b], T, "cuda")
+        for d, plus, less in ((5, own[:, inf], own[:, two]), (70, own[:, nan], own[:, nan]),
+                              (127, torch.zeros_like(own[:, 0]), own[:, minus])):
+            x, y = got[b, :, :, d], clean[b, :, :, d]
+            assert torch.equal(x[~plus & ~less], y[~plus & ~less]), (b, d)
+            assert bool((x[plus & ~less] == math.inf).all()) and bool((x[~plus & less] == -math.inf).all()), (b, d)
+            assert bool(torch.isnan(x[plus & less]).all()), (b, d)
+    assert g * hkv == hq
