@@ -762,6 +762,10 @@ __device__ __noinline__ Row soften_tiles(uint32_t tmem, uint32_t tile0, int n, i
                 o_done();
                 X.store(w);
             }
+        } else if (i > 0) {
+            // (so that both warps of a row come to the same barriers whatever they have read: after a wait that gave up a tile's
+            // Info may still be written, and `apart` differ)
+            pair_all(false);
         }
         if (!done) {
             // the row's maximum: that of its two threads
