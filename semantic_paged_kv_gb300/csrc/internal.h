@@ -27,9 +27,9 @@ inline int units_of(const ice_params &p) { return p.batch * p.n_kv_heads; }
 //   hostpool  ice_host_pool_create fails after its allocations, at the device
 //             mapping (ICE_ERR_CUDA; everything allocated is freed)
 //   copy      ice_host_pool_gather_h2d fails its bulk copy (ICE_ERR_CUDA)
-//   timeout   the page producers of the decode step's and the trees'
-//             attention deliver nothing, and the bounded waits give up after
-//             kFaultWaitNs (ICE_ERR_TIMEOUT)
+//   timeout   the page producer of the decode step's attention delivers
+//             nothing, those of the trees' attention no values, and the
+//             bounded waits give up after kFaultWaitNs (ICE_ERR_TIMEOUT)
 // Read at every call; unset (the default) nothing changes.
 bool fault_armed(const char *what);
 constexpr unsigned long long kFaultWaitNs = 20000000ull;  // 20 ms

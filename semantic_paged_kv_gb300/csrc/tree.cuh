@@ -56,7 +56,7 @@ struct Args {
     float2 *part_ml;  // [2 CTAs, kPartRows]: its maximum (powers of two) and sum (times any number, the same for all)
     Part *parts;      // [CTAs]
     int32_t *err;
-    int fault;  // ICE_FAULT's timeout: the kernel's producers deliver nothing
+    int fault;  // ICE_FAULT's timeout: the kernel's producers deliver no values
 };
 
 __device__ __forceinline__ int nodes_of(const Args &A, int b) {

@@ -94,6 +94,7 @@ struct Smem {
     PlanScratch plan;
     Args args;
     unsigned long long k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages], s_ready[2], p_ready[2], q_full;
+    unsigned long long drained[2];  // the products of the two issuing threads, after a wait that gave up
     uint32_t tmem;
     int bad;   // a node's value is not finite
     int dead;  // a wait gave up
@@ -473,7 +474,6 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
     Smem &S = shared();
     const Args &A = S.args;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kSoftWarps;
-    if (A.fault) return;  // (a test's: nothing arrives)
     Loader L(A, S, w);
     uint32_t tile0 = 0;
     Segment seg = S.plan.seg;
@@ -508,6 +508,7 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
             L.put_meta(slot, S.info[at & (kInfos - 1)]);
             L.put_k(slot, su32(S.k[stage_of(at)]));
             end(S.k_full);
+            if (A.fault) return;  // (a test's: products of scores are issued, values never arrive)
             if (next < pages) {  // (the next page's loads as soon as their registers are free)
                 L.find(seg, n);
                 L.load_k();
@@ -524,6 +525,7 @@ __device__ __noinline__ void unpack_tiles(const Run run) {
             if (!begin(S.k_empty)) return;
             L.node_k(su32(S.k[stage_of(tile_at())]), slot_at(), seg, P.b, P.h, j0, info);
             end(S.k_full);
+            if (A.fault) return;
             if (!begin(S.v_empty)) return;
             L.node_v(su32(S.v[stage_of(tile_at())]), slot_at(), seg, P.b, P.h, j0, info);
             end(S.v_full);
@@ -964,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const __grid_constant__
             mbar_init(&S.v_full[i], kTilePages), mbar_init(&S.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&S.s_ready[i], 1), mbar_init(&S.p_ready[i], kSoftWarps);
-        mbar_init(&S.q_full, kSoftWarps);
+        mbar_init(&S.q_full, kSoftWarps), mbar_init(&S.drained[0], 1), mbar_init(&S.drained[1], 1);
         mbar_init_fence();
         S.dead = 0, S.seen = 0, S.bad = 0, S.args = A;
     }
@@ -989,8 +991,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_tree_tc(const __grid_constant__
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (dead(S))  // (products that nobody waited for end long before)
-        for (int i = 0; i < 100; ++i) __nanosleep(10000);
+    // Drain: after a wait that gave up, products may be under way that nobody waited for; they end before tensor memory is freed
+    // and the CTA leaves (without one, the last segment's results have waited for all of them).
+    if (dead(S)) {  // (the same for the whole CTA: nobody waits any more)
+        const int issuer = (warp - kMmaWarp) & 1;
+        if (warp >= kMmaWarp && (tid & 31) == 0) {
+            umma_commit(&S.drained[issuer]);
+            mbar_wait(&S.drained[issuer], 0);
+        }
+        __syncwarp();
+        __syncthreads();
+    }
     if (tid == 0) A.parts[blockIdx.x] = part;
     if (warp == 0) tmem_dealloc(tmem, 512);
 }

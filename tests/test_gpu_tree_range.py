@@ -105,3 +105,21 @@ def test_infinities_of_nodes_that_weigh_nothing(B, hq, hkv, lens, dtype):
             assert bool((x[plus & ~less] == math.inf).all()) and bool((x[~plus & less] == -math.inf).all()), (b, d)
             assert bool(torch.isnan(x[plus & less]).all()), (b, d)
     assert g * hkv == hq
+
+
+@pytest.mark.parametrize("B,T,lens", [(1, 5, [17]), (2, 200, [3000, 100]), (40, 30, [500] * 40)])
+def test_products_end_before_a_call_that_gave_up(monkeypatch, B, T, lens):
+    """Values that never arrive: products of scores have been issued in every CTA; the calls end one after another, say so and
+    leave NaN, and calls behind them on the same stream are right."""
+    c = Case(B, T, 8, 2, "bf16", True, lens, counts=[T] * B)
+    want = c.run().clone()
+    monkeypatch.setenv("ICE_FAULT", "timeout")
+    for _ in range(3):
+        c.O.fill_(7)
+        c.run()
+        assert ice.ice_check(c.err) == ice.ICE_ERR_TIMEOUT and bool(torch.isnan(c.O).all())
+    c.run()
+    monkeypatch.delenv("ICE_FAULT")
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_ERR_TIMEOUT and torch.equal(c.O, want)  # (the error of the call before)
+    assert ice.ice_check(c.err) == ice.ICE_OK
