@@ -501,6 +501,7 @@ def rows(t: torch.Tensor) -> IceRows:
     # the stride of a dimension of size 1 is never used
     r = IceRows(t.data_ptr(), *(st[i] if t.shape[i] > 1 else 0 for i in range(3)))
     r.keep = t
+    r.made_of = (t.dtype, *t.shape[:3])
     return r
 
 
@@ -640,16 +641,66 @@ def _check_tree_batch(tree, batch: int) -> None:
             raise IceError(ICE_ERR_INVALID_ARG, f"{name} are of {t.shape[0]} sequences, the call of {batch}")
 
 
+def _check_ints(name: str, t, rows: int, cols: int | None = None) -> None:
+    """t (None or a pointer passes) is contiguous int32 [rows, cols] or, without cols, [rows]; more rows may be there."""
+    if not isinstance(t, torch.Tensor):
+        return
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < (rows if cols is None else rows * cols) or \
+            (cols is not None and t.shape[-1:] != (cols,)):
+        raise IceError(ICE_ERR_INVALID_ARG, f"{name} is contiguous int32 {[rows] if cols is None else [rows, cols]}: got "
+                                            f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _check_view(name: str, r, dtype, batch: int, n: int, heads: int) -> None:
+    """A ``rows(...)`` view holds rows [batch, n, heads, d] of the call's type (a dimension of size 1 has a stride of 0: the same
+    row for all)."""
+    made_of = getattr(r, "made_of", None)
+    if made_of is not None and (made_of[0] != dtype or 1 != made_of[1] < batch or 1 != made_of[2] < n or
+                                1 != made_of[3] < heads):
+        raise IceError(ICE_ERR_INVALID_ARG, f"{name} holds {made_of[0]} {list(made_of[1:])} rows, the call takes {dtype} "
+                                            f"{[batch, n, heads]}")
+
+
+def _dtype_of(params):
+    return torch.bfloat16 if params.dtype == ICE_BF16 else torch.float32
+
+
+def _check_tree_views(params, n: int, q, k, v, O) -> None:
+    dtype, batch, hq, hkv = _dtype_of(params), params.batch, params.n_q_heads, params.n_kv_heads
+    _check_view("q", q, dtype, batch, n, hq)
+    _check_view("k", k, dtype, batch, n, hkv)
+    _check_view("v", v, dtype, batch, n, hkv)
+    _check_view("O", O, dtype, batch, n, hq)
+
+
+def _check_cache(params, cache) -> None:
+    records, table = getattr(cache, "keep", None) or (None, None)
+    if records is not None and (records.shape[1] != params.n_kv_heads or table.shape[0] < params.batch):
+        raise IceError(ICE_ERR_INVALID_ARG, f"a cache of {records.shape[1]} KV heads and {table.shape[0]} sequences, the call "
+                                            f"of {params.n_kv_heads} and {params.batch}")
+
+
 def ice_cache4_attn_tree(params, tree, q, cache, lens, k, v, scale, O, ws, err, stream=None):
-    """q, k, v and O are ``rows(...)`` views, tree a Tree, cache a Cache4 (or None, with lens None)."""
+    """q, k, v and O are ``rows(...)`` views, tree a Tree, cache a Cache4 and lens [B] int32 (or both None)."""
     _check_tree_batch(tree, params.batch)
+    _check_tree_views(params, tree.n_nodes, q, k, v, O)
+    _check_cache(params, cache)
+    _check_ints("lens", lens, params.batch)
     _check(load().ice_cache4_attn_tree(params, tree, q, cache, _ptr(lens), k, v, float(scale), O, _ptr(ws),
                                        _nbytes(ws), _ptr(err), _stream(stream)))
 
 
 def ice_sparse_attn_tree4(params, tree, q, records, page_len, sel_pages, sel_count, cache, lens, k, v, scale, O, ws,
                           err, stream=None):
+    """The same, with records the pool's (uint8), page_len [U, page_cap], sel_pages [U, max_sel] and sel_count [U] int32."""
     _check_tree_batch(tree, params.batch)
+    _check_tree_views(params, tree.n_nodes, q, k, v, O)
+    _check_cache(params, cache)
+    units = params.batch * params.n_kv_heads
+    _check_ints("lens", lens, params.batch)
+    _check_ints("page_len", page_len, units, params.page_cap)
+    _check_ints("sel_pages", sel_pages, units, sel_pages.shape[-1])
+    _check_ints("sel_count", sel_count, units)
     _check(load().ice_sparse_attn_tree4(params, tree, q, _ptr(records), _ptr(page_len), _ptr(sel_pages),
                                         _ptr(sel_count), sel_pages.shape[-1], cache, _ptr(lens), k, v, float(scale),
                                         O, _ptr(ws), _nbytes(ws), _ptr(err), _stream(stream)))
@@ -677,7 +728,14 @@ def ice_tree_verify(tree, target, draft, tokens, uniform, path, n_path, next_tok
 def ice_cache4_commit(params, n_layers, n_nodes, k, v, path, n_path, start, cache, err, *, k_layer=0, v_layer=0,
                       records_layer=0, stream=None):
     """k and v are layer 0's ``rows(...)`` views, k_layer and v_layer the elements and records_layer the bytes from a
-    layer to the next (not read with one layer)."""
+    layer to the next (not read with one layer), path [B, n_nodes], n_path and start [B] int32."""
+    dtype, batch, hkv = _dtype_of(params), params.batch, params.n_kv_heads
+    _check_view("k", k, dtype, batch, n_nodes, hkv)
+    _check_view("v", v, dtype, batch, n_nodes, hkv)
+    _check_cache(params, cache)
+    _check_ints("path", path, batch, n_nodes)
+    _check_ints("n_path", n_path, batch)
+    _check_ints("start", start, batch)
     _check(load().ice_cache4_commit(params, n_layers, n_nodes, k, v, k_layer, v_layer, _ptr(path), _ptr(n_path),
                                     _ptr(start), cache, records_layer, _ptr(err), _stream(stream)))
 
