@@ -755,13 +755,16 @@ ice_status ice_tree_workspace_bytes(const ice_params *p, size_t *bytes);
  *  - Every run of a call gives the same bits.
  *  - A bounded wait that gives up sets ICE_ERR_TIMEOUT in err_dev and leaves
  *    NaN in O.
- * Arithmetic: O is rounded once, to dtype.  bf16: keys, values and weights go in
- * as fp16 numbers (11 bits; a token whose |mid| + 7.5 step, or a node whose
- * largest element, lies outside 2^-4 .. 2^8 has a power of two of its own),
- * weights from 2^-30 of the row's largest on, fp32 sums; queries are exact.  fp32:
- * fp32 throughout.  The products q k and their sums have to stay within fp32's
- * range (keys, queries and scale may lie anywhere in it), and the largest |v|
- * times the number of tokens below 2^119.
+ * Arithmetic: O is rounded once, to dtype.  bf16: keys and values go in as fp16
+ * numbers under one power of two a token (1 where its |mid| + 7.5 step, or a
+ * node's largest element, lies in 2^-4 .. 2^8; otherwise the one of that
+ * largest): an element is off by up to 2^-11 of itself and 2^-24 of that power,
+ * so that one far below its token's largest keeps fewer bits than its type has.
+ * Weights are fp16 numbers, off by up to 2^-11 of themselves and 2^-31 of the
+ * row's largest; queries are exact down to 2^-29 of their row's largest element;
+ * sums are fp32.  fp32: fp32 throughout.  The products q k and their sums have to
+ * stay within fp32's range (keys, queries and scale may lie anywhere in it), and
+ * the largest |v| times the number of tokens below 2^119.
  */
 ice_status ice_cache4_attn_tree(const ice_params *p, const ice_tree *tree, const ice_rows *q, const ice_cache4 *cache,
                                 const int32_t *lens, const ice_rows *k, const ice_rows *v, float scale,

@@ -28,8 +28,9 @@
 // by 4).
 //
 // Numbers: a code's value mid + step (c - 7.5) is rounded once, to fp16 (half a
-// step, 2^-11, where the plain bf16 operand would lose 2^-9), queries (bf16) are
-// exact in fp16 after a power of two of their row.  Tokens whose |mid| + 7.5
+// step, 2^-11, where the plain bf16 operand would lose 2^-9; elements below 2^-14,
+// where fp16's steps stop shrinking, 2^-25, and so does a mid there), queries
+// (bf16) are exact in fp16 after a power of two of their row.  Tokens whose |mid| + 7.5
 // step lies outside 2^-4 .. 2^8 take a power of two of their own, which the
 // softmax gives back: on scores for keys; for values on the weights, whose
 // maximum is then kept apart from that of the sum, so that neither a large value

@@ -123,3 +123,43 @@ def test_products_end_before_a_call_that_gave_up(monkeypatch, B, T, lens):
     c.run()
     assert ice.ice_check(c.err) == ice.ICE_ERR_TIMEOUT and torch.equal(c.O, want)  # (the error of the call before)
     assert ice.ice_check(c.err) == ice.ICE_OK
+
+
+@pytest.mark.parametrize("small", [2.0 ** -12, 2.0 ** -20, 2.0 ** -24])
+@pytest.mark.parametrize("v_scale", [1.0, 1000.0])
+def test_elements_far_below_their_row(small, v_scale):
+    """The two halves of V's rows of very different size, element by element, bf16: a row's elements go in as fp16 numbers under
+    one power of two f (1 where the row's largest lies in 2^-4 .. 2^8, otherwise the one that brings it to 1 .. 2): off by up
+    to 2^-11 of themselves and 2^-24 / f (2^-25 each for a group's mid and for the value)."""
+    c = Case(2, 40, 8, 2, "bf16", True, [300, 45], seed=31)
+    k, v = ref4.decode(c.recs.view(-1, 2304))
+    fine = torch.isfinite(k).all(-1).all(-1) & torch.isfinite(v).all(-1).all(-1)
+    half = torch.ones(D, device="cuda")
+    half[64:] = small
+    new = ref4.encode(torch.nan_to_num(k).bfloat16(), (torch.nan_to_num(v) * half * v_scale).bfloat16())
+    c.recs.copy_(torch.where(fine[:, None], new, c.recs.view(-1, 2304)).view_as(c.recs))
+    c.v.mul_(half * v_scale)
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    for b in range(c.B):
+        n = c.counts[b]
+        own = ref.sees(c.parents[b], n, "cuda")
+        for j in range(c.hq):
+            h = j // 4
+            k0, v0 = c.cached(b, h)
+            k1, v1 = torch.cat((k0, c.k[b, :n, h].double())), torch.cat((v0, c.v[b, :n, h].double()))
+            keep = torch.cat((torch.ones((n, k0.shape[0]), dtype=torch.bool, device="cuda"), own), 1)
+            q = c.q[b, :n, j].double()
+            w = torch.softmax((q @ k1.T * c.scale).masked_fill(~keep, -math.inf), -1)
+            o = w @ v1
+            # as tree_ref.tolerance, an element at a time: scores' errors e move it by w e |v - o|, a weight's and a value's
+            # own roundings by 2^-11 w |v| each and 2^-24 / f w; weights below 2^-20 of the largest are off by 2^-31 of it
+            e = c.scale * 2.0 ** -11 * (q.square() @ k1.square().T).sqrt() + 2.0 ** -22 * (q @ k1.T * c.scale).abs()
+            big = v1.abs().amax(-1)  # (7.5 steps beyond mid: at most this, up to the roundings of both)
+            up = torch.where((big >= 0.06) & (big <= 250), torch.ones_like(big), 2.0 ** torch.ceil(big.log2()))
+            moved = (w * e).square() @ v1.square() + o.square() * (w * e).square().sum(-1, keepdim=True)  # |v - o|^2 <= 2 (..)
+            own_err = 2 * 2.0 ** -22 * (w.square() @ v1.square()) + (2.0 ** -24 * w * up).square().sum(-1, keepdim=True)
+            tol = 4 * (2 * moved + own_err).sqrt() + 2.0 ** -31 * w.amax(-1, keepdim=True) * v1.abs().sum(0) \
+                + (2.0 ** -18 + 2.0 ** -8) * o.abs()
+            off = (c.O[b, :n, j].double() - o).abs()
+            assert bool((off <= tol).all()), (b, j, float((off / tol).max()))
