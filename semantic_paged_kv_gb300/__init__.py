@@ -532,6 +532,7 @@ class Cache4(IceCache4):
             raise IceError(ICE_ERR_INVALID_ARG, "a block table is contiguous int32 [B, max_pages]")
         super().__init__(records.data_ptr(), table.data_ptr(), records.shape[0], table.shape[1])
         self.keep = (records, table)
+        self.made_of = (records.shape[1], table.shape[0])
 
 
 def ice_rope_table(inv_freq, n_positions: int, table, stream=None):
@@ -646,7 +647,7 @@ def _check_ints(name: str, t, rows: int, cols: int | None = None) -> None:
     if not isinstance(t, torch.Tensor):
         return
     if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < (rows if cols is None else rows * cols) or \
-            (cols is not None and t.shape[-1:] != (cols,)):
+            (cols is not None and (t.dim() < 2 or t.size(-1) != cols)):
         raise IceError(ICE_ERR_INVALID_ARG, f"{name} is contiguous int32 {[rows] if cols is None else [rows, cols]}: got "
                                             f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}")
 
@@ -665,26 +666,26 @@ def _dtype_of(params):
     return torch.bfloat16 if params.dtype == ICE_BF16 else torch.float32
 
 
-def _check_tree_views(params, n: int, q, k, v, O) -> None:
+def _check_tree_views(params, n: int, q, k, v, O, cache) -> None:
     dtype, batch, hq, hkv = _dtype_of(params), params.batch, params.n_q_heads, params.n_kv_heads
     _check_view("q", q, dtype, batch, n, hq)
     _check_view("k", k, dtype, batch, n, hkv)
     _check_view("v", v, dtype, batch, n, hkv)
     _check_view("O", O, dtype, batch, n, hq)
+    _check_cache(cache, batch, hkv)
 
 
-def _check_cache(params, cache) -> None:
-    records, table = getattr(cache, "keep", None) or (None, None)
-    if records is not None and (records.shape[1] != params.n_kv_heads or table.shape[0] < params.batch):
-        raise IceError(ICE_ERR_INVALID_ARG, f"a cache of {records.shape[1]} KV heads and {table.shape[0]} sequences, the call "
-                                            f"of {params.n_kv_heads} and {params.batch}")
+def _check_cache(cache, batch: int, heads: int) -> None:
+    made_of = getattr(cache, "made_of", None)
+    if made_of is not None and (made_of[0] != heads or made_of[1] < batch):
+        raise IceError(ICE_ERR_INVALID_ARG, f"a cache of {made_of[0]} KV heads and {made_of[1]} sequences, the call of {heads} "
+                                            f"and {batch}")
 
 
 def ice_cache4_attn_tree(params, tree, q, cache, lens, k, v, scale, O, ws, err, stream=None):
     """q, k, v and O are ``rows(...)`` views, tree a Tree, cache a Cache4 and lens [B] int32 (or both None)."""
     _check_tree_batch(tree, params.batch)
-    _check_tree_views(params, tree.n_nodes, q, k, v, O)
-    _check_cache(params, cache)
+    _check_tree_views(params, tree.n_nodes, q, k, v, O, cache)
     _check_ints("lens", lens, params.batch)
     _check(load().ice_cache4_attn_tree(params, tree, q, cache, _ptr(lens), k, v, float(scale), O, _ptr(ws),
                                        _nbytes(ws), _ptr(err), _stream(stream)))
@@ -694,8 +695,7 @@ def ice_sparse_attn_tree4(params, tree, q, records, page_len, sel_pages, sel_cou
                           err, stream=None):
     """The same, with records the pool's (uint8), page_len [U, page_cap], sel_pages [U, max_sel] and sel_count [U] int32."""
     _check_tree_batch(tree, params.batch)
-    _check_tree_views(params, tree.n_nodes, q, k, v, O)
-    _check_cache(params, cache)
+    _check_tree_views(params, tree.n_nodes, q, k, v, O, cache)
     units = params.batch * params.n_kv_heads
     _check_ints("lens", lens, params.batch)
     _check_ints("page_len", page_len, units, params.page_cap)
@@ -732,7 +732,7 @@ def ice_cache4_commit(params, n_layers, n_nodes, k, v, path, n_path, start, cach
     dtype, batch, hkv = _dtype_of(params), params.batch, params.n_kv_heads
     _check_view("k", k, dtype, batch, n_nodes, hkv)
     _check_view("v", v, dtype, batch, n_nodes, hkv)
-    _check_cache(params, cache)
+    _check_cache(cache, batch, hkv)
     _check_ints("path", path, batch, n_nodes)
     _check_ints("n_path", n_path, batch)
     _check_ints("start", start, batch)
