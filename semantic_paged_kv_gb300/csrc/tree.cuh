@@ -25,7 +25,8 @@ constexpr int kMaxNodes = ICE_TREE_NODES;   // of a tree with parents
 constexpr int kWords = kMaxNodes / 32;
 constexpr int kPartRows = 128;              // rows of a partial result, at most
 // Tiles that a segment takes beside its own (queries, ancestors, results), by the rows of a block.  128 rows: 9 ragged
-// sequences of 32 heads take 79 us with 3, 73 with 4, 68 with 5, 65 with 6 and 67 with 8, one tree at 16k 29 and then 27.
+// sequences of 32 heads and four sets of lengths take 75, 50, 51 and 151 us with 4, 70, 50, 52 and 134 with 5, 67, 49, 50 and 124
+// with 6, 69, 49, 55 and 108 with 8; one tree at 16k 27.4 with 4, 28.2 with 6, 27.8 with 8.
 template <int R> constexpr int kTreeOver = R == 128 ? 6 : 1;
 // Places by which the longest segment may pass an equal run so that, where there is a CTA for each and they fill a quarter of the
 // CTAs, all stay whole: a cut costs another start and end, and the join.  128 rows, whole and cut: 26 places against equal runs

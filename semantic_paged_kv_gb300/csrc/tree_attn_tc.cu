@@ -22,10 +22,10 @@
 // 10 of them 8 pages in 2300) and the softmax (2000 for a tile, two warps a scheduler) share the schedulers' issue; neither
 // waits long for the other, and neither for memory.  10 unpacking warps leave 96 registers a thread: 8 take 136 us for 4 x 50k
 // tokens of 64/8 heads and 16 nodes, 9 133, 10 126, 12 and 14 (80 registers) 139, 16 (72) 165.  Measured: that case 125 us
-// (0.84 PFLOP/s, 1.8 TB/s), 16 x 100k 838 us (0.76), a chunk of 1000 tokens of 32/8 heads behind 36,864 690 us (0.88).  Short
-// calls are bound by what a CTA does once (12,000 clocks before the first tile, 5,000 after the last), much of it the first pass
-// through its code: loops that run once or twice are not unrolled (node rows: 9 ragged sequences of 32 heads 68 us, 83 unrolled
-// by 4).
+// (0.84 PFLOP/s, 1.8 TB/s), 16 x 100k 817 to 850 us (0.75 to 0.78), a chunk of 1000 tokens of 32/8 heads behind 36,864 693 us
+// (0.88).  Short calls are bound by what a CTA does once (12,000 clocks before the first tile, 5,000 after the last), much of it the
+// first pass through its code: loops that run once or twice are not unrolled (node rows: 9 sequences of 32 heads and one set of
+// lengths 68 us, 83 unrolled by 4).
 //
 // Numbers: a code's value mid + step (c - 7.5) is rounded once, to fp16 (half a
 // step, 2^-11, where the plain bf16 operand would lose 2^-9; elements below 2^-14,

@@ -16,10 +16,13 @@
 // 1e-12 of its border.  The order of additions is fixed, so a call always gives
 // the same answer.
 //
+// Where no child of a node was refused its weights are p alone, and q's row is not read.
+//
 // Bound by latencies: the gather (parents, tokens, probabilities: three loads one after another), then about 2.5 us a refusal
-// (its pass over two rows, a cluster barrier, 64 sums read across it) and the draw.  Measured: a tree of 26 nodes over 128,000
-// fp32 probabilities 14 us, 64 trees of up to 61 nodes in bf16 38 us.  Two CTAs an SM with four vectors a lane ahead; three with
-// two ahead take 14.7 and 35.9 us, four with two ahead 16.4 and 36.9 (spills).
+// (its pass over two rows, a cluster barrier, 64 sums read across it) and the draw.  Measured, by the refusals of four draws: a
+// tree of 26 nodes over 128,000 fp32 probabilities 14.1 to 26.6 us, 64 trees of up to 61 nodes in bf16 41 to 52 us (greedy 18 to
+// 24 us, a pass a node of the path, and 17 to 22).  Two CTAs an SM with four vectors a lane ahead; three with two ahead take 14.2
+// to 27.8 and 37 to 50 us, four with two ahead (spills) 14.2 to 32.1 and 35 to 43.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
