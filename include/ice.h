@@ -815,9 +815,10 @@ typedef struct ice_probs {
  *  - A token outside [0, vocab) sets ICE_ERR_CAPACITY in err_dev and its node is
  *    not accepted; nodes that follow none (a second root) are not reached.
  *  - NaN and negative probabilities, of target and of draft, count as 0.  An
- *    infinite one of draft is refused and leaves its token no weight.  draft's
- *    row of a node is read only where a child of that node was refused, and at
- *    its children's tokens: rows of leaves may hold anything.
+ *    infinite one of draft is refused and leaves its token no weight; target's
+ *    have to be finite or NaN.  draft's row of a node is read only where a child
+ *    of that node was refused, and at its children's tokens: rows of leaves may
+ *    hold anything.
  *  - A row of no probability at all gives next_token -1 and ICE_ERR_INVALID_ARG
  *    in err_dev; greedy, none of its node's children is accepted (log-probabilities
  *    and logits are not probabilities).

@@ -406,12 +406,12 @@ struct Loader {
     __device__ __forceinline__ void node_k(uint32_t dst, int slot, const Segment &s, int b, int h, int j0, Info &info) {
         const int c = lane & 15;
         bool odd = false, bad = false;
-        // the power of two of a row, from its finite elements
-        auto power = [&](const float (&x)[8]) {
+        // the power of two of a row, from its finite elements (a key of infinities has a power of 1 at least: times a smaller one
+        // and a small factor its scores would be 0 times infinity)
+        auto power = [&](const float (&x)[8], float infinite) {
             float big = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (fabsf(x[e]) < INFINITY) big = fmaxf(big, fabsf(x[e]));
+            for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : infinite);
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
             return exponent_for(big);
@@ -432,7 +432,7 @@ struct Loader {
             float x[8], y[8];
             kk.get(x);
             vv.get(y);
-            const int ek = power(x), ev = power(y);  // (the softmax needs V's with the scores, before V itself is put)
+            const int ek = power(x, 1.f), ev = power(y, 0.f);  // (the softmax needs V's with the scores, before V itself is put)
             const float f = pow2(-ek);
             sts128(dst + (c >> 3) * kHalfBytes + token * 128 + (((c & 7) ^ (token & 7)) << 4),
                    half2_of(x[0] * f, x[4] * f), half2_of(x[1] * f, x[5] * f), half2_of(x[2] * f, x[6] * f),

@@ -163,3 +163,38 @@ def test_elements_far_below_their_row(small, v_scale):
                 + (2.0 ** -18 + 2.0 ** -8) * o.abs()
             off = (c.O[b, :n, j].double() - o).abs()
             assert bool((off <= tol).all()), (b, j, float((off / tol).max()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rest,qs", [(1e-38, 1.0), (1e-38, 1e-4), (1e-38, 1e-30), (1.0, 1.0), (1e30, 1.0)])
+def test_a_key_of_minus_infinity_beside_any_others(rest, qs, dtype):
+    """A node's key with one element of -inf and others of any size: its score is -inf, so that it weighs nothing with rows that
+    see others too, and gives NaN alone."""
+    c = Case(2, 6, 8, 2, dtype, True, [40, 0], seed=41, counts=[6, 6])
+    c.parents_dev.copy_(torch.tensor([[-1, 0, 1, -1, 3, 2]] * 2, dtype=torch.int32))
+    c.parents = [[-1, 0, 1, -1, 3, 2]] * 2
+    c.q.abs_().add_(0.01).mul_(qs)
+    c.k[:, 1].mul_(rest)
+    c.k[:, 1, :, 7] = -math.inf
+    c.k[1, 3].mul_(rest)
+    c.k[1, 3, :, 100] = -math.inf
+    c.run()
+    assert ice.ice_check(c.err) == ice.ICE_OK
+    for b in range(2):
+        n = c.counts[b]
+        own = ref.sees(c.parents[b], n, "cuda")
+        for j in range(c.hq):
+            h = j // 4
+            k0, v0 = c.cached(b, h)
+            k1, v1 = torch.cat((k0, c.k[b, :n, h].double())), torch.cat((v0, c.v[b, :n, h].double()))
+            # a node of -inf has no part in anything
+            gone = torch.isinf(k1).any(-1)
+            keep = torch.cat((torch.ones((n, k0.shape[0]), dtype=torch.bool, device="cuda"), own), 1) & ~gone
+            k1[gone] = 0
+            alone = ~keep.any(-1)  # (the second sequence's node 3: a root without cached tokens)
+            q, got = c.q[b, :n, j].double(), c.O[b, :n, j].double()
+            assert bool(torch.isnan(got[alone]).all()) and alone.tolist() == [b == 1 and i == 3 for i in range(n)]
+            q, got, keep = q[~alone], got[~alone], keep[~alone]
+            want, tol = ref.attention(q, k1, v1, keep, c.scale), ref.tolerance(q, k1, v1, keep, c.scale, c.dt)
+            off = (got - want).norm(dim=-1)
+            assert bool((off <= tol).all()), (b, j, float((off / tol).max()))
